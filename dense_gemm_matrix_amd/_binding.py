@@ -61,6 +61,7 @@ DGEMM_ERR_TOO_LARGE = 5
 DGEMM_ERR_DEVICE = 6
 DGEMM_ERR_LAUNCH = 7
 DGEMM_ERR_SCRATCH_SIZE = 8
+DGEMM_ERR_WORKSPACE = 9
 DGEMM_STATIC_SCRATCH_BYTES = 32 << 20
 DGEMM_OUT_F32 = 0
 DGEMM_OUT_SAME = 1

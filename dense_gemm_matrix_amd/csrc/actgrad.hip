@@ -1,0 +1,178 @@
+// actgrad.hip -- the elementwise half of a linear layer's backward pass, for
+// gfx950 (MI355X): dZ = dC act'(Z) with the bias gradient's column sums, the
+// reduction that finishes column sums, and the fp32 transpose.
+//
+// dZ is written in the products' input format: the matrix instructions take
+// 16-bit operands, so for 16-bit layers this is the one rounding between dC and
+// the gradients (half a step, 2^-9 relative for bf16, below the rounding of the
+// gradients it feeds).  dbias sums the unrounded fp32 values.
+
+#include "kern_common.h"
+
+namespace dgemm {
+namespace {
+
+// act'(z) times d, with the forward's own forms (kern_common.h):
+//   z sigmoid(p), p = a z + b z^3:  s (1 + z (1 - s)(a + 3 b z^2)), s = sigmoid(p)
+//   z Phi(z):                       Phi(z) + z phi(z)
+//   relu:                           z > 0
+// Far out, s (1 - s) is 0 while z^3 stays finite, so the product is 0; where
+// z^2 itself overflows, the factor is taken as 0 or 1 by z's sign.
+template <int NE>
+__device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[NE], int act) {
+    if (act >= ACT_GELU_TANH) {
+        const float a = gate_a(act), b = gate_b(act);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const float s = gate(z[i], a, b);
+            const float f = s + z[i] * (s * (1.0f - s)) * (a + 3.0f * b * z[i] * z[i]);
+            const float far = z[i] > 0.0f ? 1.0f : 0.0f;
+            d[i] *= __builtin_fabsf(z[i]) > 1e4f ? far : f;
+        }
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) {
+            const float x = z[i];
+            const float phi = 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * LOG2E * x * x);
+            const float far = x > 0.0f ? 1.0f : 0.0f;
+            const float f = 0.5f * (1.0f + erff(x * 0.7071067811865476f)) + x * phi;
+            d[i] *= __builtin_fabsf(x) > 1e4f ? far : f;
+        }
+    } else if (act == ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) d[i] = z[i] > 0.0f ? d[i] : (z[i] != z[i] ? z[i] : 0.0f);
+    }
+}
+
+constexpr int AG_COLS = 512;     // columns per workgroup: 64 lanes x 8
+constexpr int AG_LANES = 4;      // rows at a time
+
+// One workgroup: columns blockIdx.x * 512 .., rows blockIdx.y * rows_per ...
+// Wave w takes every fourth row; the four waves' column sums are added in LDS in
+// wave order and go to the workspace, one row of partial sums per blockIdx.y.
+template <int CF, int DF>
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
+    __shared__ float sums[AG_LANES][AG_COLS];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c = (int)blockIdx.x * AG_COLS + lane * 8;
+    const int nvalid = a.N - c;
+    const int64_t r0 = (int64_t)blockIdx.y * a.rows_per;
+    const int64_t r1 = r0 + a.rows_per < a.M ? r0 + a.rows_per : a.M;
+    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (nvalid > 0) {
+#pragma unroll 2
+        for (int64_t row = r0 + wave; row < r1; row += AG_LANES) {
+            Row8<CF> x, zz;
+            const auto rc = make_rsrc(a.dC + row * a.lddc * fmt_es<CF>, (int64_t)a.N * fmt_es<CF>);
+            x.load(rc, (uint32_t)c * fmt_es<CF>, nvalid);
+            float d[8];
+            if (a.Z) {
+                const auto rz = make_rsrc(a.Z + row * a.ldz * fmt_es<CF>, (int64_t)a.N * fmt_es<CF>);
+                zz.load(rz, (uint32_t)c * fmt_es<CF>, nvalid);
+                float z[8];
+                x.get(d);
+                zz.get(z);
+                apply_act_grad(d, z, a.act);
+            } else {
+                x.get(d);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] += d[j];
+            if (a.dZ) {
+                const auto rd = make_rsrc(a.dZ + row * a.lddz * fmt_es<DF>, (int64_t)a.N * fmt_es<DF>);
+                Row8<DF> o;
+                o.set(d);
+                o.store(rd, (uint32_t)c * fmt_es<DF>, nvalid);
+            }
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = sum[j];
+    __syncthreads();
+    for (int j = threadIdx.x; j < AG_COLS; j += 256) {
+        const int col = (int)blockIdx.x * AG_COLS + j;
+        if (col >= a.N) break;
+        a.part[(int64_t)blockIdx.y * a.ldp + col] =
+            ((sums[0][j] + sums[1][j]) + sums[2][j]) + sums[3][j];
+    }
+}
+
+template <int CF, int DF>
+hipError_t go_ag(const ActGradArgs& a, hipStream_t stream) {
+    ActGradArgs b = a;
+    void* args[] = {&b};
+    return hipLaunchKernel((const void*)act_grad_kernel<CF, DF>,
+                           dim3((unsigned)((a.N + AG_COLS - 1) / AG_COLS),
+                                (unsigned)((a.M + a.rows_per - 1) / a.rows_per)),
+                           dim3(256), args, 0, stream);
+}
+
+// out[n] = sum over g < G of part[g][n], in a fixed order: 16 threads per column
+// take every sixteenth row, then LDS adds the sixteen.
+__global__ __launch_bounds__(1024) void col_reduce_kernel(const float* part, int G, int ldp, int N,
+                                                          float* out) {
+    __shared__ float s[16][64];
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int col = (int)blockIdx.x * 64 + lane;
+    float v = 0.0f;
+    if (col < N)
+        for (int g = q; g < G; g += 16) v += part[(int64_t)g * ldp + col];
+    s[q][lane] = v;
+    __syncthreads();
+    if (q == 0 && col < N) {
+        for (int i = 1; i < 16; ++i) v += s[i][lane];
+        out[col] = v;
+    }
+}
+
+// Y[n][m] = X[m][n], fp32, in 64 x 64 tiles through LDS (rows padded to 65 words).
+__global__ __launch_bounds__(256) void transpose32_kernel(const float* X, int ldx, int M, int N,
+                                                          float* Y, int ldy, int tiles_n) {
+    __shared__ float tile[64][65];
+    const int m0 = (int)(blockIdx.x / tiles_n) * 64, n0 = (int)(blockIdx.x % tiles_n) * 64;
+    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
+    for (int i = r; i < 64; i += 4)
+        if (m0 + i < M && n0 + c < N) tile[i][c] = X[(int64_t)(m0 + i) * ldx + n0 + c];
+    __syncthreads();
+    for (int i = r; i < 64; i += 4)
+        if (n0 + i < N && m0 + c < M) Y[(int64_t)(n0 + i) * ldy + m0 + c] = tile[c][i];
+}
+
+}  // namespace
+
+// Rows per workgroup of act_grad_kernel: at most 256 rows of partial sums, and
+// no fewer than 8 rows each.
+int act_grad_rows(int M) {
+    const int64_t r = ((int64_t)M + 255) / 256;
+    return (int)(r < 8 ? 8 : (r + 3) / 4 * 4);
+}
+
+hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream) {
+    if (cf == OUT_F32 && df == OUT_F32) return go_ag<OUT_F32, OUT_F32>(a, stream);
+    if (cf == OUT_F32 && df == OUT_BF16) return go_ag<OUT_F32, OUT_BF16>(a, stream);
+    if (cf == OUT_F32 && df == OUT_F16) return go_ag<OUT_F32, OUT_F16>(a, stream);
+    if (cf == OUT_BF16 && df == OUT_BF16) return go_ag<OUT_BF16, OUT_BF16>(a, stream);
+    if (cf == OUT_F16 && df == OUT_F16) return go_ag<OUT_F16, OUT_F16>(a, stream);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_col_reduce(const float* part, int G, int ldp, int N, float* out,
+                             hipStream_t stream) {
+    void* args[] = {&part, &G, &ldp, &N, &out};
+    return hipLaunchKernel((const void*)col_reduce_kernel, dim3((unsigned)((N + 63) / 64)), dim3(1024),
+                           args, 0, stream);
+}
+
+hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,
+                              hipStream_t stream) {
+    const int64_t tm = (M + 63) / 64, tn = (N + 63) / 64;
+    if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
+    int tiles_n = (int)tn;
+    void* args[] = {&X, &ldx, &M, &N, &Y, &ldy, &tiles_n};
+    return hipLaunchKernel((const void*)transpose32_kernel, dim3((unsigned)(tm * tn)), dim3(256), args,
+                           0, stream);
+}
+
+}  // namespace dgemm

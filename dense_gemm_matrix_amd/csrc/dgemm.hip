@@ -15,17 +15,17 @@
 
 #include "dgemm.h"
 #include "dgemm_internal.h"
+#include "plan.h"
 
 namespace dgemm {
 namespace {
-
-constexpr int64_t DESC_LIMIT = (int64_t)1 << 31;  // 32-bit buffer offsets
-constexpr int PANEL_ROWS = 256;                   // rows of A one descriptor spans
 
 // K per step: the k rows of B one descriptor spans.
 int bk_of(int in) { return (in == IN_BF16 || in == IN_F16) ? 64 : 32; }
 
 std::atomic<int> g_device_state[256];  // 0 unknown, 1 gfx950, 2 other
+
+}  // namespace
 
 int check_device() {
     int dev = -1;
@@ -40,25 +40,26 @@ int check_device() {
     return st == 1 ? DGEMM_OK : DGEMM_ERR_DEVICE;
 }
 
+namespace {
+
 bool ranges_overlap(uintptr_t a0, int64_t alen, uintptr_t b0, int64_t blen) {
     if (alen <= 0 || blen <= 0) return false;
     return a0 < b0 + (uintptr_t)blen && b0 < a0 + (uintptr_t)alen;
 }
 
-// The bytes a row-major operand occupies: `rows` rows of `row_bytes` each,
-// `pitch` bytes apart.  A contiguous range is one row.
-struct Span {
-    uintptr_t base;
-    int64_t rows, row_bytes, pitch;
-};
+}  // namespace
 
 Span matrix_span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t esize) {
     return Span{(uintptr_t)p, rows, cols * esize, ld * esize};
 }
 
+namespace {
+
 int64_t floor_div(int64_t a, int64_t b) {  // b > 0
     return a >= 0 ? a / b : -((-a + b - 1) / b);
 }
+
+}  // namespace
 
 // Whether any byte of x's rows is also a byte of y's rows.  With equal pitches
 // (a one-row span takes the other's pitch) row i of x and row j of y overlap
@@ -111,6 +112,8 @@ int validate(int M, int N, int K, const void* A, int lda, const void* B, int ldb
     return DGEMM_OK;
 }
 
+namespace {
+
 // ------------------------------------------------------------------ planning
 //
 // Macro-tile and split-K choice by an estimated time: for a candidate tile
@@ -160,19 +163,10 @@ int validate(int M, int N, int K, const void* A, int lda, const void* B, int ldb
 // fp32 (9 shapes): the fastest on all; 3 x bf16 (12 shapes, after the 128 x 128
 // tile's two staging sets): the fastest on 10, within 7.2 % on all.
 
-constexpr int MAX_SPLITS = 16;
 constexpr double WG_FIXED_US = 1.0;       // prologue + epilogue per round of workgroups
 constexpr double REDUCE_FIXED_US = 3.0;   // launch and tail of the reduction kernel
 constexpr double HBM_BYTES_PER_US = 5.0e6;
-constexpr double SPLIT_MARGIN = 0.9;      // a split plan must be predicted 10% faster
 
-// pair = 0: one workgroup per CU.  fp32 has the 128 x 128 tile only: in a
-// sweep of forced plans 256 x 256 was slower at every shape (4096^3: 1049 us
-// against 1002 us), and the cost model never chose it; eff stays relative to
-// a 256 x 256 workgroup so that step_us keeps one meaning.
-// `pair2`: the pair factor of grids of two or more rounds of pairs; `last`: the
-// cost of a last, partly filled round at zero fill (1: whole rounds).
-struct TileCand { int bm, bn; double eff, pair, pair2, eff1, last; };
 constexpr TileCand TILES16[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6},
                                 {192, 256, 0.95, 0.0, 0.0, 0.95, 0.6},
                                 {128, 128, 0.6, 1.26, 1.35, 0.8, 1.0}};
@@ -206,28 +200,21 @@ const TileCand* tiles_for(int in, int& n) {
     return TILES32X3;
 }
 
+}  // namespace
+
 // Microseconds per K step of one 256 x 256 workgroup at 4096^3.
 double step_us(int in) {
     switch (in) {
     case IN_BF16:
     case IN_F16: return 1.7;   // BK 64
+    case IN_F8: return 1.7;    // BK 128 at twice the matrix rate
+    case IN_F8W: return 3.4;   // BK 128 at the bf16 rate
     case IN_F32X3: return 3.5; // BK 32, three bf16 products per term
     default: return 8.3;       // BK 32, fp32 matrix instruction
     }
 }
 
-enum PlanKind { PLAN_GRID = 0, PLAN_STREAM_K = 1 };
-
-struct Plan {
-    int bm, bn;
-    int splits, kchunk;   // kchunk: K per split (a multiple of the K step)
-    int ldw;              // row pitch of the fp32 partials, in elements
-    int64_t ws_bytes;     // workspace the plan uses (0 when unsplit)
-    int kind = PLAN_GRID;
-    int waves = 0;        // slice-K plans: waves per workgroup (0: a grid plan)
-};
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+namespace {
 
 // ------------------------------------------------------------------ slice-K
 //
@@ -387,6 +374,8 @@ TileCand pick_tile(int in, int M, int N) {
     return best;
 }
 
+}  // namespace
+
 double estimate_us(int in, int es_out, int M, int N, const TileCand& t, int splits,
                    int steps_per_split, int ldw) {
     const int64_t tiles = ceil_div(M, t.bm) * ceil_div(N, t.bn);
@@ -399,6 +388,8 @@ double estimate_us(int in, int es_out, int M, int N, const TileCand& t, int spli
                                     HBM_BYTES_PER_US;
     return us;
 }
+
+namespace {
 
 // ------------------------------------------------------------------ Stream-K
 //
@@ -500,6 +491,16 @@ Plan make_plan_auto(int in, int es_out, int M, int N, int K, uint64_t ws_avail, 
     return plan;
 }
 
+}  // namespace
+
+bool forced_grid(int& bm, int& bn, int& splits) {
+    if (g_override_kind.load(std::memory_order_relaxed) != DGEMM_PLAN_GRID) return false;
+    bm = g_override_bm.load(std::memory_order_relaxed);
+    bn = g_override_bn.load(std::memory_order_relaxed);
+    splits = g_override_splits.load(std::memory_order_relaxed);
+    return true;
+}
+
 // The plan of a call: the override when one is set and this call can take
 // it, else the estimate's choice.
 Plan make_plan(int in, int es_out, int M, int N, int K, uint64_t ws_avail, bool allow_sk) {
@@ -543,6 +544,8 @@ Plan make_plan(int in, int es_out, int M, int N, int K, uint64_t ws_avail, bool 
     return make_plan_auto(in, es_out, M, N, K, ws_avail, allow_sk && kind != DGEMM_PLAN_NO_STREAM_K);
 }
 
+namespace {
+
 // Stream-K launches tag their partials with a value no earlier launch used:
 // a process-wide counter from a start drawn from the clock and an address, so
 // that flags another process left in a reused buffer are not taken either.
@@ -579,22 +582,28 @@ bool capturing(hipStream_t stream) {
     return st != hipStreamCaptureStatusNone;
 }
 
-bool epi_needed(const EpiArgs& e) {
-    return e.alpha != 1.0f || e.beta != 0.0f || e.bias != nullptr || e.relu != 0;
+int epi_needed(const EpiArgs& e) {
+    const bool basic = e.alpha != 1.0f || e.beta != 0.0f || e.bias != nullptr || e.relu != 0;
+    return basic ? EPI_BASIC : EPI_NONE;
 }
 
-hipError_t launch_family(const GemmLaunch& L) {
+hipError_t launch_family(const GemmLaunch& L, int kind) {
+    if (kind == PLAN_SKINNY) return launch_skinny(L);
+    if (L.layout != LAY_NN) return launch_gemmt(L);
     if (L.in == IN_BF16 || L.in == IN_F16)
         return L.slice_waves > 0 ? launch_slicek16(L) : launch_gemm16(L);
     return launch_gemm32(L);
 }
 
+}  // namespace
+
 // Validated arguments and a plan -> one GEMM launch, a split GEMM into the
 // workspace followed by the reduction, or a Stream-K launch.
 int run(int in, int outfmt, int M, int N, int K, const void* A, int lda, const void* B, int ldb,
-        void* C, int ldc, const EpiArgs& e, const Plan& p, void* ws, hipStream_t stream) {
+        void* C, int ldc, const EpiArgs& e, int epi, const Plan& p, void* ws, hipStream_t stream) {
     GemmLaunch L{};
     L.in = in;
+    L.layout = p.layout;
     L.tbm = p.bm;
     L.tbn = p.bn;
     L.A = (const char*)A;
@@ -613,11 +622,11 @@ int run(int in, int outfmt, int M, int N, int K, const void* A, int lda, const v
     // no second one to hide load latency, and a 4-stage ring (128 KiB, loads
     // issued three steps ahead) measured 17-27 % faster.
     const int64_t wgs = (int64_t)L.tiles_m * L.tiles_n * p.splits;
-    L.stages = (p.bm == 128 && (in == IN_BF16 || in == IN_F16) && wgs <= NUM_CU) ? 4 : 2;
+    L.stages = (p.bm == 128 && in != IN_F32 && in != IN_F32X3 && wgs <= NUM_CU) ? 4 : 2;
     L.slice_waves = p.waves;
     if (p.kind == PLAN_STREAM_K) {
         L.out = outfmt;
-        L.epi = epi_needed(e);
+        L.epi = epi;
         L.C = (char*)C;
         L.ldc = ldc;
         L.splits = 1;
@@ -635,26 +644,26 @@ int run(int in, int outfmt, int M, int N, int K, const void* A, int lda, const v
     }
     if (p.splits == 1) {
         L.out = outfmt;
-        L.epi = epi_needed(e);
+        L.epi = epi;
         L.C = (char*)C;
         L.ldc = ldc;
         L.splits = 1;
         L.kchunk = K;
         L.c_zstride = 0;
         L.e = e;
-        return launch_family(L) == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH;
+        return launch_family(L, p.kind) == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH;
     }
     L.out = OUT_F32;
-    L.epi = false;
+    L.epi = EPI_NONE;
     L.C = (char*)ws;
     L.ldc = p.ldw;
     L.splits = p.splits;
     L.kchunk = p.kchunk;
     L.c_zstride = (int64_t)M * p.ldw * 4;
     L.e = EpiArgs{1.0f, 0.0f, nullptr, 0};
-    if (launch_family(L) != hipSuccess) return DGEMM_ERR_LAUNCH;
+    if (launch_family(L, p.kind) != hipSuccess) return DGEMM_ERR_LAUNCH;
     const hipError_t r = launch_splitk_reduce((const float*)ws, p.splits, (int64_t)M * p.ldw, p.ldw,
-                                              (char*)C, ldc, M, N, outfmt, epi_needed(e), e, stream);
+                                              (char*)C, ldc, M, N, outfmt, epi, e, stream);
     return r == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH;
 }
 
@@ -663,6 +672,8 @@ int out_format(int in, int out) {
     if (out == DGEMM_OUT_F32 || in == IN_F32 || in == IN_F32X3) return OUT_F32;
     return in == IN_BF16 ? OUT_BF16 : OUT_F16;
 }
+
+namespace {
 
 // The plain entry points: no epilogue, no workspace.  For fp32 inputs `out`
 // must be DGEMM_OUT_F32.
@@ -677,8 +688,8 @@ int gemm_plain(int in, int M, int N, int K, const void* A, int lda, const void* 
     st = check_device();
     if (st != DGEMM_OK) return st;
     const Plan p = make_plan_auto(in, out_esize(of), M, N, K, 0, false);
-    return run(in, of, M, N, K, A, lda, B, ldb, C, ldc, EpiArgs{1.0f, 0.0f, nullptr, 0}, p, nullptr,
-               (hipStream_t)stream);
+    return run(in, of, M, N, K, A, lda, B, ldb, C, ldc, EpiArgs{1.0f, 0.0f, nullptr, 0}, EPI_NONE, p,
+               nullptr, (hipStream_t)stream);
 }
 
 // Device memory of gemm_ex_static's split-K partials: one array on every GPU
@@ -750,7 +761,8 @@ int gemm_ex_impl(int in, int out, int M, int N, int K, const void* A, int lda, c
             workspace_bytes = 0;
         }
     }
-    return run(in, of, M, N, K, A, lda, B, ldb, C, ldc, EpiArgs{alpha, beta, bias, act}, p, workspace,
+    const EpiArgs e{alpha, beta, bias, act};
+    return run(in, of, M, N, K, A, lda, B, ldb, C, ldc, e, epi_needed(e), p, workspace,
                (hipStream_t)stream);
 }
 
@@ -894,6 +906,8 @@ const char* dgemm_status_string(int status) {
     case DGEMM_ERR_SCRATCH_SIZE:
         return "DGEMM_ERR_SCRATCH_SIZE: scratch_bytes exceeds the static scratch array "
                "(DGEMM_STATIC_SCRATCH_BYTES)";
+    case DGEMM_ERR_WORKSPACE:
+        return "DGEMM_ERR_WORKSPACE: the workspace is smaller than the call needs";
     default: return "DGEMM: unknown status";
     }
 }

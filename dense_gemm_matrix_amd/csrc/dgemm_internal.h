@@ -9,7 +9,10 @@
 
 namespace dgemm {
 
-enum InFmt { IN_F32 = 0, IN_BF16 = 1, IN_F16 = 2, IN_F32X3 = 3 };  // F32X3: fp32 via 3 x bf16
+enum InFmt { IN_F32 = 0, IN_BF16 = 1, IN_F16 = 2, IN_F32X3 = 3,  // F32X3: fp32 via 3 x bf16
+             // e4m3 (gemm_f8): on the 8-bit matrix instructions, and with the values
+             // widened to bf16 for the fp32 accumulation of fp32 outputs
+             IN_F8 = 4, IN_F8W = 5 };
 enum OutFmt { OUT_F32 = 0, OUT_BF16 = 1, OUT_F16 = 2 };
 
 constexpr int NTHREADS = 256;   // 4 waves: the fp32 kernels' workgroup
@@ -17,7 +20,7 @@ constexpr int GROUP_M = 4;      // tile rows per strip in the tile walk
 constexpr int NUM_XCD = 8;      // XCDs that workgroups are dealt across
 constexpr int NUM_CU = 256;     // compute units of an MI355X
 
-inline int in_esize(int in) { return (in == IN_F32 || in == IN_F32X3) ? 4 : 2; }
+inline int in_esize(int in) { return (in == IN_F32 || in == IN_F32X3) ? 4 : in >= IN_F8 ? 1 : 2; }
 inline int out_esize(int out) { return out == OUT_F32 ? 4 : 2; }
 
 // Workgroup -> output tile.  Step 1: workgroups are dealt to XCDs in turn, so
@@ -42,14 +45,35 @@ __host__ __device__ inline void map_tile(int wg, int tiles_m, int tiles_n, int& 
     tn = rem / rows_in_strip;
 }
 
-// Fused epilogue: C := act(alpha * acc + beta * C_old + bias[col]).  C_old is
-// read only when beta != 0; bias may be NULL; relu != 0 clamps negatives to 0.
+// Epilogue levels of the GEMM kernels.
+//   EPI_BASIC (gemm_ex): C := relu(alpha * acc + beta * C_old + bias[col]).
+//     C_old is read only when beta != 0; bias may be NULL; relu != 0 clamps
+//     negatives to 0.
+//   EPI_FULL (gemm_act, gemm_f8): z := acc * scale_a[row] * scale_b[col] +
+//     bias[col]; Z := z; C := act(z) + R.  The scales, bias, Z and R may be
+//     NULL; Z and R have C's format.
+enum EpiLevel { EPI_NONE = 0, EPI_BASIC = 1, EPI_FULL = 2 };
+
 struct EpiArgs {
     float alpha;
     float beta;
     const float* bias;
     int relu;
+    // EPI_FULL only
+    int act;               // a dgemm_act code
+    const char* res;       // R, row pitch ldr
+    char* pre;             // Z, row pitch ldz
+    int ldr, ldz;
+    const float* scale_a;  // both or neither
+    const float* scale_b;
 };
+
+// dgemm_act codes, for the device code.
+enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+// How the operands lie in memory: A[M x K] B[K x N]; A[M x K] B[N x K] (both
+// K-contiguous); A[K x M] B[K x N].
+enum Layout { LAY_NN = 0, LAY_NT = 1, LAY_TN = 2 };
 
 // One GEMM launch.  The grid is (tiles_m * tiles_n, splits): workgroup
 // (x, z) computes tile map_tile(x) over k in [z * kchunk, min(K, (z + 1) *
@@ -57,9 +81,10 @@ struct EpiArgs {
 // splits = 1 and kchunk = K.
 struct GemmLaunch {
     int in, out, tbm, tbn;
+    int layout;  // a Layout; the transposed ones are gemmt.hip's
     int stages;  // LDS stages of the 16-bit kernel's 128 x 128 tile (2, or 4 alone on a CU)
     int slice_waves;  // waves per workgroup of a slice-K launch (0: a grid launch)
-    bool epi;    // apply `e` in the kernel (only with splits == 1)
+    int epi;     // the EpiLevel at which the kernel applies `e` (only with splits == 1)
     const char* A;
     const char* B;
     char* C;
@@ -182,12 +207,72 @@ hipError_t launch_gemm16(const GemmLaunch& L);  // IN_BF16, IN_F16
 // splits = 1; `grid` workgroups, a multiple of NUM_XCD.
 hipError_t launch_gemm16_sk(const GemmLaunch& L, const SkSched& s, int grid);
 hipError_t launch_gemm32(const GemmLaunch& L);  // IN_F32, IN_F32X3
+hipError_t launch_gemmt(const GemmLaunch& L);   // LAY_NT, LAY_TN: 16-bit; LAY_NT: IN_F8, IN_F8W
 hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_waves > 0
+
+// Products of at most SKINNY_M rows (skinny.hip): 16-bit LAY_NN, IN_F8W LAY_NT.
+// L.tbn names the strip of columns per workgroup, L.slice_waves the waves that
+// share a strip's K; splits, kchunk and the partials' C as for a grid launch.
+constexpr int SKINNY_M = 16;
+hipError_t launch_skinny(const GemmLaunch& L);
 
 // Split-K reduction: C[i][j] = epilogue(sum_{z < splits} W[z][i][j]) with W
 // fp32, row pitch ldw (a multiple of 4) and split stride zstride elements.
 hipError_t launch_splitk_reduce(const float* W, int splits, int64_t zstride, int ldw, char* C,
-                                int ldc, int M, int N, int out, bool epi, const EpiArgs& e,
+                                int ldc, int M, int N, int out, int epi, const EpiArgs& e,
                                 hipStream_t stream);
+
+// ------------------------------------------- norms, quantizers, activations
+
+constexpr int ROW_MAX = 32768;       // longest row of the norm and the row quantizer
+constexpr int NORM_BWD_MAX = 16384;  // of the norm's backward pass
+
+// A pass over the rows of X (norm.hip).  R, S, rstd may be NULL; Y is in X's
+// format, or e4m3 with `scale` (per row; per column for launch_quant_cols,
+// which writes Y transposed and uses X, Y and scale only).
+struct RowArgs {
+    const char* X;
+    const char* R;
+    char* S;
+    const float* weight;
+    char* Y;
+    float* scale;
+    float* rstd;
+    float eps;
+    int M, N, ldx, ldr, lds, ldy;
+};
+hipError_t launch_rows(const RowArgs& a, int fmt, bool norm, bool f8, hipStream_t stream);
+hipError_t launch_quant_cols(const RowArgs& a, int fmt, hipStream_t stream);
+
+// The norm's backward pass; part: norm_bwd_grid(M, N) rows of ldp fp32 partial
+// sums of dweight, or NULL.
+struct NormBwdArgs {
+    const char* dY;
+    const char* S;
+    const char* dS;
+    const float* weight;
+    const float* rstd;
+    char* dX;
+    float* part;
+    int M, N, lddy, lds, ldds, lddx, ldp;
+};
+int norm_bwd_grid(int M, int N);
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream);
+
+// dZ = dC act'(Z) (actgrad.hip).  Z NULL: dZ = dC.  dZ may be NULL; part: one row
+// of ldp fp32 column sums per rows_per rows, or NULL.
+struct ActGradArgs {
+    const char* dC;
+    const char* Z;
+    char* dZ;
+    float* part;
+    int M, N, lddc, ldz, lddz, ldp, rows_per, act;
+};
+int act_grad_rows(int M);
+hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream);
+hipError_t launch_col_reduce(const float* part, int G, int ldp, int N, float* out,
+                             hipStream_t stream);
+hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,
+                              hipStream_t stream);
 
 }  // namespace dgemm

@@ -46,14 +46,10 @@
 #include <type_traits>
 
 #include "kern_common.h"
+#include "stage16.h"
 
 namespace dgemm {
 namespace {
-
-constexpr int BKA = 64;                        // K per A slab
-constexpr int A16_CH = BKA / 8;                // 16-byte chunks per A row
-constexpr int A16_ROW = BKA * 2;               // bytes per staged A row
-constexpr int A16_RPB = 1024 / A16_ROW;        // A rows per 1 KiB load block
 
 enum Sched16 { SLAB2 = 0, RING = 1 };
 
@@ -90,23 +86,6 @@ struct Tile16 {
                   "stages, vmcnt range");
     static_assert(NREAD <= 15, "lgkmcnt range");
 };
-
-// Byte offset of chunk c (0..7) of A row r in a slab.  ds_read_b128 serves
-// groups of 4 consecutive lanes from a 64-byte window of banks (measured on
-// gfx950 with SQ_LDS_BANK_CONFLICT), and the 4 lanes of a group read 4
-// consecutive rows at one chunk: a16_phi gives those rows 4 distinct slots.
-__device__ __forceinline__ int a16_phi(int row) { return (row ^ (row >> 2)) & (A16_CH - 1); }
-__device__ __forceinline__ int a16_off(int row, int chunk) {
-    return row * A16_ROW + ((chunk ^ a16_phi(row)) << 4);
-}
-// Byte offset of chunk c of B row k in a stage with row pitch `row_bytes` (a
-// multiple of 256).  ds_read_b64_tr_b16 serves 32 lanes from a 256-byte
-// window (measured), and those 32 lanes read 4 consecutive k rows x 64 bytes;
-// the XOR puts the four rows' pieces in distinct quarters of the window.
-__device__ __forceinline__ int b16_swz(int k) { return ((k & 3) << 1) ^ ((k & 1) << 3); }
-__device__ __forceinline__ int b16_off(int k, int chunk, int row_bytes) {
-    return k * row_bytes + ((chunk ^ b16_swz(k)) << 4);
-}
 
 // The K loop of one macro-tile: acc := A[m0 .. m0 + TBM) x B[.., n0 .. n0 + TBN)
 // over k in [0, K), with A and B already offset to the first k and rows_a /
@@ -461,7 +440,7 @@ __device__ __forceinline__ void mainloop16(const char* __restrict__ A, const cha
 }
 
 // One macro-tile per workgroup: tile map_tile(blockIdx.x), k range blockIdx.y.
-template <int IN, int OUT, int TBM, int TBN, bool EPI, bool PAIRS, int SCHED, int S>
+template <int IN, int OUT, int TBM, int TBN, int EPI, bool PAIRS, int SCHED, int S>
 __global__ __launch_bounds__(256) void gemm16_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* __restrict__ C,
     int M, int N, int K, int lda, int ldb, int ldc, int tiles_m, int tiles_n,
@@ -488,8 +467,16 @@ __global__ __launch_bounds__(256) void gemm16_kernel(
     mainloop16<IN, TBM, TBN, SCHED, S>(A, B, K, lda, ldb, m0, n0, rows_a, cols_b, smem, acc);
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    store_tile<OUT, T::MI, T::NJ, EPI, PAIRS>(acc, C, M, N, ldc, m0 + (wave >> 1) * (TBM / 2),
-                                              n0 + (wave & 1) * (TBN / 2), lane >> 5, lane & 31, epi);
+    const int row0 = m0 + (wave >> 1) * (TBM / 2), col0 = n0 + (wave & 1) * (TBN / 2);
+    if constexpr (EPI == EPI_FULL) {
+        static_assert(4 * full_lds<T::NJ> <= T::LDS, "LDS for the full epilogue");
+        __syncthreads();  // every wave is done with the operand ring
+        store_tile_full<OUT, T::MI, T::NJ>(acc, C, M, N, ldc, row0, col0, lane, epi,
+                                           smem + wave * full_lds<T::NJ>);
+    } else {
+        store_tile<OUT, T::MI, T::NJ, EPI, PAIRS>(acc, C, M, N, ldc, row0, col0, lane >> 5,
+                                                  lane & 31, epi);
+    }
 }
 
 // ------------------------------------------------------------------ Stream-K
@@ -531,7 +518,7 @@ constexpr int SK_BATCH = 8;  // contributors whose partials are loaded ahead of 
 // accumulator layout the slot keeps).  Every partial is in its slot and
 // visible to this workgroup.  A function of its own (arguments in registers),
 // so that its registers are allocated apart from the K loop's.
-template <int OUT, bool EPI, bool PAIRS>
+template <int OUT, int EPI, bool PAIRS>
 __device__ __attribute__((noinline)) void sk_reduce(int x, int j, int W, int nk, int u, int tm,
                                                     int tn, const char* part, char* C, int M,
                                                     int N, int ldc, int wave, int lane,
@@ -581,7 +568,7 @@ __device__ __attribute__((noinline)) void sk_reduce(int x, int j, int W, int nk,
     }
 }
 
-template <int IN, int OUT, bool EPI, bool PAIRS>
+template <int IN, int OUT, int EPI, bool PAIRS>
 __global__ __launch_bounds__(256) void gemm16_sk_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* __restrict__ C, int M, int N,
     int K, int lda, int ldb, int ldc, SkSched sk, EpiArgs epi) {
@@ -689,7 +676,7 @@ __global__ __launch_bounds__(256) void gemm16_sk_kernel(
     }
 }
 
-template <int IN, int OUT, bool EPI, bool PAIRS>
+template <int IN, int OUT, int EPI, bool PAIRS>
 hipError_t go_sk(const GemmLaunch& L, const SkSched& s, int grid) {
     const char* a = L.A;
     const char* b = L.B;
@@ -702,7 +689,7 @@ hipError_t go_sk(const GemmLaunch& L, const SkSched& s, int grid) {
                            dim3(256), args, 0, L.stream);
 }
 
-template <int IN, int OUT, bool EPI>
+template <int IN, int OUT, int EPI>
 hipError_t sk_by_pairs(const GemmLaunch& L, const SkSched& s, int grid) {
     if (OUT != OUT_F32 && L.N % 2 == 0) return go_sk<IN, OUT, EPI, true>(L, s, grid);
     return go_sk<IN, OUT, EPI, false>(L, s, grid);
@@ -710,10 +697,11 @@ hipError_t sk_by_pairs(const GemmLaunch& L, const SkSched& s, int grid) {
 
 template <int IN, int OUT>
 hipError_t sk_by_epi(const GemmLaunch& L, const SkSched& s, int grid) {
-    return L.epi ? sk_by_pairs<IN, OUT, true>(L, s, grid) : sk_by_pairs<IN, OUT, false>(L, s, grid);
+    return L.epi ? sk_by_pairs<IN, OUT, EPI_BASIC>(L, s, grid)
+                 : sk_by_pairs<IN, OUT, EPI_NONE>(L, s, grid);
 }
 
-template <int IN, int OUT, int TBM, int TBN, bool EPI, bool PAIRS, int SCHED, int S>
+template <int IN, int OUT, int TBM, int TBN, int EPI, bool PAIRS, int SCHED, int S>
 hipError_t go(const GemmLaunch& L) {
     const char* a = L.A;
     const char* b = L.B;
@@ -728,7 +716,7 @@ hipError_t go(const GemmLaunch& L) {
                            args, 0, L.stream);
 }
 
-template <int IN, int OUT, bool EPI, bool PAIRS>
+template <int IN, int OUT, int EPI, bool PAIRS>
 hipError_t by_tile(const GemmLaunch& L) {
     if (L.tbm == 256 && L.tbn == 256) return go<IN, OUT, 256, 256, EPI, PAIRS, SLAB2, 2>(L);
     if (L.tbm == 192 && L.tbn == 256) return go<IN, OUT, 192, 256, EPI, PAIRS, RING, 3>(L);
@@ -740,7 +728,7 @@ hipError_t by_tile(const GemmLaunch& L) {
 
 // 16-bit C with an even N stores lane pairs; fp32 C, and 16-bit C with an odd
 // N, one element per store.
-template <int IN, int OUT, bool EPI>
+template <int IN, int OUT, int EPI>
 hipError_t by_pairs(const GemmLaunch& L) {
     if (OUT != OUT_F32 && L.N % 2 == 0) return by_tile<IN, OUT, EPI, true>(L);
     return by_tile<IN, OUT, EPI, false>(L);
@@ -748,13 +736,15 @@ hipError_t by_pairs(const GemmLaunch& L) {
 
 template <int IN, int OUT>
 hipError_t by_epi(const GemmLaunch& L) {
-    return L.epi ? by_pairs<IN, OUT, true>(L) : by_pairs<IN, OUT, false>(L);
+    // The full epilogue stores whole row segments for any N.
+    if (L.epi == EPI_FULL) return by_tile<IN, OUT, EPI_FULL, false>(L);
+    return L.epi ? by_pairs<IN, OUT, EPI_BASIC>(L) : by_pairs<IN, OUT, EPI_NONE>(L);
 }
 
 }  // namespace
 
 hipError_t launch_gemm16_sk(const GemmLaunch& L, const SkSched& s, int grid) {
-    if (L.tbm != SK_TILE || L.tbn != SK_TILE || grid <= 0 || grid % NUM_XCD != 0 || s.nk <= 0)
+    if (L.epi == EPI_FULL || L.tbm != SK_TILE || L.tbn != SK_TILE || grid <= 0 || grid % NUM_XCD != 0 || s.nk <= 0)
         return hipErrorInvalidValue;
     if (L.in == IN_BF16) {
         if (L.out == OUT_F32) return sk_by_epi<IN_BF16, OUT_F32>(L, s, grid);

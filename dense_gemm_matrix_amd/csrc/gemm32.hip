@@ -72,7 +72,7 @@ __device__ __forceinline__ u32x4 mask_tail32(u32x4 v, int valid) {
 // Where the operands used to pass through registers (B transposed there, then
 // written to LDS), the step now issues no LDS stores, and 4096^3 measured 4 %
 // faster (980 against 1021 us, bitwise the same results).
-template <bool EPI, int TB>
+template <int EPI, int TB>
 __global__ __launch_bounds__(NTHREADS) void gemm32_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* __restrict__ C,
     int M, int N, int K, int lda, int ldb, int ldc, int tiles_m, int tiles_n,
@@ -254,8 +254,15 @@ __global__ __launch_bounds__(NTHREADS) void gemm32_kernel(
         }
     }
 
-    store_tile<OUT_F32, MI, MI, EPI, false>(acc, C, M, N, ldc, m0 + wm * (TB / 2), n0 + wn * (TB / 2), g,
-                                     li, epi);
+    if constexpr (EPI == EPI_FULL) {
+        static_assert(4 * full_lds<MI> <= (int)sizeof(lds), "LDS for the full epilogue");
+        __syncthreads();  // every wave is done with the operand stages
+        store_tile_full<OUT_F32, MI, MI>(acc, C, M, N, ldc, m0 + wm * (TB / 2), n0 + wn * (TB / 2),
+                                         lane, epi, (char*)lds + wave * full_lds<MI>);
+    } else {
+        store_tile<OUT_F32, MI, MI, EPI, false>(acc, C, M, N, ldc, m0 + wm * (TB / 2),
+                                                n0 + wn * (TB / 2), g, li, epi);
+    }
 }
 
 // ---------------------------------------------------------------- fp32 via 3 x bf16
@@ -321,7 +328,7 @@ __device__ __forceinline__ void split8(u32x4 x, u32x4 y, u32x4& hi, u32x4& lo) {
 // pieces) of rows ar0 + 64 i (i < TB / 64); B is 32 k-rows x TB columns,
 // thread -> a KB k x 4 column block, KB = 8 at TB = 256 and 4 at TB = 128 (256
 // blocks either way).
-template <bool EPI, int TB>
+template <int EPI, int TB>
 __global__ __launch_bounds__(NTHREADS) void gemm32x3_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* __restrict__ C,
     int M, int N, int K, int lda, int ldb, int ldc, int tiles_m, int tiles_n,
@@ -653,8 +660,15 @@ __global__ __launch_bounds__(NTHREADS) void gemm32x3_kernel(
         }
     }
 
-    store_tile<OUT_F32, MI, MI, EPI, false>(acc, C, M, N, ldc, m0 + wm * (TB / 2), n0 + wn * (TB / 2), g,
-                                     li, epi);
+    if constexpr (EPI == EPI_FULL) {
+        static_assert(4 * full_lds<MI> <= (int)sizeof(smem), "LDS for the full epilogue");
+        __syncthreads();  // every wave is done with the operand stages
+        store_tile_full<OUT_F32, MI, MI>(acc, C, M, N, ldc, m0 + wm * (TB / 2), n0 + wn * (TB / 2),
+                                         lane, epi, smem + wave * full_lds<MI>);
+    } else {
+        store_tile<OUT_F32, MI, MI, EPI, false>(acc, C, M, N, ldc, m0 + wm * (TB / 2),
+                                                n0 + wn * (TB / 2), g, li, epi);
+    }
 }
 
 // ---------------------------------------------------------------- fp32, K sliced over the waves
@@ -770,7 +784,7 @@ __device__ __forceinline__ void read_b_frags64(uint32_t base, uint32_t (&rb)[2][
         }
 }
 
-template <bool EPI, int MI, int W, bool IL, bool X3>
+template <int EPI, int MI, int W, bool IL, bool X3>
 __global__ __launch_bounds__(64 * W) void gemm32_slicek_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* __restrict__ C,
     int M, int N, int K, int lda, int ldb, int ldc, int tiles_m, int tiles_n, EpiArgs epi) {
@@ -986,6 +1000,22 @@ __global__ __launch_bounds__(64 * W) void gemm32_slicek_kernel(
 #pragma unroll
         for (int r = 0; r < 16; ++r) red[(wave * NB * 16 + b * 16 + r) * 64 + lane] = acc[b / MI][b % MI][r];
     __syncthreads();
+    if constexpr (EPI == EPI_FULL) {
+        float v[PER];
+        int row[PER], col[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int idx = wave * PER + q;
+            const int b = idx / 16, r = idx % 16;
+            v[q] = red[idx * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v[q] += red[(w * NB * 16 + idx) * 64 + lane];
+            row[q] = m0 + (b / MI) * 32 + 8 * (r >> 2) + 4 * g + (r & 3);
+            col[q] = n0 + (b % MI) * 32 + li;
+        }
+        finish_full<OUT_F32, PER>(v, row, col, C, M, N, ldc, epi);
+        return;
+    }
     const __amdgpu_buffer_rsrc_t cr = c_rsrc(C, M, N, ldc, m0, n0, 4);
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
@@ -1022,8 +1052,9 @@ hipError_t go(const void* fn, const GemmLaunch& L) {
 // Slice-K launches: one workgroup of W waves per TS x TS tile.
 template <int MI, int W, bool IL, bool X3>
 hipError_t go_slicek(const GemmLaunch& L) {
-    const void* fn = L.epi ? (const void*)gemm32_slicek_kernel<true, MI, W, IL, X3>
-                           : (const void*)gemm32_slicek_kernel<false, MI, W, IL, X3>;
+    const void* fn = L.epi == EPI_FULL    ? (const void*)gemm32_slicek_kernel<EPI_FULL, MI, W, IL, X3>
+                     : L.epi == EPI_BASIC ? (const void*)gemm32_slicek_kernel<EPI_BASIC, MI, W, IL, X3>
+                                          : (const void*)gemm32_slicek_kernel<EPI_NONE, MI, W, IL, X3>;
     const char* a = L.A;
     const char* b = L.B;
     char* c = L.C;
@@ -1050,16 +1081,17 @@ hipError_t launch_gemm32(const GemmLaunch& L) {
         return go_slicek<1, 8, false, true>(L);
     if (L.in == IN_F32X3 && L.splits == 1 && L.tbm == 64 && L.slice_waves == 4)
         return go_slicek<2, 4, true, true>(L);
-    if (L.in == IN_F32 && L.tbm == 128)
-        return go(L.epi ? (const void*)gemm32_kernel<true, 128> : (const void*)gemm32_kernel<false, 128>,
-                  L);
-    if (L.in == IN_F32X3 && L.tbm == 256)
-        return go(L.epi ? (const void*)gemm32x3_kernel<true, 256>
-                        : (const void*)gemm32x3_kernel<false, 256>, L);
-    if (L.in == IN_F32X3 && L.tbm == 128)
-        return go(L.epi ? (const void*)gemm32x3_kernel<true, 128>
-                        : (const void*)gemm32x3_kernel<false, 128>, L);
-    return hipErrorInvalidValue;
+    // The grid kernels at launch L's epilogue level.
+    auto grid = [&](auto epi_tag) -> hipError_t {
+        constexpr int EPI = decltype(epi_tag)::value;
+        if (L.in == IN_F32 && L.tbm == 128) return go((const void*)gemm32_kernel<EPI, 128>, L);
+        if (L.in == IN_F32X3 && L.tbm == 256) return go((const void*)gemm32x3_kernel<EPI, 256>, L);
+        if (L.in == IN_F32X3 && L.tbm == 128) return go((const void*)gemm32x3_kernel<EPI, 128>, L);
+        return hipErrorInvalidValue;
+    };
+    if (L.epi == EPI_FULL) return grid(std::integral_constant<int, EPI_FULL>{});
+    if (L.epi == EPI_BASIC) return grid(std::integral_constant<int, EPI_BASIC>{});
+    return grid(std::integral_constant<int, EPI_NONE>{});
 }
 
 }  // namespace dgemm

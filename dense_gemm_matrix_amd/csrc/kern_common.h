@@ -166,6 +166,17 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
+// Eight e4m3 values (two words) as bf16, exactly: the four significant bits and
+// exponents down to 2^-9 fit.
+__device__ __forceinline__ bf16x8 widen_f8(uint32_t lo, uint32_t hi) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
 // DPP quad permutation [1, 0, 3, 2]: lane l reads lane l ^ 1.
 constexpr int DPP_QUAD_XOR1 = 1 | (0 << 2) | (3 << 4) | (2 << 6);
 
@@ -175,7 +186,7 @@ __device__ __forceinline__ uint32_t swap_adjacent_lanes(uint32_t v) {
 
 // One store per element: fp32 C, or 16-bit C when a tile's column edge falls
 // between the two columns of a lane pair (N odd).
-template <int OUT, int MI, int NJ, bool EPI>
+template <int OUT, int MI, int NJ, int EPI>
 __device__ __forceinline__ void store_elems(const f32x16 (&acc)[MI][NJ], __amdgpu_buffer_rsrc_t r,
                                            int N, int ldc, int col0, int g, int li,
                                            const EpiArgs& e) {
@@ -213,7 +224,7 @@ __device__ __forceinline__ void store_elems(const f32x16 (&acc)[MI][NJ], __amdgp
 // store writes two 64-byte row pieces instead of one.  The epilogue and the
 // rounding act on each value before the exchange, so the stored values are
 // those of store_elems.  Needs every lane of the wave active.
-template <int OUT, int MI, int NJ, bool EPI>
+template <int OUT, int MI, int NJ, int EPI>
 __device__ __forceinline__ void store_pairs16(const f32x16 (&acc)[MI][NJ], __amdgpu_buffer_rsrc_t r,
                                               int N, int ldc, int col0, int g, int li,
                                               const EpiArgs& e) {
@@ -253,7 +264,7 @@ __device__ __forceinline__ void store_pairs16(const f32x16 (&acc)[MI][NJ], __amd
 // column edge and every tile takes store_pairs16; with N odd the kernel is
 // instantiated with store_elems instead (deciding inside the kernel costs
 // registers on every tile).
-template <int OUT, int MI, int NJ, bool EPI, bool PAIRS>
+template <int OUT, int MI, int NJ, int EPI, bool PAIRS>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[MI][NJ], char* C, int M, int N,
                                            int ldc, int row0, int col0, int g, int li,
                                            const EpiArgs& e) {
@@ -264,6 +275,259 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[MI][NJ], char* C,
         store_pairs16<OUT, MI, NJ, EPI>(acc, r, N, ldc, col0, g, li, e);
     else
         store_elems<OUT, MI, NJ, EPI>(acc, r, N, ldc, col0, g, li, e);
+}
+
+// ------------------------------------------------------- the full epilogue
+//
+// z := acc * scale_a[row] * scale_b[col] + bias[col];  Z := z;  C := act(z) + R.
+//
+// GELU and its tanh form, with Phi the normal distribution's integral:
+//   gelu(z) = z Phi(z) = z (1 + erf(z / sqrt 2)) / 2
+//   gelu_tanh(z) = z (1 + tanh(t)) / 2 = z / (1 + exp(-2 t)),
+//     t = sqrt(2 / pi) (z + 0.044715 z^3)
+// so gelu_tanh and silu(z) = z / (1 + exp(-z)) are one form z / (1 + exp(-p(z)))
+// with p(z) = z (a + b z^2), evaluated with the hardware's exp2 and reciprocal
+// (1 ulp each).  As z falls, exp overflows to infinity and its reciprocal to 0:
+// the limit -0.  Infinite z gives infinity or, at -infinity, NaN (-inf * 0), as
+// the formula itself does in floating point; a NaN stays a NaN.
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float SQRT_2_PI = 0.7978845608028654f;
+constexpr float GELU_C = 0.044715f;
+
+// The sigmoid of p(z) = z (a + b z^2).
+__device__ __forceinline__ float gate(float z, float a, float b) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * (z * (a + b * z * z))));
+}
+
+__device__ __forceinline__ float gate_a(int act) { return act == ACT_SILU ? 1.0f : 2.0f * SQRT_2_PI; }
+__device__ __forceinline__ float gate_b(int act) {
+    return act == ACT_SILU ? 0.0f : 2.0f * SQRT_2_PI * GELU_C;
+}
+
+// act applied to NE values; `act` is wave-uniform, so one branch serves them all.
+template <int NE>
+__device__ __forceinline__ void apply_act(float (&v)[NE], int act) {
+    if (act >= ACT_GELU_TANH) {
+        const float a = gate_a(act), b = gate_b(act);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] *= gate(v[i], a, b);
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.7071067811865476f));
+    } else if (act == ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+    }
+}
+
+template <int FMT>
+constexpr int fmt_es = FMT == OUT_F32 ? 4 : 2;
+
+// Eight consecutive elements of one row, in its storage format, moved through
+// a buffer resource in 16-byte pieces.  Only the first `nvalid` of them belong
+// to the row: the others load as 0 (the 16 bytes that hold the row's last
+// element are inside the resource, bases and pitches being multiples of 16) and
+// are not stored.  `off` is a byte offset, OOB_LANE where nvalid <= 0 would
+// leave it inside the resource.
+template <int FMT>
+struct Row8 {
+    u32x4 w[FMT == OUT_F32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, int nvalid) {
+        w[0] = load16(r, (int)off);
+        if constexpr (FMT == OUT_F32) w[1] = load16(r, (int)(off + 16));
+        if (nvalid < 8) mask(nvalid);
+    }
+    // The same from a plain 16-byte aligned address (lanes on different rows).
+    __device__ __forceinline__ void load_from(const char* p, int nvalid) {
+        w[0] = nvalid > 0 ? *(const u32x4*)p : u32x4{0u, 0u, 0u, 0u};
+        if constexpr (FMT == OUT_F32)
+            w[1] = nvalid > 4 ? *(const u32x4*)(p + 16) : u32x4{0u, 0u, 0u, 0u};
+        if (nvalid < 8) mask(nvalid);
+    }
+    __device__ __forceinline__ void mask(int nvalid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (FMT == OUT_F32)
+                w[j >> 2][j & 3] = j < nvalid ? w[j >> 2][j & 3] : 0u;
+            else
+                w[0][j >> 1] &= j < nvalid ? 0xffffffffu : (j & 1) ? 0x0000ffffu : 0xffff0000u;
+        }
+    }
+    __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off, int nvalid) const {
+        constexpr int ES = fmt_es<FMT>;
+        if (nvalid >= 8) {
+            __builtin_amdgcn_raw_buffer_store_b128(w[0], r, (int)off, 0, 0);
+            if constexpr (FMT == OUT_F32)
+                __builtin_amdgcn_raw_buffer_store_b128(w[1], r, (int)(off + 16), 0, 0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 7; ++j) {
+                const uint32_t o = j < nvalid ? off + j * ES : OOB_LANE;
+                if constexpr (FMT == OUT_F32)
+                    __builtin_amdgcn_raw_buffer_store_b32(w[j >> 2][j & 3], r, (int)o, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b16(
+                        (unsigned short)(w[0][j >> 1] >> (16 * (j & 1))), r, (int)o, 0, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (FMT == OUT_F32) {
+                v[j] = as_float(w[j >> 2][j & 3]);
+            } else {
+                const uint32_t h = w[0][j >> 1] >> (16 * (j & 1)) & 0xffffu;
+                if constexpr (FMT == OUT_BF16) v[j] = as_float(h << 16);
+                else v[j] = (float)__builtin_bit_cast(_Float16, (unsigned short)h);
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        if constexpr (FMT == OUT_F32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j >> 2][j & 3] = __builtin_bit_cast(uint32_t, v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[0][j] = pack16<FMT>(v[2 * j], v[2 * j + 1]);
+        }
+    }
+};
+
+// LDS bytes store_tile_full needs per wave: 32 rows of the wave's NJ * 32
+// columns, the pitch padded by 8 floats so that the two lane groups, whose
+// rows are 4 apart, write to different halves of the 64 banks (4 pitches are
+// 32 modulo 64 floats) and rows stay 16-byte aligned.
+template <int NJ>
+constexpr int full_pitch = NJ * 32 + 8;
+template <int NJ>
+constexpr int full_lds = 32 * full_pitch<NJ> * 4;
+
+// The full epilogue of one wave's MI x NJ blocks.  The accumulator layout has
+// one column per lane, which would read R and write C and Z two bytes at a
+// time; instead each 32-row strip goes through the wave's own LDS region (free
+// after the K loop; the caller has a barrier before) and comes back eight
+// consecutive columns per lane, so R, Z and C move in 16-byte pieces of whole
+// row segments.  R of the next strip is loaded while this one is worked on.
+// The strip loop stays a loop (only the accumulators' copy to LDS is written
+// out per strip), which keeps the activation code in the instruction cache.
+// bias and scales are read straight from memory: a lane's columns are the same
+// in every strip.
+template <int OUT, int MI, int NJ>
+__device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], char* C, int M, int N,
+                                                int ldc, int row0, int col0, int lane,
+                                                const EpiArgs& e, char* lds) {
+    if (row0 >= M || col0 >= N) return;  // this wave's part of the tile lies outside C
+    constexpr int ES = fmt_es<OUT>;
+    constexpr int P = full_pitch<NJ>;
+    constexpr int LPR = NJ * 4;        // lanes per row
+    constexpr int RPI = 64 / LPR;      // rows per pass of the wave
+    constexpr int IT = 32 / RPI;       // passes per strip
+    const int g = lane >> 5, li = lane & 31;
+    const int c8 = (lane % LPR) * 8, r_in = lane / LPR;
+    const int nvalid = N - (col0 + c8);
+    float* const buf = (float*)lds;
+    const __amdgpu_buffer_rsrc_t rc = c_rsrc(C, M, N, ldc, row0, col0, ES);
+    // NULL operands get empty ranges: their loads give zeros, their stores drop.
+    const __amdgpu_buffer_rsrc_t rr =
+        e.res ? c_rsrc((char*)e.res, M, N, e.ldr, row0, col0, ES) : make_rsrc(C, 0);
+    const __amdgpu_buffer_rsrc_t rz =
+        e.pre ? c_rsrc(e.pre, M, N, e.ldz, row0, col0, ES) : make_rsrc(C, 0);
+    float bias[8], sb[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        bias[j] = (e.bias && j < nvalid) ? e.bias[col0 + c8 + j] : 0.0f;
+        sb[j] = (e.scale_b && j < nvalid) ? e.scale_b[col0 + c8 + j] : 1.0f;
+    }
+    // Byte offset of this lane's eight columns in row `r` of the wave's rows.
+    auto at = [&](int r, int ld) {
+        return nvalid > 0 ? (uint32_t)((r * ld + c8) * ES) : OOB_LANE;
+    };
+    Row8<OUT> res[IT];
+    if (e.res) {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) res[it].load(rr, at(it * RPI + r_in, e.ldr), nvalid);
+    }
+#pragma unroll 1
+    for (int mi = 0; mi < MI; ++mi) {
+        if (row0 + mi * 32 >= M) break;
+        // This lane's values of the strip to LDS (after the previous strip's reads).
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int k = 0; k < MI; ++k) {
+            if (k != mi) continue;
+#pragma unroll
+            for (int nj = 0; nj < NJ; ++nj)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    buf[(8 * (r >> 2) + 4 * g + (r & 3)) * P + nj * 32 + li] = acc[k][nj][r];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int r = it * RPI + r_in;  // row within the strip
+            const int row = mi * 32 + r;    // row within the wave's rows
+            float v[8];
+            const f32x4 lo = *(const f32x4*)(buf + r * P + c8);
+            const f32x4 hi = *(const f32x4*)(buf + r * P + c8 + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[j] = lo[j];
+                v[4 + j] = hi[j];
+            }
+            if (e.scale_a) {
+                const float sa = row0 + row < M ? e.scale_a[row0 + row] : 0.0f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * sa * sb[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += bias[j];
+            Row8<OUT> o;
+            if (e.pre) {
+                o.set(v);
+                o.store(rz, at(row, e.ldz), nvalid);
+            }
+            apply_act(v, e.act);
+            if (e.res) {
+                float x[8];
+                res[it].get(x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] += x[j];
+                if (mi + 1 < MI) res[it].load(rr, at(row + 32, e.ldr), nvalid);
+            }
+            o.set(v);
+            o.store(rc, at(row, ldc), nvalid);
+        }
+    }
+}
+
+// The full epilogue on NE fp32 sums v[i] of C's elements (row[i], col[i]),
+// through plain pointers, for kernels that finish few elements per lane;
+// elements outside M x N are skipped.  R is read before anything is stored.
+template <int OUT, int NE>
+__device__ __forceinline__ void finish_full(float (&v)[NE], const int (&row)[NE],
+                                            const int (&col)[NE], char* C, int M, int N, int ldc,
+                                            const EpiArgs& e) {
+    float res[NE];
+    bool in[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+        in[i] = row[i] < M && col[i] < N;
+        res[i] = e.res && in[i] ? load_c<OUT>(e.res, (int64_t)row[i] * e.ldr + col[i]) : 0.0f;
+        if (e.scale_a && in[i]) v[i] = v[i] * e.scale_a[row[i]] * e.scale_b[col[i]];
+        if (e.bias && in[i]) v[i] += e.bias[col[i]];
+    }
+    if (e.pre) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+            if (in[i]) store_c<OUT>(e.pre, (int64_t)row[i] * e.ldz + col[i], v[i]);
+    }
+    apply_act(v, e.act);
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+        if (in[i]) store_c<OUT>(C, (int64_t)row[i] * ldc + col[i], e.res ? v[i] + res[i] : v[i]);
 }
 
 }  // namespace dgemm

@@ -1,0 +1,536 @@
+// linear.hip -- the C ABI of the linear layer's operators: products with the
+// full epilogue and their gradients (gemm_act, gemm_act_bwd), 8-bit products
+// (gemm_f8), norms and quantizers.  Host code only: validation, plans and
+// launches; the kernels live in the files that dgemm_internal.h names.
+
+#include <algorithm>
+#include <cmath>
+
+#include "dgemm.h"
+#include "dgemm_internal.h"
+#include "plan.h"
+
+namespace dgemm {
+namespace {
+
+constexpr int64_t WS_ALIGN = 256;  // pieces of a workspace start on this
+
+int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
+
+// A row-major matrix operand of a call.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, ld, es;
+    Span span() const { return matrix_span(p, rows, cols, ld, es); }
+    bool empty() const { return rows <= 0 || cols <= 0; }
+};
+
+// Pitch, pointer, alignment and the 32-bit panel limit of one matrix.
+int check_mat(const Mat& m) {
+    if (m.ld < std::max<int64_t>(m.cols, 1)) return DGEMM_ERR_LEADING_DIM;
+    if (!m.empty()) {
+        if (!m.p) return DGEMM_ERR_INVALID_VALUE;
+        if (((uintptr_t)m.p & 15) || (m.ld * m.es) % 16) return DGEMM_ERR_MISALIGNED;
+    }
+    if ((int64_t)PANEL_ROWS * m.ld * m.es >= DESC_LIMIT) return DGEMM_ERR_TOO_LARGE;
+    return DGEMM_OK;
+}
+
+// An fp32 vector operand (NULL: absent).
+Mat vec(const void* p, int64_t n) { return Mat{p, p ? 1 : 0, n, n, 4}; }
+
+int check_vec(const void* p, int align) {
+    return ((uintptr_t)p & (uintptr_t)(align - 1)) ? DGEMM_ERR_MISALIGNED : DGEMM_OK;
+}
+
+// Whether any of `outs` shares a byte with another of them or with any of `ins`.
+bool any_overlap(const Mat* outs, int n_out, const Mat* ins, int n_in) {
+    for (int i = 0; i < n_out; ++i) {
+        if (!outs[i].p) continue;
+        for (int j = 0; j < n_in; ++j)
+            if (ins[j].p && spans_overlap(outs[i].span(), ins[j].span())) return true;
+        for (int j = 0; j < i; ++j)
+            if (outs[j].p && spans_overlap(outs[i].span(), outs[j].span())) return true;
+    }
+    return false;
+}
+
+Mat bytes_of(void* p, int64_t n) { return Mat{p, n > 0 ? 1 : 0, n, n, 1}; }
+
+bool valid_act(int act) { return act >= DGEMM_ACT_NONE && act <= DGEMM_ACT_SILU; }
+
+// -------------------------------------------------------------------- plans
+
+// Tiles of gemmt.hip: gemm16's constants, whose schedule and bytes per step it
+// shares (an 8-bit step is 128 k in the same time).
+constexpr TileCand TILES_T[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6},
+                                {128, 128, 0.6, 1.26, 1.35, 0.8, 1.0}};
+
+int t_step(int in) { return in >= IN_F8 ? 128 : 64; }
+
+// Plan of one tile at `splits` K pieces (1: unsplit); splits = 0 if it does not fit.
+Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uint64_t ws_avail) {
+    Plan p{t.bm, t.bn, 1, K, 0, 0};
+    if (splits <= 1 || K <= 0) return p;
+    const int nk = (int)ceil_div(K, bk);
+    const int steps = (int)ceil_div(nk, std::min(splits, nk));
+    p.splits = (int)ceil_div(nk, steps);
+    p.kchunk = steps * bk;
+    if (p.splits == 1) { p.kchunk = K; return p; }
+    p.ldw = (int)up(N, 4);
+    p.ws_bytes = (int64_t)p.splits * M * p.ldw * 4;
+    if ((uint64_t)p.ws_bytes > ws_avail || (int64_t)PANEL_ROWS * p.ldw * 4 >= DESC_LIMIT ||
+        ceil_div(M, t.bm) * ceil_div(N, t.bn) * p.splits > INT32_MAX)
+        p.splits = 0;
+    return p;
+}
+
+// The transposed layouts' plan: the estimate's choice among the two tiles and 1
+// to 16 splits, by the same terms and margin as the other grid plans.
+Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail) {
+    const int bk = t_step(in);
+    int fm, fn, fs;
+    if (forced_grid(fm, fn, fs))
+        for (const TileCand& t : TILES_T)
+            if (t.bm == fm && t.bn == fn) {
+                Plan p = plan_pieces(t, bk, M, N, K, fs, ws_avail);
+                p.layout = layout;
+                if (p.splits > 0) return p;
+            }
+    Plan best{};
+    double best_us = -1.0;
+    const int nk = (int)ceil_div(std::max(K, 1), bk);
+    for (const TileCand& t : TILES_T) {
+        const double us = estimate_us(in, es_out, M, N, t, 1, nk, 0);
+        if (best_us < 0.0 || us < best_us) {
+            best_us = us;
+            best = plan_pieces(t, bk, M, N, K, 1, 0);
+        }
+    }
+    best_us *= SPLIT_MARGIN;
+    for (const TileCand& t : TILES_T)
+        for (int s = 2; s <= MAX_SPLITS && s <= nk; ++s) {
+            const Plan p = plan_pieces(t, bk, M, N, K, s, ws_avail);
+            if (p.splits != s) continue;
+            const double us = estimate_us(in, es_out, M, N, t, s, p.kchunk / bk, p.ldw);
+            if (us < best_us) {
+                best_us = us;
+                best = p;
+            }
+        }
+    best.layout = layout;
+    return best;
+}
+
+// At most SKINNY_M rows.  8-bit: strips of 16 columns.  16-bit: strips of 32
+// columns with 16 waves.
+Plan plan_skinny(int in, int M, int N, int K, uint64_t ws_avail) {
+    Plan p{SKINNY_M, 32, 1, K, 0, 0};
+    p.waves = 16;
+    if (in == IN_F8W) {
+        p.bn = 16;
+        p.waves = 16;
+        p.layout = LAY_NT;
+    } else {
+        int fm, fn, fs;
+        if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || fn == 128)) {
+            const Plan f = plan_pieces(TileCand{SKINNY_M, fn, 1, 0, 0, 1, 1}, 32, M, N, K, fs, ws_avail);
+            if (f.splits > 0) {
+                p = f;
+                p.waves = fn == 32 ? 16 : 8;
+            }
+        }
+    }
+    p.kind = PLAN_SKINNY;
+    return p;
+}
+
+Plan plan_act(int in, int es_out, int M, int N, int K, uint64_t ws_avail) {
+    if ((in == IN_BF16 || in == IN_F16) && M > 0 && M <= SKINNY_M && N > 0)
+        return plan_skinny(in, M, N, K, ws_avail);
+    return make_plan(in, es_out, M, N, K, ws_avail, false);
+}
+
+// fp32 outputs and few rows: the widened products, whose sums are fp32.
+int f8_in(int of, int M) { return of == OUT_F32 || M <= SKINNY_M ? IN_F8W : IN_F8; }
+
+Plan plan_f8(int of, int M, int N, int K, uint64_t ws_avail) {
+    const int in = f8_in(of, M);
+    if (M > 0 && M <= SKINNY_M && N > 0) return plan_skinny(in, M, N, K, ws_avail);
+    return plan_t(in, LAY_NT, out_esize(of), M, N, K, ws_avail);
+}
+
+int report(const Plan& p, int* tile_rows, int* tile_cols, int* splits, size_t* used) {
+    if (tile_rows) *tile_rows = p.bm;
+    if (tile_cols) *tile_cols = p.bn;
+    if (splits) *splits = p.splits;
+    if (used) *used = (size_t)p.ws_bytes;
+    return DGEMM_OK;
+}
+
+// ------------------------------------------------- the forward products' call
+
+struct Fwd {
+    Mat A, B, C, R, Z, bias, sa, sb;
+    int act;
+};
+
+int check_fwd(const Fwd& f, const Mat& ws) {
+    if (f.R.p && check_mat(f.R) != DGEMM_OK) return check_mat(f.R);
+    if (f.Z.p && check_mat(f.Z) != DGEMM_OK) return check_mat(f.Z);
+    if (check_vec(f.bias.p, 4) != DGEMM_OK || check_vec(f.sa.p, 4) != DGEMM_OK ||
+        check_vec(f.sb.p, 4) != DGEMM_OK || check_vec(ws.p, 16) != DGEMM_OK)
+        return DGEMM_ERR_MISALIGNED;
+    // R may be C itself (each element is read before it is written), not overlap
+    // it in any other way.
+    const bool in_place = f.R.p == f.C.p && (f.R.ld == f.C.ld || f.C.rows == 1);
+    const Mat none{nullptr, 0, 0, 0, 0};
+    const Mat ins[] = {f.A, f.B, in_place ? none : f.R, f.bias, f.sa, f.sb};
+    const Mat outs[] = {f.C, f.Z, ws};
+    if (any_overlap(outs, 3, ins, 6)) return DGEMM_ERR_ALIAS;
+    return DGEMM_OK;
+}
+
+EpiArgs epi_of(const Fwd& f) {
+    EpiArgs e{};
+    e.alpha = 1.0f;
+    e.bias = (const float*)f.bias.p;
+    e.act = f.act;
+    e.res = (const char*)f.R.p;
+    e.pre = (char*)f.Z.p;
+    e.ldr = (int)f.R.ld;
+    e.ldz = (int)f.Z.ld;
+    e.scale_a = (const float*)f.sa.p;
+    e.scale_b = (const float*)f.sb.p;
+    return e;
+}
+
+// ---------------------------------------------------------- the backward call
+
+// The pieces of gemm_act_bwd's workspace, in order: dZ (unless dC serves), the
+// column sums of dbias, an operand's transpose (fp32), then what the products'
+// plans may use.
+struct BwdParts {
+    bool own_dz;
+    int lddz, ldp, chunks, ldt;
+    int64_t dz, part, trans, required;
+};
+
+BwdParts bwd_parts(int in, int cfmt, int M, int N, int K, int act, bool products, bool dbias) {
+    BwdParts b{};
+    const int es = in_esize(in);
+    const int dfmt = out_format(in, DGEMM_OUT_SAME);
+    b.own_dz = products && (act != DGEMM_ACT_NONE || cfmt != dfmt);
+    b.lddz = (int)up(N, 16 / es);
+    b.ldp = (int)up(N, 4);
+    b.chunks = (int)ceil_div(M, act_grad_rows(M));
+    b.dz = b.own_dz ? up((int64_t)M * b.lddz * es, WS_ALIGN) : 0;
+    b.part = dbias ? up((int64_t)b.chunks * b.ldp * 4, WS_ALIGN) : 0;
+    if (products && es == 4)
+        b.trans = up(std::max((int64_t)N * up(K, 4), (int64_t)K * up(M, 4)) * 4, WS_ALIGN);
+    b.required = b.dz + b.part + b.trans;
+    return b;
+}
+
+Plan plan_bwd(int in, int layout, int M, int N, int K, uint64_t ws) {
+    if (in == IN_BF16 || in == IN_F16) return plan_t(in, layout, 2, M, N, K, ws);
+    return make_plan(in, 4, M, N, K, ws, false);
+}
+
+int run_bwd_product(int in, int layout, int M, int N, int K, const void* X, int ldx, const void* Y,
+                    int ldy, const Mat& out, char* ws, int64_t ws_bytes, hipStream_t stream) {
+    if (out.empty()) return DGEMM_OK;
+    const Plan p = plan_bwd(in, layout, M, N, K, (uint64_t)ws_bytes);
+    EpiArgs e{};
+    e.alpha = 1.0f;
+    // The transposed-layout kernels store through the full epilogue's row segments.
+    return run(in, out_format(in, DGEMM_OUT_SAME), M, N, K, X, ldx, Y, ldy, (void*)out.p, (int)out.ld,
+               e, in == IN_BF16 || in == IN_F16 ? EPI_FULL : EPI_NONE, p, ws, stream);
+}
+
+// Format codes DGEMM_IN_F32 / _BF16 / _F16 of an elementwise operator.
+int row_fmt(int in) {
+    return in == DGEMM_IN_F32 ? OUT_F32 : in == DGEMM_IN_BF16 ? OUT_BF16 : in == DGEMM_IN_F16 ? OUT_F16 : -1;
+}
+
+int launched(hipError_t e) { return e == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH; }
+
+}  // namespace
+}  // namespace dgemm
+
+using namespace dgemm;
+
+extern "C" {
+
+int gemm_act(int in, int out, int M, int N, int K, const void* A, int lda, const void* B, int ldb,
+             void* C, int ldc, const float* bias, int act, const void* R, int ldr, void* Z, int ldz,
+             void* workspace, size_t workspace_bytes, void* stream) {
+    if (in < IN_F32 || in > IN_F32X3) return DGEMM_ERR_INVALID_VALUE;
+    const int of = out_format(in, out);
+    if (of < 0 || !valid_act(act) || (workspace_bytes > 0 && !workspace)) return DGEMM_ERR_INVALID_VALUE;
+    const int eo = out_esize(of), es = in_esize(in);
+    int st = validate(M, N, K, A, lda, B, ldb, C, ldc, in, eo);
+    if (st != DGEMM_OK) return st;
+    if (M == 0 || N == 0) return DGEMM_OK;
+    const Plan p = plan_act(in, eo, M, N, K, workspace ? workspace_bytes : 0);
+    const Fwd f{{A, M, K, lda, es}, {B, K, N, ldb, es}, {C, M, N, ldc, eo}, {R, M, N, ldr, eo},
+                {Z, M, N, ldz, eo}, vec(bias, N), vec(nullptr, 0), vec(nullptr, 0), act};
+    st = check_fwd(f, bytes_of(workspace, p.ws_bytes));
+    if (st != DGEMM_OK) return st;
+    st = check_device();
+    if (st != DGEMM_OK) return st;
+    return run(in, of, M, N, K, A, lda, B, ldb, C, ldc, epi_of(f), EPI_FULL, p, workspace,
+               (hipStream_t)stream);
+}
+
+int gemm_act_plan(int in, int out, int M, int N, int K, size_t workspace_bytes, int* tile_rows,
+                  int* tile_cols, int* splits, size_t* workspace_used) {
+    if (in < IN_F32 || in > IN_F32X3 || M < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_VALUE;
+    const int of = out_format(in, out);
+    if (of < 0) return DGEMM_ERR_INVALID_VALUE;
+    if (ceil_div(M, 128) * ceil_div(N, 128) > INT32_MAX) return DGEMM_ERR_TOO_LARGE;
+    return report(plan_act(in, out_esize(of), M, N, K, workspace_bytes), tile_rows, tile_cols, splits,
+                  workspace_used);
+}
+
+int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, const void* B, int ldb,
+                 const void* dC, int lddc, const void* Z, int ldz, int act, void* dA, int ldda,
+                 void* dB, int lddb, float* dbias, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+    if (in < IN_F32 || in > IN_F32X3 || M < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_VALUE;
+    const int cf = out_format(in, out);
+    if (cf < 0 || !valid_act(act) || (workspace_bytes > 0 && !workspace)) return DGEMM_ERR_INVALID_VALUE;
+    const int es = in_esize(in), ec = out_esize(cf);
+    const bool use_z = act != DGEMM_ACT_NONE;
+    const Mat mA{A, dB ? M : 0, K, lda, es}, mB{B, dA ? K : 0, N, ldb, es}, mdC{dC, M, N, lddc, ec};
+    const Mat mZ{use_z ? Z : nullptr, use_z ? M : 0, N, ldz, ec};
+    const Mat mdA{dA, dA ? M : 0, K, ldda, es}, mdB{dB, dB ? K : 0, N, lddb, es};
+    int st;
+    if (dB && (st = check_mat(mA)) != DGEMM_OK) return st;
+    if (dA && (st = check_mat(mB)) != DGEMM_OK) return st;
+    if ((st = check_mat(mdC)) != DGEMM_OK) return st;
+    if (use_z && (st = check_mat(mZ)) != DGEMM_OK) return st;
+    if (dA && (st = check_mat(mdA)) != DGEMM_OK) return st;
+    if (dB && (st = check_mat(mdB)) != DGEMM_OK) return st;
+    if (check_vec(dbias, 4) != DGEMM_OK || check_vec(workspace, 16) != DGEMM_OK) return DGEMM_ERR_MISALIGNED;
+    const BwdParts b = bwd_parts(in, cf, M, N, K, act, dA || dB, dbias != nullptr);
+    if ((uint64_t)b.required > workspace_bytes) return DGEMM_ERR_WORKSPACE;
+    // The kernels that fill the workspace address dZ and the transposes in panels too.
+    if ((int64_t)PANEL_ROWS * up(std::max(std::max(M, N), K), 16) * 4 >= DESC_LIMIT)
+        return DGEMM_ERR_TOO_LARGE;
+    const Mat ws = bytes_of(workspace, (int64_t)std::min<uint64_t>(workspace_bytes, INT64_MAX));
+    const Mat ins[] = {mA, mB, mdC, mZ}, outs[] = {mdA, mdB, vec(dbias, N), ws};
+    if (any_overlap(outs, 4, ins, 4)) return DGEMM_ERR_ALIAS;
+    if ((st = check_device()) != DGEMM_OK) return st;
+
+    char* const w = (char*)workspace;
+    char* const w_part = w + b.dz;
+    float* const w_trans = (float*)(w + b.dz + b.part);
+    char* const w_gemm = w + b.required;
+    const int64_t gemm_bytes = (int64_t)workspace_bytes - b.required;
+    hipStream_t s = (hipStream_t)stream;
+    const void* dz = dC;
+    int lddz = lddc;
+    if (b.own_dz) {
+        dz = w;
+        lddz = b.lddz;
+    }
+    if (M > 0 && N > 0 && (b.own_dz || dbias)) {
+        const ActGradArgs a{(const char*)dC, (const char*)mZ.p, b.own_dz ? w : nullptr,
+                            dbias ? (float*)w_part : nullptr, M, N, lddc, ldz, b.lddz, b.ldp,
+                            act_grad_rows(M), act};
+        if (launch_act_grad(a, cf, out_format(in, DGEMM_OUT_SAME), s) != hipSuccess)
+            return DGEMM_ERR_LAUNCH;
+    }
+    if (dbias && N > 0 &&
+        launch_col_reduce((const float*)w_part, b.chunks, b.ldp, N, dbias, s) != hipSuccess)
+        return DGEMM_ERR_LAUNCH;
+    const bool f32 = es == 4;
+    if (dA) {
+        const void* y = B;
+        int ldy = ldb;
+        if (f32 && !mB.empty() && M > 0) {
+            ldy = (int)up(K, 4);
+            if (launch_transpose32((const float*)B, ldb, K, N, w_trans, ldy, s) != hipSuccess)
+                return DGEMM_ERR_LAUNCH;
+            y = w_trans;
+        }
+        st = run_bwd_product(in, LAY_NT, M, K, N, dz, lddz, y, ldy, mdA, w_gemm, gemm_bytes, s);
+        if (st != DGEMM_OK) return st;
+    }
+    if (dB) {
+        const void* x = A;
+        int ldx = lda;
+        if (f32 && !mA.empty() && N > 0) {
+            ldx = (int)up(M, 4);
+            if (launch_transpose32((const float*)A, lda, M, K, w_trans, ldx, s) != hipSuccess)
+                return DGEMM_ERR_LAUNCH;
+            x = w_trans;
+        }
+        st = run_bwd_product(in, LAY_TN, K, N, M, x, ldx, dz, lddz, mdB, w_gemm, gemm_bytes, s);
+        if (st != DGEMM_OK) return st;
+    }
+    return DGEMM_OK;
+}
+
+int gemm_act_bwd_workspace(int in, int out, int M, int N, int K, int act, size_t* required,
+                           size_t* best) {
+    if (in < IN_F32 || in > IN_F32X3 || M < 0 || N < 0 || K < 0 || !valid_act(act))
+        return DGEMM_ERR_INVALID_VALUE;
+    const int cf = out_format(in, out);
+    if (cf < 0) return DGEMM_ERR_INVALID_VALUE;
+    const BwdParts b = bwd_parts(in, cf, M, N, K, act, true, true);
+    int64_t more = 0;
+    const uint64_t any = (uint64_t)1 << 40;
+    if (M > 0 && K > 0) more = std::max(more, plan_bwd(in, LAY_NT, M, K, N, any).ws_bytes);
+    if (K > 0 && N > 0) more = std::max(more, plan_bwd(in, LAY_TN, K, N, M, any).ws_bytes);
+    if (required) *required = (size_t)b.required;
+    if (best) *best = (size_t)(b.required + more);
+    return DGEMM_OK;
+}
+
+int gemm_f8(int out, int M, int N, int K, const void* A, int lda, const void* B, int ldb, void* C,
+            int ldc, const float* scale_a, const float* scale_b, const float* bias, int act,
+            const void* R, int ldr, void* workspace, size_t workspace_bytes, void* stream) {
+    const int of = row_fmt(out);
+    if (of < 0 || M < 0 || N < 0 || K < 0 || !valid_act(act) || (workspace_bytes > 0 && !workspace))
+        return DGEMM_ERR_INVALID_VALUE;
+    const int eo = out_esize(of);
+    const bool reads = M > 0 && N > 0;
+    const Fwd f{{A, reads ? M : 0, K, lda, 1}, {B, reads ? N : 0, K, ldb, 1}, {C, M, N, ldc, eo},
+                {R, M, N, ldr, eo}, {nullptr, 0, 0, 0, eo}, vec(bias, N), vec(scale_a, M),
+                vec(scale_b, N), act};
+    int st;
+    if ((st = check_mat(f.A)) != DGEMM_OK || (st = check_mat(f.B)) != DGEMM_OK ||
+        (st = check_mat(f.C)) != DGEMM_OK)
+        return st;
+    if (!reads) return DGEMM_OK;
+    if (!scale_a || !scale_b) return DGEMM_ERR_INVALID_VALUE;
+    const Plan p = plan_f8(of, M, N, K, workspace ? workspace_bytes : 0);
+    if ((st = check_fwd(f, bytes_of(workspace, p.ws_bytes))) != DGEMM_OK) return st;
+    if ((st = check_device()) != DGEMM_OK) return st;
+    return run(f8_in(of, M), of, M, N, K, A, lda, B, ldb, C, ldc, epi_of(f), EPI_FULL, p, workspace,
+               (hipStream_t)stream);
+}
+
+int gemm_f8_plan(int out, int M, int N, int K, size_t workspace_bytes, int* tile_rows, int* tile_cols,
+                 int* splits, size_t* workspace_used) {
+    const int of = row_fmt(out);
+    if (of < 0 || M < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_VALUE;
+    if (ceil_div(M, 128) * ceil_div(N, 128) > INT32_MAX) return DGEMM_ERR_TOO_LARGE;
+    return report(plan_f8(of, M, N, K, workspace_bytes), tile_rows, tile_cols, splits,
+                  workspace_used);
+}
+
+int rmsnorm(int in, int out, int M, int N, const void* X, int ldx, const void* R, int ldr, void* S,
+            int lds, const float* weight, float eps, void* Y, int ldy, float* scale, float* rstd,
+            void* stream) {
+    const int fmt = row_fmt(in);
+    if (fmt < 0 || M < 0 || N < 0 || !(eps >= 0.0f) || (out != DGEMM_ROWS_SAME && out != DGEMM_ROWS_F8))
+        return DGEMM_ERR_INVALID_VALUE;
+    const bool f8 = out == DGEMM_ROWS_F8;
+    const int es = out_esize(fmt);
+    const Mat mX{X, M, N, ldx, es}, mR{R, M, N, ldr, es}, mS{S, M, N, lds, es}, mY{Y, M, N, ldy, f8 ? 1 : es};
+    int st;
+    if ((st = check_mat(mX)) != DGEMM_OK || (st = check_mat(mY)) != DGEMM_OK) return st;
+    if (R && (st = check_mat(mR)) != DGEMM_OK) return st;
+    if (S && (st = check_mat(mS)) != DGEMM_OK) return st;
+    if (M == 0 || N == 0) return DGEMM_OK;
+    if (!weight || (f8 && !scale) || (!f8 && scale)) return DGEMM_ERR_INVALID_VALUE;
+    if (N > ROW_MAX) return DGEMM_ERR_TOO_LARGE;
+    if (check_vec(weight, 16) != DGEMM_OK || check_vec(scale, 4) != DGEMM_OK || check_vec(rstd, 4) != DGEMM_OK)
+        return DGEMM_ERR_MISALIGNED;
+    // S and Y may each be X or R themselves (a row is read before it is written;
+    // for Y only in X's format), and share nothing else with the inputs.
+    const auto same = [&](const Mat& o, const Mat& i) {
+        return o.p == i.p && o.es == i.es && (o.ld == i.ld || M == 1);
+    };
+    const Mat none{nullptr, 0, 0, 0, 0};
+    const Mat outs[] = {mS, mY, vec(scale, M), vec(rstd, M)};
+    if (any_overlap(outs, 4, nullptr, 0)) return DGEMM_ERR_ALIAS;
+    for (const Mat& o : outs) {
+        const bool whole = o.p && o.cols == N && o.rows == M && (o.p == S || o.p == Y);
+        const Mat ins[] = {whole && same(o, mX) ? none : mX, R ? (whole && same(o, mR) ? none : mR) : none,
+                           vec(weight, N)};
+        if (any_overlap(&o, 1, ins, 3)) return DGEMM_ERR_ALIAS;
+    }
+    if ((st = check_device()) != DGEMM_OK) return st;
+    const RowArgs a{(const char*)X, (const char*)R, (char*)S, weight, (char*)Y, scale, rstd, eps, M, N,
+                    ldx, ldr, lds, ldy};
+    return launched(launch_rows(a, fmt, true, f8, (hipStream_t)stream));
+}
+
+int rmsnorm_bwd(int in, int M, int N, const void* dY, int lddy, const void* S, int lds,
+                const float* weight, const float* rstd, const void* dS, int ldds, void* dX, int lddx,
+                float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+    const int fmt = row_fmt(in);
+    if (fmt < 0 || M < 0 || N < 0 || (workspace_bytes > 0 && !workspace)) return DGEMM_ERR_INVALID_VALUE;
+    const int es = out_esize(fmt);
+    const Mat mdY{dY, M, N, lddy, es}, mS{S, M, N, lds, es}, mdS{dS, M, N, ldds, es}, mdX{dX, M, N, lddx, es};
+    int st;
+    if ((st = check_mat(mdY)) != DGEMM_OK || (st = check_mat(mS)) != DGEMM_OK ||
+        (st = check_mat(mdX)) != DGEMM_OK)
+        return st;
+    if (dS && (st = check_mat(mdS)) != DGEMM_OK) return st;
+    if (N == 0 || (M == 0 && !dweight)) return DGEMM_OK;
+    if (M > 0 && (!weight || !rstd)) return DGEMM_ERR_INVALID_VALUE;
+    if (N > NORM_BWD_MAX) return DGEMM_ERR_TOO_LARGE;
+    if (check_vec(weight, 16) != DGEMM_OK || check_vec(rstd, 4) != DGEMM_OK ||
+        check_vec(dweight, 4) != DGEMM_OK || check_vec(workspace, 16) != DGEMM_OK)
+        return DGEMM_ERR_MISALIGNED;
+    const int grid = norm_bwd_grid(M, N), ldp = (int)up(N, 4);
+    const int64_t need = dweight ? (int64_t)grid * ldp * 4 : 0;
+    if ((uint64_t)need > workspace_bytes) return DGEMM_ERR_WORKSPACE;
+    // dX may be dY or dS itself (a row is read before it is written).
+    const auto same = [&](const Mat& i) { return mdX.p == i.p && (mdX.ld == i.ld || M == 1); };
+    const Mat none{nullptr, 0, 0, 0, 0};
+    const Mat ws = bytes_of(workspace, need);
+    const Mat out_x[] = {mdX}, in_x[] = {same(mdY) ? none : mdY, mS, dS ? (same(mdS) ? none : mdS) : none,
+                                         vec(weight, N), vec(rstd, M), vec(dweight, N), ws};
+    const Mat out_w[] = {vec(dweight, N), ws};
+    const Mat in_w[] = {mdY, mS, dS ? mdS : none, vec(weight, N), vec(rstd, M)};
+    if (any_overlap(out_x, 1, in_x, 7) || any_overlap(out_w, 2, in_w, 5)) return DGEMM_ERR_ALIAS;
+    if ((st = check_device()) != DGEMM_OK) return st;
+    hipStream_t s = (hipStream_t)stream;
+    const NormBwdArgs a{(const char*)dY, (const char*)S, (const char*)dS, weight, rstd, (char*)dX,
+                        dweight ? (float*)workspace : nullptr, M, N, lddy, lds, ldds, lddx, ldp};
+    if (M > 0 && launch_norm_bwd(a, fmt, s) != hipSuccess) return DGEMM_ERR_LAUNCH;
+    if (dweight) return launched(launch_col_reduce((const float*)workspace, grid, ldp, N, dweight, s));
+    return DGEMM_OK;
+}
+
+int rmsnorm_bwd_workspace(int M, int N, size_t* required) {
+    if (M < 0 || N < 0) return DGEMM_ERR_INVALID_VALUE;
+    if (N > NORM_BWD_MAX) return DGEMM_ERR_TOO_LARGE;
+    if (required) *required = (size_t)norm_bwd_grid(M, N) * (size_t)up(N, 4) * 4;
+    return DGEMM_OK;
+}
+
+int quant_f8(int in, int transpose, int M, int N, const void* X, int ldx, void* Q, int ldq,
+             float* scale, void* stream) {
+    const int fmt = row_fmt(in);
+    if (fmt < 0 || M < 0 || N < 0 || (transpose != 0 && transpose != 1)) return DGEMM_ERR_INVALID_VALUE;
+    const Mat mX{X, M, N, ldx, out_esize(fmt)};
+    const Mat mQ{Q, transpose ? N : M, transpose ? M : N, ldq, 1};
+    int st;
+    if ((st = check_mat(mX)) != DGEMM_OK || (st = check_mat(mQ)) != DGEMM_OK) return st;
+    if (M == 0 || N == 0) return DGEMM_OK;
+    if (!scale) return DGEMM_ERR_INVALID_VALUE;
+    if (!transpose && N > ROW_MAX) return DGEMM_ERR_TOO_LARGE;
+    if (check_vec(scale, 4) != DGEMM_OK) return DGEMM_ERR_MISALIGNED;
+    const Mat ins[] = {mX}, outs[] = {mQ, vec(scale, transpose ? N : M)};
+    if (any_overlap(outs, 2, ins, 1)) return DGEMM_ERR_ALIAS;
+    if ((st = check_device()) != DGEMM_OK) return st;
+    RowArgs a{};
+    a.X = (const char*)X;
+    a.Y = (char*)Q;
+    a.scale = scale;
+    a.M = M;
+    a.N = N;
+    a.ldx = ldx;
+    a.ldy = ldq;
+    if (transpose) return launched(launch_quant_cols(a, fmt, (hipStream_t)stream));
+    return launched(launch_rows(a, fmt, false, true, (hipStream_t)stream));
+}
+
+}  // extern "C"

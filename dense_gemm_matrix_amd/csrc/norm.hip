@@ -1,0 +1,502 @@
+// norm.hip -- root-mean-square norms with the residual's addition, forward and
+// backward, and the quantizers that make 8-bit operands, for gfx950 (MI355X).
+//
+// Forward, per row: s = x + r, S := s, rstd = (mean s^2 + eps)^-1/2,
+// y = s rstd w, then Y := y or, in 8 bits, scale = max(max|y| / 448, 2^-100),
+// Y := e4m3(y / scale).  The quantizer alone is the same row pass without the
+// norm.  Bound by HBM: every row is read once, held in registers (eight columns
+// per lane and piece) between the sum of squares, the row maximum and the
+// stores, and written once.
+//
+// A row of up to 1024 columns belongs to one wave (four rows per workgroup, no
+// barrier), longer ones to a workgroup of 256 or 1024 threads, so that a lane
+// holds at most 32 columns (64 columns in registers spill at 1024 threads, so
+// longer rows are refused).
+
+#include <type_traits>
+
+#include "kern_common.h"
+
+namespace dgemm {
+namespace {
+
+constexpr float F8_MAX = 448.0f;                       // largest e4m3 value
+constexpr float SCALE_MIN = 7.888609052210118e-31f;    // 2^-100: a row of zeros divides by it
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int m = 32; m > 0; m >>= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)v, m);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// Reductions over the T threads that share a row (T = 64: one wave; else the
+// whole workgroup, in wave order, so every thread gets the same bits).  `red`
+// holds T / 64 words and is not shared with another reduction of the row.
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    v = wave_sum(v);
+    if constexpr (T == 64) return v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = red[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) s += red[i];
+    return s;
+}
+template <int T>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+    v = wave_max(v);
+    if constexpr (T == 64) return v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    uint32_t s = red[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) s = red[i] > s ? red[i] : s;
+    return s;
+}
+
+// |v| as an integer that orders like the magnitudes, infinities and NaN on top.
+__device__ __forceinline__ uint32_t mag_bits(float v) {
+    return __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
+}
+
+// The scale of a row (or column) whose largest magnitude is `bits`.  A row that
+// holds an infinity or a NaN has no scale: NaN, so every value it stands for is one.
+__device__ __forceinline__ float f8_scale(uint32_t bits) {
+    if (bits >= 0x7f800000u) return __builtin_nanf("");
+    const float s = as_float(bits) / F8_MAX;
+    return s > SCALE_MIN ? s : SCALE_MIN;
+}
+
+// v / scale rounded to the nearest e4m3 value, ties to even; the exact quotient
+// (not a product with the reciprocal), so a tie falls as the definition says.
+__device__ __forceinline__ float f8_clamp(float q) {
+    return q > F8_MAX ? F8_MAX : q < -F8_MAX ? -F8_MAX : q;
+}
+__device__ __forceinline__ uint32_t f8_pack4(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+    return (uint32_t)w;
+}
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// Eight values quantized and stored at byte offset `off` of a row of bytes.
+__device__ __forceinline__ void store_f8(__amdgpu_buffer_rsrc_t r, uint32_t off, int nvalid,
+                                         const float (&v)[8], float scale) {
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = f8_clamp(v[j] / scale);
+    const u32x2 w = {f8_pack4(q[0], q[1], q[2], q[3]), f8_pack4(q[4], q[5], q[6], q[7])};
+    if (nvalid >= 8) {
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, (int)off, 0, 0);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < nvalid)
+                __builtin_amdgcn_raw_buffer_store_b8((unsigned char)(w[j >> 2] >> (8 * (j & 3))), r,
+                                                     (int)(off + j), 0, 0);
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* p, int64_t row, int ld, int N) {
+    return make_rsrc((const char*)p + row * ld * fmt_es<FMT>, (int64_t)N * fmt_es<FMT>);
+}
+
+// FMT: format of X, R, S and (MODE NORM) Y.
+enum RowMode { NORM = 0, NORM_F8 = 1, QUANT = 2 };
+
+template <int FMT, int MODE, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
+    constexpr int WG = T < 256 ? 256 : T;
+    constexpr int RPW = WG / T;  // rows per workgroup
+    __shared__ float red_s[WG / 64];
+    __shared__ uint32_t red_m[WG / 64];
+    // wave-uniform, so that the rows' resources live in scalar registers
+    const int sub = RPW > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+    const int64_t row = (int64_t)blockIdx.x * RPW + sub;
+    if (row >= a.M) return;  // T == 64 only: no barrier follows
+    const int t = threadIdx.x % T;
+    float v[NV][8];
+    Row8<FMT> x[NV], r[NV];
+    const auto rx = row_rsrc<FMT>(a.X, row, a.ldx, a.N);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * T + t) * 8;
+        x[i].load(rx, (uint32_t)c * fmt_es<FMT>, a.N - c);
+    }
+    const bool res = MODE != QUANT && a.R;
+    if (res) {
+        const auto rr = row_rsrc<FMT>(a.R, row, a.ldr, a.N);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * 8;
+            r[i].load(rr, (uint32_t)c * fmt_es<FMT>, a.N - c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        x[i].get(v[i]);
+        if (res) {
+            float w[8];
+            r[i].get(w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] += w[j];
+        }
+    }
+    if constexpr (MODE != QUANT) {
+        if (a.S) {
+            const auto rs = row_rsrc<FMT>(a.S, row, a.lds, a.N);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * T + t) * 8;
+                Row8<FMT> o;
+                o.set(v[i]);
+                o.store(rs, (uint32_t)c * fmt_es<FMT>, a.N - c);
+            }
+        }
+        float ss = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+        ss = row_sum<T>(ss, red_s);
+        const float rstd = rsqrtf(ss / (float)a.N + a.eps);
+        if (a.rstd && t == 0) a.rstd[row] = rstd;
+        const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * 8;
+            Row8<OUT_F32> w8;
+            w8.load(rw, (uint32_t)c * 4, a.N - c);
+            float w[8];
+            w8.get(w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+        }
+    }
+    if constexpr (MODE == NORM) {
+        const auto ry = row_rsrc<FMT>(a.Y, row, a.ldy, a.N);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * 8;
+            Row8<FMT> o;
+            o.set(v[i]);
+            o.store(ry, (uint32_t)c * fmt_es<FMT>, a.N - c);
+        }
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = (i * T + t) * 8 + j < a.N ? mag_bits(v[i][j]) : 0u;
+                m = b > m ? b : m;
+            }
+        m = row_max<T>(m, red_m);
+        const float scale = f8_scale(m);
+        if (t == 0) a.scale[row] = scale;
+        const auto ry = make_rsrc((const char*)a.Y + row * a.ldy, a.N);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * 8;
+            if (c < a.N) store_f8(ry, (uint32_t)c, a.N - c, v[i], scale);
+        }
+    }
+}
+
+template <int FMT, int MODE, int T, int NV>
+hipError_t go_row(const RowArgs& a, hipStream_t stream) {
+    constexpr int WG = T < 256 ? 256 : T;
+    const int64_t blocks = ((int64_t)a.M + WG / T - 1) / (WG / T);
+    RowArgs b = a;
+    void* args[] = {&b};
+    return hipLaunchKernel((const void*)row_kernel<FMT, MODE, T, NV>, dim3((unsigned)blocks), dim3(WG),
+                           args, 0, stream);
+}
+
+template <int FMT, int MODE>
+hipError_t row_by_size(const RowArgs& a, hipStream_t s) {
+    if (a.N <= 512) return go_row<FMT, MODE, 64, 1>(a, s);
+    if (a.N <= 1024) return go_row<FMT, MODE, 64, 2>(a, s);
+    if (a.N <= 2048) return go_row<FMT, MODE, 256, 1>(a, s);
+    if (a.N <= 4096) return go_row<FMT, MODE, 256, 2>(a, s);
+    if (a.N <= 8192) return go_row<FMT, MODE, 256, 4>(a, s);
+    if (a.N <= 16384) return go_row<FMT, MODE, 1024, 2>(a, s);
+    if (a.N <= ROW_MAX) return go_row<FMT, MODE, 1024, 4>(a, s);
+    return hipErrorInvalidValue;
+}
+
+template <int FMT>
+hipError_t row_by_mode(const RowArgs& a, bool norm, bool f8, hipStream_t s) {
+    if (!norm) return row_by_size<FMT, QUANT>(a, s);
+    return f8 ? row_by_size<FMT, NORM_F8>(a, s) : row_by_size<FMT, NORM>(a, s);
+}
+
+// ------------------------------------------------------- columns to 8 bits
+//
+// Q[n][m] := e4m3(X[m][n] / scale[n]), scale[n] from column n's largest
+// magnitude: a weight matrix stored per input becomes gemm_f8's operand, stored
+// per output.  One workgroup of 512 threads per 64 columns, two passes over
+// them: the columns' maxima, then 64 x 64 tiles quantized and transposed in LDS
+// (byte rows padded to 68 so that the eight columns a lane writes fall in
+// different banks).  Done once per weight.
+
+constexpr int QT_THREADS = 512;
+
+template <int FMT>
+__global__ __launch_bounds__(QT_THREADS) void quant_cols_kernel(RowArgs a) {
+    __shared__ uint32_t cmax[64][64];  // [row lane][column]
+    __shared__ float cscale[64];
+    __shared__ __attribute__((aligned(16))) unsigned char tile[64][68];
+    const int n0 = (int)blockIdx.x * 64;
+    const int t = threadIdx.x;
+    const int c8 = (t & 7) * 8, rl = t >> 3;  // this thread's columns and row lane
+    const int nvalid = a.N - (n0 + c8);
+    uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int row = rl; row < a.M; row += 64) {
+        Row8<FMT> x;
+        x.load_from(a.X + ((int64_t)row * a.ldx + n0 + c8) * fmt_es<FMT>, nvalid);
+        float v[8];
+        x.get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t b = mag_bits(v[j]);
+            m[j] = b > m[j] ? b : m[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) cmax[rl][c8 + j] = m[j];
+    __syncthreads();
+    if (t < 64) {
+        uint32_t s = 0;
+        for (int i = 0; i < 64; ++i) s = cmax[i][t] > s ? cmax[i][t] : s;
+        const float scale = f8_scale(s);
+        cscale[t] = scale;
+        if (n0 + t < a.N) a.scale[n0 + t] = scale;
+    }
+    __syncthreads();
+    float sc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sc[j] = cscale[c8 + j];
+    for (int k0 = 0; k0 < a.M; k0 += 64) {
+        const int row = k0 + rl;
+        if (row < a.M) {
+            Row8<FMT> x;
+            x.load_from(a.X + ((int64_t)row * a.ldx + n0 + c8) * fmt_es<FMT>, nvalid);
+            float v[8];
+            x.get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t w = f8_pack4(f8_clamp(v[j] / sc[j]), 0.0f, 0.0f, 0.0f);
+                tile[c8 + j][rl] = (unsigned char)(w & 0xffu);
+            }
+        }
+        __syncthreads();
+        // thread t: bytes 8 (t & 7) .. + 7 of output row t >> 3
+        const int n = n0 + (t >> 3), k = k0 + (t & 7) * 8;
+        if (n < a.N && k < a.M) {
+            unsigned char* q = (unsigned char*)a.Y + (int64_t)n * a.ldy + k;
+            const unsigned char* p = &tile[t >> 3][(t & 7) * 8];
+            if (k + 8 <= a.M) {
+                const uint32_t lo = *(const uint32_t*)p, hi = *(const uint32_t*)(p + 4);
+                *(u32x2*)q = u32x2{lo, hi};
+            } else {
+                for (int j = 0; j < a.M - k; ++j) q[j] = p[j];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int FMT>
+hipError_t go_quant_cols(const RowArgs& a, hipStream_t stream) {
+    RowArgs b = a;
+    void* args[] = {&b};
+    return hipLaunchKernel((const void*)quant_cols_kernel<FMT>, dim3((unsigned)((a.N + 63) / 64)),
+                           dim3(QT_THREADS), args, 0, stream);
+}
+
+// --------------------------------------------------------------- backward
+//
+// With xh = s rstd, g = dy w:  dx = rstd (g - xh mean(g xh)) + ds, and
+// dw = sum over rows of dy xh.  Each workgroup walks rows blockIdx, blockIdx +
+// grid, ...; a row's dy and s are loaded once, held in registers over the row's
+// reduction, and the next row's loads are issued before it.  The thread's
+// columns are the same in every row, so dw is a running fp32 sum in registers,
+// written once per workgroup to the workspace and added over workgroups by
+// col_reduce_kernel in a fixed order: no atomics, the same bits every time.
+
+template <int FMT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr int WG = T < 256 ? 256 : T;
+    constexpr int RPW = WG / T;
+    constexpr int ES = fmt_es<FMT>;
+    __shared__ float red[2][WG / 64];
+    __shared__ float dwl[RPW > 1 ? RPW * T * NV * 8 : 1];
+    const int t = threadIdx.x % T;
+    const int sub = RPW > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+    const int64_t step = (int64_t)gridDim.x * RPW;
+    float w[NV][8], dw[NV][8];
+    const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * T + t) * 8;
+        Row8<OUT_F32> w8;
+        w8.load(rw, (uint32_t)c * 4, a.N - c);
+        w8.get(w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    }
+    Row8<FMT> y[NV], s[NV], d[NV];
+    auto load = [&](int64_t row) {
+        const auto ry = row_rsrc<FMT>(a.dY, row, a.lddy, a.N);
+        const auto rs = row_rsrc<FMT>(a.S, row, a.lds, a.N);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * 8;
+            y[i].load(ry, (uint32_t)c * ES, a.N - c);
+            s[i].load(rs, (uint32_t)c * ES, a.N - c);
+        }
+        if (a.dS) {
+            const auto rd = row_rsrc<FMT>(a.dS, row, a.ldds, a.N);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * T + t) * 8;
+                d[i].load(rd, (uint32_t)c * ES, a.N - c);
+            }
+        }
+    };
+    int64_t row = (int64_t)blockIdx.x * RPW + sub;
+    if (row < a.M) load(row);
+    int par = 0;
+    for (; row < a.M; row += step, par ^= 1) {
+        const float rstd = a.rstd[row];
+        // The row stays in its storage format (half the registers of fp32 for
+        // 16-bit rows); the few products are formed again after the reduction.
+        Row8<FMT> cy[NV], cs[NV], cd[NV];
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            cy[i] = y[i];
+            cs[i] = s[i];
+            cd[i] = d[i];
+            float dy[8], x[8];
+            cy[i].get(dy);
+            cs[i].get(x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float xh = x[j] * rstd;
+                dot += dy[j] * w[i][j] * xh;
+                dw[i][j] += dy[j] * xh;
+            }
+        }
+        if (row + step < a.M) load(row + step);
+        // The reduction's words alternate between rows, so one barrier per row
+        // is enough: a wave reaches the next but one row's write only after
+        // every wave has passed the next row's barrier.
+        const float mean = row_sum<T>(dot, red[par]) / (float)a.N;
+        const auto ro = row_rsrc<FMT>(a.dX, row, a.lddx, a.N);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * T + t) * 8;
+            float dy[8], x[8], o[8], e[8];
+            cy[i].get(dy);
+            cs[i].get(x);
+            if (a.dS) cd[i].get(e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j] = rstd * (dy[j] * w[i][j] - x[j] * rstd * mean);
+                if (a.dS) o[j] += e[j];
+            }
+            Row8<FMT> out;
+            out.set(o);
+            out.store(ro, (uint32_t)c * ES, a.N - c);
+        }
+    }
+    if (!a.part) return;
+    if constexpr (RPW > 1) {
+        // The workgroup's waves hold the same columns: add them in wave order.
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) dwl[(sub * NV * 8 + i * 8 + j) * T + t] = dw[i][j];
+        __syncthreads();
+        if (sub != 0) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                for (int q = 1; q < RPW; ++q) dw[i][j] += dwl[(q * NV * 8 + i * 8 + j) * T + t];
+    }
+    const auto rp = make_rsrc((const char*)(a.part + (int64_t)blockIdx.x * a.ldp), (int64_t)a.N * 4);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (i * T + t) * 8;
+        Row8<OUT_F32> out;
+        out.set(dw[i]);
+        out.store(rp, (uint32_t)c * 4, a.N - c);
+    }
+}
+
+template <int FMT, int T, int NV>
+hipError_t go_bwd(const NormBwdArgs& a, int grid, hipStream_t stream) {
+    NormBwdArgs b = a;
+    void* args[] = {&b};
+    return hipLaunchKernel((const void*)norm_bwd_kernel<FMT, T, NV>, dim3((unsigned)grid),
+                           dim3(T < 256 ? 256 : T), args, 0, stream);
+}
+
+template <int FMT>
+hipError_t bwd_by_size(const NormBwdArgs& a, int grid, hipStream_t s) {
+    if (a.N <= 512) return go_bwd<FMT, 64, 1>(a, grid, s);
+    if (a.N <= 1024) return go_bwd<FMT, 64, 2>(a, grid, s);
+    if (a.N <= 2048) return go_bwd<FMT, 256, 1>(a, grid, s);
+    if (a.N <= 4096) return go_bwd<FMT, 256, 2>(a, grid, s);
+    if (a.N <= 8192) return go_bwd<FMT, 256, 4>(a, grid, s);
+    if (a.N <= NORM_BWD_MAX) return go_bwd<FMT, 512, 4>(a, grid, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_rows(const RowArgs& a, int fmt, bool norm, bool f8, hipStream_t stream) {
+    if (fmt == OUT_F32) return row_by_mode<OUT_F32>(a, norm, f8, stream);
+    if (fmt == OUT_BF16) return row_by_mode<OUT_BF16>(a, norm, f8, stream);
+    if (fmt == OUT_F16) return row_by_mode<OUT_F16>(a, norm, f8, stream);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_quant_cols(const RowArgs& a, int fmt, hipStream_t stream) {
+    if (fmt == OUT_F32) return go_quant_cols<OUT_F32>(a, stream);
+    if (fmt == OUT_BF16) return go_quant_cols<OUT_BF16>(a, stream);
+    if (fmt == OUT_F16) return go_quant_cols<OUT_F16>(a, stream);
+    return hipErrorInvalidValue;
+}
+
+// Two workgroups of 256 threads per CU keep enough rows in flight; more only
+// adds partial sums of dw.
+int norm_bwd_grid(int M, int N) {
+    const int64_t rows = N <= 1024 ? ((int64_t)M + 3) / 4 : M;
+    const int64_t most = N <= 8192 ? 2 * NUM_CU : NUM_CU;
+    return (int)(rows < most ? rows : most);
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream) {
+    const int grid = norm_bwd_grid(a.M, a.N);
+    if (fmt == OUT_F32) return bwd_by_size<OUT_F32>(a, grid, stream);
+    if (fmt == OUT_BF16) return bwd_by_size<OUT_BF16>(a, grid, stream);
+    if (fmt == OUT_F16) return bwd_by_size<OUT_F16>(a, grid, stream);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace dgemm

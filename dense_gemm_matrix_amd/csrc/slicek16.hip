@@ -138,7 +138,7 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
                                                       __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-template <int IN, int OUT, bool EPI, int MI, int W, bool IL>
+template <int IN, int OUT, int EPI, int MI, int W, bool IL>
 __global__ __launch_bounds__(64 * W) void slicek16_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* __restrict__ C,
     int M, int N, int K, int lda, int ldb, int ldc, int tiles_m, int tiles_n, EpiArgs epi) {
@@ -304,6 +304,22 @@ __global__ __launch_bounds__(64 * W) void slicek16_kernel(
         for (int r = 0; r < 16; ++r)
             red[(wave * NB * 16 + b * 16 + r) * 64 + lane] = acc[b / MI][b % MI][r];
     __syncthreads();
+    if constexpr (EPI == EPI_FULL) {
+        float v[PER];
+        int row[PER], col[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int idx = wave * PER + q;
+            const int b = idx / 16, r = idx % 16;
+            v[q] = red[idx * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v[q] += red[(w * NB * 16 + idx) * 64 + lane];
+            row[q] = m0 + (b / MI) * 32 + 8 * (r >> 2) + 4 * g + (r & 3);
+            col[q] = n0 + (b % MI) * 32 + li;
+        }
+        finish_full<OUT, PER>(v, row, col, C, M, N, ldc, epi);
+        return;
+    }
     const __amdgpu_buffer_rsrc_t cr = c_rsrc(C, M, N, ldc, m0, n0, ES);
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
@@ -330,8 +346,9 @@ __global__ __launch_bounds__(64 * W) void slicek16_kernel(
 
 template <int IN, int OUT, int MI, int W, bool IL>
 hipError_t go_slice16(const GemmLaunch& L) {
-    const void* fn = L.epi ? (const void*)slicek16_kernel<IN, OUT, true, MI, W, IL>
-                           : (const void*)slicek16_kernel<IN, OUT, false, MI, W, IL>;
+    const void* fn = L.epi == EPI_FULL    ? (const void*)slicek16_kernel<IN, OUT, EPI_FULL, MI, W, IL>
+                     : L.epi == EPI_BASIC ? (const void*)slicek16_kernel<IN, OUT, EPI_BASIC, MI, W, IL>
+                                          : (const void*)slicek16_kernel<IN, OUT, EPI_NONE, MI, W, IL>;
     const char* a = L.A;
     const char* b = L.B;
     char* c = L.C;

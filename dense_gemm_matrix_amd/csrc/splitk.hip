@@ -15,7 +15,7 @@ namespace {
 
 constexpr int RED_THREADS = 256;
 
-template <int OUT, bool EPI>
+template <int OUT, int EPI>
 __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
     const float* __restrict__ W, int splits, int64_t zstride, int ldw, char* __restrict__ C,
     int ldc, int M, int N, EpiArgs e) {
@@ -30,12 +30,19 @@ __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
     f32x4 s = *(const f32x4*)p;
     for (int z = 1; z < splits; ++z) s += *(const f32x4*)(p + z * zstride);
 
+    if constexpr (EPI == EPI_FULL) {
+        float f[4] = {s[0], s[1], s[2], s[3]};
+        const int rows[4] = {row, row, row, row};
+        const int cols[4] = {col0, col0 + 1, col0 + 2, col0 + 3};
+        finish_full<OUT, 4>(f, rows, cols, C, M, N, ldc, e);
+        return;
+    }
     const int64_t base = (int64_t)row * ldc + col0;
     float v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         v[j] = s[j];
-        if constexpr (EPI) {
+        if constexpr (EPI == EPI_BASIC) {
             if (col0 + j < N) {
                 const float bias = e.bias ? e.bias[col0 + j] : 0.0f;
                 v[j] = epilogue<OUT>(v[j], C, base + j, bias, e);
@@ -65,7 +72,7 @@ __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
     }
 }
 
-template <int OUT, bool EPI>
+template <int OUT, int EPI>
 hipError_t go(const float* W, int splits, int64_t zstride, int ldw, char* C, int ldc, int M, int N,
               const EpiArgs& e, hipStream_t stream) {
     const int64_t threads = (int64_t)M * (ldw / 4);
@@ -79,16 +86,17 @@ hipError_t go(const float* W, int splits, int64_t zstride, int ldw, char* C, int
 }
 
 template <int OUT>
-hipError_t by_epi(bool epi, const float* W, int splits, int64_t zstride, int ldw, char* C, int ldc,
+hipError_t by_epi(int epi, const float* W, int splits, int64_t zstride, int ldw, char* C, int ldc,
                   int M, int N, const EpiArgs& e, hipStream_t stream) {
-    return epi ? go<OUT, true>(W, splits, zstride, ldw, C, ldc, M, N, e, stream)
-               : go<OUT, false>(W, splits, zstride, ldw, C, ldc, M, N, e, stream);
+    if (epi == EPI_FULL) return go<OUT, EPI_FULL>(W, splits, zstride, ldw, C, ldc, M, N, e, stream);
+    if (epi == EPI_BASIC) return go<OUT, EPI_BASIC>(W, splits, zstride, ldw, C, ldc, M, N, e, stream);
+    return go<OUT, EPI_NONE>(W, splits, zstride, ldw, C, ldc, M, N, e, stream);
 }
 
 }  // namespace
 
 hipError_t launch_splitk_reduce(const float* W, int splits, int64_t zstride, int ldw, char* C,
-                                int ldc, int M, int N, int out, bool epi, const EpiArgs& e,
+                                int ldc, int M, int N, int out, int epi, const EpiArgs& e,
                                 hipStream_t stream) {
     if (ldw % 4 != 0 || splits < 1) return hipErrorInvalidValue;
     if (out == OUT_F32) return by_epi<OUT_F32>(epi, W, splits, zstride, ldw, C, ldc, M, N, e, stream);

@@ -69,7 +69,8 @@ typedef enum {
     DGEMM_ERR_TOO_LARGE = 5,     /* 256*lda*esize, 128*ldb or 256*ldc*esize_out bytes reach 2 GiB */
     DGEMM_ERR_DEVICE = 6,        /* no current device, or it is not a gfx950                     */
     DGEMM_ERR_LAUNCH = 7,        /* the kernel launch reported an error                          */
-    DGEMM_ERR_SCRATCH_SIZE = 8   /* gemm_ex_static: scratch_bytes > DGEMM_STATIC_SCRATCH_BYTES   */
+    DGEMM_ERR_SCRATCH_SIZE = 8,  /* gemm_ex_static: scratch_bytes > DGEMM_STATIC_SCRATCH_BYTES   */
+    DGEMM_ERR_WORKSPACE = 9      /* a backward pass: the workspace is smaller than the call needs */
 } dgemm_status;
 
 /* Format of C for the 16-bit entry points. */
@@ -145,10 +146,14 @@ typedef enum {
     DGEMM_IN_F32_3XBF16 = 3  /* fp32 through the 3 x bf16 split (as gemm_f32_3xbf16) */
 } dgemm_in;
 
-/* Activation of gemm_ex's epilogue. */
+/* Activations.  gemm_ex takes the first two; gemm_act, gemm_act_bwd and gemm_f8
+   take all.  Phi is the normal distribution's integral. */
 typedef enum {
     DGEMM_ACT_NONE = 0,
-    DGEMM_ACT_RELU = 1  /* x < 0 -> 0; NaN passes through */
+    DGEMM_ACT_RELU = 1,       /* x < 0 -> 0; NaN passes through                              */
+    DGEMM_ACT_GELU = 2,       /* x Phi(x) = x (1 + erf(x / sqrt 2)) / 2                      */
+    DGEMM_ACT_GELU_TANH = 3,  /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2           */
+    DGEMM_ACT_SILU = 4        /* x / (1 + exp(-x))                                           */
 } dgemm_act;
 
 /*
@@ -259,6 +264,178 @@ int gemm_ex_static(int in, int out, int M, int N, int K,
 int gemm_ex_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
                  int* tile_rows, int* tile_cols, int* splits, size_t* workspace_used);
 
+/*
+ * A linear layer: the product with bias, activation and residual in its
+ * epilogue, and its gradients.
+ *
+ *     Z[i][j] := sum_k A[i][k] * B[k][j] + bias[j]
+ *     C[i][j] := act(Z[i][j]) + R[i][j]
+ *
+ * Evaluated in fp32 on the fp32 sum and rounded once (to nearest even) to C's
+ * format; the activation takes the unrounded Z.  bias: NULL or N fp32 values
+ * (4-byte aligned).  R: NULL or an M x N matrix in C's format, row pitch ldr;
+ * it may be C itself (same pointer and pitch: C := act(..) + C), and overlaps C
+ * in no other way.  Z: NULL, or where to keep the pre-activations for
+ * gemm_act_bwd, in C's format, row pitch ldz.  R and Z obey C's rules of
+ * alignment, pitch and panel size; ldr and ldz are not looked at where the
+ * pointer is NULL.  Any dgemm_act.  in, out, sizes and the other arguments,
+ * errors and execution as gemm_ex; a workspace allows split plans as in gemm_ex
+ * (gemm_act_plan tells the bytes), never a Stream-K plan.
+ *
+ * At most 16 rows of bf16 / fp16 run a kernel of their own that streams B
+ * through registers (tokens being generated: bound by reading B once).
+ */
+int gemm_act(int in, int out, int M, int N, int K,
+             const void* A, int lda,
+             const void* B, int ldb,
+             void* C, int ldc,
+             const float* bias, int act,
+             const void* R, int ldr,
+             void* Z, int ldz,
+             void* workspace, size_t workspace_bytes,
+             void* stream);
+
+/* As gemm_ex_plan, for gemm_act (a 16-row tile: the kernel for few rows). */
+int gemm_act_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
+                  int* tile_rows, int* tile_cols, int* splits, size_t* workspace_used);
+
+/*
+ * gemm_act's backward pass.  Given dC, the gradient of C (M x N in C's format,
+ * which `out` names as in gemm_act), and Z as gemm_act stored it:
+ *
+ *     dZ = dC o act'(Z)        dA := dZ * B^T       (M x K, input format)
+ *     dbias := column sums of dZ (fp32)
+ *                              dB := A^T * dZ       (K x N, input format)
+ *
+ * The residual's gradient is dC itself.  dA, dB and dbias may each be NULL
+ * (not wanted); A is read only for dB, B only for dA, and with act =
+ * DGEMM_ACT_NONE Z is not read.  relu'(0) = 0.  dZ is rounded once to the input
+ * format for the products (unless it is dC itself); dbias sums unrounded fp32
+ * values, in an order that depends on the shape only: results are
+ * deterministic.  Empty sums are zero: M == 0 writes dB = 0 and dbias = 0, N == 0
+ * writes dA = 0.  Outputs overlap no input and no other output.
+ *
+ * The workspace (16-byte aligned) holds dZ, partial column sums, transposes
+ * (fp32) and split plans' partial products; its contents before and after are
+ * unspecified.  DGEMM_ERR_WORKSPACE if it is smaller than `required` bytes of
+ * gemm_act_bwd_workspace; with `best` bytes the products take their fastest
+ * plans.  Both figures are those of a call that wants all three gradients.
+ */
+int gemm_act_bwd(int in, int out, int M, int N, int K,
+                 const void* A, int lda,
+                 const void* B, int ldb,
+                 const void* dC, int lddc,
+                 const void* Z, int ldz, int act,
+                 void* dA, int ldda,
+                 void* dB, int lddb,
+                 float* dbias,
+                 void* workspace, size_t workspace_bytes,
+                 void* stream);
+
+int gemm_act_bwd_workspace(int in, int out, int M, int N, int K, int act,
+                           size_t* required, size_t* best);
+
+/*
+ * The product of 8-bit operands (OCP e4m3: 448 the largest value, no
+ * infinities) with a scale per row of A and per row of B:
+ *
+ *     C[i][j] := act(scale_a[i] * scale_b[j] * sum_k A[i][k] * B[j][k] + bias[j])
+ *                + R[i][j]
+ *
+ * A: M x K, B: N x K, both K-contiguous (a weight is stored per output, as
+ * quant_f8 with transpose = 1 makes it from a K x N matrix); bases 16-byte
+ * aligned, lda and ldb multiples of 16.  scale_a: M, scale_b: N fp32 values.
+ * out: C's format (and R's) by its dgemm_in code DGEMM_IN_F32, _BF16 or _F16.
+ * fp32 accumulation: exactly that for fp32 C and for at most 16 rows (a kernel
+ * that streams B through registers); for 16-bit C the 8-bit matrix instruction,
+ * which drops bits below 2^-13 of the largest of neighbouring products (in all
+ * 1.5e-5 to 5e-5 of the result's 2-norm, below C's rounding).  bias, act, R,
+ * workspace, errors and execution as gemm_act.
+ */
+int gemm_f8(int out, int M, int N, int K,
+            const void* A, int lda,
+            const void* B, int ldb,
+            void* C, int ldc,
+            const float* scale_a, const float* scale_b,
+            const float* bias, int act,
+            const void* R, int ldr,
+            void* workspace, size_t workspace_bytes,
+            void* stream);
+
+/* As gemm_ex_plan, for gemm_f8. */
+int gemm_f8_plan(int out, int M, int N, int K, size_t workspace_bytes,
+                 int* tile_rows, int* tile_cols, int* splits, size_t* workspace_used);
+
+/* Output of rmsnorm: X's format, or gemm_f8's 8-bit rows and their scales. */
+typedef enum { DGEMM_ROWS_SAME = 0, DGEMM_ROWS_F8 = 1 } dgemm_rows;
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition and an output in
+ * 8 bits for gemm_f8:
+ *
+ *     s = X[i] + R[i]                    S[i] := s
+ *     rstd[i] := (mean_j s_j^2 + eps)^-1/2
+ *     y = s * rstd[i] * weight           Y[i] := y,  or in 8 bits
+ *     scale[i] := max(max_j |y_j| / 448, 2^-100),  Y[i] := e4m3(y / scale[i])
+ *
+ * in: the format of X, R, S and a DGEMM_ROWS_SAME Y (DGEMM_IN_F32, _BF16 or
+ * _F16).  R (NULL: none), S and rstd (NULL: not wanted) are optional; scale is
+ * given with DGEMM_ROWS_F8 and only then.  weight: N fp32 values, 16-byte
+ * aligned.  All arithmetic is fp32 on the unrounded sum, each output rounded
+ * once.  S and Y may each be X or R itself (same pointer, pitch and format).
+ * A row holding an infinity or a NaN gets scale NaN in 8 bits.  1 <= N <= 32768
+ * (DGEMM_ERR_TOO_LARGE above); M == 0 or N == 0 is a no-op; eps >= 0.  Rows obey
+ * C's rules of alignment, pitch and panel size; errors and execution as gemm_ex.
+ */
+int rmsnorm(int in, int out, int M, int N,
+            const void* X, int ldx,
+            const void* R, int ldr,
+            void* S, int lds,
+            const float* weight, float eps,
+            void* Y, int ldy,
+            float* scale, float* rstd,
+            void* stream);
+
+/*
+ * rmsnorm's backward pass.  Given dY, the gradient of Y, dS (or NULL), the
+ * gradient that reaches S by other ways, S (X where there was no residual) and
+ * rstd as rmsnorm stored them:
+ *
+ *     h = S[i] * rstd[i],  g = dY[i] * weight
+ *     dX[i] := rstd[i] * (g - h * mean_j(g_j h_j)) + dS[i]   (R's gradient too)
+ *     dweight := sum_i dY[i] * h                              (fp32)
+ *
+ * dX may be dY or dS itself.  dweight may be NULL; if not, a workspace of
+ * rmsnorm_bwd_workspace's bytes (16-byte aligned) holds its partial sums, added
+ * in a fixed order.  N <= 16384 (DGEMM_ERR_TOO_LARGE above); M == 0 writes
+ * dweight = 0.  Otherwise as rmsnorm.
+ */
+int rmsnorm_bwd(int in, int M, int N,
+                const void* dY, int lddy,
+                const void* S, int lds,
+                const float* weight, const float* rstd,
+                const void* dS, int ldds,
+                void* dX, int lddx,
+                float* dweight,
+                void* workspace, size_t workspace_bytes,
+                void* stream);
+
+int rmsnorm_bwd_workspace(int M, int N, size_t* required);
+
+/*
+ * Rows to 8 bits: scale[i] := max(max_j |X[i][j]| / 448, 2^-100), Q[i][j] :=
+ * e4m3(X[i][j] / scale[i]), the exact quotient rounded to nearest even.  With
+ * transpose = 1 by columns: scale[j] from column j, Q (N x M, row pitch ldq)
+ * [j][i] := e4m3(X[i][j] / scale[j]): a K x N weight becomes gemm_f8's N x K
+ * operand.  A row (column) holding an infinity or a NaN gets scale NaN.  in: X's
+ * format (DGEMM_IN_F32, _BF16 or _F16).  Without transpose N <= 32768.
+ */
+int quant_f8(int in, int transpose, int M, int N,
+             const void* X, int ldx,
+             void* Q, int ldq,
+             float* scale,
+             void* stream);
+
 /* Plan kinds of dgemm_set_plan_override. */
 typedef enum {
     DGEMM_PLAN_AUTO = 0,      /* the cost model's choice (the default)                */
@@ -281,6 +458,9 @@ typedef enum {
  * out (tile and split arguments ignored by both).  A forced plan the call cannot take (tile shape the kernel lacks,
  * workspace too small, Stream-K for fp32 inputs or under graph capture) falls
  * back to the cost model's choice, which gemm_ex_plan then reports.
+ * gemm_act, gemm_act_bwd and gemm_f8 follow DGEMM_PLAN_GRID too: gemm_act the
+ * tiles above and, for at most 16 rows of 16-bit inputs, 16 x 32, 16 x 64 and
+ * 16 x 128; the other two's 16-bit and 8-bit products 256 x 256 and 128 x 128.
  * DGEMM_PLAN_AUTO clears the override.  Not synchronised with calls running
  * on other host threads.  Returns DGEMM_OK, or DGEMM_ERR_INVALID_VALUE for a
  * bad kind or splits < 1 with DGEMM_PLAN_GRID.
