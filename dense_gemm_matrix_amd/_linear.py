@@ -9,7 +9,7 @@ import ctypes
 import torch
 
 from ._binding import (DGEMM_OUT_F32, DGEMM_OUT_SAME, IN_CODES, _TORCH_IN, _check, _lib, _on_device,
-                       _pitch, _shapes, _stream)
+                       _shapes, _stream)
 
 _i, _p, _sz, _f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 _P, _PS = ctypes.POINTER(_i), ctypes.POINTER(_sz)
@@ -40,43 +40,77 @@ def _act(act: str) -> int:
     return ACT_CODES[act]
 
 
-def _vector(t, n: int, device, name: str):
-    """Pointer of an optional fp32 vector of length n."""
+# The checks below run on every call and are most of a small call's host time, so
+# each is one pass over attributes that torch answers without building objects
+# (device indices, dtypes and sizes compared as such), and the messages are made
+# only when one fails.
+_FP32 = torch.float32
+_PER16 = {torch.float32: 4, torch.bfloat16: 8, torch.float16: 8, F8: 16}
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
+    else torch.cuda.current_device
+
+
+def _vector(t, n: int, dev: int, name: str):
+    """Pointer of an optional fp32 vector of length n on device index dev."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() \
-            or t.device != device:
+    if t.dtype is not _FP32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() \
+            or t.get_device() != dev:
         raise ValueError(f"{name} must be a contiguous float32 device vector of length {n}")
     return t.data_ptr()
 
 
-def _matrix(t, shape, dtype, device, name: str):
-    """(pointer, pitch) of an optional matrix operand."""
+def _ld(t, rows: int, cols: int) -> int:
+    """_pitch, for a matrix of known size."""
+    pitch, inner = t.stride()
+    if inner != 1 and cols > 1 and rows > 0:
+        raise ValueError("operands must be row-major with unit inner stride")
+    if rows > 1:
+        return pitch
+    per16 = _PER16[t.dtype]
+    return (max(cols, 1) + per16 - 1) // per16 * per16
+
+
+def _matrix(t, rows: int, cols: int, dtype, dev: int, name: str):
+    """(pointer, pitch) of an optional matrix operand on device index dev."""
     if t is None:
         return None, 0
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError(f"{name} must be a {tuple(shape)} matrix on {device}")
-    return t.data_ptr(), _pitch(t, shape[1])
+    if t.shape != (rows, cols) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {(rows, cols)} matrix on device {dev}")
+    return t.data_ptr(), _ld(t, rows, cols)
 
 
-def _workspace(ws, device):
+def _workspace(ws, dev: int):
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
+    if ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the output's device")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _call(fn, t, *args) -> None:
+    """Calls a C entry point with t's device current."""
+    if t.get_device() == _current_device():
+        status = fn(*args)
+    else:
+        with _on_device(t):
+            status = fn(*args)
+    if status:
+        _check(status)
+
+
 def _formats(A, B, C_dtype, in_fmt):
     """(input code, output code) of a product of A and B with C_dtype results."""
-    fmt = in_fmt or _TORCH_IN.get(A.dtype)
-    if fmt not in IN_CODES or B.dtype != A.dtype or _TORCH_IN.get(A.dtype) != ("f32" if fmt == "f32x3" else fmt):
+    dtype = A.dtype
+    own = _TORCH_IN.get(dtype)
+    fmt = in_fmt or own
+    if own is None or B.dtype is not dtype or (fmt != own and not (fmt == "f32x3" and own == "f32")):
         raise TypeError("unsupported input dtypes")
-    if C_dtype == torch.float32:
+    if C_dtype is _FP32:
         return IN_CODES[fmt], DGEMM_OUT_F32
-    if C_dtype != A.dtype:
+    if C_dtype is not dtype:
         raise TypeError("C must be float32 or the input dtype")
     return IN_CODES[fmt], DGEMM_OUT_SAME
 
@@ -88,6 +122,15 @@ def _device_tensor(t, name):
         raise ValueError(f"{name} must be a device tensor")
 
 
+def _sizes(A, B, C):
+    """_shapes, for the calls of this module."""
+    sa, sb = A.shape, B.shape
+    if len(sa) != 2 or len(sb) != 2 or sa[1] != sb[0] or C.shape != (sa[0], sb[1]) \
+            or not (A.get_device() == B.get_device() == C.get_device() >= 0):
+        return _shapes(A, B, C)  # raises
+    return sa[0], sb[1], sa[1]
+
+
 def gemm_act(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *, bias: torch.Tensor = None,
              act: str = "none", residual: torch.Tensor = None, preact: torch.Tensor = None,
              workspace: torch.Tensor = None, in_fmt: str = None, stream=None) -> None:
@@ -95,16 +138,15 @@ def gemm_act(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *, bias: torch.T
 
     `residual` and `preact` have C's shape and dtype; `residual` may be C itself.
     `workspace` and `in_fmt` as in gemm_ex."""
-    M, N, K = _shapes(A, B, C)
+    M, N, K = _sizes(A, B, C)
     code, out = _formats(A, B, C.dtype, in_fmt)
-    r, ldr = _matrix(residual, (M, N), C.dtype, C.device, "residual")
-    z, ldz = _matrix(preact, (M, N), C.dtype, C.device, "preact")
-    ws, ws_bytes = _workspace(workspace, C.device)
-    with _on_device(C):
-        _check(_lib.gemm_act(code, out, M, N, K, A.data_ptr(), _pitch(A, K), B.data_ptr(),
-                             _pitch(B, N), C.data_ptr(), _pitch(C, N),
-                             _vector(bias, N, C.device, "bias"), _act(act), r, ldr, z, ldz, ws,
-                             ws_bytes, _stream(C, stream)))
+    dev, dtype = C.get_device(), C.dtype
+    r, ldr = _matrix(residual, M, N, dtype, dev, "residual")
+    z, ldz = _matrix(preact, M, N, dtype, dev, "preact")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call(_lib.gemm_act, C, code, out, M, N, K, A.data_ptr(), _ld(A, M, K), B.data_ptr(),
+          _ld(B, K, N), C.data_ptr(), _ld(C, M, N), _vector(bias, N, dev, "bias"), _act(act), r, ldr, z,
+          ldz, ws, ws_bytes, _stream(C, stream))
 
 
 def gemm_act_bwd(A: torch.Tensor, B: torch.Tensor, dC: torch.Tensor, *, dA: torch.Tensor = None,
@@ -114,20 +156,19 @@ def gemm_act_bwd(A: torch.Tensor, B: torch.Tensor, dC: torch.Tensor, *, dA: torc
     """Gradients of gemm_act: dA (A's shape and dtype), dB (B's) and dbias
     (float32), each written if given; `preact` as gemm_act stored it (not needed
     with act "none").  The workspace is at least gemm_act_bwd_workspace's."""
-    M, N, K = _shapes(A, B, dC)
+    M, N, K = _sizes(A, B, dC)
     code, out = _formats(A, B, dC.dtype, in_fmt)
     a = _act(act)
     if a and preact is None:
         raise ValueError("the gradient of an activation needs preact")
-    z, ldz = _matrix(preact if a else None, (M, N), dC.dtype, dC.device, "preact")
-    da, ldda = _matrix(dA, (M, K), A.dtype, dC.device, "dA")
-    db, lddb = _matrix(dB, (K, N), A.dtype, dC.device, "dB")
-    ws, ws_bytes = _workspace(workspace, dC.device)
-    with _on_device(dC):
-        _check(_lib.gemm_act_bwd(code, out, M, N, K, A.data_ptr(), _pitch(A, K), B.data_ptr(),
-                                 _pitch(B, N), dC.data_ptr(), _pitch(dC, N), z, ldz, a, da, ldda,
-                                 db, lddb, _vector(dbias, N, dC.device, "dbias"), ws, ws_bytes,
-                                 _stream(dC, stream)))
+    dev = dC.get_device()
+    z, ldz = _matrix(preact if a else None, M, N, dC.dtype, dev, "preact")
+    da, ldda = _matrix(dA, M, K, A.dtype, dev, "dA")
+    db, lddb = _matrix(dB, K, N, A.dtype, dev, "dB")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call(_lib.gemm_act_bwd, dC, code, out, M, N, K, A.data_ptr(), _ld(A, M, K), B.data_ptr(),
+          _ld(B, K, N), dC.data_ptr(), _ld(dC, M, N), z, ldz, a, da, ldda, db, lddb,
+          _vector(dbias, N, dev, "dbias"), ws, ws_bytes, _stream(dC, stream))
 
 
 def gemm_f8(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, scale_a: torch.Tensor,
@@ -141,23 +182,21 @@ def gemm_f8(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, scale_a: torch.Te
     N = B.shape[0]
     if B.shape[1] != K or tuple(C.shape) != (M, N):
         raise ValueError(f"shapes {tuple(A.shape)} x {tuple(B.shape)}^T -> {tuple(C.shape)}")
-    if not (A.device == B.device == C.device):
+    dev = C.get_device()
+    if not (A.get_device() == B.get_device() == dev):
         raise ValueError(f"operands on different devices: {A.device}, {B.device}, {C.device}")
-    if A.dtype != F8 or B.dtype != F8:
+    if A.dtype is not F8 or B.dtype is not F8:
         raise TypeError(f"A and B must be {F8}")
     if C.dtype not in _TORCH_IN:
         raise TypeError("C must be float32, bfloat16 or float16")
     if scale_a is None or scale_b is None:
         raise ValueError("scale_a and scale_b are required")
-    r, ldr = _matrix(residual, (M, N), C.dtype, C.device, "residual")
-    ws, ws_bytes = _workspace(workspace, C.device)
-    with _on_device(C):
-        _check(_lib.gemm_f8(IN_CODES[_TORCH_IN[C.dtype]], M, N, K, A.data_ptr(), _pitch(A, K),
-                            B.data_ptr(), _pitch(B, K), C.data_ptr(), _pitch(C, N),
-                            _vector(scale_a, M, C.device, "scale_a"),
-                            _vector(scale_b, N, C.device, "scale_b"),
-                            _vector(bias, N, C.device, "bias"), _act(act), r, ldr, ws, ws_bytes,
-                            _stream(C, stream)))
+    r, ldr = _matrix(residual, M, N, C.dtype, dev, "residual")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call(_lib.gemm_f8, C, IN_CODES[_TORCH_IN[C.dtype]], M, N, K, A.data_ptr(), _ld(A, M, K),
+          B.data_ptr(), _ld(B, N, K), C.data_ptr(), _ld(C, M, N), _vector(scale_a, M, dev, "scale_a"),
+          _vector(scale_b, N, dev, "scale_b"), _vector(bias, N, dev, "bias"), _act(act), r, ldr, ws,
+          ws_bytes, _stream(C, stream))
 
 
 def _plan(fn, *args) -> dict:
@@ -202,19 +241,18 @@ def rmsnorm(X: torch.Tensor, weight: torch.Tensor, Y: torch.Tensor, *, residual:
     M, N = X.shape
     if X.dtype not in _TORCH_IN:
         raise TypeError("X must be float32, bfloat16 or float16")
-    f8 = Y.dtype == F8
+    f8 = Y.dtype is F8
     if f8 != (scale is not None):
         raise ValueError("a float8_e4m3fn Y takes a scale, and only that")
     if weight is None:
         raise ValueError("weight is required")
-    y, ldy = _matrix(Y, (M, N), F8 if f8 else X.dtype, X.device, "Y")
-    r, ldr = _matrix(residual, (M, N), X.dtype, X.device, "residual")
-    s, lds = _matrix(total, (M, N), X.dtype, X.device, "total")
-    with _on_device(X):
-        _check(_lib.rmsnorm(IN_CODES[_TORCH_IN[X.dtype]], int(f8), M, N, X.data_ptr(), _pitch(X, N), r,
-                            ldr, s, lds, _vector(weight, N, X.device, "weight"), float(eps), y, ldy,
-                            _vector(scale, M, X.device, "scale"), _vector(rstd, M, X.device, "rstd"),
-                            _stream(X, stream)))
+    dev, dtype = X.get_device(), X.dtype
+    y, ldy = _matrix(Y, M, N, F8 if f8 else dtype, dev, "Y")
+    r, ldr = _matrix(residual, M, N, dtype, dev, "residual")
+    s, lds = _matrix(total, M, N, dtype, dev, "total")
+    _call(_lib.rmsnorm, X, IN_CODES[_TORCH_IN[dtype]], int(f8), M, N, X.data_ptr(), _ld(X, M, N), r, ldr,
+          s, lds, _vector(weight, N, dev, "weight"), eps, y, ldy, _vector(scale, M, dev, "scale"),
+          _vector(rstd, M, dev, "rstd"), _stream(X, stream))
 
 
 def rmsnorm_bwd(dY: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -230,16 +268,14 @@ def rmsnorm_bwd(dY: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, rst
         raise TypeError("dY must be float32, bfloat16 or float16")
     if weight is None or rstd is None:
         raise ValueError("weight and rstd are required")
-    s, lds = _matrix(total, (M, N), dY.dtype, dY.device, "total")
-    d, ldd = _matrix(dtotal, (M, N), dY.dtype, dY.device, "dtotal")
-    x, ldx = _matrix(dX, (M, N), dY.dtype, dY.device, "dX")
-    ws, ws_bytes = _workspace(workspace, dY.device)
-    with _on_device(dY):
-        _check(_lib.rmsnorm_bwd(IN_CODES[_TORCH_IN[dY.dtype]], M, N, dY.data_ptr(), _pitch(dY, N), s,
-                                lds, _vector(weight, N, dY.device, "weight"),
-                                _vector(rstd, M, dY.device, "rstd"), d, ldd, x, ldx,
-                                _vector(dweight, N, dY.device, "dweight"), ws, ws_bytes,
-                                _stream(dY, stream)))
+    dev, dtype = dY.get_device(), dY.dtype
+    s, lds = _matrix(total, M, N, dtype, dev, "total")
+    d, ldd = _matrix(dtotal, M, N, dtype, dev, "dtotal")
+    x, ldx = _matrix(dX, M, N, dtype, dev, "dX")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call(_lib.rmsnorm_bwd, dY, IN_CODES[_TORCH_IN[dtype]], M, N, dY.data_ptr(), _ld(dY, M, N), s, lds,
+          _vector(weight, N, dev, "weight"), _vector(rstd, M, dev, "rstd"), d, ldd, x, ldx,
+          _vector(dweight, N, dev, "dweight"), ws, ws_bytes, _stream(dY, stream))
 
 
 def rmsnorm_bwd_workspace(M: int, N: int) -> int:
@@ -260,12 +296,11 @@ def quant_f8(X: torch.Tensor, Q: torch.Tensor, scale: torch.Tensor, *, transpose
         raise TypeError("X must be float32, bfloat16 or float16")
     if scale is None:
         raise ValueError("scale is required")
-    q, ldq = _matrix(Q, (N, M) if transpose else (M, N), F8, X.device, "Q")
-    with _on_device(X):
-        _check(_lib.quant_f8(IN_CODES[_TORCH_IN[X.dtype]], int(transpose), M, N, X.data_ptr(),
-                             _pitch(X, N), q, ldq,
-                             _vector(scale, N if transpose else M, X.device, "scale"),
-                             _stream(X, stream)))
+    dev = X.get_device()
+    qrows, qcols = (N, M) if transpose else (M, N)
+    q, ldq = _matrix(Q, qrows, qcols, F8, dev, "Q")
+    _call(_lib.quant_f8, X, IN_CODES[_TORCH_IN[X.dtype]], int(transpose), M, N, X.data_ptr(),
+          _ld(X, M, N), q, ldq, _vector(scale, qrows, dev, "scale"), _stream(X, stream))
 
 
 # ------------------------------------------------------------ allocating forms
@@ -315,7 +350,7 @@ def linear_backward(A, B, dC, *, preact=None, act: str = "none", bias: bool = Fa
                     in_fmt: str = None):
     """(dA, dB, dbias) of linear; dbias is None unless `bias`.  The residual's
     gradient is dC itself."""
-    M, N, K = _shapes(A, B, dC)
+    M, N, K = _sizes(A, B, dC)
     code, out = _formats(A, B, dC.dtype, in_fmt)
     dA, dB = _empty(M, K, A.dtype, A.device), _empty(K, N, A.dtype, A.device)
     dbias = torch.empty(N, dtype=torch.float32, device=A.device) if bias else None

@@ -35,7 +35,7 @@ __device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[
             const float x = z[i];
             const float phi = 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * LOG2E * x * x);
             const float far = x > 0.0f ? 1.0f : 0.0f;
-            const float f = 0.5f * (1.0f + erff(x * 0.7071067811865476f)) + x * phi;
+            const float f = normal_cdf(x) + x * phi;
             d[i] *= __builtin_fabsf(x) > 1e4f ? far : f;
         }
     } else if (act == ACT_RELU) {

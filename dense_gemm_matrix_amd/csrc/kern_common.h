@@ -299,6 +299,21 @@ __device__ __forceinline__ float gate(float z, float a, float b) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * (z * (a + b * z * z))));
 }
 
+// Phi(z), the normal distribution's integral, from Abramowitz and Stegun's
+// 7.1.26: for x >= 0, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) within 1.5e-7,
+// t = 1 / (1 + 0.3275911 x).  One branch-free form for a whole tile's epilogue
+// (the library's erff branches on |x|, per value); z Phi(z) is within about one
+// half step of |z|, whichever sign.  A NaN stays a NaN.
+__device__ __forceinline__ float normal_cdf(float z) {
+    const float x = __builtin_fabsf(z) * 0.7071067811865476f;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+    const float p =
+        t * (0.254829592f +
+             t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float q = 0.5f * p * __builtin_amdgcn_exp2f(-LOG2E * x * x);
+    return z < 0.0f ? q : 1.0f - q;
+}
+
 __device__ __forceinline__ float gate_a(int act) { return act == ACT_SILU ? 1.0f : 2.0f * SQRT_2_PI; }
 __device__ __forceinline__ float gate_b(int act) {
     return act == ACT_SILU ? 0.0f : 2.0f * SQRT_2_PI * GELU_C;
@@ -313,7 +328,7 @@ __device__ __forceinline__ void apply_act(float (&v)[NE], int act) {
         for (int i = 0; i < NE; ++i) v[i] *= gate(v[i], a, b);
     } else if (act == ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.7071067811865476f));
+        for (int i = 0; i < NE; ++i) v[i] *= normal_cdf(v[i]);
     } else if (act == ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
@@ -334,9 +349,18 @@ struct Row8 {
     u32x4 w[FMT == OUT_F32 ? 2 : 1];
 
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t off, int nvalid) {
+        load_whole(r, off);
+        if (nvalid < 8) mask(nvalid);
+    }
+    // All eight, or none (`off` outside the resource).
+    __device__ __forceinline__ void load_whole(__amdgpu_buffer_rsrc_t r, uint32_t off) {
         w[0] = load16(r, (int)off);
         if constexpr (FMT == OUT_F32) w[1] = load16(r, (int)(off + 16));
-        if (nvalid < 8) mask(nvalid);
+    }
+    __device__ __forceinline__ void store_whole(__amdgpu_buffer_rsrc_t r, uint32_t off) const {
+        __builtin_amdgcn_raw_buffer_store_b128(w[0], r, (int)off, 0, 0);
+        if constexpr (FMT == OUT_F32)
+            __builtin_amdgcn_raw_buffer_store_b128(w[1], r, (int)(off + 16), 0, 0);
     }
     // The same from a plain 16-byte aligned address (lanes on different rows).
     __device__ __forceinline__ void load_from(const char* p, int nvalid) {
@@ -357,9 +381,7 @@ struct Row8 {
     __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t r, uint32_t off, int nvalid) const {
         constexpr int ES = fmt_es<FMT>;
         if (nvalid >= 8) {
-            __builtin_amdgcn_raw_buffer_store_b128(w[0], r, (int)off, 0, 0);
-            if constexpr (FMT == OUT_F32)
-                __builtin_amdgcn_raw_buffer_store_b128(w[1], r, (int)(off + 16), 0, 0);
+            store_whole(r, off);
         } else {
 #pragma unroll
             for (int j = 0; j < 7; ++j) {
@@ -409,11 +431,12 @@ constexpr int full_lds = 32 * full_pitch<NJ> * 4;
 // time; instead each 32-row strip goes through the wave's own LDS region (free
 // after the K loop; the caller has a barrier before) and comes back eight
 // consecutive columns per lane, so R, Z and C move in 16-byte pieces of whole
-// row segments.  R of the next strip is loaded while this one is worked on.
-// The strip loop stays a loop (only the accumulators' copy to LDS is written
-// out per strip), which keeps the activation code in the instruction cache.
-// bias and scales are read straight from memory: a lane's columns are the same
-// in every strip.
+// row segments.  With one wave per SIMD nothing else hides a wait, so a strip is
+// straight code: all its LDS reads, then the arithmetic with one branch per
+// strip (none per value), then the stores; R of the next strip is loaded as
+// soon as this one's is used.  The strips themselves are a loop (only the
+// accumulators' copy to LDS is written out per strip), which keeps the code in
+// the instruction cache.
 template <int OUT, int MI, int NJ>
 __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], char* C, int M, int N,
                                                 int ldc, int row0, int col0, int lane,
@@ -427,6 +450,8 @@ __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], cha
     const int g = lane >> 5, li = lane & 31;
     const int c8 = (lane % LPR) * 8, r_in = lane / LPR;
     const int nvalid = N - (col0 + c8);
+    // Wave-uniform: whether the last column falls inside some lane's eight.
+    const bool ragged = (N & 7) != 0 && N - col0 < NJ * 32;
     float* const buf = (float*)lds;
     const __amdgpu_buffer_rsrc_t rc = c_rsrc(C, M, N, ldc, row0, col0, ES);
     // NULL operands get empty ranges: their loads give zeros, their stores drop.
@@ -434,11 +459,14 @@ __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], cha
         e.res ? c_rsrc((char*)e.res, M, N, e.ldr, row0, col0, ES) : make_rsrc(C, 0);
     const __amdgpu_buffer_rsrc_t rz =
         e.pre ? c_rsrc(e.pre, M, N, e.ldz, row0, col0, ES) : make_rsrc(C, 0);
+    // Columns and rows past the edges read the last one's values: in bounds, and
+    // what they feed is not stored.
     float bias[8], sb[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        bias[j] = (e.bias && j < nvalid) ? e.bias[col0 + c8 + j] : 0.0f;
-        sb[j] = (e.scale_b && j < nvalid) ? e.scale_b[col0 + c8 + j] : 1.0f;
+        const int col = col0 + c8 + j < N ? col0 + c8 + j : N - 1;
+        bias[j] = e.bias ? e.bias[col] : 0.0f;
+        sb[j] = e.scale_b ? e.scale_b[col] : 1.0f;
     }
     // Byte offset of this lane's eight columns in row `r` of the wave's rows.
     auto at = [&](int r, int ld) {
@@ -447,7 +475,7 @@ __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], cha
     Row8<OUT> res[IT];
     if (e.res) {
 #pragma unroll
-        for (int it = 0; it < IT; ++it) res[it].load(rr, at(it * RPI + r_in, e.ldr), nvalid);
+        for (int it = 0; it < IT; ++it) res[it].load_whole(rr, at(it * RPI + r_in, e.ldr));
     }
 #pragma unroll 1
     for (int mi = 0; mi < MI; ++mi) {
@@ -465,41 +493,65 @@ __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], cha
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
+        float v[IT * 8];
 #pragma unroll
         for (int it = 0; it < IT; ++it) {
-            const int r = it * RPI + r_in;  // row within the strip
-            const int row = mi * 32 + r;    // row within the wave's rows
-            float v[8];
-            const f32x4 lo = *(const f32x4*)(buf + r * P + c8);
-            const f32x4 hi = *(const f32x4*)(buf + r * P + c8 + 4);
+            const float* p = buf + (it * RPI + r_in) * P + c8;
+            const f32x4 lo = *(const f32x4*)p, hi = *(const f32x4*)(p + 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                v[j] = lo[j];
-                v[4 + j] = hi[j];
+                v[it * 8 + j] = lo[j];
+                v[it * 8 + 4 + j] = hi[j];
             }
-            if (e.scale_a) {
-                const float sa = row0 + row < M ? e.scale_a[row0 + row] : 0.0f;
+        }
+        if (e.scale_a) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = v[j] * sa * sb[j];
+            for (int it = 0; it < IT; ++it) {
+                const int row = row0 + mi * 32 + it * RPI + r_in;
+                const float sa = e.scale_a[row < M ? row : M - 1];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[it * 8 + j] = v[it * 8 + j] * sa * sb[j];
             }
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] += bias[j];
+        for (int i = 0; i < IT * 8; ++i) v[i] += bias[i & 7];
+        // Rows it of the strip, from v, to an output.
+        auto put = [&](__amdgpu_buffer_rsrc_t r, int ld) {
             Row8<OUT> o;
-            if (e.pre) {
-                o.set(v);
-                o.store(rz, at(row, e.ldz), nvalid);
+            if (!ragged) {
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = v[it * 8 + j];
+                    o.set(x);
+                    o.store_whole(r, at(mi * 32 + it * RPI + r_in, ld));
+                }
+            } else {
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    float x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = v[it * 8 + j];
+                    o.set(x);
+                    o.store(r, at(mi * 32 + it * RPI + r_in, ld), nvalid);
+                }
             }
-            apply_act(v, e.act);
-            if (e.res) {
+        };
+        if (e.pre) put(rz, e.ldz);
+        apply_act(v, e.act);
+        if (e.res) {
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
                 float x[8];
                 res[it].get(x);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] += x[j];
-                if (mi + 1 < MI) res[it].load(rr, at(row + 32, e.ldr), nvalid);
+                for (int j = 0; j < 8; ++j) v[it * 8 + j] += x[j];
+                // past the tile's last strip: rows of other tiles, or outside R
+                res[it].load_whole(rr, at((mi + 1) * 32 + it * RPI + r_in, e.ldr));
             }
-            o.set(v);
-            o.store(rc, at(row, ldc), nvalid);
         }
+        put(rc, ldc);
     }
 }
 
