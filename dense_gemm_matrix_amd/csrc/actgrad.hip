@@ -117,8 +117,18 @@ __global__ __launch_bounds__(1024) void col_reduce_kernel(const float* part, int
     const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
     const int col = (int)blockIdx.x * 64 + lane;
     float v = 0.0f;
-    if (col < N)
-        for (int g = q; g < G; g += 16) v += part[(int64_t)g * ldp + col];
+    if (col < N) {
+        const float* p = part + col;
+        int g = q;
+        for (; g + 16 * 15 < G; g += 16 * 16) {  // sixteen loads in flight
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = p[(int64_t)(g + 16 * i) * ldp];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v += x[i];
+        }
+        for (; g < G; g += 16) v += p[(int64_t)g * ldp];
+    }
     s[q][lane] = v;
     __syncthreads();
     if (q == 0 && col < N) {

@@ -64,6 +64,13 @@ struct TileT {
     static constexpr int NREAD = RPF * (MI + NJ);        // LDS reads per k group
     static constexpr int NMFMA = MI * NJ;
     static constexpr int LDS = S * (A_STAGE + B_STAGE);
+    // The step's schedule (mainloop_t), in slots of one matrix instruction.
+#ifndef VBAR
+#define VBAR 16
+#define VLEND 32
+#endif
+    static constexpr int BAR = IN == IN_F8 && TBM == 256 ? VBAR : KP * NMFMA / 2;
+    static constexpr int LEND = IN == IN_F8 && TBM == 256 ? VLEND : KP * NMFMA;
     static_assert(!F8 || KC, "8-bit operands are K-contiguous");
     static_assert(LDS <= 160 * 1024 && (S - 1) * LOADS <= 63, "LDS budget, vmcnt range");
 };
@@ -247,10 +254,10 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
     };
     using FirstIn = std::integral_constant<int, (S - 1) * T::LOADS>;
     using NextIn = std::integral_constant<int, (S - 2) * T::LOADS>;
-    constexpr int HP = T::KP / 2;                    // k groups before the barrier
-    constexpr int SLOTS1 = HP * T::NMFMA;            // matrix instructions before it
-    constexpr int SLOTS2 = (T::KP - HP) * T::NMFMA;  // and after it
-    constexpr int NR = T::NREAD * (T::KP - 1);
+    constexpr int NR = T::NREAD * (T::KP - 1);       // reads of a step's k groups 1 ..
+    constexpr int TOT = T::KP * T::NMFMA;            // matrix instructions per step
+    constexpr int BAR = T::BAR, LEND = T::LEND, RBEG = T::NMFMA > BAR ? T::NMFMA : BAR;
+    static_assert(BAR <= TOT - T::NMFMA && LEND > BAR && LEND <= TOT, "schedule");
 
     if (nk > 0) {
 #pragma unroll
@@ -266,34 +273,41 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
             read_piece(0, 0, o);
             __builtin_amdgcn_sched_barrier(0);
         }
-        // Step kt: the first half of its matrix instructions carries the reads of
-        // its other k groups; the wait for step kt + 1 and the barrier, which
-        // retires every wave's reads of the stage; the second half carries the
-        // stage's refill (step kt + S) and the reads of step kt + 1's group 0.
+        // Step kt, in slots of one matrix instruction: slots 0 .. BAR - 1 carry the
+        // reads of its k groups 1 .., each group's before its first use; then the
+        // wait for step kt + 1 and the barrier, which retires every wave's reads of
+        // the stage; slots BAR .. LEND - 1 carry the stage's refill (step kt + S),
+        // and from slot RBEG on, group 0's registers being free, the reads of step
+        // kt + 1's group 0.
         for (int kt = 0; kt < nk; ++kt) {
+            Desc d;
 #pragma unroll
-            for (int i = 0; i < SLOTS1; ++i) {
+            for (int i = 0; i < TOT; ++i) {
+                if (i == BAR) {
+                    d = desc(kt + S);
+                    sync(NextIn{});
+                    if (ragged && kt + 2 == nk) { fix_tail(); sync(NextIn{}); }
+                }
                 mfma_one(i / T::NMFMA, i % T::NMFMA);
                 __builtin_amdgcn_sched_barrier(0);
+                if (i < BAR) {
 #pragma unroll
-                for (int r = (i * NR) / SLOTS1; r < ((i + 1) * NR) / SLOTS1; ++r)
-                    read_piece(kt, 1 + r / T::NREAD, r % T::NREAD);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            const Desc d = desc(kt + S);
-            sync(NextIn{});
-            if (ragged && kt + 2 == nk) { fix_tail(); sync(NextIn{}); }
+                    for (int r = (i * NR) / BAR; r < ((i + 1) * NR) / BAR; ++r)
+                        read_piece(kt, 1 + r / T::NREAD, r % T::NREAD);
+                }
+                if (i >= BAR && i < LEND) {
 #pragma unroll
-            for (int i = 0; i < SLOTS2; ++i) {
-                mfma_one(HP + i / T::NMFMA, i % T::NMFMA);
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int j = ((i - BAR) * T::LOADS) / (LEND - BAR);
+                         j < ((i - BAR + 1) * T::LOADS) / (LEND - BAR); ++j)
+                        dma_one(d, j);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (i >= RBEG) {
 #pragma unroll
-                for (int j = (i * T::LOADS) / SLOTS2; j < ((i + 1) * T::LOADS) / SLOTS2; ++j)
-                    dma_one(d, j);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int r = (i * T::NREAD) / SLOTS2; r < ((i + 1) * T::NREAD) / SLOTS2; ++r)
-                    read_piece(kt + 1, 0, r);
+                    for (int r = ((i - RBEG) * T::NREAD) / (TOT - RBEG);
+                         r < ((i - RBEG + 1) * T::NREAD) / (TOT - RBEG); ++r)
+                        read_piece(kt + 1, 0, r);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }

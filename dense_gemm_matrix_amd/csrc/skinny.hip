@@ -42,38 +42,115 @@ __device__ __forceinline__ u32x4 mask_bytes(u32x4 v, int valid) {
     return out;
 }
 
-// NACC accumulators of 16 x 16 per wave: value (j, r) of lane (g, c) is row
-// 4 g + r, column n0 + CPL c + j.  Sums them over the W waves in LDS and
-// finishes the strip: the full epilogue, or an fp32 partial.
+// The elements of a strip that a lane finishes, and what the epilogue reads for
+// them, loaded before the K loop (at its end they would wait for memory once
+// more).  CPL accumulators of 16 x 16 per wave: value idx = 4 j + r of lane (g, c)
+// is row 4 g + r, column n0 + CPL c + j; wave w finishes idx in [w PER, ..).
 template <int OUT, int EPI, int CPL, int W>
-__device__ __forceinline__ void finish_strip(const f32x4 (&acc)[CPL], float* red, char* C, int M,
-                                             int N, int ldc, int n0, int wave, int lane,
-                                             const EpiArgs& e) {
-    constexpr int NV = CPL * 4;                 // values per lane
-    constexpr int PER = (NV + W - 1) / W;       // values a wave finishes
-#pragma unroll
-    for (int j = 0; j < CPL; ++j)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[(wave * NV + j * 4 + r) * 64 + lane] = acc[j][r];
-    __syncthreads();
-    float v[PER];
+struct Strip {
+    static constexpr int NV = CPL * 4;            // values per lane
+    static constexpr int PER = (NV + W - 1) / W;  // of them, finished by one wave
     int row[PER], col[PER];
+    float res[PER], bias[PER], scale[PER];
+
+    __device__ __forceinline__ void prefetch(int M, int N, int n0, int wave, int lane,
+                                             const EpiArgs& e) {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-        const int idx = wave * PER + q;
-        if (PER * W > NV && idx >= NV) { row[q] = M; col[q] = N; v[q] = 0.0f; continue; }
-        row[q] = 4 * (lane >> 4) + idx % 4;
-        col[q] = n0 + CPL * (lane & 15) + idx / 4;
-        v[q] = red[idx * 64 + lane];
-#pragma unroll
-        for (int w = 1; w < W; ++w) v[q] += red[(w * NV + idx) * 64 + lane];
+        for (int q = 0; q < PER; ++q) {
+            const int idx = wave * PER + q;
+            row[q] = 4 * (lane >> 4) + idx % 4;
+            col[q] = n0 + CPL * (lane & 15) + idx / 4;
+            if (idx >= NV) row[q] = M;  // W larger than the values: none
+            if constexpr (EPI == EPI_FULL) {
+                const bool in = row[q] < M && col[q] < N;
+                res[q] = in && e.res ? load_c<OUT>(e.res, (int64_t)row[q] * e.ldr + col[q]) : 0.0f;
+                bias[q] = in && e.bias ? e.bias[col[q]] : 0.0f;
+                scale[q] = in && e.scale_a ? e.scale_a[row[q]] * e.scale_b[col[q]] : 1.0f;
+            }
+        }
     }
-    if constexpr (EPI == EPI_FULL) {
-        finish_full<OUT, PER>(v, row, col, C, M, N, ldc, e);
-    } else {
+    // Adds the W waves' sums in wave order and stores: the full epilogue, or an
+    // fp32 partial.
+    __device__ __forceinline__ void finish(const f32x4 (&acc)[CPL], float* red, char* C, int M, int N,
+                                           int ldc, int wave, int lane, const EpiArgs& e) {
 #pragma unroll
-        for (int q = 0; q < PER; ++q)
+        for (int j = 0; j < CPL; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[(wave * NV + j * 4 + r) * 64 + lane] = acc[j][r];
+        __syncthreads();
+        if (wave * PER >= NV) return;
+        float v[PER];
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int idx = wave * PER + q;
+            v[q] = red[idx * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) v[q] += red[(w * NV + idx) * 64 + lane];
+            if constexpr (EPI == EPI_FULL) {
+                v[q] = v[q] * scale[q] + bias[q];
+                if (e.pre && row[q] < M && col[q] < N)
+                    store_c<OUT>(e.pre, (int64_t)row[q] * e.ldz + col[q], v[q]);
+            }
+        }
+        if constexpr (EPI == EPI_FULL) apply_act(v, e.act);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            if constexpr (EPI == EPI_FULL) v[q] = e.res ? v[q] + res[q] : v[q];
             if (row[q] < M && col[q] < N) store_c<OUT>(C, (int64_t)row[q] * ldc + col[q], v[q]);
+        }
+    }
+};
+
+// A wave's n steps in chunks of D: the next chunk's loads are issued before the
+// current one is used, so D to 2 D steps are in flight, and the last chunk loads
+// only the steps there are (a load past the end costs as much issue as a real
+// one).  load(i, slot) and use(i, slot): step i in register slot `slot`, which is
+// a constant once unrolled.
+template <int D, class Load, class Use>
+__device__ __forceinline__ void run_steps(int n, Load load, Use use) {
+    const int full = n > 0 ? n / D : 0, rem = n > 0 ? n - full * D : 0;
+    auto rest = [&](int base) {  // the last chunk's loads, into slots base ..
+#pragma unroll
+        for (int s = 0; s < D - 1; ++s)
+            if (s < rem) load(full * D + s, base + s);
+    };
+    auto use_rest = [&](int base) {
+#pragma unroll
+        for (int s = 0; s < D - 1; ++s)
+            if (s < rem) use(full * D + s, base + s);
+    };
+    if (full == 0) {
+        rest(0);
+        use_rest(0);
+        return;
+    }
+#pragma unroll
+    for (int s = 0; s < D; ++s) load(s, s);
+    int c = 0;
+    for (; c + 2 < full; c += 2) {
+#pragma unroll
+        for (int s = 0; s < D; ++s) load((c + 1) * D + s, D + s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use(c * D + s, s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) load((c + 2) * D + s, s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use((c + 1) * D + s, D + s);
+    }
+    if (c + 1 < full) {
+#pragma unroll
+        for (int s = 0; s < D; ++s) load((c + 1) * D + s, D + s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use(c * D + s, s);
+        rest(0);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use((c + 1) * D + s, D + s);
+        use_rest(0);
+    } else {
+        rest(D);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use(c * D + s, s);
+        use_rest(D);
     }
 }
 
@@ -91,7 +168,7 @@ __global__ __launch_bounds__(64 * W) void skinny16_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* C, int M, int N, int K, int lda,
     int ldb, int ldc, int strips, int kchunk, int64_t c_zstride, EpiArgs epi) {
     constexpr int WD = CPL / 2;   // words per lane and k-row
-    constexpr int D = CPL == 8 ? 2 : 4;  // steps in the load ring (registers: 32 per step at CPL 8)
+    constexpr int D = CPL == 8 ? 2 : 4;  // steps per chunk; two chunks in registers
     __shared__ float red[W * CPL * 4 * 64];
     {
         const int kbeg = (int)blockIdx.y * kchunk;
@@ -106,10 +183,11 @@ __global__ __launch_bounds__(64 * W) void skinny16_kernel(
     const int n0 = strip_of((int)blockIdx.x, strips) * 16 * CPL;
     const int cols = (N - n0) < 16 * CPL ? (N - n0) : 16 * CPL;
     const int nstep = (K + 31) / 32;
+    Strip<OUT, EPI, CPL, W> strip;
+    strip.prefetch(M, N, n0, wave, lane, epi);
 
-    uint32_t b[D][8][WD];
-    u32x4 a[D];
-    // Steps at or past the end get empty resources: their loads give zeros.
+    uint32_t b[2 * D][8][WD];
+    u32x4 a[2 * D];
     auto load = [&](int t, int S) {  // S: a constant once unrolled
         const int k0 = t * 32;
         const int rows = (K - k0) < 32 ? (K - k0) : 32;
@@ -161,17 +239,9 @@ __global__ __launch_bounds__(64 * W) void skinny16_kernel(
             }
     };
     // Wave w takes steps w, w + W, ...: the workgroup reads B's rows in order.
-#pragma unroll
-    for (int s = 0; s < D - 1; ++s) load(wave + s * W, s);
-    for (int t = wave; t < nstep; t += D * W) {
-#pragma unroll
-        for (int s = 0; s < D; ++s) {
-            if (t + s * W >= nstep) break;
-            load(t + (s + D - 1) * W, (s + D - 1) % D);
-            use(t + s * W, s);
-        }
-    }
-    finish_strip<OUT, EPI, CPL, W>(acc, red, C, M, N, ldc, n0, wave, lane, epi);
+    run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
+                 [&](int i, int slot) { use(wave + i * W, slot); });
+    strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
 }
 
 template <int OUT, int W>
@@ -185,8 +255,10 @@ __global__ __launch_bounds__(64 * W) void skinny8_kernel(
     const int n0 = strip_of((int)blockIdx.x, strips) * 16;
     const int rows_b = (N - n0) < 16 ? (N - n0) : 16;
     const int nstep = (K + 127) / 128;
-    constexpr int D = 4;
-    u32x4 a[D][2], b[D][2];
+    Strip<OUT, EPI_FULL, 1, W> strip;
+    strip.prefetch(M, N, n0, wave, lane, epi);
+    constexpr int D = 2;  // steps per chunk; two chunks in registers
+    u32x4 a[2 * D][2], b[2 * D][2];
     auto load = [&](int t, int S) {  // S: a constant once unrolled
         const int k0 = t * 128;
         const int krem = (K - k0) < 128 ? (K - k0) : 128;
@@ -221,17 +293,9 @@ __global__ __launch_bounds__(64 * W) void skinny8_kernel(
                                                                  widen_f8(y[h][q], y[h][q + 1]), acc[0],
                                                                  0, 0, 0);
     };
-#pragma unroll
-    for (int s = 0; s < D - 1; ++s) load(wave + s * W, s);
-    for (int t = wave; t < nstep; t += D * W) {
-#pragma unroll
-        for (int s = 0; s < D; ++s) {
-            if (t + s * W >= nstep) break;
-            load(t + (s + D - 1) * W, (s + D - 1) % D);
-            use(t + s * W, s);
-        }
-    }
-    finish_strip<OUT, EPI_FULL, 1, W>(acc, red, C, M, N, ldc, n0, wave, lane, epi);
+    run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
+                 [&](int i, int slot) { use(wave + i * W, slot); });
+    strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
 }
 
 template <int IN, int OUT, int EPI, int CPL, int W>
