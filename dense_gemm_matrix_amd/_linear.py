@@ -1,15 +1,18 @@
-"""ctypes binding of the linear layer's operators (include/dgemm.h): products
+"""Binding of the linear layer's operators (include/dgemm.h): products
 with bias, activation and residual and their gradients, 8-bit products, norms
 and quantizers.  As in _binding, the functions named like the C entry points
-only marshal tensors the caller has allocated; `linear`, `linear_backward`,
+(in _marshal, csrc/marshal.cpp) only marshal tensors the caller has allocated;
+the host queries go through ctypes; `linear`, `linear_backward`,
 `matmul_f8`, `rms_norm`, `rms_norm_backward` and `quantize_f8` allocate their
 results and workspaces the way `matmul` does."""
 import ctypes
 
 import torch
 
-from ._binding import (DGEMM_OUT_F32, DGEMM_OUT_SAME, IN_CODES, _TORCH_IN, _check, _lib, _on_device,
-                       _shapes, _stream)
+from ._binding import DGEMM_OUT_F32, DGEMM_OUT_SAME, IN_CODES, _TORCH_IN, _check, _lib, _shapes
+from ._marshal import (  # noqa: F401
+    gemm_act, gemm_act_bwd, gemm_f8, quant_f8, rmsnorm, rmsnorm_bwd,
+)
 
 _i, _p, _sz, _f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 _P, _PS = ctypes.POINTER(_i), ctypes.POINTER(_sz)
@@ -40,67 +43,6 @@ def _act(act: str) -> int:
     return ACT_CODES[act]
 
 
-# The checks below run on every call and are most of a small call's host time, so
-# each is one pass over attributes that torch answers without building objects
-# (device indices, dtypes and sizes compared as such), and the messages are made
-# only when one fails.
-_FP32 = torch.float32
-_PER16 = {torch.float32: 4, torch.bfloat16: 8, torch.float16: 8, F8: 16}
-_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") \
-    else torch.cuda.current_device
-
-
-def _vector(t, n: int, dev: int, name: str):
-    """Pointer of an optional fp32 vector of length n on device index dev."""
-    if t is None:
-        return None
-    if t.dtype is not _FP32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() \
-            or t.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous float32 device vector of length {n}")
-    return t.data_ptr()
-
-
-def _ld(t, rows: int, cols: int) -> int:
-    """_pitch, for a matrix of known size."""
-    pitch, inner = t.stride()
-    if inner != 1 and cols > 1 and rows > 0:
-        raise ValueError("operands must be row-major with unit inner stride")
-    if rows > 1:
-        return pitch
-    per16 = _PER16[t.dtype]
-    return (max(cols, 1) + per16 - 1) // per16 * per16
-
-
-def _matrix(t, rows: int, cols: int, dtype, dev: int, name: str):
-    """(pointer, pitch) of an optional matrix operand on device index dev."""
-    if t is None:
-        return None, 0
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}")
-    if t.shape != (rows, cols) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a {(rows, cols)} matrix on device {dev}")
-    return t.data_ptr(), _ld(t, rows, cols)
-
-
-def _workspace(ws, dev: int):
-    if ws is None:
-        return None, 0
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the output's device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _call(fn, t, *args) -> None:
-    """Calls a C entry point with t's device current."""
-    if t.get_device() == _current_device():
-        status = fn(*args)
-    else:
-        with _on_device(t):
-            status = fn(*args)
-    if status:
-        _check(status)
-
-
 def _formats(A, B, C_dtype, in_fmt):
     """(input code, output code) of a product of A and B with C_dtype results."""
     dtype = A.dtype
@@ -108,7 +50,7 @@ def _formats(A, B, C_dtype, in_fmt):
     fmt = in_fmt or own
     if own is None or B.dtype is not dtype or (fmt != own and not (fmt == "f32x3" and own == "f32")):
         raise TypeError("unsupported input dtypes")
-    if C_dtype is _FP32:
+    if C_dtype is torch.float32:
         return IN_CODES[fmt], DGEMM_OUT_F32
     if C_dtype is not dtype:
         raise TypeError("C must be float32 or the input dtype")
@@ -120,83 +62,6 @@ def _device_tensor(t, name):
         raise ValueError("operands must be 2-D")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-
-
-def _sizes(A, B, C):
-    """_shapes, for the calls of this module."""
-    sa, sb = A.shape, B.shape
-    if len(sa) != 2 or len(sb) != 2 or sa[1] != sb[0] or C.shape != (sa[0], sb[1]) \
-            or not (A.get_device() == B.get_device() == C.get_device() >= 0):
-        return _shapes(A, B, C)  # raises
-    return sa[0], sb[1], sa[1]
-
-
-def gemm_act(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, *, bias: torch.Tensor = None,
-             act: str = "none", residual: torch.Tensor = None, preact: torch.Tensor = None,
-             workspace: torch.Tensor = None, in_fmt: str = None, stream=None) -> None:
-    """C = act(A @ B + bias) + residual; preact (optional) = A @ B + bias.
-
-    `residual` and `preact` have C's shape and dtype; `residual` may be C itself.
-    `workspace` and `in_fmt` as in gemm_ex."""
-    M, N, K = _sizes(A, B, C)
-    code, out = _formats(A, B, C.dtype, in_fmt)
-    dev, dtype = C.get_device(), C.dtype
-    r, ldr = _matrix(residual, M, N, dtype, dev, "residual")
-    z, ldz = _matrix(preact, M, N, dtype, dev, "preact")
-    ws, ws_bytes = _workspace(workspace, dev)
-    _call(_lib.gemm_act, C, code, out, M, N, K, A.data_ptr(), _ld(A, M, K), B.data_ptr(),
-          _ld(B, K, N), C.data_ptr(), _ld(C, M, N), _vector(bias, N, dev, "bias"), _act(act), r, ldr, z,
-          ldz, ws, ws_bytes, _stream(C, stream))
-
-
-def gemm_act_bwd(A: torch.Tensor, B: torch.Tensor, dC: torch.Tensor, *, dA: torch.Tensor = None,
-                 dB: torch.Tensor = None, dbias: torch.Tensor = None, preact: torch.Tensor = None,
-                 act: str = "none", workspace: torch.Tensor = None, in_fmt: str = None,
-                 stream=None) -> None:
-    """Gradients of gemm_act: dA (A's shape and dtype), dB (B's) and dbias
-    (float32), each written if given; `preact` as gemm_act stored it (not needed
-    with act "none").  The workspace is at least gemm_act_bwd_workspace's."""
-    M, N, K = _sizes(A, B, dC)
-    code, out = _formats(A, B, dC.dtype, in_fmt)
-    a = _act(act)
-    if a and preact is None:
-        raise ValueError("the gradient of an activation needs preact")
-    dev = dC.get_device()
-    z, ldz = _matrix(preact if a else None, M, N, dC.dtype, dev, "preact")
-    da, ldda = _matrix(dA, M, K, A.dtype, dev, "dA")
-    db, lddb = _matrix(dB, K, N, A.dtype, dev, "dB")
-    ws, ws_bytes = _workspace(workspace, dev)
-    _call(_lib.gemm_act_bwd, dC, code, out, M, N, K, A.data_ptr(), _ld(A, M, K), B.data_ptr(),
-          _ld(B, K, N), dC.data_ptr(), _ld(dC, M, N), z, ldz, a, da, ldda, db, lddb,
-          _vector(dbias, N, dev, "dbias"), ws, ws_bytes, _stream(dC, stream))
-
-
-def gemm_f8(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, scale_a: torch.Tensor,
-            scale_b: torch.Tensor, *, bias: torch.Tensor = None, act: str = "none",
-            residual: torch.Tensor = None, workspace: torch.Tensor = None, stream=None) -> None:
-    """C = act(scale_a[:, None] * scale_b * (A @ B.T) + bias) + residual for
-    float8_e4m3fn A [M, K] and B [N, K]; C (and residual) fp32, bf16 or fp16."""
-    for name, t in (("A", A), ("B", B), ("C", C)):
-        _device_tensor(t, name)
-    M, K = A.shape
-    N = B.shape[0]
-    if B.shape[1] != K or tuple(C.shape) != (M, N):
-        raise ValueError(f"shapes {tuple(A.shape)} x {tuple(B.shape)}^T -> {tuple(C.shape)}")
-    dev = C.get_device()
-    if not (A.get_device() == B.get_device() == dev):
-        raise ValueError(f"operands on different devices: {A.device}, {B.device}, {C.device}")
-    if A.dtype is not F8 or B.dtype is not F8:
-        raise TypeError(f"A and B must be {F8}")
-    if C.dtype not in _TORCH_IN:
-        raise TypeError("C must be float32, bfloat16 or float16")
-    if scale_a is None or scale_b is None:
-        raise ValueError("scale_a and scale_b are required")
-    r, ldr = _matrix(residual, M, N, C.dtype, dev, "residual")
-    ws, ws_bytes = _workspace(workspace, dev)
-    _call(_lib.gemm_f8, C, IN_CODES[_TORCH_IN[C.dtype]], M, N, K, A.data_ptr(), _ld(A, M, K),
-          B.data_ptr(), _ld(B, N, K), C.data_ptr(), _ld(C, M, N), _vector(scale_a, M, dev, "scale_a"),
-          _vector(scale_b, N, dev, "scale_b"), _vector(bias, N, dev, "bias"), _act(act), r, ldr, ws,
-          ws_bytes, _stream(C, stream))
 
 
 def _plan(fn, *args) -> dict:
@@ -228,79 +93,11 @@ def gemm_act_bwd_workspace(in_fmt: str, M: int, N: int, K: int, act: str = "none
     return req.value, best.value
 
 
-def rmsnorm(X: torch.Tensor, weight: torch.Tensor, Y: torch.Tensor, *, residual: torch.Tensor = None,
-            total: torch.Tensor = None, scale: torch.Tensor = None, rstd: torch.Tensor = None,
-            eps: float = 1e-6, stream=None) -> None:
-    """Y = s * rstd * weight row by row, s = X + residual, rstd = (mean s^2 + eps)^-1/2.
-
-    Y has X's dtype, or is float8_e4m3fn with a float32 `scale` per row (gemm_f8's
-    A and scale_a).  `total` (X's dtype) receives s and `rstd` (float32, one per
-    row) its root where given: what rmsnorm_bwd reads.  `total` and Y may be X or
-    residual themselves."""
-    _device_tensor(X, "X")
-    M, N = X.shape
-    if X.dtype not in _TORCH_IN:
-        raise TypeError("X must be float32, bfloat16 or float16")
-    f8 = Y.dtype is F8
-    if f8 != (scale is not None):
-        raise ValueError("a float8_e4m3fn Y takes a scale, and only that")
-    if weight is None:
-        raise ValueError("weight is required")
-    dev, dtype = X.get_device(), X.dtype
-    y, ldy = _matrix(Y, M, N, F8 if f8 else dtype, dev, "Y")
-    r, ldr = _matrix(residual, M, N, dtype, dev, "residual")
-    s, lds = _matrix(total, M, N, dtype, dev, "total")
-    _call(_lib.rmsnorm, X, IN_CODES[_TORCH_IN[dtype]], int(f8), M, N, X.data_ptr(), _ld(X, M, N), r, ldr,
-          s, lds, _vector(weight, N, dev, "weight"), eps, y, ldy, _vector(scale, M, dev, "scale"),
-          _vector(rstd, M, dev, "rstd"), _stream(X, stream))
-
-
-def rmsnorm_bwd(dY: torch.Tensor, total: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
-                dX: torch.Tensor, *, dtotal: torch.Tensor = None, dweight: torch.Tensor = None,
-                workspace: torch.Tensor = None, stream=None) -> None:
-    """Gradients of rmsnorm: dX (the residual's too) and, where given, dweight
-    (float32; needs rmsnorm_bwd_workspace's bytes).  `total` and `rstd` as rmsnorm
-    stored them (total is X where there was no residual); `dtotal` is the
-    gradient that reaches total by other ways.  dX may be dY or dtotal itself."""
-    _device_tensor(dY, "dY")
-    M, N = dY.shape
-    if dY.dtype not in _TORCH_IN:
-        raise TypeError("dY must be float32, bfloat16 or float16")
-    if weight is None or rstd is None:
-        raise ValueError("weight and rstd are required")
-    dev, dtype = dY.get_device(), dY.dtype
-    s, lds = _matrix(total, M, N, dtype, dev, "total")
-    d, ldd = _matrix(dtotal, M, N, dtype, dev, "dtotal")
-    x, ldx = _matrix(dX, M, N, dtype, dev, "dX")
-    ws, ws_bytes = _workspace(workspace, dev)
-    _call(_lib.rmsnorm_bwd, dY, IN_CODES[_TORCH_IN[dtype]], M, N, dY.data_ptr(), _ld(dY, M, N), s, lds,
-          _vector(weight, N, dev, "weight"), _vector(rstd, M, dev, "rstd"), d, ldd, x, ldx,
-          _vector(dweight, N, dev, "dweight"), ws, ws_bytes, _stream(dY, stream))
-
-
 def rmsnorm_bwd_workspace(M: int, N: int) -> int:
     """Workspace bytes of rmsnorm_bwd with dweight."""
     need = _sz(0)
     _check(_lib.rmsnorm_bwd_workspace(M, N, ctypes.byref(need)))
     return need.value
-
-
-def quant_f8(X: torch.Tensor, Q: torch.Tensor, scale: torch.Tensor, *, transpose: bool = False,
-             stream=None) -> None:
-    """Q, scale = X's rows in 8 bits (float8_e4m3fn, one float32 scale per row);
-    with transpose its columns, Q being X.T's shape: gemm_f8's B from a [K, N]
-    weight."""
-    _device_tensor(X, "X")
-    M, N = X.shape
-    if X.dtype not in _TORCH_IN:
-        raise TypeError("X must be float32, bfloat16 or float16")
-    if scale is None:
-        raise ValueError("scale is required")
-    dev = X.get_device()
-    qrows, qcols = (N, M) if transpose else (M, N)
-    q, ldq = _matrix(Q, qrows, qcols, F8, dev, "Q")
-    _call(_lib.quant_f8, X, IN_CODES[_TORCH_IN[X.dtype]], int(transpose), M, N, X.data_ptr(),
-          _ld(X, M, N), q, ldq, _vector(scale, qrows, dev, "scale"), _stream(X, stream))
 
 
 # ------------------------------------------------------------ allocating forms
@@ -350,7 +147,7 @@ def linear_backward(A, B, dC, *, preact=None, act: str = "none", bias: bool = Fa
                     in_fmt: str = None):
     """(dA, dB, dbias) of linear; dbias is None unless `bias`.  The residual's
     gradient is dC itself."""
-    M, N, K = _sizes(A, B, dC)
+    M, N, K = _shapes(A, B, dC)
     code, out = _formats(A, B, dC.dtype, in_fmt)
     dA, dB = _empty(M, K, A.dtype, A.device), _empty(K, N, A.dtype, A.device)
     dbias = torch.empty(N, dtype=torch.float32, device=A.device) if bias else None

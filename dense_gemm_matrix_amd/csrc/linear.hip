@@ -122,27 +122,57 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     return best;
 }
 
-// At most SKINNY_M rows.  8-bit: strips of 16 columns.  16-bit: strips of 32
-// columns with 16 waves.
+// At most SKINNY_M rows.
+//
+// 8-bit: strips of 16 columns, 16 waves, never split (B's rows are K-contiguous,
+// so a strip of 16 outputs already reads whole lines).
+//
+// 16-bit: strips of 32 columns with 16 waves, or from 160 strips of 64 columns on
+// (enough to fill the CUs) 64 with 8 waves: 1 x 12288 x 4096 36 us with 32, 23 with
+// 64; 1 x 8192 x 4096 14.5 with 32, 15.7 with 64.  Deep K leaves a wave many steps
+// one after another, each a round of memory latency; given a workspace, K is then
+// split over workgroups, in wider strips (longer pieces of B's rows), for a second
+// launch of about 2.7 us in a graph and 3 us more on a stream: from K = 8192 on,
+// up to 8 pieces of at least 512 k (16 from K = 16384 on) and 256 workgroups.  One
+// row in a replayed graph, B in the last-level cache / from HBM, in us:
+//                      unsplit        split
+//   2048 x 8192      18.5 / 30.5   11.9 / 14.6  (128 columns, 8 pieces)
+//   1024 x 16384     30.3 / 54.3   14.0 / 17.4  (128, 16)
+//   4096 x 4096      12.0 / 18.1   11.4 / 13.2  (128, 8; on a stream 12.0 / 14.6
+//                                  from the cache, so kept unsplit)
+//   512 x 4104        6.3 /  9.6    7.8 /  8.8  (128, 8; kept unsplit)
+// More rows make the partial products bigger and the wide strips' sums longer: 16
+// rows of 4096 x 4096 take 14.9 / 16.1 in 128 columns and 8 pieces, 13.0 / 14.6 in
+// 64 columns and 4.
 Plan plan_skinny(int in, int M, int N, int K, uint64_t ws_avail) {
-    Plan p{SKINNY_M, 32, 1, K, 0, 0};
+    Plan p{SKINNY_M, 16, 1, K, 0, 0};
     p.waves = 16;
+    p.kind = PLAN_SKINNY;
     if (in == IN_F8W) {
-        p.bn = 16;
-        p.waves = 16;
         p.layout = LAY_NT;
-    } else {
-        int fm, fn, fs;
-        if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || fn == 128)) {
-            const Plan f = plan_pieces(TileCand{SKINNY_M, fn, 1, 0, 0, 1, 1}, 32, M, N, K, fs, ws_avail);
-            if (f.splits > 0) {
-                p = f;
-                p.waves = fn == 32 ? 16 : 8;
-            }
+        return p;
+    }
+    auto strips = [&](int cols, int splits) {  // splits = 0 if it does not fit
+        Plan q = plan_pieces(TileCand{SKINNY_M, cols, 1, 0, 0, 1, 1}, 32, M, N, K, splits, ws_avail);
+        q.waves = cols == 32 ? 16 : 8;
+        q.kind = PLAN_SKINNY;
+        return q;
+    };
+    int fm, fn, fs;
+    if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || fn == 128)) {
+        const Plan q = strips(fn, fs);
+        if (q.splits > 0) return q;
+    }
+    if (K >= 8192) {
+        const int cols = M <= 4 ? 128 : 64, most = K >= 16384 ? 16 : 8;
+        const int wgs = (int)ceil_div(N, cols);
+        const int s = (int)std::min<int64_t>(std::min(most, K / (M <= 4 ? 512 : 1024)), 256 / wgs);
+        if (s >= 2) {
+            const Plan q = strips(cols, s);
+            if (q.splits > 1) return q;
         }
     }
-    p.kind = PLAN_SKINNY;
-    return p;
+    return strips(ceil_div(N, 64) >= 160 ? 64 : 32, 1);
 }
 
 Plan plan_act(int in, int es_out, int M, int N, int K, uint64_t ws_avail) {

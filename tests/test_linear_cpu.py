@@ -158,6 +158,12 @@ def test_workspace_status_string():
 def test_plans():
     p = dg.gemm_act_plan("bf16", 1, 4096, 4096, 0, True)
     assert p["tile_rows"] == 16 and p["splits"] == 1 and p["workspace_bytes"] == 0
+    # deep K is split where a workspace allows it
+    for M, N, K in [(1, 2048, 8192), (16, 4096, 8192), (1, 1024, 16384), (4, 12288, 8200)]:
+        p = dg.gemm_act_plan("bf16", M, N, K, 1 << 30, True)
+        assert p["tile_rows"] == 16 and p["splits"] > 1
+        assert p["workspace_bytes"] == p["splits"] * M * N * 4
+        assert dg.gemm_act_plan("bf16", M, N, K, p["workspace_bytes"] - 1, True)["splits"] == 1
     # above the few-row kernel's 16 rows: gemm_ex's plan, never Stream-K
     assert dg.gemm_act_plan("bf16", 512, 4096, 4096, 0, True) == {
         k: v for k, v in dg.gemm_ex_plan("bf16", 512, 4096, 4096, 0, True).items() if k != "stream_k"}
