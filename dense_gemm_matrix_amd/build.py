@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 # the C ABI and planner, then one file per kernel family
 SOURCES = [os.path.join(CSRC, f)
            for f in ("dgemm.hip", "linear.hip", "gemm16.hip", "gemm32.hip", "gemmt.hip",
-                     "slicek16.hip", "skinny.hip", "splitk.hip", "norm.hip", "actgrad.hip")]
+                     "slicek16.hip", "slicet.hip", "skinny.hip", "splitk.hip", "norm.hip", "actgrad.hip")]
 LIB = os.path.join(PKG, "libdgemm.so")
 # The benchmark's matrix-instruction ceiling kernel: a library of its own,
 # loaded only by bench.py, never by the package.

@@ -152,9 +152,11 @@ __global__ __launch_bounds__(256) void transpose32_kernel(const float* X, int ld
 
 }  // namespace
 
-// Rows per workgroup of act_grad_kernel: at most 256 rows of partial sums, and
-// no fewer than 8 rows each.
+// Rows per workgroup of act_grad_kernel: at most 256 rows of partial sums, no
+// fewer than 8 rows each, and up to 64 rows in one chunk, whose sums need no
+// second launch (16 rows per wave take less than a launch).
 int act_grad_rows(int M) {
+    if (M <= 64) return 64;
     const int64_t r = ((int64_t)M + 255) / 256;
     return (int)(r < 8 ? 8 : (r + 3) / 4 * 4);
 }

@@ -353,6 +353,19 @@ Plan slice_plan(int in, int M, int N, int K) {
     return p;
 }
 
+}  // namespace
+
+bool slice_plan_t(int M, int N, int K, Plan& p, double& us) {
+    if (!slice_eligible(IN_BF16, M, N)) return false;
+    p = slice_plan(IN_BF16, M, N, K);
+    us = estimate_slice_us(IN_BF16, *slice_cand(IN_BF16, p.bm, p.waves), M, N, K);
+    return true;
+}
+
+bool slice_waves_t(int ts, int waves) { return slice_cand(IN_BF16, ts, waves) != nullptr; }
+
+namespace {
+
 // Unsplit macro-tile choice: minimise rounds(tiles) x area / eff.  It depends
 // on M, N and the input format only, so the host query reports exactly what
 // an unsplit launch uses.
@@ -589,7 +602,7 @@ int epi_needed(const EpiArgs& e) {
 
 hipError_t launch_family(const GemmLaunch& L, int kind) {
     if (kind == PLAN_SKINNY) return launch_skinny(L);
-    if (L.layout != LAY_NN) return launch_gemmt(L);
+    if (L.layout != LAY_NN) return L.slice_waves > 0 ? launch_slicet(L) : launch_gemmt(L);
     if (L.in == IN_BF16 || L.in == IN_F16)
         return L.slice_waves > 0 ? launch_slicek16(L) : launch_gemm16(L);
     return launch_gemm32(L);

@@ -208,11 +208,14 @@ hipError_t launch_gemm16(const GemmLaunch& L);  // IN_BF16, IN_F16
 hipError_t launch_gemm16_sk(const GemmLaunch& L, const SkSched& s, int grid);
 hipError_t launch_gemm32(const GemmLaunch& L);  // IN_F32, IN_F32X3
 hipError_t launch_gemmt(const GemmLaunch& L);   // LAY_NT, LAY_TN: 16-bit; LAY_NT: IN_F8, IN_F8W
+hipError_t launch_slicet(const GemmLaunch& L);  // as launch_gemmt with slice_waves > 0
 hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_waves > 0
 
-// Products of at most SKINNY_M rows (skinny.hip): 16-bit LAY_NN, IN_F8W LAY_NT.
-// L.tbn names the strip of columns per workgroup, L.slice_waves the waves that
-// share a strip's K; splits, kchunk and the partials' C as for a grid launch.
+// Products of at most SKINNY_M rows (skinny.hip): LAY_NN of 16-bit and fp32
+// operands, LAY_NT of those and IN_F8W, and the rank-K update LAY_TN with at most
+// SKINNY_M terms (K) per sum.  L.tbn names the strip of columns per workgroup,
+// L.slice_waves the waves that share a strip's K; splits (LAY_NN only), kchunk and
+// the partials' C as for a grid launch.
 constexpr int SKINNY_M = 16;
 hipError_t launch_skinny(const GemmLaunch& L);
 

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "dgemm_internal.h"
 
@@ -275,6 +276,73 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[MI][NJ], char* C,
         store_pairs16<OUT, MI, NJ, EPI>(acc, r, N, ldc, col0, g, li, e);
     else
         store_elems<OUT, MI, NJ, EPI>(acc, r, N, ldc, col0, g, li, e);
+}
+
+// Zero the bytes of a 16-byte piece at and past `valid` (<= 0: all of them).
+__device__ __forceinline__ u32x4 mask_bytes(u32x4 v, int valid) {
+    u32x4 out;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int n = valid - 4 * w;  // bytes of this word to keep
+        out[w] = n >= 4 ? v[w] : n <= 0 ? 0u : v[w] & (0xffffffffu >> (32 - 8 * n));
+    }
+    return out;
+}
+
+// A wave's n steps in chunks of D: the next chunk's loads are issued before the
+// current one is used, so D to 2 D steps are in flight, and the last chunk loads
+// only the steps there are (a load past the end costs as much issue as a real
+// one).  load(i, slot) and use(i, slot, newer): step i in slot `slot`, a constant
+// once unrolled; newer (an integral_constant) steps have surely been loaded after
+// the chunk, for a use that waits for its own loads by count.
+template <int D, class Load, class Use>
+__device__ __forceinline__ void run_steps(int n, Load load, Use use) {
+    const int full = n > 0 ? n / D : 0, rem = n > 0 ? n - full * D : 0;
+    auto rest = [&](int base) {  // the last chunk's loads, into slots base ..
+#pragma unroll
+        for (int s = 0; s < D - 1; ++s)
+            if (s < rem) load(full * D + s, base + s);
+    };
+    using None = std::integral_constant<int, 0>;
+    using Next = std::integral_constant<int, D>;
+    auto use_rest = [&](int base) {
+#pragma unroll
+        for (int s = 0; s < D - 1; ++s)
+            if (s < rem) use(full * D + s, base + s, None{});
+    };
+    if (full == 0) {
+        rest(0);
+        use_rest(0);
+        return;
+    }
+#pragma unroll
+    for (int s = 0; s < D; ++s) load(s, s);
+    int c = 0;
+    for (; c + 2 < full; c += 2) {
+#pragma unroll
+        for (int s = 0; s < D; ++s) load((c + 1) * D + s, D + s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use(c * D + s, s, Next{});
+#pragma unroll
+        for (int s = 0; s < D; ++s) load((c + 2) * D + s, s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use((c + 1) * D + s, D + s, Next{});
+    }
+    if (c + 1 < full) {
+#pragma unroll
+        for (int s = 0; s < D; ++s) load((c + 1) * D + s, D + s);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use(c * D + s, s, Next{});
+        rest(0);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use((c + 1) * D + s, D + s, None{});
+        use_rest(0);
+    } else {
+        rest(D);
+#pragma unroll
+        for (int s = 0; s < D; ++s) use(c * D + s, s, None{});
+        use_rest(D);
+    }
 }
 
 // ------------------------------------------------------- the full epilogue

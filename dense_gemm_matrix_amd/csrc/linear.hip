@@ -85,11 +85,18 @@ Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uin
     return p;
 }
 
-// The transposed layouts' plan: the estimate's choice among the two tiles and 1
-// to 16 splits, by the same terms and margin as the other grid plans.
+// The transposed layouts' plan: the estimate's choice among the slice-K tiles
+// (slicet.hip; slicek16's constants, an 8-bit block being 128 k), the two grid
+// tiles and 1 to 16 splits, by the same terms and margin as the other plans.
 Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail) {
     const int bk = t_step(in);
     int fm, fn, fs;
+    if (forced_grid(fm, fn, fs) && fm == fn && (fm == 32 || fm == 64)) {
+        Plan p{fm, fm, 1, K, 0, 0};
+        p.waves = fs == 1 ? 4 : fs;
+        p.layout = layout;
+        if (slice_waves_t(fm, p.waves) && ceil_div(M, fm) * ceil_div(N, fm) <= INT32_MAX) return p;
+    }
     if (forced_grid(fm, fn, fs))
         for (const TileCand& t : TILES_T)
             if (t.bm == fm && t.bn == fn) {
@@ -100,7 +107,10 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     Plan best{};
     double best_us = -1.0;
     const int nk = (int)ceil_div(std::max(K, 1), bk);
+    const bool slice = slice_plan_t(M, N, std::min(K, nk * 64), best, best_us);
+    best.kchunk = K;
     for (const TileCand& t : TILES_T) {
+        if (slice) break;  // as for A[M x K] B[K x N]: unsplit small outputs are the slice-K kernel's
         const double us = estimate_us(in, es_out, M, N, t, 1, nk, 0);
         if (best_us < 0.0 || us < best_us) {
             best_us = us;
@@ -124,10 +134,10 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 
 // At most SKINNY_M rows.
 //
-// 8-bit: strips of 16 columns, 16 waves, never split (B's rows are K-contiguous,
-// so a strip of 16 outputs already reads whole lines).
+// K-contiguous B: strips of 16 columns, 16 waves, never split (a strip of 16
+// outputs already reads whole lines).
 //
-// 16-bit: strips of 32 columns with 16 waves, or from 160 strips of 64 columns on
+// B stored along the output: strips of 32 columns with 16 waves, or from 160 strips of 64 columns on
 // (enough to fill the CUs) 64 with 8 waves: 1 x 12288 x 4096 36 us with 32, 23 with
 // 64; 1 x 8192 x 4096 14.5 with 32, 15.7 with 64.  Deep K leaves a wave many steps
 // one after another, each a round of memory latency; given a workspace, K is then
@@ -144,11 +154,11 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 // More rows make the partial products bigger and the wide strips' sums longer: 16
 // rows of 4096 x 4096 take 14.9 / 16.1 in 128 columns and 8 pieces, 13.0 / 14.6 in
 // 64 columns and 4.
-Plan plan_skinny(int in, int M, int N, int K, uint64_t ws_avail) {
+Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     Plan p{SKINNY_M, 16, 1, K, 0, 0};
     p.waves = 16;
     p.kind = PLAN_SKINNY;
-    if (in == IN_F8W) {
+    if (layout == LAY_NT) {
         p.layout = LAY_NT;
         return p;
     }
@@ -159,12 +169,13 @@ Plan plan_skinny(int in, int M, int N, int K, uint64_t ws_avail) {
         return q;
     };
     int fm, fn, fs;
-    if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || fn == 128)) {
+    const bool f32 = in == IN_F32;
+    if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || (fn == 128 && !f32))) {
         const Plan q = strips(fn, fs);
         if (q.splits > 0) return q;
     }
     if (K >= 8192) {
-        const int cols = M <= 4 ? 128 : 64, most = K >= 16384 ? 16 : 8;
+        const int cols = M <= 4 && !f32 ? 128 : 64, most = K >= 16384 ? 16 : 8;
         const int wgs = (int)ceil_div(N, cols);
         const int s = (int)std::min<int64_t>(std::min(most, K / (M <= 4 ? 512 : 1024)), 256 / wgs);
         if (s >= 2) {
@@ -176,8 +187,8 @@ Plan plan_skinny(int in, int M, int N, int K, uint64_t ws_avail) {
 }
 
 Plan plan_act(int in, int es_out, int M, int N, int K, uint64_t ws_avail) {
-    if ((in == IN_BF16 || in == IN_F16) && M > 0 && M <= SKINNY_M && N > 0)
-        return plan_skinny(in, M, N, K, ws_avail);
+    if (in != IN_F32X3 && M > 0 && M <= SKINNY_M && N > 0)
+        return plan_skinny(in, LAY_NN, M, N, K, ws_avail);
     return make_plan(in, es_out, M, N, K, ws_avail, false);
 }
 
@@ -186,7 +197,7 @@ int f8_in(int of, int M) { return of == OUT_F32 || M <= SKINNY_M ? IN_F8W : IN_F
 
 Plan plan_f8(int of, int M, int N, int K, uint64_t ws_avail) {
     const int in = f8_in(of, M);
-    if (M > 0 && M <= SKINNY_M && N > 0) return plan_skinny(in, M, N, K, ws_avail);
+    if (M > 0 && M <= SKINNY_M && N > 0) return plan_skinny(in, LAY_NT, M, N, K, ws_avail);
     return plan_t(in, LAY_NT, out_esize(of), M, N, K, ws_avail);
 }
 
@@ -255,27 +266,39 @@ BwdParts bwd_parts(int in, int cfmt, int M, int N, int K, int act, bool products
     b.ldp = (int)up(N, 4);
     b.chunks = (int)ceil_div(M, act_grad_rows(M));
     b.dz = b.own_dz ? up((int64_t)M * b.lddz * es, WS_ALIGN) : 0;
-    b.part = dbias ? up((int64_t)b.chunks * b.ldp * 4, WS_ALIGN) : 0;
-    if (products && es == 4)
+    // One chunk's column sums are dbias itself.
+    b.part = dbias && b.chunks != 1 ? up((int64_t)b.chunks * b.ldp * 4, WS_ALIGN) : 0;
+    if (products && es == 4 && M > SKINNY_M)
         b.trans = up(std::max((int64_t)N * up(K, 4), (int64_t)K * up(M, 4)) * 4, WS_ALIGN);
     b.required = b.dz + b.part + b.trans;
     return b;
 }
 
-Plan plan_bwd(int in, int layout, int M, int N, int K, uint64_t ws) {
+// The product of a backward pass over `rows` rows, M x N with K terms per sum.
+// Few rows: B once through registers for dA, a rank-`rows` update for dB (fp32
+// arithmetic for 3 x bf16 too).
+Plan plan_bwd(int in, int layout, int rows, int M, int N, int K, uint64_t ws) {
+    if (rows <= SKINNY_M && M > 0 && N > 0) {
+        if (layout == LAY_NT) return plan_skinny(in, LAY_NT, M, N, K, 0);
+        Plan p{32, 512, 1, K, 0, 0};
+        p.kind = PLAN_SKINNY;
+        p.layout = LAY_TN;
+        return p;
+    }
     if (in == IN_BF16 || in == IN_F16) return plan_t(in, layout, 2, M, N, K, ws);
     return make_plan(in, 4, M, N, K, ws, false);
 }
 
-int run_bwd_product(int in, int layout, int M, int N, int K, const void* X, int ldx, const void* Y,
+int run_bwd_product(int in, int layout, int rows, int M, int N, int K, const void* X, int ldx, const void* Y,
                     int ldy, const Mat& out, char* ws, int64_t ws_bytes, hipStream_t stream) {
     if (out.empty()) return DGEMM_OK;
-    const Plan p = plan_bwd(in, layout, M, N, K, (uint64_t)ws_bytes);
+    const Plan p = plan_bwd(in, layout, rows, M, N, K, (uint64_t)ws_bytes);
     EpiArgs e{};
     e.alpha = 1.0f;
-    // The transposed-layout kernels store through the full epilogue's row segments.
-    return run(in, out_format(in, DGEMM_OUT_SAME), M, N, K, X, ldx, Y, ldy, (void*)out.p, (int)out.ld,
-               e, in == IN_BF16 || in == IN_F16 ? EPI_FULL : EPI_NONE, p, ws, stream);
+    // The kernels of transposed layouts store through the full epilogue's row segments.
+    return run(p.kind == PLAN_SKINNY && in == IN_F32X3 ? IN_F32 : in, out_format(in, DGEMM_OUT_SAME), M,
+               N, K, X, ldx, Y, ldy, (void*)out.p, (int)out.ld, e,
+               p.layout != LAY_NN ? EPI_FULL : EPI_NONE, p, ws, stream);
 }
 
 // Format codes DGEMM_IN_F32 / _BF16 / _F16 of an elementwise operator.
@@ -367,15 +390,15 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
     }
     if (M > 0 && N > 0 && (b.own_dz || dbias)) {
         const ActGradArgs a{(const char*)dC, (const char*)mZ.p, b.own_dz ? w : nullptr,
-                            dbias ? (float*)w_part : nullptr, M, N, lddc, ldz, b.lddz, b.ldp,
+                            !dbias ? nullptr : b.chunks == 1 ? dbias : (float*)w_part, M, N, lddc, ldz, b.lddz, b.ldp,
                             act_grad_rows(M), act};
         if (launch_act_grad(a, cf, out_format(in, DGEMM_OUT_SAME), s) != hipSuccess)
             return DGEMM_ERR_LAUNCH;
     }
-    if (dbias && N > 0 &&
+    if (dbias && N > 0 && b.chunks != 1 &&
         launch_col_reduce((const float*)w_part, b.chunks, b.ldp, N, dbias, s) != hipSuccess)
         return DGEMM_ERR_LAUNCH;
-    const bool f32 = es == 4;
+    const bool f32 = es == 4 && M > SKINNY_M;  // the fp32 kernels take A[M x K] B[K x N] only
     if (dA) {
         const void* y = B;
         int ldy = ldb;
@@ -385,7 +408,7 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
                 return DGEMM_ERR_LAUNCH;
             y = w_trans;
         }
-        st = run_bwd_product(in, LAY_NT, M, K, N, dz, lddz, y, ldy, mdA, w_gemm, gemm_bytes, s);
+        st = run_bwd_product(in, LAY_NT, M, M, K, N, dz, lddz, y, ldy, mdA, w_gemm, gemm_bytes, s);
         if (st != DGEMM_OK) return st;
     }
     if (dB) {
@@ -397,7 +420,7 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
                 return DGEMM_ERR_LAUNCH;
             x = w_trans;
         }
-        st = run_bwd_product(in, LAY_TN, K, N, M, x, ldx, dz, lddz, mdB, w_gemm, gemm_bytes, s);
+        st = run_bwd_product(in, LAY_TN, M, K, N, M, x, ldx, dz, lddz, mdB, w_gemm, gemm_bytes, s);
         if (st != DGEMM_OK) return st;
     }
     return DGEMM_OK;
@@ -412,8 +435,8 @@ int gemm_act_bwd_workspace(int in, int out, int M, int N, int K, int act, size_t
     const BwdParts b = bwd_parts(in, cf, M, N, K, act, true, true);
     int64_t more = 0;
     const uint64_t any = (uint64_t)1 << 40;
-    if (M > 0 && K > 0) more = std::max(more, plan_bwd(in, LAY_NT, M, K, N, any).ws_bytes);
-    if (K > 0 && N > 0) more = std::max(more, plan_bwd(in, LAY_TN, K, N, M, any).ws_bytes);
+    if (M > 0 && K > 0) more = std::max(more, plan_bwd(in, LAY_NT, M, M, K, N, any).ws_bytes);
+    if (K > 0 && N > 0) more = std::max(more, plan_bwd(in, LAY_TN, M, K, N, M, any).ws_bytes);
     if (required) *required = (size_t)b.required;
     if (best) *best = (size_t)(b.required + more);
     return DGEMM_OK;

@@ -61,6 +61,11 @@ double estimate_us(int in, int es_out, int M, int N, const TileCand& t, int spli
                    int steps_per_split, int ldw);
 // The tile and split count forced by dgemm_set_plan_override, if a grid plan is.
 bool forced_grid(int& bm, int& bn, int& splits);
+// The 16-bit slice-K plan for an M x N output with K terms and its estimate; false
+// where the output is too large for one.  slice_waves_t: whether the kernels have
+// tile ts with `waves` waves.
+bool slice_plan_t(int M, int N, int K, Plan& p, double& us);
+bool slice_waves_t(int ts, int waves);
 Plan make_plan(int in, int es_out, int M, int N, int K, uint64_t ws_avail, bool allow_sk);
 
 // Validated arguments and a plan -> its launches, with epilogue e at level epi.

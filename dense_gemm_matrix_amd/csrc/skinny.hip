@@ -1,5 +1,6 @@
 // skinny.hip -- products of at most 16 rows (tokens being generated) on gfx950
-// (MI355X): bf16 / fp16 A[M x K] B[K x N], and e4m3 A[M x K] B[N x K]^T.
+// (MI355X): A[M x K] B[K x N] (NN) and A[M x K] B[N x K]^T (NT), and the rank-M
+// update A[M x K]^T D[M x N] of their backward pass.
 //
 // Such a product reads B once and computes little: the floor is B's bytes over
 // the HBM rate.  So no LDS staging: B goes straight from memory into the
@@ -8,21 +9,24 @@
 // their partial sums are added in LDS in wave order (deterministic).  K may be
 // split over workgroups too, with fp32 partials in the caller's workspace.
 //
-// 16-bit: lane (g, c) of 64 (g = lane / 16, c = lane % 16) loads the CPL
-// consecutive columns CPL c .. of the eight k-rows 8 g .. 8 g + 7 of a 32-k
-// step.  v_mfma_f32_16x16x32 wants eight k of one column per lane; the lane
+// NN (bf16, fp16, fp32): lane (g, c) of 64 (g = lane / 16, c = lane % 16) loads
+// the CPL consecutive columns CPL c .. of the eight k-rows 8 g .. 8 g + 7 of a
+// 32-k step, and matrix instruction j covers columns n0 + CPL c + j, c = 0 .. 15.
+// 16-bit: v_mfma_f32_16x16x32 wants eight k of one column per lane; the lane
 // holds eight rows of CPL columns, and one v_perm_b32 per output word picks a
 // column's halves from two rows' words: half an operation per element, instead
-// of a transpose through LDS.  Matrix instruction j covers columns n0 + CPL c +
-// j, c = 0 .. 15.  Rows past M come as zeros from A's resource.
+// of a transpose through LDS.  fp32: v_mfma_f32_16x16x4_f32 wants one k per lane,
+// which each loaded word is.
 //
-// e4m3: B's rows are K-contiguous, so a lane loads its operand as it is: 32 k
-// of row n0 + c per 128-k step, in two 16-byte pieces 64 bytes apart, so that
-// the four lane groups read 64 consecutive bytes of a row at a time (A's pieces
-// the same: the order of k inside the instruction cancels).  The values are
-// widened to bf16 in registers, exactly, for the bf16 instruction: the kernel
-// waits for memory, and the sums are fp32 (the 8-bit instruction's are not quite:
-// gemmt.hip).
+// NT (bf16, fp16, fp32, e4m3): B's rows are K-contiguous, so a lane loads its
+// operand as it is: row n0 + c, two 16-byte pieces 64 bytes apart per 128-byte
+// step, so that the four lane groups read 64 consecutive bytes of a row at a time
+// (A's pieces the same: the order of k inside the instructions cancels).  e4m3
+// values are widened to bf16 in registers, exactly, for the bf16 instruction: the
+// kernel waits for memory, and the sums are fp32 (the 8-bit instruction's are not
+// quite: gemmt.hip).
+//
+// Rows past M come as zeros from A's resource.
 
 #include <type_traits>
 
@@ -31,15 +35,16 @@
 namespace dgemm {
 namespace {
 
-// Zero the bytes of a 16-byte piece at and past `valid` (<= 0: all of them).
-__device__ __forceinline__ u32x4 mask_bytes(u32x4 v, int valid) {
-    u32x4 out;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const int n = valid - 4 * w;  // bytes of this word to keep
-        out[w] = n >= 4 ? v[w] : n <= 0 ? 0u : v[w] & (0xffffffffu >> (32 - 8 * n));
-    }
-    return out;
+constexpr int NT_WAVES = 16;  // waves that share a strip's K in the NT kernel
+
+template <int IN>
+__device__ __forceinline__ f32x4 mfma_16(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (IN == IN_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
 // The elements of a strip that a lane finishes, and what the epilogue reads for
@@ -101,59 +106,6 @@ struct Strip {
     }
 };
 
-// A wave's n steps in chunks of D: the next chunk's loads are issued before the
-// current one is used, so D to 2 D steps are in flight, and the last chunk loads
-// only the steps there are (a load past the end costs as much issue as a real
-// one).  load(i, slot) and use(i, slot): step i in register slot `slot`, which is
-// a constant once unrolled.
-template <int D, class Load, class Use>
-__device__ __forceinline__ void run_steps(int n, Load load, Use use) {
-    const int full = n > 0 ? n / D : 0, rem = n > 0 ? n - full * D : 0;
-    auto rest = [&](int base) {  // the last chunk's loads, into slots base ..
-#pragma unroll
-        for (int s = 0; s < D - 1; ++s)
-            if (s < rem) load(full * D + s, base + s);
-    };
-    auto use_rest = [&](int base) {
-#pragma unroll
-        for (int s = 0; s < D - 1; ++s)
-            if (s < rem) use(full * D + s, base + s);
-    };
-    if (full == 0) {
-        rest(0);
-        use_rest(0);
-        return;
-    }
-#pragma unroll
-    for (int s = 0; s < D; ++s) load(s, s);
-    int c = 0;
-    for (; c + 2 < full; c += 2) {
-#pragma unroll
-        for (int s = 0; s < D; ++s) load((c + 1) * D + s, D + s);
-#pragma unroll
-        for (int s = 0; s < D; ++s) use(c * D + s, s);
-#pragma unroll
-        for (int s = 0; s < D; ++s) load((c + 2) * D + s, s);
-#pragma unroll
-        for (int s = 0; s < D; ++s) use((c + 1) * D + s, D + s);
-    }
-    if (c + 1 < full) {
-#pragma unroll
-        for (int s = 0; s < D; ++s) load((c + 1) * D + s, D + s);
-#pragma unroll
-        for (int s = 0; s < D; ++s) use(c * D + s, s);
-        rest(0);
-#pragma unroll
-        for (int s = 0; s < D; ++s) use((c + 1) * D + s, D + s);
-        use_rest(0);
-    } else {
-        rest(D);
-#pragma unroll
-        for (int s = 0; s < D; ++s) use(c * D + s, s);
-        use_rest(D);
-    }
-}
-
 // Workgroup strip map: consecutive strips to one XCD (workgroups are dealt to
 // the 8 XCDs in turn), so that strips narrower than a 128-byte line share it in
 // one L2.
@@ -164,16 +116,20 @@ __device__ __forceinline__ int strip_of(int wg, int strips) {
 }
 
 template <int IN, int OUT, int EPI, int CPL, int W>
-__global__ __launch_bounds__(64 * W) void skinny16_kernel(
+__global__ __launch_bounds__(64 * W) void skinny_nn_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* C, int M, int N, int K, int lda,
     int ldb, int ldc, int strips, int kchunk, int64_t c_zstride, EpiArgs epi) {
-    constexpr int WD = CPL / 2;   // words per lane and k-row
-    constexpr int D = CPL == 8 ? 2 : 4;  // steps per chunk; two chunks in registers
+    constexpr bool F32 = IN == IN_F32;
+    constexpr int ES = F32 ? 4 : 2;
+    constexpr int WD = CPL * ES / 4;    // words per lane and k-row
+    constexpr int AW = ES / 2;          // 16-byte pieces of A per lane and step
+    // Steps per chunk; two chunks in registers, within 128 of them for 16 waves.
+    constexpr int D = WD == 4 || F32 ? 2 : 4;
     __shared__ float red[W * CPL * 4 * 64];
     {
         const int kbeg = (int)blockIdx.y * kchunk;
-        A += (int64_t)kbeg * 2;
-        B += (int64_t)kbeg * ldb * 2;
+        A += (int64_t)kbeg * ES;
+        B += (int64_t)kbeg * ldb * ES;
         C += (int)blockIdx.y * c_zstride;
         K = (K - kbeg) < kchunk ? (K - kbeg) : kchunk;
     }
@@ -187,18 +143,19 @@ __global__ __launch_bounds__(64 * W) void skinny16_kernel(
     strip.prefetch(M, N, n0, wave, lane, epi);
 
     uint32_t b[2 * D][8][WD];
-    u32x4 a[2 * D];
+    u32x4 a[2 * D][AW];
     auto load = [&](int t, int S) {  // S: a constant once unrolled
         const int k0 = t * 32;
         const int rows = (K - k0) < 32 ? (K - k0) : 32;
-        const auto rb = make_rsrc(B + ((int64_t)k0 * ldb + n0) * 2,
-                                  rows > 0 ? ((int64_t)(rows - 1) * ldb + cols) * 2 : 0);
-        const auto ra = make_rsrc(A + (int64_t)k0 * 2,
-                                  rows > 0 ? ((int64_t)(M - 1) * lda + rows) * 2 : 0);
-        a[S] = load16(ra, (c * lda + 8 * g) * 2);
+        const auto rb = make_rsrc(B + ((int64_t)k0 * ldb + n0) * ES,
+                                  rows > 0 ? ((int64_t)(rows - 1) * ldb + cols) * ES : 0);
+        const auto ra = make_rsrc(A + (int64_t)k0 * ES,
+                                  rows > 0 ? ((int64_t)(M - 1) * lda + rows) * ES : 0);
+#pragma unroll
+        for (int h = 0; h < AW; ++h) a[S][h] = load16(ra, (c * lda + 8 * g) * ES + 16 * h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int off = ((8 * g + j) * ldb + CPL * c) * 2;
+            const int off = ((8 * g + j) * ldb + CPL * c) * ES;
             if constexpr (WD == 4) {
                 const u32x4 v = load16(rb, off);
 #pragma unroll
@@ -218,88 +175,146 @@ __global__ __launch_bounds__(64 * W) void skinny16_kernel(
     for (int j = 0; j < CPL; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     auto use = [&](int t, int S) {
         const int k0 = t * 32;
-        u32x4 av = a[S];
-        if (k0 + 32 > K) av = mask_bytes(av, (K - k0 - 8 * g) * 2);  // A's row padding
+        u32x4 av[AW];
 #pragma unroll
-        for (int w = 0; w < WD; ++w)
+        for (int h = 0; h < AW; ++h) {
+            av[h] = a[S][h];
+            if (k0 + 32 > K) av[h] = mask_bytes(av[h], (K - k0 - 8 * g) * ES - 16 * h);  // row padding
+        }
+        if constexpr (F32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u32x4 bv;
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    bv[p] = __builtin_amdgcn_perm(b[S][2 * p + 1][w], b[S][2 * p][w],
-                                                  h ? 0x07060302u : 0x05040100u);
-                const int j = 2 * w + h;
-                if constexpr (IN == IN_BF16)
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8, av), __builtin_bit_cast(bf16x8, bv), acc[j], 0, 0, 0);
-                else
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        __builtin_bit_cast(f16x8, av), __builtin_bit_cast(f16x8, bv), acc[j], 0, 0, 0);
-            }
+                for (int w = 0; w < WD; ++w)
+                    acc[w] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_float(av[j >> 2][j & 3]),
+                                                                  as_float(b[S][j][w]), acc[w], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int w = 0; w < WD; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u32x4 bv;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        bv[p] = __builtin_amdgcn_perm(b[S][2 * p + 1][w], b[S][2 * p][w],
+                                                      h ? 0x07060302u : 0x05040100u);
+                    acc[2 * w + h] = mfma_16<IN>(av[0], bv, acc[2 * w + h]);
+                }
+        }
     };
     // Wave w takes steps w, w + W, ...: the workgroup reads B's rows in order.
     run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
-                 [&](int i, int slot) { use(wave + i * W, slot); });
+                 [&](int i, int slot, auto) { use(wave + i * W, slot); });
     strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
 }
 
-template <int OUT, int W>
-__global__ __launch_bounds__(64 * W) void skinny8_kernel(
+template <int IN, int OUT, int W>
+__global__ __launch_bounds__(64 * W) void skinny_nt_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* C, int M, int N, int K, int lda,
     int ldb, int ldc, int strips, EpiArgs epi) {
+    constexpr int ES = IN == IN_F32 ? 4 : IN == IN_F8W ? 1 : 2;
     __shared__ float red[W * 4 * 64];
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int c = lane & 15, g = lane >> 4;
     const int n0 = strip_of((int)blockIdx.x, strips) * 16;
     const int rows_b = (N - n0) < 16 ? (N - n0) : 16;
-    const int nstep = (K + 127) / 128;
+    constexpr int SK = 128 / ES;  // k per step
+    const int nstep = (K + SK - 1) / SK;
     Strip<OUT, EPI_FULL, 1, W> strip;
     strip.prefetch(M, N, n0, wave, lane, epi);
     constexpr int D = 2;  // steps per chunk; two chunks in registers
     u32x4 a[2 * D][2], b[2 * D][2];
     auto load = [&](int t, int S) {  // S: a constant once unrolled
-        const int k0 = t * 128;
-        const int krem = (K - k0) < 128 ? (K - k0) : 128;
-        const auto ra = make_rsrc(A + k0, krem > 0 ? (int64_t)(M - 1) * lda + krem : 0);
-        const auto rb = make_rsrc(B + (int64_t)n0 * ldb + k0,
-                                  krem > 0 ? (int64_t)(rows_b - 1) * ldb + krem : 0);
+        const int k0 = t * SK;
+        const int krem = (K - k0) < SK ? (K - k0) : SK;
+        const auto ra = make_rsrc(A + (int64_t)k0 * ES,
+                                  krem > 0 ? ((int64_t)(M - 1) * lda + krem) * ES : 0);
+        const auto rb = make_rsrc(B + ((int64_t)n0 * ldb + k0) * ES,
+                                  krem > 0 ? ((int64_t)(rows_b - 1) * ldb + krem) * ES : 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            a[S][h] = load16(ra, c * lda + 64 * h + 16 * g);
-            b[S][h] = load16(rb, c * ldb + 64 * h + 16 * g);
+            a[S][h] = load16(ra, c * lda * ES + 64 * h + 16 * g);
+            b[S][h] = load16(rb, c * ldb * ES + 64 * h + 16 * g);
         }
     };
     f32x4 acc[1] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
     auto use = [&](int t, int S) {
-        const int k0 = t * 128;
-        u32x4 x[2], y[2];
+        const int k0 = t * SK;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            x[h] = a[S][h];
-            y[h] = b[S][h];
-            if (k0 + 128 > K) {  // the rows' padding: 0 * NaN would be a NaN, so both
-                const int valid = K - (k0 + 64 * h + 16 * g);
-                x[h] = mask_bytes(x[h], valid);
-                y[h] = mask_bytes(y[h], valid);
+            u32x4 x = a[S][h], y = b[S][h];
+            if (k0 + SK > K) {  // the rows' padding: 0 * NaN would be a NaN, so both
+                const int valid = (K - k0) * ES - (64 * h + 16 * g);
+                x = mask_bytes(x, valid);
+                y = mask_bytes(y, valid);
+            }
+            if constexpr (IN == IN_F32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[0] = __builtin_amdgcn_mfma_f32_16x16x4f32(as_float(x[q]), as_float(y[q]), acc[0],
+                                                                  0, 0, 0);
+            } else if constexpr (IN == IN_F8W) {
+#pragma unroll
+                for (int q = 0; q < 4; q += 2)
+                    acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        widen_f8(x[q], x[q + 1]), widen_f8(y[q], y[q + 1]), acc[0], 0, 0, 0);
+            } else {
+                acc[0] = mfma_16<IN>(x, y, acc[0]);
             }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 0; q < 4; q += 2)
-                acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_f8(x[h][q], x[h][q + 1]),
-                                                                 widen_f8(y[h][q], y[h][q + 1]), acc[0],
-                                                                 0, 0, 0);
     };
     run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
-                 [&](int i, int slot) { use(wave + i * W, slot); });
+                 [&](int i, int slot, auto) { use(wave + i * W, slot); });
     strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
 }
 
+// The rank-M update: C[k][n] = sum over m < M <= 16 of A[m][k] D[m][n], a weight's
+// gradient from a few tokens.  Bound by writing C: a wave owns 8 rows of 512
+// columns (8 per lane), reads D's pieces once, takes its rows' eight values of
+// A[m] as wave-uniform scalars, and stores 16-byte pieces.
+template <int FMT>
+__global__ __launch_bounds__(256) void outer_kernel(const char* __restrict__ A,
+                                                    const char* __restrict__ D, char* C, int M, int N,
+                                                    int K, int lda, int ldd, int ldc, int col_blocks) {
+    constexpr int ES = fmt_es<FMT>;
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c = ((int)blockIdx.x % col_blocks) * 512 + lane * 8;
+    const int k0 = ((int)blockIdx.x / col_blocks) * 32 + wave * 8;
+    if (k0 >= K) return;
+    const int nvalid = N - c;
+    float acc[8][8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
+#pragma unroll 4
+    for (int m = 0; m < M; ++m) {
+        Row8<FMT> d, a;
+        d.load(make_rsrc(D + (int64_t)m * ldd * ES, (int64_t)N * ES), (uint32_t)c * ES, nvalid);
+        a.load(make_rsrc(A + (int64_t)m * lda * ES, (int64_t)K * ES), (uint32_t)k0 * ES, K - k0);
+        float x[8], y[8];
+        d.get(x);
+        a.get(y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[j][i] += y[j] * x[i];
+    }
+    const __amdgpu_buffer_rsrc_t rc =
+        make_rsrc(C + (int64_t)k0 * ldc * ES,
+                  ((int64_t)((K - k0 < 8 ? K - k0 : 8) - 1) * ldc + N) * ES);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        Row8<FMT> o;
+        o.set(acc[j]);
+        if (k0 + j < K && nvalid > 0) o.store(rc, (uint32_t)(j * ldc + c) * ES, nvalid);
+    }
+}
+
 template <int IN, int OUT, int EPI, int CPL, int W>
-hipError_t go16(const GemmLaunch& L) {
+hipError_t go_nn(const GemmLaunch& L) {
     const char* a = L.A;
     const char* b = L.B;
     char* c = L.C;
@@ -308,59 +323,84 @@ hipError_t go16(const GemmLaunch& L) {
     int64_t zs = L.c_zstride;
     EpiArgs e = L.e;
     void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &strips, &kchunk, &zs, &e};
-    return hipLaunchKernel((const void*)skinny16_kernel<IN, OUT, EPI, CPL, W>,
+    return hipLaunchKernel((const void*)skinny_nn_kernel<IN, OUT, EPI, CPL, W>,
                            dim3((unsigned)strips, (unsigned)L.splits), dim3(64 * W), args, 0, L.stream);
 }
 
 template <int IN, int OUT, int EPI>
 hipError_t by_strip(const GemmLaunch& L) {
-    if (L.tbn == 128 && L.slice_waves == 8) return go16<IN, OUT, EPI, 8, 8>(L);
-    if (L.tbn == 64 && L.slice_waves == 8) return go16<IN, OUT, EPI, 4, 8>(L);
-    if (L.tbn == 32 && L.slice_waves == 16) return go16<IN, OUT, EPI, 2, 16>(L);
+    if constexpr (IN != IN_F32)
+        if (L.tbn == 128 && L.slice_waves == 8) return go_nn<IN, OUT, EPI, 8, 8>(L);
+    if (L.tbn == 64 && L.slice_waves == 8) return go_nn<IN, OUT, EPI, 4, 8>(L);
+    if (L.tbn == 32 && L.slice_waves == 16) return go_nn<IN, OUT, EPI, 2, 16>(L);
     return hipErrorInvalidValue;
 }
 
 template <int IN>
-hipError_t by_out16(const GemmLaunch& L) {
-    constexpr int SAME = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
+hipError_t nn_by_out(const GemmLaunch& L) {
     if (L.epi == EPI_NONE && L.out == OUT_F32) return by_strip<IN, OUT_F32, EPI_NONE>(L);
     if (L.epi != EPI_FULL) return hipErrorInvalidValue;
     if (L.out == OUT_F32) return by_strip<IN, OUT_F32, EPI_FULL>(L);
-    if (L.out == SAME) return by_strip<IN, SAME, EPI_FULL>(L);
+    if constexpr (IN == IN_BF16)
+        if (L.out == OUT_BF16) return by_strip<IN, OUT_BF16, EPI_FULL>(L);
+    if constexpr (IN == IN_F16)
+        if (L.out == OUT_F16) return by_strip<IN, OUT_F16, EPI_FULL>(L);
     return hipErrorInvalidValue;
 }
 
-template <int OUT, int W>
-hipError_t go8(const GemmLaunch& L) {
+template <int IN, int OUT>
+hipError_t go_nt(const GemmLaunch& L) {
+    if (L.tbn != 16 || L.slice_waves != NT_WAVES || L.splits != 1 || L.epi != EPI_FULL)
+        return hipErrorInvalidValue;
     const char* a = L.A;
     const char* b = L.B;
     char* c = L.C;
     int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc, strips = L.tiles_n;
     EpiArgs e = L.e;
     void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &strips, &e};
-    return hipLaunchKernel((const void*)skinny8_kernel<OUT, W>, dim3((unsigned)strips), dim3(64 * W),
-                           args, 0, L.stream);
+    return hipLaunchKernel((const void*)skinny_nt_kernel<IN, OUT, NT_WAVES>, dim3((unsigned)strips),
+                           dim3(64 * NT_WAVES), args, 0, L.stream);
 }
 
-template <int OUT>
-hipError_t by_waves8(const GemmLaunch& L) {
-    if (L.tbn != 16) return hipErrorInvalidValue;
-    if (L.slice_waves == 8) return go8<OUT, 8>(L);
-    if (L.slice_waves == 16) return go8<OUT, 16>(L);
-    return hipErrorInvalidValue;
+template <int FMT>
+hipError_t go_outer(const GemmLaunch& L) {
+    const char* a = L.A;
+    const char* d = L.B;
+    char* c = L.C;
+    int M = L.K, N = L.N, K = L.M, lda = L.lda, ldd = L.ldb, ldc = L.ldc;
+    int col_blocks = (N + 511) / 512;
+    const int64_t blocks = (int64_t)col_blocks * (((int64_t)K + 31) / 32);
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+    void* args[] = {&a, &d, &c, &M, &N, &K, &lda, &ldd, &ldc, &col_blocks};
+    return hipLaunchKernel((const void*)outer_kernel<FMT>, dim3((unsigned)blocks), dim3(256), args, 0,
+                           L.stream);
 }
 
 }  // namespace
 
 hipError_t launch_skinny(const GemmLaunch& L) {
-    if (L.M < 1 || L.M > SKINNY_M || L.splits < 1) return hipErrorInvalidValue;
-    if (L.in == IN_BF16 && L.layout == LAY_NN) return by_out16<IN_BF16>(L);
-    if (L.in == IN_F16 && L.layout == LAY_NN) return by_out16<IN_F16>(L);
-    if (L.in != IN_F8W || L.layout != LAY_NT || L.splits != 1 || L.epi != EPI_FULL)
+    if (L.layout == LAY_TN) {
+        if (L.K < 0 || L.K > SKINNY_M || L.splits != 1) return hipErrorInvalidValue;
+        if (L.in == IN_F32 && L.out == OUT_F32) return go_outer<OUT_F32>(L);
+        if (L.in == IN_BF16 && L.out == OUT_BF16) return go_outer<OUT_BF16>(L);
+        if (L.in == IN_F16 && L.out == OUT_F16) return go_outer<OUT_F16>(L);
         return hipErrorInvalidValue;
-    if (L.out == OUT_F32) return by_waves8<OUT_F32>(L);
-    if (L.out == OUT_BF16) return by_waves8<OUT_BF16>(L);
-    if (L.out == OUT_F16) return by_waves8<OUT_F16>(L);
+    }
+    if (L.M < 1 || L.M > SKINNY_M || L.splits < 1) return hipErrorInvalidValue;
+    if (L.layout == LAY_NN) {
+        if (L.in == IN_BF16) return nn_by_out<IN_BF16>(L);
+        if (L.in == IN_F16) return nn_by_out<IN_F16>(L);
+        if (L.in == IN_F32) return nn_by_out<IN_F32>(L);
+        return hipErrorInvalidValue;
+    }
+    if (L.in == IN_F8W) {
+        if (L.out == OUT_F32) return go_nt<IN_F8W, OUT_F32>(L);
+        if (L.out == OUT_BF16) return go_nt<IN_F8W, OUT_BF16>(L);
+        if (L.out == OUT_F16) return go_nt<IN_F8W, OUT_F16>(L);
+    }
+    if (L.in == IN_F32 && L.out == OUT_F32) return go_nt<IN_F32, OUT_F32>(L);
+    if (L.in == IN_BF16 && L.out == OUT_BF16) return go_nt<IN_BF16, OUT_BF16>(L);
+    if (L.in == IN_F16 && L.out == OUT_F16) return go_nt<IN_F16, OUT_F16>(L);
     return hipErrorInvalidValue;
 }
 

@@ -1,0 +1,276 @@
+// slicet.hip -- small outputs of the transposed layouts and of 8-bit operands
+// (gemmt.hip's products), for gfx950 (MI355X).
+//
+// As slicek16.hip does for A[M x K] B[K x N]: a workgroup of W waves owns a small
+// TS x TS tile (TS = 32 MI), each wave takes an equal run of 128-byte K blocks
+// (64 k of 16-bit operands, 128 of e4m3) and holds the whole tile's accumulators
+// for its own k; the W partial tiles are added in LDS in wave order, and each wave
+// finishes its share of the tile with the full epilogue.  No workspace, no second
+// kernel: such a product is a few us, a split's second launch another three.
+//
+// No operand is shared between the waves, so each wave moves its own:
+//   NT: both operands K-contiguous: 16-byte loads straight into the registers the
+//     matrix instruction reads.  Per 16-k half h of a 16-bit block lane (g, li)
+//     takes chunk 2 h + g of row li; of an e4m3 block, per 64 k, chunks 4 q + 2 g
+//     and 4 q + 2 g + 1 (the order of k inside the instruction cancels).
+//   TN: both along the output: 64 k-rows x TS columns of each go into the wave's
+//     own LDS region as they lie in memory (direct-to-LDS loads) and come back
+//     through the transpose read (slicek16.hip's B).
+// D to 2 D blocks are in flight per wave.
+
+#include <type_traits>
+
+#include "kern_common.h"
+
+namespace dgemm {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int cmax(int a, int b) { return a > b ? a : b; }
+
+template <int IN, int LAY, int OUT, int MI, int W>
+__global__ __launch_bounds__(64 * W) void slicet_kernel(
+    const char* __restrict__ X, const char* __restrict__ Y, char* C, int M, int N, int K, int ldx,
+    int ldy, int ldc, int tiles_m, int tiles_n, EpiArgs epi) {
+    constexpr bool KC = LAY == LAY_NT;
+    constexpr bool F8 = IN == IN_F8 || IN == IN_F8W;
+    static_assert(KC || !F8, "8-bit operands are K-contiguous");
+    constexpr int ES = F8 ? 1 : 2;
+    constexpr int BK = 128 / ES;
+    constexpr int TS = 32 * MI;
+    constexpr int NB = MI * MI;
+    // Blocks per chunk, two chunks in flight: registers (NT) or LDS (TN).
+    constexpr int D = MI == 1 && (KC || W == 4) ? 2 : 1;
+    constexpr int BLKB = 128 * TS;            // bytes of one operand's block
+    constexpr int NDB = BLKB / 1024;          // its direct-to-LDS loads
+    constexpr int STAGES = KC ? 0 : W * 2 * D * 2 * BLKB;
+    constexpr int RED = W * NB * 16 * 64 * 4;
+    __shared__ __attribute__((aligned(1024))) char smem[cmax(STAGES, RED)];
+    int tm, tn;
+    map_tile((int)blockIdx.x, tiles_m, tiles_n, tm, tn);
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 5, li = lane & 31;
+    const int m0 = tm * TS, n0 = tn * TS;
+    const int rows_x = (M - m0) < TS ? (M - m0) : TS;
+    const int rows_y = (N - n0) < TS ? (N - n0) : TS;
+    const int nblk = (K + BK - 1) / BK;
+    const int kb0 = (int)((int64_t)wave * nblk / W);
+    const int nb = (int)((int64_t)(wave + 1) * nblk / W) - kb0;
+
+    f32x16 acc[MI][MI];
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int nj = 0; nj < MI; ++nj)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[mi][nj][r] = 0.0f;
+
+    // One block's operand fragments: [32-row block][16-byte chunk].
+    struct Block {
+        u32x4 x[MI][4], y[MI][4];
+    };
+    auto mul = [&](const Block& f) {
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int nj = 0; nj < MI; ++nj) {
+                f32x16 c = acc[mi][nj];
+                if constexpr (IN == IN_F8) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const i32x8 a = __builtin_shufflevector(
+                            __builtin_bit_cast(i32x4, f.x[mi][2 * q]),
+                            __builtin_bit_cast(i32x4, f.x[mi][2 * q + 1]), 0, 1, 2, 3, 4, 5, 6, 7);
+                        const i32x8 b = __builtin_shufflevector(
+                            __builtin_bit_cast(i32x4, f.y[nj][2 * q]),
+                            __builtin_bit_cast(i32x4, f.y[nj][2 * q + 1]), 0, 1, 2, 3, 4, 5, 6, 7);
+                        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+                    }
+                } else if constexpr (IN == IN_F8W) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int w = 0; w < 4; w += 2)
+                            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                widen_f8(f.x[mi][q][w], f.x[mi][q][w + 1]),
+                                widen_f8(f.y[nj][q][w], f.y[nj][q][w + 1]), c, 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if constexpr (IN == IN_BF16)
+                            c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                                __builtin_bit_cast(bf16x8, f.x[mi][h]),
+                                __builtin_bit_cast(bf16x8, f.y[nj][h]), c, 0, 0, 0);
+                        else
+                            c = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                                __builtin_bit_cast(f16x8, f.x[mi][h]),
+                                __builtin_bit_cast(f16x8, f.y[nj][h]), c, 0, 0, 0);
+                    }
+                }
+                acc[mi][nj] = c;
+            }
+    };
+
+    if constexpr (KC) {
+        Block blk[2 * D];
+        auto chunk = [&](int h) { return F8 ? 4 * (h >> 1) + 2 * g + (h & 1) : 2 * h + g; };
+        auto load = [&](int i, int s) {
+            const int k0 = (kb0 + i) * BK;
+            const int krem = (K - k0) < BK ? (K - k0) : BK;
+            const auto rx = make_rsrc(X + ((int64_t)m0 * ldx + k0) * ES,
+                                      ((int64_t)(rows_x - 1) * ldx + krem) * ES);
+            const auto ry = make_rsrc(Y + ((int64_t)n0 * ldy + k0) * ES,
+                                      ((int64_t)(rows_y - 1) * ldy + krem) * ES);
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    blk[s].x[mi][h] = load16(rx, (mi * 32 + li) * ldx * ES + 16 * chunk(h));
+                    blk[s].y[mi][h] = load16(ry, (mi * 32 + li) * ldy * ES + 16 * chunk(h));
+                }
+        };
+        run_steps<D>(nb, load, [&](int i, int s, auto) {
+            const int k0 = (kb0 + i) * BK;
+            if (k0 + BK > K) {  // the rows' padding: 0 * NaN would be a NaN, so both operands
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi) {
+                        const int valid = (K - k0) * ES - 16 * chunk(h);
+                        blk[s].x[mi][h] = mask_bytes(blk[s].x[mi][h], valid);
+                        blk[s].y[mi][h] = mask_bytes(blk[s].y[mi][h], valid);
+                    }
+            }
+            mul(blk[s]);
+        });
+    } else {
+        char* const mine = smem + wave * 2 * D * 2 * BLKB;
+        // Load j's 16 bytes of this lane: bytes 1024 j + 16 lane of the stage, k-row
+        // q / 2TS, byte q % 2TS of the row.
+        int vx[NDB], vy[NDB];
+#pragma unroll
+        for (int j = 0; j < NDB; ++j) {
+            const int q = 1024 * j + 16 * lane;
+            vx[j] = (q / (2 * TS)) * ldx * 2 + q % (2 * TS);
+            vy[j] = (q / (2 * TS)) * ldy * 2 + q % (2 * TS);
+        }
+        // The transpose read's slot: lane 16 G + 4 a + q reads k-row 8 (G / 2) + a,
+        // columns 16 (G & 1) + 4 q ...
+        const int grp = lane >> 4;
+        const int slot =
+            ((8 * (grp >> 1) + ((lane >> 2) & 3)) * TS + 16 * (grp & 1) + 4 * (lane & 3)) * 2;
+        auto load = [&](int i, int s) {
+            const int k0 = (kb0 + i) * BK;
+            const int krows = (K - k0) < BK ? (K - k0) : BK;
+            const auto rx = make_rsrc(X + ((int64_t)k0 * ldx + m0) * 2,
+                                      ((int64_t)(krows - 1) * ldx + rows_x) * 2);
+            const auto ry = make_rsrc(Y + ((int64_t)k0 * ldy + n0) * 2,
+                                      ((int64_t)(krows - 1) * ldy + rows_y) * 2);
+            char* st = mine + s * 2 * BLKB;
+#pragma unroll
+            for (int j = 0; j < NDB; ++j) dma16(rx, lds_addr(st + 1024 * j), vx[j]);
+#pragma unroll
+            for (int j = 0; j < NDB; ++j) dma16(ry, lds_addr(st + BLKB + 1024 * j), vy[j]);
+        };
+        run_steps<D>(nb, load, [&](int i, int s, auto newer) {
+            (void)i;
+            // This step's loads have landed; at most the newer steps' are in flight.
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(decltype(newer)::value * 2 * NDB, 15));
+            __builtin_amdgcn_sched_barrier(0);
+            const char* st = mine + s * 2 * BLKB + slot;
+            Block f;
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi) {
+                        const int at = ((16 * h + 4 * t) * TS + 32 * mi) * 2;
+                        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                        const u32x2 p = __builtin_bit_cast(
+                            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(st + at)));
+                        const u32x2 q = __builtin_bit_cast(
+                            u32x2,
+                            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(st + BLKB + at)));
+                        f.x[mi][h][2 * t] = p[0];
+                        f.x[mi][h][2 * t + 1] = p[1];
+                        f.y[mi][h][2 * t] = q[0];
+                        f.y[mi][h][2 * t + 1] = q[1];
+                    }
+            // The reads are done before the slot's next loads are issued.
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            __builtin_amdgcn_sched_barrier(0);
+            mul(f);
+        });
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        __syncthreads();  // every wave is done with its stages: the sums reuse them
+    }
+
+    // As in slicek16.hip: value idx = 16 b + r of every lane, wave w finishing
+    // idx in [w PER, w PER + PER).
+    float* const red = (float*)smem;
+    constexpr int PER = NB * 16 / W;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            red[(wave * NB * 16 + b * 16 + r) * 64 + lane] = acc[b / MI][b % MI][r];
+    __syncthreads();
+    float v[PER];
+    int row[PER], col[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int idx = wave * PER + q;
+        const int b = idx / 16, r = idx % 16;
+        v[q] = red[idx * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v[q] += red[(w * NB * 16 + idx) * 64 + lane];
+        row[q] = m0 + (b / MI) * 32 + 8 * (r >> 2) + 4 * g + (r & 3);
+        col[q] = n0 + (b % MI) * 32 + li;
+    }
+    finish_full<OUT, PER>(v, row, col, C, M, N, ldc, epi);
+}
+
+template <int IN, int LAY, int OUT, int MI, int W>
+hipError_t go(const GemmLaunch& L) {
+    const char* a = L.A;
+    const char* b = L.B;
+    char* c = L.C;
+    int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc;
+    int tiles_m = L.tiles_m, tiles_n = L.tiles_n;
+    EpiArgs e = L.e;
+    void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &tiles_n, &e};
+    return hipLaunchKernel((const void*)slicet_kernel<IN, LAY, OUT, MI, W>,
+                           dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * W), args, 0, L.stream);
+}
+
+template <int IN, int LAY, int OUT>
+hipError_t by_variant(const GemmLaunch& L) {
+    if (L.tbm == 32 && L.slice_waves == 4) return go<IN, LAY, OUT, 1, 4>(L);
+    if (L.tbm == 32 && L.slice_waves == 8) return go<IN, LAY, OUT, 1, 8>(L);
+    if (L.tbm == 64 && L.slice_waves == 4) return go<IN, LAY, OUT, 2, 4>(L);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_slicet(const GemmLaunch& L) {
+    if (L.splits != 1 || L.tbm != L.tbn || L.epi != EPI_FULL) return hipErrorInvalidValue;
+    if (L.layout == LAY_NT) {
+        if (L.in == IN_F8W && L.out == OUT_F32) return by_variant<IN_F8W, LAY_NT, OUT_F32>(L);
+        if (L.in == IN_F8 && L.out == OUT_BF16) return by_variant<IN_F8, LAY_NT, OUT_BF16>(L);
+        if (L.in == IN_F8 && L.out == OUT_F16) return by_variant<IN_F8, LAY_NT, OUT_F16>(L);
+        if (L.in == IN_BF16 && L.out == OUT_BF16) return by_variant<IN_BF16, LAY_NT, OUT_BF16>(L);
+        if (L.in == IN_F16 && L.out == OUT_F16) return by_variant<IN_F16, LAY_NT, OUT_F16>(L);
+    } else if (L.layout == LAY_TN) {
+        if (L.in == IN_BF16 && L.out == OUT_BF16) return by_variant<IN_BF16, LAY_TN, OUT_BF16>(L);
+        if (L.in == IN_F16 && L.out == OUT_F16) return by_variant<IN_F16, LAY_TN, OUT_F16>(L);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace dgemm

@@ -59,7 +59,7 @@ def run_act(fmt, out, M, N, K, act, seed=0, bias=True, residual=True, preact=Tru
 
 # Sizes: few rows (the register-streaming kernel), one slice-K tile and more,
 # odd everything, one column, and K of 1, below, at and above a step.
-SHAPES = [(1, 1, 1), (1, 33, 40), (1, 200, 515), (5, 130, 33), (16, 97, 257), (17, 70, 65), (33, 8, 130),
+SHAPES = [(1, 1, 1), (1, 33, 40), (1, 200, 515), (2, 40, 9000), (5, 130, 33), (16, 97, 257), (17, 70, 65), (33, 8, 130),
           (70, 129, 200), (130, 300, 72)]
 
 
@@ -95,7 +95,7 @@ def test_forward_grid_tiles(grid_plan, fmt, tile, splits):
 
 @pytest.mark.parametrize("cols", [32, 64, 128])
 @pytest.mark.parametrize("splits", [1, 3])
-@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "f32"])
 def test_forward_few_row_strips(grid_plan, cols, splits, fmt):
     grid_plan(16, cols, splits)
     ws = 0 if splits == 1 else 1 << 20
@@ -261,6 +261,16 @@ def test_backward_grid_tiles(grid_plan, tile, splits, fmt):
     run_bwd(fmt, "same", 520, 136, 390, "none", seed=9)
 
 
+@pytest.mark.parametrize("tile, waves", [(32, 4), (32, 8), (64, 4)])
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+def test_backward_slice_tiles(grid_plan, tile, waves, fmt):
+    """The slice-K tiles, runs of blocks from none to several per wave, K tails."""
+    grid_plan(tile, tile, waves)
+    for i, (M, N, K) in enumerate([(17, 40, 33), (70, 136, 90), (130, 72, 261), (1000, 65, 70), (40, 1100, 24)]):
+        run_bwd(fmt, "same", M, N, K, "silu", seed=40 + i)
+        run_bwd(fmt, "same", M, N, K, "none", seed=50 + i)
+
+
 @pytest.mark.parametrize("want", [("dA",), ("dB",), ("dbias",), ("dA", "dbias"), ("dB", "dbias"), ("dA", "dB")])
 def test_backward_parts(want):
     for act in ("none", "gelu"):
@@ -357,20 +367,30 @@ def test_f8_grid_tiles(grid_plan, tile, splits):
         run_f8(M, N, K, torch.float32, "none", seed=i, ws_bytes=4 << 20)
 
 
+@pytest.mark.parametrize("tile, waves", [(32, 4), (32, 8), (64, 4)])
+def test_f8_slice_tiles(grid_plan, tile, waves):
+    grid_plan(tile, tile, waves)
+    for i, (M, N, K) in enumerate([(17, 40, 100), (64, 31, 272), (70, 100, 1025), (130, 72, 2300)]):
+        for od in (torch.float32, torch.bfloat16, torch.float16):
+            run_f8(M, N, K, od, "silu", seed=i)
+
+
 def test_f8_every_value():
     """Every finite e4m3 code times 1 in each position of a 128-k step."""
     codes = torch.arange(256, dtype=torch.uint8)
     codes = codes[(codes & 0x7f) != 0x7f]
     v = codes.view(F8)
-    for M in (2, 40):  # the few-row kernel and a tile
+    for M in (2, 40, 1100):  # the few-row kernel, a slice-K tile, a grid tile
+        B_rows = len(v) if M < 1000 else 1024
         for k in (0, 31, 32, 63, 64, 100, 127, 128):
             A = torch.zeros(M, 129, dtype=F8)
             A[:, k] = torch.ones(M).to(F8)
-            B = torch.zeros(len(v), 129, dtype=F8)
-            B[:, k] = v
-            C = dg.matmul_f8(padded(A, F8), padded(B, F8), torch.ones(M).cuda(), torch.ones(len(v)).cuda(),
-                             out_dtype=torch.float32)
-            assert torch.equal(C.cpu(), v.float().expand(M, len(v)))
+            B = torch.zeros(B_rows, 129, dtype=F8)
+            B[:len(v), k] = v
+            for od in (torch.float32, torch.bfloat16):
+                C = dg.matmul_f8(padded(A, F8), padded(B, F8), torch.ones(M).cuda(),
+                                 torch.ones(B_rows).cuda(), out_dtype=od)
+                assert torch.equal(C[:, :len(v)].cpu().float(), v.float().expand(M, len(v)))
 
 
 def test_f8_row_scales_of_nan_fill_their_rows():

@@ -176,6 +176,9 @@ def test_plans():
         for act in dg.ACT_CODES:
             req, best = dg.gemm_act_bwd_workspace(fmt, 100, 200, 300, act)
             assert 0 < req <= best
+            # few rows: no transposes, no partial sums; nothing at all where dC serves as dZ
+            few, few_best = dg.gemm_act_bwd_workspace(fmt, 16, 200, 300, act, fmt[:3] != "f32")
+            assert few == few_best and (few == 0) == (act == "none")
     assert dg.rmsnorm_bwd_workspace(16384, 4096) >= 4096 * 4
     assert dg.rmsnorm_bwd_workspace(0, 64) == 0
     with pytest.raises(dg.DgemmError):
