@@ -45,14 +45,14 @@ __device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[
 }
 
 constexpr int AG_COLS = 512;     // columns per workgroup: 64 lanes x 8
-constexpr int AG_LANES = 4;      // rows at a time
 
-// One workgroup: columns blockIdx.x * 512 .., rows blockIdx.y * rows_per ...
-// Wave w takes every fourth row; the four waves' column sums are added in LDS in
-// wave order and go to the workspace, one row of partial sums per blockIdx.y.
-template <int CF, int DF>
-__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
-    __shared__ float sums[AG_LANES][AG_COLS];
+// One workgroup of W waves: columns blockIdx.x * 512 .., rows blockIdx.y *
+// rows_per ...  Wave w takes every W-th row; the waves' column sums are added in
+// LDS in wave order and go to the workspace, one row of partial sums per
+// blockIdx.y.  Sixteen waves where one workgroup takes all the rows.
+template <int CF, int DF, int W>
+__global__ __launch_bounds__(64 * W) void act_grad_kernel(ActGradArgs a) {
+    __shared__ float sums[W][AG_COLS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int c = (int)blockIdx.x * AG_COLS + lane * 8;
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (nvalid > 0) {
 #pragma unroll 2
-        for (int64_t row = r0 + wave; row < r1; row += AG_LANES) {
+        for (int64_t row = r0 + wave; row < r1; row += W) {
             Row8<CF> x, zz;
             const auto rc = make_rsrc(a.dC + row * a.lddc * fmt_es<CF>, (int64_t)a.N * fmt_es<CF>);
             x.load(rc, (uint32_t)c * fmt_es<CF>, nvalid);
@@ -91,11 +91,13 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = sum[j];
     __syncthreads();
-    for (int j = threadIdx.x; j < AG_COLS; j += 256) {
+    for (int j = threadIdx.x; j < AG_COLS; j += 64 * W) {
         const int col = (int)blockIdx.x * AG_COLS + j;
         if (col >= a.N) break;
-        a.part[(int64_t)blockIdx.y * a.ldp + col] =
-            ((sums[0][j] + sums[1][j]) + sums[2][j]) + sums[3][j];
+        float v = sums[0][j];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += sums[w][j];
+        a.part[(int64_t)blockIdx.y * a.ldp + col] = v;
     }
 }
 
@@ -103,10 +105,12 @@ template <int CF, int DF>
 hipError_t go_ag(const ActGradArgs& a, hipStream_t stream) {
     ActGradArgs b = a;
     void* args[] = {&b};
-    return hipLaunchKernel((const void*)act_grad_kernel<CF, DF>,
+    const bool one = a.M > 16 && a.M <= a.rows_per;
+    const void* fn = one ? (const void*)act_grad_kernel<CF, DF, 16> : (const void*)act_grad_kernel<CF, DF, 4>;
+    return hipLaunchKernel(fn,
                            dim3((unsigned)((a.N + AG_COLS - 1) / AG_COLS),
                                 (unsigned)((a.M + a.rows_per - 1) / a.rows_per)),
-                           dim3(256), args, 0, stream);
+                           dim3(one ? 1024 : 256), args, 0, stream);
 }
 
 // out[n] = sum over g < G of part[g][n], in a fixed order: 16 threads per column
@@ -137,24 +141,28 @@ __global__ __launch_bounds__(1024) void col_reduce_kernel(const float* part, int
     }
 }
 
-// Y[n][m] = X[m][n], fp32, in 64 x 64 tiles through LDS (rows padded to 65 words).
+// Y[n][m] = X[m][n], fp32, in 32 x 32 tiles through LDS (rows padded to 33 words):
+// small enough that the backward pass of a small layer still fills the CUs.
 __global__ __launch_bounds__(256) void transpose32_kernel(const float* X, int ldx, int M, int N,
                                                           float* Y, int ldy, int tiles_n) {
-    __shared__ float tile[64][65];
-    const int m0 = (int)(blockIdx.x / tiles_n) * 64, n0 = (int)(blockIdx.x % tiles_n) * 64;
-    const int c = threadIdx.x & 63, r = threadIdx.x >> 6;
-    for (int i = r; i < 64; i += 4)
-        if (m0 + i < M && n0 + c < N) tile[i][c] = X[(int64_t)(m0 + i) * ldx + n0 + c];
+    __shared__ float tile[32][33];
+    const int m0 = (int)(blockIdx.x / tiles_n) * 32, n0 = (int)(blockIdx.x % tiles_n) * 32;
+    const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        if (m0 + r + i < M && n0 + c < N) tile[r + i][c] = X[(int64_t)(m0 + r + i) * ldx + n0 + c];
     __syncthreads();
-    for (int i = r; i < 64; i += 4)
-        if (n0 + i < N && m0 + c < M) Y[(int64_t)(n0 + i) * ldy + m0 + c] = tile[c][i];
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        if (n0 + r + i < N && m0 + c < M) Y[(int64_t)(n0 + r + i) * ldy + m0 + c] = tile[c][r + i];
 }
 
 }  // namespace
 
 // Rows per workgroup of act_grad_kernel: at most 256 rows of partial sums, no
-// fewer than 8 rows each, and up to 64 rows in one chunk, whose sums need no
-// second launch (16 rows per wave take less than a launch).
+// fewer than 8 rows each, and up to 64 rows in one chunk, whose sums are dbias
+// without a second launch (4 rows for each of 16 waves; 16 rows each measured
+// 16-35 us where two launches take 10).
 int act_grad_rows(int M) {
     if (M <= 64) return 64;
     const int64_t r = ((int64_t)M + 255) / 256;
@@ -179,7 +187,7 @@ hipError_t launch_col_reduce(const float* part, int G, int ldp, int N, float* ou
 
 hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,
                               hipStream_t stream) {
-    const int64_t tm = (M + 63) / 64, tn = (N + 63) / 64;
+    const int64_t tm = ((int64_t)M + 31) / 32, tn = ((int64_t)N + 31) / 32;
     if (tm * tn > INT32_MAX) return hipErrorInvalidValue;
     int tiles_n = (int)tn;
     void* args[] = {&X, &ldx, &M, &N, &Y, &ldy, &tiles_n};

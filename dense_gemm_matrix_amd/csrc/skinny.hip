@@ -56,7 +56,8 @@ struct Strip {
     static constexpr int NV = CPL * 4;            // values per lane
     static constexpr int PER = (NV + W - 1) / W;  // of them, finished by one wave
     int row[PER], col[PER];
-    float res[PER], bias[PER], scale[PER];
+    // As loaded (a conversion or a product would wait for the loads here).
+    uint32_t res[PER], bias[PER], sa[PER], sb[PER];
 
     __device__ __forceinline__ void prefetch(int M, int N, int n0, int wave, int lane,
                                              const EpiArgs& e) {
@@ -66,13 +67,38 @@ struct Strip {
             row[q] = 4 * (lane >> 4) + idx % 4;
             col[q] = n0 + CPL * (lane & 15) + idx / 4;
             if (idx >= NV) row[q] = M;  // W larger than the values: none
-            if constexpr (EPI == EPI_FULL) {
-                const bool in = row[q] < M && col[q] < N;
-                res[q] = in && e.res ? load_c<OUT>(e.res, (int64_t)row[q] * e.ldr + col[q]) : 0.0f;
-                bias[q] = in && e.bias ? e.bias[col[q]] : 0.0f;
-                scale[q] = in && e.scale_a ? e.scale_a[row[q]] * e.scale_b[col[q]] : 1.0f;
+        }
+        if constexpr (EPI == EPI_FULL) {
+            constexpr int ES = fmt_es<OUT>;
+#pragma unroll
+            for (int q = 0; q < PER; ++q) res[q] = bias[q] = sa[q] = sb[q] = 0u;
+            if (wave * PER >= NV) return;
+            // Elements outside C: an offset outside the resource, which loads 0.
+            if (e.res) {
+                const auto r = c_rsrc((char*)e.res, M, N, e.ldr, 0, 0, ES);
+#pragma unroll
+                for (int q = 0; q < PER; ++q) {
+                    const int at = inside(q, M, N) ? (row[q] * e.ldr + col[q]) * ES : (int)OOB_LANE;
+                    if constexpr (OUT == OUT_F32) res[q] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+                    else res[q] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+                }
+            }
+            auto words = [&](const float* p, int n, auto index, uint32_t (&to)[PER]) {
+                const auto r = make_rsrc((const char*)p, (int64_t)n * 4);
+#pragma unroll
+                for (int q = 0; q < PER; ++q)
+                    to[q] = __builtin_amdgcn_raw_buffer_load_b32(
+                        r, inside(q, M, N) ? index(q) * 4 : (int)OOB_LANE, 0, 0);
+            };
+            if (e.bias) words(e.bias, N, [&](int q) { return col[q]; }, bias);
+            if (e.scale_a) {
+                words(e.scale_a, M, [&](int q) { return row[q]; }, sa);
+                words(e.scale_b, N, [&](int q) { return col[q]; }, sb);
             }
         }
+    }
+    __device__ __forceinline__ bool inside(int q, int M, int N) const {
+        return row[q] < M && col[q] < N;
     }
     // Adds the W waves' sums in wave order and stores: the full epilogue, or an
     // fp32 partial.
@@ -92,7 +118,8 @@ struct Strip {
 #pragma unroll
             for (int w = 1; w < W; ++w) v[q] += red[(w * NV + idx) * 64 + lane];
             if constexpr (EPI == EPI_FULL) {
-                v[q] = v[q] * scale[q] + bias[q];
+                if (e.scale_a) v[q] = v[q] * as_float(sa[q]) * as_float(sb[q]);
+                v[q] += as_float(bias[q]);
                 if (e.pre && row[q] < M && col[q] < N)
                     store_c<OUT>(e.pre, (int64_t)row[q] * e.ldz + col[q], v[q]);
             }
@@ -100,7 +127,11 @@ struct Strip {
         if constexpr (EPI == EPI_FULL) apply_act(v, e.act);
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
-            if constexpr (EPI == EPI_FULL) v[q] = e.res ? v[q] + res[q] : v[q];
+            if constexpr (EPI == EPI_FULL) {
+                if (e.res) v[q] += OUT == OUT_F32    ? as_float(res[q])
+                                   : OUT == OUT_BF16 ? as_float(res[q] << 16)
+                                   : (float)__builtin_bit_cast(_Float16, (unsigned short)res[q]);
+            }
             if (row[q] < M && col[q] < N) store_c<OUT>(C, (int64_t)row[q] * ldc + col[q], v[q]);
         }
     }
@@ -289,19 +320,27 @@ __global__ __launch_bounds__(256) void outer_kernel(const char* __restrict__ A,
     for (int j = 0; j < 8; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[j][i] = 0.0f;
-#pragma unroll 4
-    for (int m = 0; m < M; ++m) {
-        Row8<FMT> d, a;
-        d.load(make_rsrc(D + (int64_t)m * ldd * ES, (int64_t)N * ES), (uint32_t)c * ES, nvalid);
-        a.load(make_rsrc(A + (int64_t)m * lda * ES, (int64_t)K * ES), (uint32_t)k0 * ES, K - k0);
-        float x[8], y[8];
-        d.get(x);
-        a.get(y);
+    // Every row's loads in flight at once.  Pieces past a row's end hold other
+    // data or zeros and feed outputs that are not stored.
+    Row8<FMT> d[SKINNY_M], a[SKINNY_M];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+    for (int m = 0; m < SKINNY_M; ++m)
+        if (m < M) {
+            d[m].load_whole(make_rsrc(D + (int64_t)m * ldd * ES, (int64_t)N * ES),
+                            nvalid > 0 ? (uint32_t)c * ES : OOB_LANE);
+            a[m].load_whole(make_rsrc(A + (int64_t)m * lda * ES, (int64_t)K * ES), (uint32_t)k0 * ES);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[j][i] += y[j] * x[i];
-    }
+    for (int m = 0; m < SKINNY_M; ++m)
+        if (m < M) {
+            float x[8], y[8];
+            d[m].get(x);
+            a[m].get(y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[j][i] += y[j] * x[i];
+        }
     const __amdgpu_buffer_rsrc_t rc =
         make_rsrc(C + (int64_t)k0 * ldc * ES,
                   ((int64_t)((K - k0 < 8 ? K - k0 : 8) - 1) * ldc + N) * ES);

@@ -9,18 +9,22 @@
 // kernel: such a product is a few us, a split's second launch another three.
 //
 // No operand is shared between the waves, so each wave moves its own:
-//   NT: both operands K-contiguous: 16-byte loads straight into the registers the
-//     matrix instruction reads.  Per 16-k half h of a 16-bit block lane (g, li)
-//     takes chunk 2 h + g of row li; of an e4m3 block, per 64 k, chunks 4 q + 2 g
-//     and 4 q + 2 g + 1 (the order of k inside the instruction cancels).
-//   TN: both along the output: 64 k-rows x TS columns of each go into the wave's
-//     own LDS region as they lie in memory (direct-to-LDS loads) and come back
-//     through the transpose read (slicek16.hip's B).
+//   NT: both operands K-contiguous: TS rows x 128 bytes of each go into the wave's
+//     own LDS region by direct-to-LDS loads, eight lanes to a row's line (loading
+//     the matrix instruction's operands straight from memory touches 32 lines per
+//     instruction: 299 x 2164 with 2517 terms took 24.9 us that way, 17.0 this), in
+//     gemm16's swizzled layout, and are read with ds_read_b128.  Per 16-k half h of a 16-bit
+//     block lane (g, li) takes chunk 2 h + g of row li; of an e4m3 block, per 64 k,
+//     chunks 4 q + 2 g and 4 q + 2 g + 1 (the order of k inside the instruction
+//     cancels).
+//   TN: both along the output: 64 k-rows x TS columns of each as they lie in
+//     memory, read back through the transpose read (slicek16.hip's B).
 // D to 2 D blocks are in flight per wave.
 
 #include <type_traits>
 
 #include "kern_common.h"
+#include "stage16.h"
 
 namespace dgemm {
 namespace {
@@ -41,11 +45,10 @@ __global__ __launch_bounds__(64 * W) void slicet_kernel(
     constexpr int BK = 128 / ES;
     constexpr int TS = 32 * MI;
     constexpr int NB = MI * MI;
-    // Blocks per chunk, two chunks in flight: registers (NT) or LDS (TN).
-    constexpr int D = MI == 1 && (KC || W == 4) ? 2 : 1;
+    constexpr int D = MI == 1 && W == 4 ? 2 : 1;  // blocks per chunk, two chunks in LDS
     constexpr int BLKB = 128 * TS;            // bytes of one operand's block
     constexpr int NDB = BLKB / 1024;          // its direct-to-LDS loads
-    constexpr int STAGES = KC ? 0 : W * 2 * D * 2 * BLKB;
+    constexpr int STAGES = W * 2 * D * 2 * BLKB;
     constexpr int RED = W * NB * 16 * 64 * 4;
     __shared__ __attribute__((aligned(1024))) char smem[cmax(STAGES, RED)];
     int tm, tn;
@@ -114,101 +117,93 @@ __global__ __launch_bounds__(64 * W) void slicet_kernel(
             }
     };
 
-    if constexpr (KC) {
-        Block blk[2 * D];
-        auto chunk = [&](int h) { return F8 ? 4 * (h >> 1) + 2 * g + (h & 1) : 2 * h + g; };
-        auto load = [&](int i, int s) {
-            const int k0 = (kb0 + i) * BK;
-            const int krem = (K - k0) < BK ? (K - k0) : BK;
-            const auto rx = make_rsrc(X + ((int64_t)m0 * ldx + k0) * ES,
-                                      ((int64_t)(rows_x - 1) * ldx + krem) * ES);
-            const auto ry = make_rsrc(Y + ((int64_t)n0 * ldy + k0) * ES,
-                                      ((int64_t)(rows_y - 1) * ldy + krem) * ES);
+    char* const mine = smem + wave * 2 * D * 2 * BLKB;
+    // Load j's 16 bytes of this lane belong at bytes 1024 j + 16 lane of the stage.
+    int vx[NDB], vy[NDB];
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) {
-                    blk[s].x[mi][h] = load16(rx, (mi * 32 + li) * ldx * ES + 16 * chunk(h));
-                    blk[s].y[mi][h] = load16(ry, (mi * 32 + li) * ldy * ES + 16 * chunk(h));
-                }
-        };
-        run_steps<D>(nb, load, [&](int i, int s, auto) {
-            const int k0 = (kb0 + i) * BK;
-            if (k0 + BK > K) {  // the rows' padding: 0 * NaN would be a NaN, so both operands
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int mi = 0; mi < MI; ++mi) {
-                        const int valid = (K - k0) * ES - 16 * chunk(h);
-                        blk[s].x[mi][h] = mask_bytes(blk[s].x[mi][h], valid);
-                        blk[s].y[mi][h] = mask_bytes(blk[s].y[mi][h], valid);
-                    }
-            }
-            mul(blk[s]);
-        });
-    } else {
-        char* const mine = smem + wave * 2 * D * 2 * BLKB;
-        // Load j's 16 bytes of this lane: bytes 1024 j + 16 lane of the stage, k-row
-        // q / 2TS, byte q % 2TS of the row.
-        int vx[NDB], vy[NDB];
-#pragma unroll
-        for (int j = 0; j < NDB; ++j) {
-            const int q = 1024 * j + 16 * lane;
+    for (int j = 0; j < NDB; ++j) {
+        if constexpr (KC) {
+            const int row = A16_RPB * j + lane / A16_CH;
+            const int c = (lane % A16_CH) ^ a16_phi(row);
+            vx[j] = row * ldx * ES + 16 * c;
+            vy[j] = row * ldy * ES + 16 * c;
+        } else {
+            const int q = 1024 * j + 16 * lane;  // k-row q / 2TS, byte q % 2TS of the row
             vx[j] = (q / (2 * TS)) * ldx * 2 + q % (2 * TS);
             vy[j] = (q / (2 * TS)) * ldy * 2 + q % (2 * TS);
         }
-        // The transpose read's slot: lane 16 G + 4 a + q reads k-row 8 (G / 2) + a,
-        // columns 16 (G & 1) + 4 q ...
-        const int grp = lane >> 4;
-        const int slot =
-            ((8 * (grp >> 1) + ((lane >> 2) & 3)) * TS + 16 * (grp & 1) + 4 * (lane & 3)) * 2;
-        auto load = [&](int i, int s) {
-            const int k0 = (kb0 + i) * BK;
-            const int krows = (K - k0) < BK ? (K - k0) : BK;
-            const auto rx = make_rsrc(X + ((int64_t)k0 * ldx + m0) * 2,
-                                      ((int64_t)(krows - 1) * ldx + rows_x) * 2);
-            const auto ry = make_rsrc(Y + ((int64_t)k0 * ldy + n0) * 2,
-                                      ((int64_t)(krows - 1) * ldy + rows_y) * 2);
-            char* st = mine + s * 2 * BLKB;
+    }
+    // The transpose read's slot: lane 16 G + 4 a + q reads k-row 8 (G / 2) + a,
+    // columns 16 (G & 1) + 4 q ...
+    const int grp = lane >> 4;
+    const int slot = ((8 * (grp >> 1) + ((lane >> 2) & 3)) * TS + 16 * (grp & 1) + 4 * (lane & 3)) * 2;
+    auto chunk = [&](int h) { return F8 ? 4 * (h >> 1) + 2 * g + (h & 1) : 2 * h + g; };
+    auto operand = [&](const char* p, int ld, int o0, int rows, int k0) {
+        const int krem = (K - k0) < BK ? (K - k0) : BK;
+        if constexpr (KC)
+            return make_rsrc(p + ((int64_t)o0 * ld + k0) * ES, ((int64_t)(rows - 1) * ld + krem) * ES);
+        else
+            return make_rsrc(p + ((int64_t)k0 * ld + o0) * 2, ((int64_t)(krem - 1) * ld + rows) * 2);
+    };
+    auto load = [&](int i, int s) {
+        const int k0 = (kb0 + i) * BK;
+        const auto rx = operand(X, ldx, m0, rows_x, k0);
+        const auto ry = operand(Y, ldy, n0, rows_y, k0);
+        char* st = mine + s * 2 * BLKB;
 #pragma unroll
-            for (int j = 0; j < NDB; ++j) dma16(rx, lds_addr(st + 1024 * j), vx[j]);
+        for (int j = 0; j < NDB; ++j) dma16(rx, lds_addr(st + 1024 * j), vx[j]);
 #pragma unroll
-            for (int j = 0; j < NDB; ++j) dma16(ry, lds_addr(st + BLKB + 1024 * j), vy[j]);
-        };
-        run_steps<D>(nb, load, [&](int i, int s, auto newer) {
-            (void)i;
-            // This step's loads have landed; at most the newer steps' are in flight.
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_waitcnt(waitcnt_imm(decltype(newer)::value * 2 * NDB, 15));
-            __builtin_amdgcn_sched_barrier(0);
-            const char* st = mine + s * 2 * BLKB + slot;
-            Block f;
+        for (int j = 0; j < NDB; ++j) dma16(ry, lds_addr(st + BLKB + 1024 * j), vy[j]);
+    };
+    run_steps<D>(nb, load, [&](int i, int s, auto newer) {
+        // This step's loads have landed; at most the newer steps' are in flight.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(decltype(newer)::value * 2 * NDB, 15));
+        __builtin_amdgcn_sched_barrier(0);
+        const char* st = mine + s * 2 * BLKB;
+        Block f;
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+        for (int h = 0; h < 4; ++h)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+            for (int mi = 0; mi < MI; ++mi) {
+                if constexpr (KC) {
+                    const int at = a16_off(mi * 32 + li, chunk(h));
+                    f.x[mi][h] = *(const u32x4*)(st + at);
+                    f.y[mi][h] = *(const u32x4*)(st + BLKB + at);
+                } else {
 #pragma unroll
-                    for (int mi = 0; mi < MI; ++mi) {
-                        const int at = ((16 * h + 4 * t) * TS + 32 * mi) * 2;
+                    for (int t = 0; t < 2; ++t) {
+                        const char* at = st + slot + ((16 * h + 4 * t) * TS + 32 * mi) * 2;
                         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
                         const u32x2 p = __builtin_bit_cast(
-                            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(st + at)));
+                            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)at));
                         const u32x2 q = __builtin_bit_cast(
-                            u32x2,
-                            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(st + BLKB + at)));
+                            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(at + BLKB)));
                         f.x[mi][h][2 * t] = p[0];
                         f.x[mi][h][2 * t + 1] = p[1];
                         f.y[mi][h][2 * t] = q[0];
                         f.y[mi][h][2 * t + 1] = q[1];
                     }
-            // The reads are done before the slot's next loads are issued.
-            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-            __builtin_amdgcn_sched_barrier(0);
-            mul(f);
-        });
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-        __syncthreads();  // every wave is done with its stages: the sums reuse them
-    }
+                }
+            }
+        // The reads are done before the slot's next loads are issued.
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        __builtin_amdgcn_sched_barrier(0);
+        const int k0 = (kb0 + i) * BK;
+        if (KC && k0 + BK > K) {  // the rows' padding: 0 * NaN would be a NaN, so both operands
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    const int valid = (K - k0) * ES - 16 * chunk(h);
+                    f.x[mi][h] = mask_bytes(f.x[mi][h], valid);
+                    f.y[mi][h] = mask_bytes(f.y[mi][h], valid);
+                }
+        }
+        mul(f);
+    });
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __syncthreads();  // every wave is done with its stages: the sums reuse them
 
     // As in slicek16.hip: value idx = 16 b + r of every lane, wave w finishing
     // idx in [w PER, w PER + PER).

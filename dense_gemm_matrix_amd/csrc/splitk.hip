@@ -15,6 +15,43 @@ namespace {
 
 constexpr int RED_THREADS = 256;
 
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+
+// Four consecutive elements, an aligned 16- or 8-byte piece.
+template <int OUT>
+__device__ __forceinline__ void store4(char* p, int64_t idx, const float (&v)[4]) {
+    if constexpr (OUT == OUT_F32) {
+        *(f32x4*)(p + idx * 4) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+        u16x4 h;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (OUT == OUT_BF16)
+                h[j] = __builtin_bit_cast(unsigned short, (__bf16)v[j]);
+            else
+                h[j] = __builtin_bit_cast(unsigned short, (_Float16)v[j]);
+        }
+        *(u16x4*)(p + idx * 2) = h;
+    }
+}
+
+template <int OUT>
+__device__ __forceinline__ void load4(const char* p, int64_t idx, float (&v)[4]) {
+    if constexpr (OUT == OUT_F32) {
+        const f32x4 x = *(const f32x4*)(p + idx * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = x[j];
+    } else {
+        const u16x4 x = *(const u16x4*)(p + idx * 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned short h = x[j];
+            if constexpr (OUT == OUT_BF16) v[j] = as_float((uint32_t)h << 16);
+            else v[j] = (float)__builtin_bit_cast(_Float16, h);
+        }
+    }
+}
+
 template <int OUT, int EPI>
 __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
     const float* __restrict__ W, int splits, int64_t zstride, int ldw, char* __restrict__ C,
@@ -28,13 +65,33 @@ __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
 
     const float* p = W + (int64_t)row * ldw + col0;
     f32x4 s = *(const f32x4*)p;
+    // In ascending z, four partials' loads in flight.
+#pragma unroll 4
     for (int z = 1; z < splits; ++z) s += *(const f32x4*)(p + z * zstride);
 
     if constexpr (EPI == EPI_FULL) {
         float f[4] = {s[0], s[1], s[2], s[3]};
-        const int rows[4] = {row, row, row, row};
-        const int cols[4] = {col0, col0 + 1, col0 + 2, col0 + 3};
-        finish_full<OUT, 4>(f, rows, cols, C, M, N, ldc, e);
+        if (col0 + 4 <= N) {
+            // Four columns of one row, 8- or 16-byte aligned in R, Z and C.
+            float res[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (e.res) load4<OUT>(e.res, (int64_t)row * e.ldr + col0, res);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (e.scale_a) f[j] = f[j] * e.scale_a[row] * e.scale_b[col0 + j];
+                if (e.bias) f[j] += e.bias[col0 + j];
+            }
+            if (e.pre) store4<OUT>(e.pre, (int64_t)row * e.ldz + col0, f);
+            apply_act(f, e.act);
+            if (e.res) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] += res[j];
+            }
+            store4<OUT>(C, (int64_t)row * ldc + col0, f);
+        } else {
+            const int rows[4] = {row, row, row, row};
+            const int cols[4] = {col0, col0 + 1, col0 + 2, col0 + 3};
+            finish_full<OUT, 4>(f, rows, cols, C, M, N, ldc, e);
+        }
         return;
     }
     const int64_t base = (int64_t)row * ldc + col0;
@@ -52,20 +109,7 @@ __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
     if (col0 + 4 <= N) {
         // C's base and row pitch are 16-byte aligned and col0 is a multiple
         // of 4, so the four outputs form one aligned 16- or 8-byte piece.
-        if constexpr (OUT == OUT_F32) {
-            *(f32x4*)(C + base * 4) = f32x4{v[0], v[1], v[2], v[3]};
-        } else {
-            typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
-            u16x4 h;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if constexpr (OUT == OUT_BF16)
-                    h[j] = __builtin_bit_cast(unsigned short, (__bf16)v[j]);
-                else
-                    h[j] = __builtin_bit_cast(unsigned short, (_Float16)v[j]);
-            }
-            *(u16x4*)(C + base * 2) = h;
-        }
+        store4<OUT>(C, base, v);
     } else {
         for (int j = 0; j < 4; ++j)
             if (col0 + j < N) store_c<OUT>(C, base + j, v[j]);
