@@ -62,15 +62,16 @@ struct TileT {
     static constexpr int LOADS = A_DMA + B_DMA;
     static constexpr int RPF = (F8 || !KC) ? 2 : 1;      // LDS reads per 32-row fragment
     static constexpr int NREAD = RPF * (MI + NJ);        // LDS reads per k group
-    static constexpr int NMFMA = MI * NJ;
+    // Matrix instructions per k group: IN_F8W takes a 64-k group in four 16-k slices.
+    static constexpr int SL = IN == IN_F8W ? 4 : 1;
+    static constexpr int NMFMA = MI * NJ * SL;
     static constexpr int LDS = S * (A_STAGE + B_STAGE);
     // The step's schedule (mainloop_t), in slots of one matrix instruction.
-#ifndef VBAR
-#define VBAR 16
-#define VLEND 32
-#endif
-    static constexpr int BAR = IN == IN_F8 && TBM == 256 ? VBAR : KP * NMFMA / 2;
-    static constexpr int LEND = IN == IN_F8 && TBM == 256 ? VLEND : KP * NMFMA;
+    // Half a step each for the reads and the refill: issuing the refill earlier or
+    // in a shorter burst was never faster (8-bit 4096^3: 61 us with the loads spread
+    // over slots 16-31, 61.1-61.6 over 12-27 and 8-23, 63-65 in bursts of 8).
+    static constexpr int BAR = KP * NMFMA / 2;
+    static constexpr int LEND = KP * NMFMA;
     static_assert(!F8 || KC, "8-bit operands are K-contiguous");
     static_assert(LDS <= 160 * 1024 && (S - 1) * LOADS <= 63, "LDS budget, vmcnt range");
 };
@@ -201,30 +202,34 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
             read_frag(smB + (kt % S) * T::B_STAGE, TBN, wn * (TBN / 2) + nj * 32, kp, h, fb[kp][nj]);
         }
     };
-    // IN_F8W: the k group's fragments as bf16, four matrix instructions' worth each.
+    // IN_F8W: the fragments of a 16-k slice as bf16.  While a slice's matrix
+    // instructions run, the next slice's fragments are widened, a piece after each,
+    // into the other half of the buffer (all at once before the group, the
+    // conversions took half as long again as the matrix instructions).
     constexpr bool WIDE = IN == IN_F8W;
-    bf16x8 wa[WIDE ? MI : 1][4], wb[WIDE ? NJ : 1][4];
-    auto widen = [&](int kp) {
-#pragma unroll
-        for (int f = 0; f < MI + NJ; ++f)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const u32x4& w = f < MI ? fa[kp][f].w[q >> 1] : fb[kp][f - MI].w[q >> 1];
-                const bf16x8 v = widen_f8(w[2 * (q & 1)], w[2 * (q & 1) + 1]);
-                if (f < MI) wa[f][q] = v;
-                else wb[f - MI][q] = v;
-            }
+    constexpr int NP = MI + NJ;  // fragments per slice
+    bf16x8 wide[WIDE ? 2 : 1][WIDE ? NP : 1];
+    auto widen = [&](int kp, int q, int f) {
+        const u32x4& w = f < MI ? fa[kp][f].w[q >> 1] : fb[kp][f - MI].w[q >> 1];
+        wide[q & 1][f] = widen_f8(w[2 * (q & 1)], w[2 * (q & 1) + 1]);
     };
     auto snake = [](int i) { return ((i / NJ) & 1) ? NJ - 1 - i % NJ : i % NJ; };
-    auto mfma_one = [&](int kp, int i) {
+    auto mfma_one = [&](int kp, int n) {
+        constexpr int PER = MI * NJ;
+        const int q = n / PER, i = n % PER;  // slice (0 but for IN_F8W), block
         const int mi = i / NJ, nj = snake(i);
         const Frag<F8>&a = fa[kp][mi], &b = fb[kp][nj];
         if constexpr (WIDE) {
-            if (i == 0) widen(kp);
+            if (n == 0) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                acc[mi][nj] =
-                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(wa[mi][q], wb[nj][q], acc[mi][nj], 0, 0, 0);
+                for (int f = 0; f < NP; ++f) widen(kp, 0, f);
+            }
+            acc[mi][nj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wide[q & 1][mi], wide[q & 1][MI + nj],
+                                                                  acc[mi][nj], 0, 0, 0);
+            if (q < 3) {
+#pragma unroll
+                for (int f = (i * NP) / PER; f < ((i + 1) * NP) / PER; ++f) widen(kp, q + 1, f);
+            }
         } else if constexpr (F8) {
             const i32x8 av = __builtin_shufflevector(__builtin_bit_cast(i32x4, a.w[0]),
                                                      __builtin_bit_cast(i32x4, a.w[1]), 0, 1, 2, 3, 4,

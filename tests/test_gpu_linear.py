@@ -134,6 +134,28 @@ def test_residual_in_place_and_column_window():
         assert bool((wide[:, :16] == 7).all()) and bool((wide[:, 16 + N:] == 7).all())
 
 
+@pytest.mark.parametrize("tile, splits", [((256, 256), 1), ((128, 128), 1), ((128, 128), 3), ((64, 64), 4),
+                                          ((32, 32), 8)])
+def test_residual_in_place_in_every_plan(grid_plan, tile, splits):
+    """C := act(..) + C where the residual is C itself, in the 16-bit and 8-bit products."""
+    grid_plan(*tile, splits)
+    M, N, K = 290, 270, 200
+    A, B, b, R = inputs(M, N, K, torch.bfloat16, 15)
+    pad = lambda x: padded(x, torch.bfloat16)  # noqa: E731
+    Rd = pad(R)
+    ws = torch.empty(4 << 20, dtype=torch.uint8, device="cuda")
+    want, C = sentinel(M, N, torch.bfloat16), pad(R)
+    dg.gemm_act(pad(A), pad(B), want, bias=b.cuda(), act="silu", residual=Rd, workspace=ws)
+    dg.gemm_act(pad(A), pad(B), C, bias=b.cuda(), act="silu", residual=C, workspace=ws)
+    assert torch.equal(C, want)
+    A8, B8, sa, sb, _, _ = f8_inputs(M, N, K, 16)
+    A8, B8, sa, sb = padded(A8, F8), padded(B8, F8), sa.cuda(), sb.cuda()
+    want, C = sentinel(M, N, torch.bfloat16), pad(R)
+    dg.gemm_f8(A8, B8, want, sa, sb, act="gelu", residual=Rd, workspace=ws)
+    dg.gemm_f8(A8, B8, C, sa, sb, act="gelu", residual=C, workspace=ws)
+    assert torch.equal(C, want)
+
+
 def test_empty_sums_and_sizes():
     b = torch.randn(40, generator=gen(1))
     for M in (1, 20, 300):
@@ -309,8 +331,11 @@ def test_backward_empty_sums():
     z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     dA, dB, db = dg.linear_backward(z(0, 8), z(8, 16), z(0, 16), bias=True)
     assert dA.shape == (0, 8) and bool((dB == 0).all()) and bool((db == 0).all())
-    dA, dB, _ = dg.linear_backward(z(4, 8), z(8, 0), z(4, 0))
-    assert bool((dA == 0).all()) and dB.shape == (8, 0)
+    for M in (4, 40, 300):
+        dA, dB, _ = dg.linear_backward(z(M, 8), z(8, 0), z(M, 0))
+        assert bool((dA == 0).all()) and dB.shape == (8, 0)
+        dA, dB, db = dg.linear_backward(z(M, 0), z(0, 16), z(M, 16) + 1, bias=True)
+        assert dA.shape == (M, 0) and dB.shape == (0, 16) and bool((db == M).all())
 
 
 # ---------------------------------------------------------------- 8-bit product
