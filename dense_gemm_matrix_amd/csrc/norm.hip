@@ -8,10 +8,12 @@
 // per lane and piece) between the sum of squares, the row maximum and the
 // stores, and written once.
 //
-// A row of up to 1024 columns belongs to one wave (four rows per workgroup, no
-// barrier), longer ones to a workgroup of 256 or 1024 threads, so that a lane
-// holds at most 32 columns (64 columns in registers spill at 1024 threads, so
-// longer rows are refused).
+// A row of up to 1024 columns belongs to one wave (no barrier), several rows of up
+// to 256 columns (the norms of attention heads) to one wave, 16 or 32 lanes each:
+// with a wave per row, 64 columns leave 56 lanes idle (16-bit 64 Mi values: 361 us,
+// 118 with 16 lanes).  Longer rows belong to a workgroup of 256 or 1024 threads,
+// so that a lane holds at most 32 columns (64 columns in registers spill at 1024
+// threads, so longer rows are refused).
 
 #include <type_traits>
 
@@ -23,27 +25,14 @@ namespace {
 constexpr float F8_MAX = 448.0f;                       // largest e4m3 value
 constexpr float SCALE_MIN = 7.888609052210118e-31f;    // 2^-100: a row of zeros divides by it
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    return v;
-}
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, m);
-        v = o > v ? o : v;
-    }
-    return v;
-}
-
-// Reductions over the T threads that share a row (T = 64: one wave; else the
-// whole workgroup, in wave order, so every thread gets the same bits).  `red`
-// holds T / 64 words and is not shared with another reduction of the row.
+// Reductions over the T threads that share a row (T <= 64: lanes of one wave;
+// else the whole workgroup, in wave order), every thread getting the same bits.
+// `red` holds T / 64 words and is not shared with another reduction of the row.
 template <int T>
 __device__ __forceinline__ float row_sum(float v, float* red) {
-    v = wave_sum(v);
-    if constexpr (T == 64) return v;
+#pragma unroll
+    for (int m = (T < 64 ? T : 64) / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    if constexpr (T <= 64) return v;
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
     float s = red[0];
@@ -53,8 +42,12 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 }
 template <int T>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
-    v = wave_max(v);
-    if constexpr (T == 64) return v;
+#pragma unroll
+    for (int m = (T < 64 ? T : 64) / 2; m > 0; m >>= 1) {
+        const uint32_t o = (uint32_t)__shfl_xor((int)v, m);
+        v = o > v ? o : v;
+    }
+    if constexpr (T <= 64) return v;
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
     uint32_t s = red[0];
@@ -117,41 +110,59 @@ __device__ __forceinline__ void store_f8(__amdgpu_buffer_rsrc_t r, uint32_t off,
     }
 }
 
-template <int FMT>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* p, int64_t row, int ld, int N) {
-    return make_rsrc((const char*)p + row * ld * fmt_es<FMT>, (int64_t)N * fmt_es<FMT>);
-}
+// Where a lane works: the rows of its wave start at `row0` (wave-uniform, so that
+// the rows' resources live in scalar registers), its own is row0 + lr.  Fewer than
+// 64 threads per row put 64 / T rows into a wave.
+template <int T>
+struct Place {
+    static constexpr int WG = T < 256 ? 256 : T;
+    static constexpr int RPWAVE = T < 64 ? 64 / T : 1;
+    static constexpr int RPW = WG / T;  // rows per workgroup
+    int t, lr;
+
+    __device__ __forceinline__ Place() : t(threadIdx.x % T), lr(T < 64 ? (threadIdx.x & 63) / T : 0) {}
+    // The first row of this wave among the workgroup's.
+    __device__ __forceinline__ static int first() {
+        return RPW > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * RPWAVE : 0;
+    }
+    // A resource over the wave's rows of a matrix of es-byte elements.
+    __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rows(const void* p, int64_t row0, int M,
+                                                                  int N, int ld, int es) {
+        const int64_t n = M - row0 < RPWAVE ? M - row0 : RPWAVE;
+        return make_rsrc((const char*)p + row0 * ld * es, ((n - 1) * ld + N) * es);
+    }
+    // Byte offset of column c of this lane's row in it.
+    __device__ __forceinline__ uint32_t at(int64_t row0, int M, int N, int c, int ld, int es) const {
+        if constexpr (RPWAVE == 1) return (uint32_t)(c * es);  // past N: outside the resource
+        return row0 + lr < M && c < N ? (uint32_t)((lr * ld + c) * es) : OOB_LANE;
+    }
+};
 
 // FMT: format of X, R, S and (MODE NORM) Y.
 enum RowMode { NORM = 0, NORM_F8 = 1, QUANT = 2 };
 
 template <int FMT, int MODE, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
-    constexpr int WG = T < 256 ? 256 : T;
-    constexpr int RPW = WG / T;  // rows per workgroup
-    __shared__ float red_s[WG / 64];
-    __shared__ uint32_t red_m[WG / 64];
-    // wave-uniform, so that the rows' resources live in scalar registers
-    const int sub = RPW > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
-    const int64_t row = (int64_t)blockIdx.x * RPW + sub;
-    if (row >= a.M) return;  // T == 64 only: no barrier follows
-    const int t = threadIdx.x % T;
+    constexpr int ES = fmt_es<FMT>;
+    using P = Place<T>;
+    __shared__ float red_s[P::WG / 64];
+    __shared__ uint32_t red_m[P::WG / 64];
+    const P pl;
+    const int64_t row0 = (int64_t)blockIdx.x * P::RPW + P::first();
+    if (row0 >= a.M) return;  // T <= 64 only: no barrier follows
+    const int64_t row = row0 + pl.lr;
+    auto col = [&](int i) { return (i * T + pl.t) * 8; };
+    auto at = [&](int i, int ld, int es) { return pl.at(row0, a.M, a.N, col(i), ld, es); };
     float v[NV][8];
     Row8<FMT> x[NV], r[NV];
-    const auto rx = row_rsrc<FMT>(a.X, row, a.ldx, a.N);
+    const auto rx = P::rows(a.X, row0, a.M, a.N, a.ldx, ES);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * T + t) * 8;
-        x[i].load(rx, (uint32_t)c * fmt_es<FMT>, a.N - c);
-    }
+    for (int i = 0; i < NV; ++i) x[i].load(rx, at(i, a.ldx, ES), a.N - col(i));
     const bool res = MODE != QUANT && a.R;
     if (res) {
-        const auto rr = row_rsrc<FMT>(a.R, row, a.ldr, a.N);
+        const auto rr = P::rows(a.R, row0, a.M, a.N, a.ldr, ES);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * T + t) * 8;
-            r[i].load(rr, (uint32_t)c * fmt_es<FMT>, a.N - c);
-        }
+        for (int i = 0; i < NV; ++i) r[i].load(rr, at(i, a.ldr, ES), a.N - col(i));
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -165,13 +176,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
     }
     if constexpr (MODE != QUANT) {
         if (a.S) {
-            const auto rs = row_rsrc<FMT>(a.S, row, a.lds, a.N);
+            const auto rs = P::rows(a.S, row0, a.M, a.N, a.lds, ES);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = (i * T + t) * 8;
                 Row8<FMT> o;
                 o.set(v[i]);
-                o.store(rs, (uint32_t)c * fmt_es<FMT>, a.N - c);
+                o.store(rs, at(i, a.lds, ES), a.N - col(i));
             }
         }
         float ss = 0.0f;
@@ -181,13 +191,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
             for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
         ss = row_sum<T>(ss, red_s);
         const float rstd = rsqrtf(ss / (float)a.N + a.eps);
-        if (a.rstd && t == 0) a.rstd[row] = rstd;
+        if (a.rstd && pl.t == 0 && row < a.M) a.rstd[row] = rstd;
         const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * T + t) * 8;
             Row8<OUT_F32> w8;
-            w8.load(rw, (uint32_t)c * 4, a.N - c);
+            w8.load(rw, (uint32_t)col(i) * 4, a.N - col(i));
             float w[8];
             w8.get(w);
 #pragma unroll
@@ -195,13 +204,12 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
         }
     }
     if constexpr (MODE == NORM) {
-        const auto ry = row_rsrc<FMT>(a.Y, row, a.ldy, a.N);
+        const auto ry = P::rows(a.Y, row0, a.M, a.N, a.ldy, ES);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * T + t) * 8;
             Row8<FMT> o;
             o.set(v[i]);
-            o.store(ry, (uint32_t)c * fmt_es<FMT>, a.N - c);
+            o.store(ry, at(i, a.ldy, ES), a.N - col(i));
         }
     } else {
         uint32_t m = 0;
@@ -209,33 +217,33 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t b = (i * T + t) * 8 + j < a.N ? mag_bits(v[i][j]) : 0u;
+                const uint32_t b = col(i) + j < a.N ? mag_bits(v[i][j]) : 0u;
                 m = b > m ? b : m;
             }
         m = row_max<T>(m, red_m);
         const float scale = f8_scale(m), inv = 1.0f / scale;
-        if (t == 0) a.scale[row] = scale;
-        const auto ry = make_rsrc((const char*)a.Y + row * a.ldy, a.N);
+        if (pl.t == 0 && row < a.M) a.scale[row] = scale;
+        const auto ry = P::rows(a.Y, row0, a.M, a.N, a.ldy, 1);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * T + t) * 8;
-            if (c < a.N) store_f8(ry, (uint32_t)c, a.N - c, v[i], scale, inv);
-        }
+        for (int i = 0; i < NV; ++i)
+            if (col(i) < a.N) store_f8(ry, at(i, a.ldy, 1), a.N - col(i), v[i], scale, inv);
     }
 }
 
 template <int FMT, int MODE, int T, int NV>
 hipError_t go_row(const RowArgs& a, hipStream_t stream) {
-    constexpr int WG = T < 256 ? 256 : T;
-    const int64_t blocks = ((int64_t)a.M + WG / T - 1) / (WG / T);
+    using P = Place<T>;
+    const int64_t blocks = ((int64_t)a.M + P::RPW - 1) / P::RPW;
     RowArgs b = a;
     void* args[] = {&b};
-    return hipLaunchKernel((const void*)row_kernel<FMT, MODE, T, NV>, dim3((unsigned)blocks), dim3(WG),
+    return hipLaunchKernel((const void*)row_kernel<FMT, MODE, T, NV>, dim3((unsigned)blocks), dim3(P::WG),
                            args, 0, stream);
 }
 
 template <int FMT, int MODE>
 hipError_t row_by_size(const RowArgs& a, hipStream_t s) {
+    if (a.N <= 128) return go_row<FMT, MODE, 16, 1>(a, s);
+    if (a.N <= 256) return go_row<FMT, MODE, 32, 1>(a, s);
     if (a.N <= 512) return go_row<FMT, MODE, 64, 1>(a, s);
     if (a.N <= 1024) return go_row<FMT, MODE, 64, 2>(a, s);
     if (a.N <= 2048) return go_row<FMT, MODE, 256, 1>(a, s);
@@ -351,49 +359,53 @@ hipError_t go_quant_cols(const RowArgs& a, hipStream_t stream) {
 
 template <int FMT, int T, int NV>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormBwdArgs a) {
-    constexpr int WG = T < 256 ? 256 : T;
-    constexpr int RPW = WG / T;
+    using P = Place<T>;
     constexpr int ES = fmt_es<FMT>;
-    __shared__ float red[2][WG / 64];
-    __shared__ float dwl[RPW > 1 ? RPW * T * NV * 8 : 1];
-    const int t = threadIdx.x % T;
-    const int sub = RPW > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
-    const int64_t step = (int64_t)gridDim.x * RPW;
-    float w[NV][8], dw[NV][8];
+    __shared__ float red[2][P::WG / 64];
+    __shared__ float dwl[P::RPW > 1 ? P::WG * NV * 8 : 1];
+    const P pl;
+    const int t = pl.t;
+    const int64_t step = (int64_t)gridDim.x * P::RPW;
+    auto col = [&](int i) { return (i * T + t) * 8; };
+    // 1024 threads have 128 registers each: no room for the next row's loads, nor
+    // to keep the weights over the rows.
+    constexpr bool PRE = T < 1024;
+    float w[PRE ? NV : 1][8], dw[NV][8];
     const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
+    auto load_w = [&](int i, float (&to)[8]) {
+        Row8<OUT_F32> w8;
+        w8.load(rw, (uint32_t)col(i) * 4, a.N - col(i));
+        w8.get(to);
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * T + t) * 8;
-        Row8<OUT_F32> w8;
-        w8.load(rw, (uint32_t)c * 4, a.N - c);
-        w8.get(w[i]);
+        if constexpr (PRE) load_w(i, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
     }
     Row8<FMT> y[NV], s[NV], d[NV];
-    auto load = [&](int64_t row) {
-        const auto ry = row_rsrc<FMT>(a.dY, row, a.lddy, a.N);
-        const auto rs = row_rsrc<FMT>(a.S, row, a.lds, a.N);
+    // The rows of this wave from row0 on; rows past M and columns past N load as 0.
+    auto load = [&](int64_t row0) {
+        const auto ry = P::rows(a.dY, row0, a.M, a.N, a.lddy, ES);
+        const auto rs = P::rows(a.S, row0, a.M, a.N, a.lds, ES);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * T + t) * 8;
-            y[i].load(ry, (uint32_t)c * ES, a.N - c);
-            s[i].load(rs, (uint32_t)c * ES, a.N - c);
+            y[i].load(ry, pl.at(row0, a.M, a.N, col(i), a.lddy, ES), a.N - col(i));
+            s[i].load(rs, pl.at(row0, a.M, a.N, col(i), a.lds, ES), a.N - col(i));
         }
         if (a.dS) {
-            const auto rd = row_rsrc<FMT>(a.dS, row, a.ldds, a.N);
+            const auto rd = P::rows(a.dS, row0, a.M, a.N, a.ldds, ES);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * T + t) * 8;
-                d[i].load(rd, (uint32_t)c * ES, a.N - c);
-            }
+            for (int i = 0; i < NV; ++i)
+                d[i].load(rd, pl.at(row0, a.M, a.N, col(i), a.ldds, ES), a.N - col(i));
         }
     };
-    int64_t row = (int64_t)blockIdx.x * RPW + sub;
-    if (row < a.M) load(row);
+    int64_t row0 = (int64_t)blockIdx.x * P::RPW + P::first();
+    if (PRE && row0 < a.M) load(row0);
     int par = 0;
-    for (; row < a.M; row += step, par ^= 1) {
-        const float rstd = a.rstd[row];
+    for (; row0 < a.M; row0 += step, par ^= 1) {
+        const float rstd = row0 + pl.lr < a.M ? a.rstd[row0 + pl.lr] : 0.0f;
+        if (!PRE) load(row0);
         // The row stays in its storage format (half the registers of fp32 for
         // 16-bit rows); the few products are formed again after the reduction.
         Row8<FMT> cy[NV], cs[NV], cd[NV];
@@ -406,39 +418,45 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormBwdArgs
             float dy[8], x[8];
             cy[i].get(dy);
             cs[i].get(x);
+            float wt[8];
+            if constexpr (!PRE) load_w(i, wt);
+            const float(&wi)[8] = PRE ? w[PRE ? i : 0] : wt;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float xh = x[j] * rstd;
-                dot += dy[j] * w[i][j] * xh;
+                dot += dy[j] * wi[j] * xh;
                 dw[i][j] += dy[j] * xh;
             }
         }
-        if (row + step < a.M) load(row + step);
+        if (PRE && row0 + step < a.M) load(row0 + step);
         // The reduction's words alternate between rows, so one barrier per row
         // is enough: a wave reaches the next but one row's write only after
         // every wave has passed the next row's barrier.
         const float mean = row_sum<T>(dot, red[par]) / (float)a.N;
-        const auto ro = row_rsrc<FMT>(a.dX, row, a.lddx, a.N);
+        const auto ro = P::rows(a.dX, row0, a.M, a.N, a.lddx, ES);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = (i * T + t) * 8;
             float dy[8], x[8], o[8], e[8];
             cy[i].get(dy);
             cs[i].get(x);
             if (a.dS) cd[i].get(e);
+            float wt[8];
+            if constexpr (!PRE) load_w(i, wt);
+            const float(&wi)[8] = PRE ? w[PRE ? i : 0] : wt;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                o[j] = rstd * (dy[j] * w[i][j] - x[j] * rstd * mean);
+                o[j] = rstd * (dy[j] * wi[j] - x[j] * rstd * mean);
                 if (a.dS) o[j] += e[j];
             }
             Row8<FMT> out;
             out.set(o);
-            out.store(ro, (uint32_t)c * ES, a.N - c);
+            out.store(ro, pl.at(row0, a.M, a.N, col(i), a.lddx, ES), a.N - col(i));
         }
     }
     if (!a.part) return;
-    if constexpr (RPW > 1) {
-        // The workgroup's waves hold the same columns: add them in wave order.
+    if constexpr (P::RPW > 1) {
+        // The workgroup's groups of T lanes hold the same columns: add them in order.
+        const int sub = (int)threadIdx.x / T;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -449,15 +467,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_bwd_kernel(NormBwdArgs
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                for (int q = 1; q < RPW; ++q) dw[i][j] += dwl[(q * NV * 8 + i * 8 + j) * T + t];
+                for (int q = 1; q < P::RPW; ++q) dw[i][j] += dwl[(q * NV * 8 + i * 8 + j) * T + t];
     }
     const auto rp = make_rsrc((const char*)(a.part + (int64_t)blockIdx.x * a.ldp), (int64_t)a.N * 4);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = (i * T + t) * 8;
         Row8<OUT_F32> out;
         out.set(dw[i]);
-        out.store(rp, (uint32_t)c * 4, a.N - c);
+        out.store(rp, (uint32_t)col(i) * 4, a.N - col(i));
     }
 }
 
@@ -471,12 +488,14 @@ hipError_t go_bwd(const NormBwdArgs& a, int grid, hipStream_t stream) {
 
 template <int FMT>
 hipError_t bwd_by_size(const NormBwdArgs& a, int grid, hipStream_t s) {
+    if (a.N <= 128) return go_bwd<FMT, 16, 1>(a, grid, s);
+    if (a.N <= 256) return go_bwd<FMT, 32, 1>(a, grid, s);
     if (a.N <= 512) return go_bwd<FMT, 64, 1>(a, grid, s);
     if (a.N <= 1024) return go_bwd<FMT, 64, 2>(a, grid, s);
     if (a.N <= 2048) return go_bwd<FMT, 256, 1>(a, grid, s);
     if (a.N <= 4096) return go_bwd<FMT, 256, 2>(a, grid, s);
-    if (a.N <= 8192) return go_bwd<FMT, 256, 4>(a, grid, s);
-    if (a.N <= NORM_BWD_MAX) return go_bwd<FMT, 512, 4>(a, grid, s);
+    if (a.N <= 8192) return go_bwd<FMT, 512, 2>(a, grid, s);
+    if (a.N <= NORM_BWD_MAX) return go_bwd<FMT, 1024, 2>(a, grid, s);
     return hipErrorInvalidValue;
 }
 
@@ -496,11 +515,14 @@ hipError_t launch_quant_cols(const RowArgs& a, int fmt, hipStream_t stream) {
     return hipErrorInvalidValue;
 }
 
-// Two workgroups of 256 threads per CU keep enough rows in flight; more only
-// adds partial sums of dw.
+// Workgroups of the backward pass: enough to keep the rows' loads in flight (four
+// per CU where a thread holds 8 columns, two where it holds 16, one of 1024
+// threads); more only adds partial sums of dweight.
 int norm_bwd_grid(int M, int N) {
-    const int64_t rows = N <= 1024 ? ((int64_t)M + 3) / 4 : M;
-    const int64_t most = N <= 8192 ? 2 * NUM_CU : NUM_CU;
+    const int per = N <= 128 ? 16 : N <= 256 ? 8 : N <= 1024 ? 4 : 1;  // rows per workgroup
+    const int64_t rows = ((int64_t)M + per - 1) / per;
+    const bool light = N <= 512 || (N > 1024 && N <= 2048);
+    const int64_t most = (N > 8192 ? 1 : light ? 4 : 2) * NUM_CU;
     return (int)(rows < most ? rows : most);
 }
 

@@ -155,7 +155,7 @@ __global__ __launch_bounds__(64 * W) void skinny_nn_kernel(
     constexpr int WD = CPL * ES / 4;    // words per lane and k-row
     constexpr int AW = ES / 2;          // 16-byte pieces of A per lane and step
     // Steps per chunk; two chunks in registers, within 128 of them for 16 waves.
-    constexpr int D = WD == 4 || F32 ? 2 : 4;
+    constexpr int D = WD == 4 || F32 ? 2 : 3;
     __shared__ float red[W * CPL * 4 * 64];
     {
         const int kbeg = (int)blockIdx.y * kchunk;

@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 DTS = [torch.float32, torch.bfloat16, torch.float16]
 EPS = 1e-5
 # every variant of threads per row and columns per lane, odd sizes among them
-SIZES = [(1, 1), (3, 7), (5, 512), (9, 513), (2, 1024), (4, 1030), (3, 2048), (6, 3001), (2, 4096), (3, 8190),
+SIZES = [(1, 1), (3, 7), (37, 64), (70, 128), (1, 130), (19, 250), (5, 512), (9, 513), (2, 1024), (4, 1030), (3, 2048), (6, 3001), (2, 4096), (3, 8190),
          (2, 9001), (2, 16384)]
 
 
