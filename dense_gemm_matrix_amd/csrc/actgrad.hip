@@ -113,32 +113,9 @@ hipError_t go_ag(const ActGradArgs& a, hipStream_t stream) {
                            dim3(one ? 1024 : 256), args, 0, stream);
 }
 
-// out[n] = sum over g < G of part[g][n], in a fixed order: 16 threads per column
-// take every sixteenth row, then LDS adds the sixteen.
-__global__ __launch_bounds__(1024) void col_reduce_kernel(const float* part, int G, int ldp, int N,
-                                                          float* out) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int col = (int)blockIdx.x * 64 + lane;
-    float v = 0.0f;
-    if (col < N) {
-        const float* p = part + col;
-        int g = q;
-        for (; g + 16 * 15 < G; g += 16 * 16) {  // sixteen loads in flight
-            float x[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = p[(int64_t)(g + 16 * i) * ldp];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v += x[i];
-        }
-        for (; g < G; g += 16) v += p[(int64_t)g * ldp];
-    }
-    s[q][lane] = v;
-    __syncthreads();
-    if (q == 0 && col < N) {
-        for (int i = 1; i < 16; ++i) v += s[i][lane];
-        out[col] = v;
-    }
+__global__ __launch_bounds__(256) void col_reduce_kernel(ColReduceArgs a) {
+    __shared__ float lds[COL_REDUCE_LDS];
+    col_reduce((int)blockIdx.x, a, lds);
 }
 
 // Y[n][m] = X[m][n], fp32, in 32 x 32 tiles through LDS (rows padded to 33 words):
@@ -178,11 +155,11 @@ hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t str
     return hipErrorInvalidValue;
 }
 
-hipError_t launch_col_reduce(const float* part, int G, int ldp, int N, float* out,
-                             hipStream_t stream) {
-    void* args[] = {&part, &G, &ldp, &N, &out};
-    return hipLaunchKernel((const void*)col_reduce_kernel, dim3((unsigned)((N + 63) / 64)), dim3(1024),
-                           args, 0, stream);
+hipError_t launch_col_reduce(const ColReduceArgs& a, hipStream_t stream) {
+    ColReduceArgs b = a;
+    void* args[] = {&b};
+    return hipLaunchKernel((const void*)col_reduce_kernel, dim3((unsigned)col_reduce_blocks(a.N)),
+                           dim3(256), args, 0, stream);
 }
 
 hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,

@@ -362,6 +362,11 @@ bool slice_plan_t(int M, int N, int K, Plan& p, double& us) {
     return true;
 }
 
+double slice_tile_us(int ts, int K) {
+    const SliceCand& c = *slice_cand(IN_BF16, ts, 4);
+    return c.round_us + (double)ceil_div(ceil_div(K, slice_bk(IN_BF16)), 4) * (c.blk_us + c.fill_us) * c.co;
+}
+
 bool slice_waves_t(int ts, int waves) { return slice_cand(IN_BF16, ts, waves) != nullptr; }
 
 namespace {

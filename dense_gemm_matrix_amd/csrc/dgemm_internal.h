@@ -75,6 +75,14 @@ enum Act { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU
 // K-contiguous); A[K x M] B[K x N].
 enum Layout { LAY_NN = 0, LAY_NT = 1, LAY_TN = 2 };
 
+// Column sums: out[n] = sum over g < G of part[g * ldp + n], n < N.
+struct ColReduceArgs {
+    const float* part;
+    float* out;
+    int G, ldp, N;
+};
+inline int col_reduce_blocks(int N) { return (N + 15) / 16; }
+
 // One GEMM launch.  The grid is (tiles_m * tiles_n, splits): workgroup
 // (x, z) computes tile map_tile(x) over k in [z * kchunk, min(K, (z + 1) *
 // kchunk)) and writes it at C + z * c_zstride bytes.  Unsplit launches have
@@ -209,6 +217,11 @@ hipError_t launch_gemm16_sk(const GemmLaunch& L, const SkSched& s, int grid);
 hipError_t launch_gemm32(const GemmLaunch& L);  // IN_F32, IN_F32X3
 hipError_t launch_gemmt(const GemmLaunch& L);   // LAY_NT, LAY_TN: 16-bit; LAY_NT: IN_F8, IN_F8W
 hipError_t launch_slicet(const GemmLaunch& L);  // as launch_gemmt with slice_waves > 0
+// A LAY_NT and a LAY_TN launch of 4-wave slice-K tiles and (if r.N > 0) column
+// sums, in one kernel, the TN tiles first if tn_first: the backward pass of a small
+// layer.
+hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
+                              const ColReduceArgs& r);
 hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_waves > 0
 
 // Products of at most SKINNY_M rows (skinny.hip): LAY_NN of 16-bit and fp32
@@ -273,8 +286,7 @@ struct ActGradArgs {
 };
 int act_grad_rows(int M);
 hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream);
-hipError_t launch_col_reduce(const float* part, int G, int ldp, int N, float* out,
-                             hipStream_t stream);
+hipError_t launch_col_reduce(const ColReduceArgs& a, hipStream_t stream);
 hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,
                               hipStream_t stream);
 

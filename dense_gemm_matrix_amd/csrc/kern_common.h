@@ -650,4 +650,38 @@ __device__ __forceinline__ void finish_full(float (&v)[NE], const int (&row)[NE]
         if (in[i]) store_c<OUT>(C, (int64_t)row[i] * ldc + col[i], e.res ? v[i] + res[i] : v[i]);
 }
 
+// ------------------------------------------------------------- column sums
+//
+// out[n] = sum over g < G of part[g][n], in a fixed order, by a workgroup of 256
+// threads per 16 columns: 16 threads per column take every sixteenth row, sixteen
+// loads in flight, then LDS adds the sixteen.  (64 columns per workgroup left most
+// CUs idle: 256 x 4096 5.5 us.)
+constexpr int COL_REDUCE_LDS = 256;  // floats
+
+__device__ __forceinline__ void col_reduce(int block, const ColReduceArgs& a, float* lds) {
+    const int c = (int)threadIdx.x & 15, q = (int)threadIdx.x >> 4;
+    const int col = block * 16 + c;
+    float v = 0.0f;
+    if (col < a.N) {
+        const float* p = a.part + col;
+        int g = q;
+        for (; g + 16 * 15 < a.G; g += 16 * 16) {
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = p[(int64_t)(g + 16 * i) * a.ldp];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v += x[i];
+        }
+#pragma unroll 4
+        for (; g < a.G; g += 16) v += p[(int64_t)g * a.ldp];
+    }
+    lds[threadIdx.x] = v;
+    __syncthreads();
+    if (q == 0 && col < a.N) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) v += lds[i * 16 + c];
+        a.out[col] = v;
+    }
+}
+
 }  // namespace dgemm

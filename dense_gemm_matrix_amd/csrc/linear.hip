@@ -88,7 +88,7 @@ Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uin
 // The transposed layouts' plan: the estimate's choice among the slice-K tiles
 // (slicet.hip; slicek16's constants, an 8-bit block being 128 k), the two grid
 // tiles and 1 to 16 splits, by the same terms and margin as the other plans.
-Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail) {
+Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail, double* us_out = nullptr) {
     const int bk = t_step(in);
     int fm, fn, fs;
     if (forced_grid(fm, fn, fs) && fm == fn && (fm == 32 || fm == 64)) {
@@ -132,6 +132,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
             }
         }
     best.layout = layout;
+    if (us_out) *us_out = slice && best.splits == 1 ? best_us / 0.65 : best_us;
     return best;
 }
 
@@ -304,12 +305,110 @@ int run_bwd_product(int in, int layout, int rows, int M, int N, int K, const voi
                p.layout != LAY_NN ? EPI_FULL : EPI_NONE, p, ws, stream);
 }
 
+constexpr double PAIR_GAP_US = 2.0;          // a second launch
+constexpr int64_t PAIR_TILES = 4 * NUM_CU;  // more are the grid tiles' (1500^3: 45 us, together 50)
+
+Plan slice4(int layout, int ts, int K) {
+    Plan p{ts, ts, 1, K, 0, 0};
+    p.waves = 4;
+    p.layout = layout;
+    return p;
+}
+
+// The plans of a small backward pass's two products in one launch of slice-K
+// tiles (with its column sums): tile sizes, which product's workgroups come first,
+// and whether it is worth it.
+struct PairPlan {
+    Plan nt, tn;
+    bool use, tn_first;
+};
+
+// A CU holds one of these workgroups (128 KB of LDS), and each starts where one
+// ended.  `ta` tiles of `wa` us, then `tb` of `wb`: after the first product
+// ta % 256 CUs are one tile later than the others.
+double pair_us(int64_t ta, double wa, int64_t tb, double wb) {
+    const int64_t late = ta % NUM_CU, q = ta / NUM_CU;
+    const double done = (double)ceil_div(ta, NUM_CU) * wa;
+    int64_t left = tb;
+    int64_t i = 0, j = 0;  // tiles so far on each early and each late CU
+    double t = done;
+    while (left > 0) {
+        const double e = (double)q * wa + (double)(i + 1) * wb;
+        const double l = (double)(q + 1) * wa + (double)(j + 1) * wb;
+        const bool early = late == 0 || e <= l;
+        left -= early ? NUM_CU - late : late;
+        (early ? i : j) += 1;
+        t = std::max(t, early ? e : l);
+    }
+    return t;
+}
+
+// One launch saves the other launches' time (2.4 us of host time each, 1.5 to 2 us
+// of a graph) and fills the CUs that one product's tiles leave idle; the longer
+// tiles go first where that ends earlier.  In us, bf16, M x N x K, apart / together:
+//   256 x 256 x 256     14.7 /  6.8    1000 x 512 x  512   19.9 / 12.6
+//   917 x 415 x 1035    24.4 / 15.1    2000 x 300 x  600   25.7 / 18.1
+//   600 x 800 x 3000    29.4 / 33.2 (not taken)
+PairPlan plan_pair(int in, int M, int N, int K, uint64_t ws) {
+    PairPlan r{};
+    double nt_us = 0.0, tn_us = 0.0;
+    r.nt = plan_t(in, LAY_NT, 2, M, K, N, ws, &nt_us);
+    r.tn = plan_t(in, LAY_TN, 2, K, N, M, ws, &tn_us);
+    int fm, fn, fs;
+    const bool forced = forced_grid(fm, fn, fs);
+    if (forced) {
+        r.use = r.nt.waves == 4 && r.tn.waves == 4;
+        return r;
+    }
+    double best = nt_us + tn_us + PAIR_GAP_US;
+    for (int a = 32; a <= 64; a += 32)
+        for (int b = 32; b <= 64; b += 32) {
+            const int64_t ta = ceil_div(M, a) * ceil_div(K, a), tb = ceil_div(K, b) * ceil_div(N, b);
+            if (ta + tb > PAIR_TILES) continue;
+            const double wa = slice_tile_us(a, N), wb = slice_tile_us(b, M);
+            const double fwd = pair_us(ta, wa, tb, wb), rev = pair_us(tb, wb, ta, wa);
+            if (std::min(fwd, rev) >= best) continue;
+            best = std::min(fwd, rev);
+            r.use = true;
+            r.tn_first = rev < fwd;
+            r.nt = slice4(LAY_NT, a, N);
+            r.tn = slice4(LAY_TN, b, M);
+        }
+    return r;
+}
+
+GemmLaunch slice_launch(int in, const Plan& p, int M, int N, int K, const void* X, int ldx, const void* Y,
+                        int ldy, void* C, int ldc, hipStream_t stream) {
+    GemmLaunch L{};
+    L.in = in;
+    L.out = out_format(in, DGEMM_OUT_SAME);
+    L.tbm = p.bm;
+    L.tbn = p.bn;
+    L.layout = p.layout;
+    L.slice_waves = 4;
+    L.splits = 1;
+    L.epi = EPI_FULL;
+    L.A = (const char*)X;
+    L.B = (const char*)Y;
+    L.C = (char*)C;
+    L.M = M;
+    L.N = N;
+    L.K = K;
+    L.lda = ldx;
+    L.ldb = ldy;
+    L.ldc = ldc;
+    L.tiles_m = (int)ceil_div(M, p.bm);
+    L.tiles_n = (int)ceil_div(N, p.bn);
+    L.stream = stream;
+    return L;
+}
+
+int launched(hipError_t e) { return e == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH; }
+
 // Format codes DGEMM_IN_F32 / _BF16 / _F16 of an elementwise operator.
 int row_fmt(int in) {
     return in == DGEMM_IN_F32 ? OUT_F32 : in == DGEMM_IN_BF16 ? OUT_BF16 : in == DGEMM_IN_F16 ? OUT_F16 : -1;
 }
-
-int launched(hipError_t e) { return e == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH; }
 
 }  // namespace
 }  // namespace dgemm
@@ -399,9 +498,17 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
         if (launch_act_grad(a, cf, out_format(in, DGEMM_OUT_SAME), s) != hipSuccess)
             return DGEMM_ERR_LAUNCH;
     }
-    if (dbias && N > 0 && b.chunks != 1 &&
-        launch_col_reduce((const float*)w_part, b.chunks, b.ldp, N, dbias, s) != hipSuccess)
-        return DGEMM_ERR_LAUNCH;
+    ColReduceArgs sums{(const float*)w_part, dbias, b.chunks, b.ldp, dbias && b.chunks != 1 ? N : 0};
+    if (dA && dB && M > SKINNY_M && N > 0 && K > 0 && es == 2) {
+        // A small layer: both products and the column sums in one launch.
+        const PairPlan p = plan_pair(in, M, N, K, (uint64_t)gemm_bytes);
+        if (p.use) {
+            const GemmLaunch nt = slice_launch(in, p.nt, M, K, N, dz, lddz, B, ldb, dA, ldda, s);
+            const GemmLaunch tn = slice_launch(in, p.tn, K, N, M, A, lda, dz, lddz, dB, lddb, s);
+            return launched(launch_slicet_pair(nt, tn, p.tn_first, sums));
+        }
+    }
+    if (sums.N > 0 && launch_col_reduce(sums, s) != hipSuccess) return DGEMM_ERR_LAUNCH;
     const bool f32 = es == 4 && M > SKINNY_M;  // the fp32 kernels take A[M x K] B[K x N] only
     if (dA) {
         const void* y = B;
@@ -552,7 +659,7 @@ int rmsnorm_bwd(int in, int M, int N, const void* dY, int lddy, const void* S, i
     const NormBwdArgs a{(const char*)dY, (const char*)S, (const char*)dS, weight, rstd, (char*)dX,
                         dweight ? (float*)workspace : nullptr, M, N, lddy, lds, ldds, lddx, ldp};
     if (M > 0 && launch_norm_bwd(a, fmt, s) != hipSuccess) return DGEMM_ERR_LAUNCH;
-    if (dweight) return launched(launch_col_reduce((const float*)workspace, grid, ldp, N, dweight, s));
+    if (dweight) return launched(launch_col_reduce(ColReduceArgs{(const float*)workspace, dweight, grid, ldp, N}, s));
     return DGEMM_OK;
 }
 

@@ -34,10 +34,31 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int cmax(int a, int b) { return a > b ? a : b; }
 
+// One product's arguments.
+struct SliceArgs {
+    const char* X;
+    const char* Y;
+    char* C;
+    int M, N, K, ldx, ldy, ldc, tiles_m, tiles_n;
+};
+
+template <int MI, int W>
+struct SliceTile {
+    // Blocks per chunk, two chunks in LDS.
+    static constexpr int D = MI == 1 && W == 4 ? 2 : 1;
+    static constexpr int BLKB = 128 * 32 * MI;  // bytes of one operand's block
+    static constexpr int STAGES = W * 2 * D * 2 * BLKB;
+    static constexpr int RED = W * MI * MI * 16 * 64 * 4;
+    static constexpr int LDS = cmax(STAGES, RED);
+};
+
+// Tile `wg` of a product.
 template <int IN, int LAY, int OUT, int MI, int W>
-__global__ __launch_bounds__(64 * W) void slicet_kernel(
-    const char* __restrict__ X, const char* __restrict__ Y, char* C, int M, int N, int K, int ldx,
-    int ldy, int ldc, int tiles_m, int tiles_n, EpiArgs epi) {
+__device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const EpiArgs& epi, char* smem) {
+    const char* __restrict__ X = a.X;
+    const char* __restrict__ Y = a.Y;
+    char* const C = a.C;
+    const int M = a.M, N = a.N, K = a.K, ldx = a.ldx, ldy = a.ldy, ldc = a.ldc;
     constexpr bool KC = LAY == LAY_NT;
     constexpr bool F8 = IN == IN_F8 || IN == IN_F8W;
     static_assert(KC || !F8, "8-bit operands are K-contiguous");
@@ -45,14 +66,11 @@ __global__ __launch_bounds__(64 * W) void slicet_kernel(
     constexpr int BK = 128 / ES;
     constexpr int TS = 32 * MI;
     constexpr int NB = MI * MI;
-    constexpr int D = MI == 1 && W == 4 ? 2 : 1;  // blocks per chunk, two chunks in LDS
-    constexpr int BLKB = 128 * TS;            // bytes of one operand's block
-    constexpr int NDB = BLKB / 1024;          // its direct-to-LDS loads
-    constexpr int STAGES = W * 2 * D * 2 * BLKB;
-    constexpr int RED = W * NB * 16 * 64 * 4;
-    __shared__ __attribute__((aligned(1024))) char smem[cmax(STAGES, RED)];
+    using T = SliceTile<MI, W>;
+    constexpr int D = T::D, BLKB = T::BLKB;
+    constexpr int NDB = BLKB / 1024;          // an operand block's direct-to-LDS loads
     int tm, tn;
-    map_tile((int)blockIdx.x, tiles_m, tiles_n, tm, tn);
+    map_tile(wg, a.tiles_m, a.tiles_n, tm, tn);
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int g = lane >> 5, li = lane & 31;
@@ -231,16 +249,57 @@ __global__ __launch_bounds__(64 * W) void slicet_kernel(
 }
 
 template <int IN, int LAY, int OUT, int MI, int W>
+__global__ __launch_bounds__(64 * W) void slicet_kernel(SliceArgs a, EpiArgs epi) {
+    __shared__ __attribute__((aligned(1024))) char smem[SliceTile<MI, W>::LDS];
+    slice_tile<IN, LAY, OUT, MI, W>(a, (int)blockIdx.x, epi, smem);
+}
+
+// The two products of a small backward pass and its bias gradient's column sums:
+// independent, and each a few us, so one launch instead of three (2.4 us of host
+// time each).  The tiles of both products come first, NT's before TN's counted
+// from workgroup `first` on, cyclically (0, or TN's first); then the column sums.
+template <int IN, int MI_NT, int MI_TN>
+__global__ __launch_bounds__(256) void slicet_pair_kernel(SliceArgs nt, SliceArgs tn, int first,
+                                                          ColReduceArgs r) {
+    constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
+    __shared__ __attribute__((
+        aligned(1024))) char smem[cmax(SliceTile<MI_NT, 4>::LDS, SliceTile<MI_TN, 4>::LDS)];
+    const int n_nt = nt.tiles_m * nt.tiles_n, n_tn = tn.tiles_m * tn.tiles_n;
+    int wg = (int)blockIdx.x;
+    if (wg < n_nt + n_tn) {
+        wg += first;
+        if (wg >= n_nt + n_tn) wg -= n_nt + n_tn;
+    }
+    EpiArgs e{};
+    if (wg < n_nt) slice_tile<IN, LAY_NT, OUT, MI_NT, 4>(nt, wg, e, smem);
+    else if (wg < n_nt + n_tn) slice_tile<IN, LAY_TN, OUT, MI_TN, 4>(tn, wg - n_nt, e, smem);
+    else col_reduce(wg - n_nt - n_tn, r, (float*)smem);
+}
+
+SliceArgs args_of(const GemmLaunch& L) {
+    return SliceArgs{L.A, L.B, L.C, L.M, L.N, L.K, L.lda, L.ldb, L.ldc, L.tiles_m, L.tiles_n};
+}
+
+template <int IN, int LAY, int OUT, int MI, int W>
 hipError_t go(const GemmLaunch& L) {
-    const char* a = L.A;
-    const char* b = L.B;
-    char* c = L.C;
-    int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc;
-    int tiles_m = L.tiles_m, tiles_n = L.tiles_n;
+    SliceArgs a = args_of(L);
     EpiArgs e = L.e;
-    void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &tiles_n, &e};
+    void* args[] = {&a, &e};
     return hipLaunchKernel((const void*)slicet_kernel<IN, LAY, OUT, MI, W>,
-                           dim3((unsigned)(tiles_m * tiles_n)), dim3(64 * W), args, 0, L.stream);
+                           dim3((unsigned)(L.tiles_m * L.tiles_n)), dim3(64 * W), args, 0, L.stream);
+}
+
+template <int IN>
+hipError_t go_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first, const ColReduceArgs& r) {
+    const bool m2 = nt.tbm == 64, n2 = tn.tbm == 64;
+    const void* fn = m2 ? (n2 ? (const void*)slicet_pair_kernel<IN, 2, 2> : (const void*)slicet_pair_kernel<IN, 2, 1>)
+                        : (n2 ? (const void*)slicet_pair_kernel<IN, 1, 2> : (const void*)slicet_pair_kernel<IN, 1, 1>);
+    SliceArgs a = args_of(nt), b = args_of(tn);
+    ColReduceArgs c = r;
+    int first = tn_first ? nt.tiles_m * nt.tiles_n : 0;
+    void* args[] = {&a, &b, &first, &c};
+    const int blocks = nt.tiles_m * nt.tiles_n + tn.tiles_m * tn.tiles_n + (r.N > 0 ? col_reduce_blocks(r.N) : 0);
+    return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, nt.stream);
 }
 
 template <int IN, int LAY, int OUT>
@@ -265,6 +324,16 @@ hipError_t launch_slicet(const GemmLaunch& L) {
         if (L.in == IN_BF16 && L.out == OUT_BF16) return by_variant<IN_BF16, LAY_TN, OUT_BF16>(L);
         if (L.in == IN_F16 && L.out == OUT_F16) return by_variant<IN_F16, LAY_TN, OUT_F16>(L);
     }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
+                              const ColReduceArgs& r) {
+    for (const GemmLaunch* L : {&nt, &tn})
+        if (L->splits != 1 || L->tbm != L->tbn || (L->tbm != 32 && L->tbm != 64) || L->in != nt.in)
+            return hipErrorInvalidValue;
+    if (nt.in == IN_BF16) return go_pair<IN_BF16>(nt, tn, tn_first, r);
+    if (nt.in == IN_F16) return go_pair<IN_F16>(nt, tn, tn_first, r);
     return hipErrorInvalidValue;
 }
 
