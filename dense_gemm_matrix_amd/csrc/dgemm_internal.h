@@ -217,8 +217,8 @@ hipError_t launch_gemm16_sk(const GemmLaunch& L, const SkSched& s, int grid);
 hipError_t launch_gemm32(const GemmLaunch& L);  // IN_F32, IN_F32X3
 hipError_t launch_gemmt(const GemmLaunch& L);   // LAY_NT, LAY_TN: 16-bit; LAY_NT: IN_F8, IN_F8W
 hipError_t launch_slicet(const GemmLaunch& L);  // as launch_gemmt with slice_waves > 0
-// A LAY_NT and a LAY_TN launch of 4-wave slice-K tiles and (if r.N > 0) column
-// sums, in one kernel, the TN tiles first if tn_first: the backward pass of a small
+// A LAY_NT and a LAY_TN launch of 4-wave slice-K tiles (16-bit or fp32; tiles_m = 0:
+// none) and (if r.N > 0) column sums, in one kernel, the TN tiles first if tn_first: the backward pass of a small
 // layer.
 hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
                               const ColReduceArgs& r);

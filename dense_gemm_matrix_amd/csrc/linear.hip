@@ -305,8 +305,23 @@ int run_bwd_product(int in, int layout, int rows, int M, int N, int K, const voi
                p.layout != LAY_NN ? EPI_FULL : EPI_NONE, p, ws, stream);
 }
 
-constexpr double PAIR_GAP_US = 2.0;          // a second launch
-constexpr int64_t PAIR_TILES = 4 * NUM_CU;  // more are the grid tiles' (1500^3: 45 us, together 50)
+constexpr double PAIR_GAP_US = 2.0;          // another launch
+// Most tiles: more are the 16-bit grid's (1500^3: 45 us, together 50); fp32's
+// grid kernels are slower than the pair's 64 x 64 tiles at many odd sizes
+// (1500^3 181 / 155 us, 3500^3 1748 / 1487), so there the estimate decides.
+constexpr int64_t PAIR_TILES_16 = 4 * NUM_CU, PAIR_TILES_32 = 32 * NUM_CU;
+
+// A product of the backward pass by itself, M x N with K terms; in fp32 with the
+// launch that transposes an operand.
+double alone_us(int in, int layout, int M, int N, int K, uint64_t ws) {
+    double us = 0.0;
+    if (in_esize(in) == 2) {
+        plan_t(in, layout, 2, M, N, K, ws, &us);
+        return us;
+    }
+    const double transposed = (double)K * (layout == LAY_NT ? N : M) * 8.0 / 4e6;
+    return PAIR_GAP_US + transposed + plan_us(in, 4, make_plan(in, 4, M, N, K, ws, false), M, N, K);
+}
 
 Plan slice4(int layout, int ts, int K) {
     Plan p{ts, ts, 1, K, 0, 0};
@@ -349,25 +364,27 @@ double pair_us(int64_t ta, double wa, int64_t tb, double wb) {
 //   256 x 256 x 256     14.7 /  6.8    1000 x 512 x  512   19.9 / 12.6
 //   917 x 415 x 1035    24.4 / 15.1    2000 x 300 x  600   25.7 / 18.1
 //   600 x 800 x 3000    29.4 / 33.2 (not taken)
-PairPlan plan_pair(int in, int M, int N, int K, uint64_t ws) {
+// and in fp32 256^3 20.6 / 8.0, 917 x 415 x 1035 47.0 / 30.8, 1024^3 69 / 51.
+PairPlan plan_pair(int in, int M, int N, int K, bool dA, bool dB, bool sums, uint64_t ws) {
     PairPlan r{};
-    double nt_us = 0.0, tn_us = 0.0;
-    r.nt = plan_t(in, LAY_NT, 2, M, K, N, ws, &nt_us);
-    r.tn = plan_t(in, LAY_TN, 2, K, N, M, ws, &tn_us);
+    const int f = in_esize(in) == 4 ? IN_F32 : IN_BF16;  // 3 x bf16 in fp32 arithmetic here
     int fm, fn, fs;
     const bool forced = forced_grid(fm, fn, fs);
-    if (forced) {
-        r.use = r.nt.waves == 4 && r.tn.waves == 4;
-        return r;
-    }
-    double best = nt_us + tn_us + PAIR_GAP_US;
+    const bool tile = forced && fm == fn && (fm == 32 || fm == 64);
+    if (tile && fs != 1 && fs != 4) return r;
+    if (forced && !tile) return r;
+    double best = (double)((dA ? 1 : 0) + (dB ? 1 : 0) + (sums ? 1 : 0) - 1) * PAIR_GAP_US;
+    if (dA) best += alone_us(in, LAY_NT, M, K, N, ws);
+    if (dB) best += alone_us(in, LAY_TN, K, N, M, ws);
     for (int a = 32; a <= 64; a += 32)
         for (int b = 32; b <= 64; b += 32) {
-            const int64_t ta = ceil_div(M, a) * ceil_div(K, a), tb = ceil_div(K, b) * ceil_div(N, b);
-            if (ta + tb > PAIR_TILES) continue;
-            const double wa = slice_tile_us(a, N), wb = slice_tile_us(b, M);
+            if ((!dA && a > 32) || (!dB && b > 32) || (tile && ((dA && a != fm) || (dB && b != fm)))) continue;
+            const int64_t ta = dA ? ceil_div(M, a) * ceil_div(K, a) : 0;
+            const int64_t tb = dB ? ceil_div(K, b) * ceil_div(N, b) : 0;
+            if (ta + tb > (tile ? (int64_t)INT32_MAX / 2 : f == IN_F32 ? PAIR_TILES_32 : PAIR_TILES_16)) continue;
+            const double wa = slice_tile_us(f, a, N), wb = slice_tile_us(f, b, M);
             const double fwd = pair_us(ta, wa, tb, wb), rev = pair_us(tb, wb, ta, wa);
-            if (std::min(fwd, rev) >= best) continue;
+            if (!tile && std::min(fwd, rev) >= best) continue;
             best = std::min(fwd, rev);
             r.use = true;
             r.tn_first = rev < fwd;
@@ -380,7 +397,7 @@ PairPlan plan_pair(int in, int M, int N, int K, uint64_t ws) {
 GemmLaunch slice_launch(int in, const Plan& p, int M, int N, int K, const void* X, int ldx, const void* Y,
                         int ldy, void* C, int ldc, hipStream_t stream) {
     GemmLaunch L{};
-    L.in = in;
+    L.in = in == IN_F32X3 ? IN_F32 : in;
     L.out = out_format(in, DGEMM_OUT_SAME);
     L.tbm = p.bm;
     L.tbn = p.bn;
@@ -499,12 +516,14 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
             return DGEMM_ERR_LAUNCH;
     }
     ColReduceArgs sums{(const float*)w_part, dbias, b.chunks, b.ldp, dbias && b.chunks != 1 ? N : 0};
-    if (dA && dB && M > SKINNY_M && N > 0 && K > 0 && es == 2) {
-        // A small layer: both products and the column sums in one launch.
-        const PairPlan p = plan_pair(in, M, N, K, (uint64_t)gemm_bytes);
+    if ((dA || dB) && M > SKINNY_M && N > 0 && K > 0) {
+        // A small layer: the products and the column sums in one launch.
+        const PairPlan p = plan_pair(in, M, N, K, dA, dB, sums.N > 0, (uint64_t)gemm_bytes);
         if (p.use) {
-            const GemmLaunch nt = slice_launch(in, p.nt, M, K, N, dz, lddz, B, ldb, dA, ldda, s);
-            const GemmLaunch tn = slice_launch(in, p.tn, K, N, M, A, lda, dz, lddz, dB, lddb, s);
+            GemmLaunch nt = slice_launch(in, p.nt, M, K, N, dz, lddz, B, ldb, dA, ldda, s);
+            GemmLaunch tn = slice_launch(in, p.tn, K, N, M, A, lda, dz, lddz, dB, lddb, s);
+            if (!dA) nt.tiles_m = 0;
+            if (!dB) tn.tiles_m = 0;
             return launched(launch_slicet_pair(nt, tn, p.tn_first, sums));
         }
     }

@@ -66,8 +66,11 @@ bool forced_grid(int& bm, int& bn, int& splits);
 // tile ts with `waves` waves.
 bool slice_plan_t(int M, int N, int K, Plan& p, double& us);
 bool slice_waves_t(int ts, int waves);
-// Time of one 4-wave 16-bit slice-K tile of K terms on a CU, workgroup after workgroup.
-double slice_tile_us(int ts, int K);
+// Time of one 4-wave slice-K tile of K terms on a CU, workgroup after workgroup
+// (in: IN_BF16 for both 16-bit formats, IN_F32).
+double slice_tile_us(int in, int ts, int K);
+// Estimated time of plan p of A[M x K] B[K x N].
+double plan_us(int in, int es_out, const Plan& p, int M, int N, int K);
 Plan make_plan(int in, int es_out, int M, int N, int K, uint64_t ws_avail, bool allow_sk);
 
 // Validated arguments and a plan -> its launches, with epilogue e at level epi.

@@ -19,6 +19,10 @@
 //     cancels).
 //   TN: both along the output: 64 k-rows x TS columns of each as they lie in
 //     memory, read back through the transpose read (slicek16.hip's B).
+// fp32 operands (the backward pass of small fp32 layers, which would otherwise
+// transpose A and B in launches of their own): blocks of 32 k, instructions of 2 k;
+// NT takes k = 4 (2 h + g) + w of both operands together, TN reads k-row
+// 2 (4 h + w) + g as it lies.
 // D to 2 D blocks are in flight per wave.
 
 #include <type_traits>
@@ -59,10 +63,10 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
     const char* __restrict__ Y = a.Y;
     char* const C = a.C;
     const int M = a.M, N = a.N, K = a.K, ldx = a.ldx, ldy = a.ldy, ldc = a.ldc;
-    constexpr bool KC = LAY == LAY_NT;
+    constexpr bool KC = LAY == LAY_NT;  // K-contiguous operands
     constexpr bool F8 = IN == IN_F8 || IN == IN_F8W;
     static_assert(KC || !F8, "8-bit operands are K-contiguous");
-    constexpr int ES = F8 ? 1 : 2;
+    constexpr int ES = F8 ? 1 : IN == IN_F32 ? 4 : 2;
     constexpr int BK = 128 / ES;
     constexpr int TS = 32 * MI;
     constexpr int NB = MI * MI;
@@ -118,6 +122,13 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
                             c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                                 widen_f8(f.x[mi][q][w], f.x[mi][q][w + 1]),
                                 widen_f8(f.y[nj][q][w], f.y[nj][q][w + 1]), c, 0, 0, 0);
+                } else if constexpr (IN == IN_F32) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            c = __builtin_amdgcn_mfma_f32_32x32x2f32(as_float(f.x[mi][h][w]),
+                                                                     as_float(f.y[nj][h][w]), c, 0, 0, 0);
                 } else {
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
@@ -140,16 +151,12 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
     int vx[NDB], vy[NDB];
 #pragma unroll
     for (int j = 0; j < NDB; ++j) {
-        if constexpr (KC) {
-            const int row = A16_RPB * j + lane / A16_CH;
-            const int c = (lane % A16_CH) ^ a16_phi(row);
-            vx[j] = row * ldx * ES + 16 * c;
-            vy[j] = row * ldy * ES + 16 * c;
-        } else {
-            const int q = 1024 * j + 16 * lane;  // k-row q / 2TS, byte q % 2TS of the row
-            vx[j] = (q / (2 * TS)) * ldx * 2 + q % (2 * TS);
-            vy[j] = (q / (2 * TS)) * ldy * 2 + q % (2 * TS);
-        }
+        const int row = A16_RPB * j + lane / A16_CH;
+        const int c = (lane % A16_CH) ^ a16_phi(row);
+        const int q = 1024 * j + 16 * lane;  // k-row q / RB, byte q % RB of the row
+        constexpr int RB = ES * TS;
+        vx[j] = KC ? row * ldx * ES + 16 * c : (q / RB) * ldx * ES + q % RB;
+        vy[j] = KC ? row * ldy * ES + 16 * c : (q / RB) * ldy * ES + q % RB;
     }
     // The transpose read's slot: lane 16 G + 4 a + q reads k-row 8 (G / 2) + a,
     // columns 16 (G & 1) + 4 q ...
@@ -161,7 +168,7 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
         if constexpr (KC)
             return make_rsrc(p + ((int64_t)o0 * ld + k0) * ES, ((int64_t)(rows - 1) * ld + krem) * ES);
         else
-            return make_rsrc(p + ((int64_t)k0 * ld + o0) * 2, ((int64_t)(krem - 1) * ld + rows) * 2);
+            return make_rsrc(p + ((int64_t)k0 * ld + o0) * ES, ((int64_t)(krem - 1) * ld + rows) * ES);
     };
     auto load = [&](int i, int s) {
         const int k0 = (kb0 + i) * BK;
@@ -188,6 +195,13 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
                     const int at = a16_off(mi * 32 + li, chunk(h));
                     f.x[mi][h] = *(const u32x4*)(st + at);
                     f.y[mi][h] = *(const u32x4*)(st + BLKB + at);
+                } else if constexpr (IN == IN_F32) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const char* at = st + ((2 * (4 * h + w) + g) * TS + 32 * mi + li) * 4;
+                        f.x[mi][h][w] = *(const uint32_t*)at;
+                        f.y[mi][h][w] = *(const uint32_t*)(at + BLKB);
+                    }
                 } else {
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
@@ -254,14 +268,14 @@ __global__ __launch_bounds__(64 * W) void slicet_kernel(SliceArgs a, EpiArgs epi
     slice_tile<IN, LAY, OUT, MI, W>(a, (int)blockIdx.x, epi, smem);
 }
 
-// The two products of a small backward pass and its bias gradient's column sums:
-// independent, and each a few us, so one launch instead of three (2.4 us of host
+// The products of a small backward pass (either may have no tiles) and its bias
+// gradient's column sums: independent, and each a few us, so one launch instead of three (2.4 us of host
 // time each).  The tiles of both products come first, NT's before TN's counted
 // from workgroup `first` on, cyclically (0, or TN's first); then the column sums.
 template <int IN, int MI_NT, int MI_TN>
 __global__ __launch_bounds__(256) void slicet_pair_kernel(SliceArgs nt, SliceArgs tn, int first,
                                                           ColReduceArgs r) {
-    constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
+    constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : IN == IN_F16 ? OUT_F16 : OUT_F32;
     __shared__ __attribute__((
         aligned(1024))) char smem[cmax(SliceTile<MI_NT, 4>::LDS, SliceTile<MI_TN, 4>::LDS)];
     const int n_nt = nt.tiles_m * nt.tiles_n, n_tn = tn.tiles_m * tn.tiles_n;
@@ -299,6 +313,7 @@ hipError_t go_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first, co
     int first = tn_first ? nt.tiles_m * nt.tiles_n : 0;
     void* args[] = {&a, &b, &first, &c};
     const int blocks = nt.tiles_m * nt.tiles_n + tn.tiles_m * tn.tiles_n + (r.N > 0 ? col_reduce_blocks(r.N) : 0);
+    if (blocks == 0) return hipSuccess;
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, nt.stream);
 }
 
@@ -334,6 +349,7 @@ hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool t
             return hipErrorInvalidValue;
     if (nt.in == IN_BF16) return go_pair<IN_BF16>(nt, tn, tn_first, r);
     if (nt.in == IN_F16) return go_pair<IN_F16>(nt, tn, tn_first, r);
+    if (nt.in == IN_F32) return go_pair<IN_F32>(nt, tn, tn_first, r);
     return hipErrorInvalidValue;
 }
 

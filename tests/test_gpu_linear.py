@@ -293,7 +293,7 @@ def test_backward_slice_tiles(grid_plan, tile, waves, fmt):
         run_bwd(fmt, "same", M, N, K, "none", seed=50 + i)
 
 
-@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "f32", "f32x3"])
 @pytest.mark.parametrize("shape", [(50, 30, 20), (400, 70, 500), (90, 700, 150), (917, 415, 1035), (240, 1501, 430),
                                    (2000, 300, 200), (33, 2000, 1000)], ids=lambda s: "x".join(map(str, s)))
 def test_backward_products_together(fmt, shape):
@@ -301,6 +301,7 @@ def test_backward_products_together(fmt, shape):
     orders, with fewer and more workgroups than CUs."""
     run_bwd(fmt, "same", *shape, "silu", seed=60)
     run_bwd(fmt, "f32", *shape, "none", seed=61, want=("dA", "dB"))
+    run_bwd(fmt, "same", *shape, "relu", seed=62, want=("dB", "dbias"))
 
 
 @pytest.mark.parametrize("want", [("dA",), ("dB",), ("dbias",), ("dA", "dbias"), ("dB", "dbias"), ("dA", "dB")])
