@@ -222,6 +222,9 @@ hipError_t launch_slicet(const GemmLaunch& L);  // as launch_gemmt with slice_wa
 // layer.
 hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
                               const ColReduceArgs& r);
+// The same of 16-bit grid tiles, 128 x 128 or 256 x 256 for both.
+hipError_t launch_gemmt_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
+                             const ColReduceArgs& r);
 hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_waves > 0
 
 // Products of at most SKINNY_M rows (skinny.hip): LAY_NN of 16-bit and fp32

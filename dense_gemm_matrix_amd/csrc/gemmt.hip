@@ -321,40 +321,90 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
 }
 
-// One macro-tile per workgroup and K split, as gemm16_kernel.
+// One product's arguments.
+struct GridArgs {
+    const char* X;
+    const char* Y;
+    char* C;
+    int M, N, K, ldx, ldy, ldc, tiles_m, tiles_n;
+};
+
+// Macro-tile `wg` of a product (of one K split of it).
 template <int IN, int LAY, int OUT, int TBM, int TBN, int EPI, int S>
-__global__ __launch_bounds__(256) void gemmt_kernel(
-    const char* __restrict__ X, const char* __restrict__ Y, char* C, int M, int N, int K, int ldx,
-    int ldy, int ldc, int tiles_m, int tiles_n, int kchunk, int64_t c_zstride, EpiArgs epi) {
+__device__ __forceinline__ void grid_tile(const GridArgs& a, int wg, const EpiArgs& epi, char* smem) {
     using T = TileT<IN, LAY, TBM, TBN, S>;
-    {
-        const int z = (int)blockIdx.y;
-        const int kbeg = z * kchunk;
-        X += (T::KC ? (int64_t)kbeg : (int64_t)kbeg * ldx) * T::ES;
-        Y += (T::KC ? (int64_t)kbeg : (int64_t)kbeg * ldy) * T::ES;
-        C += z * c_zstride;
-        K = (K - kbeg) < kchunk ? (K - kbeg) : kchunk;
-    }
-    __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
     int tm, tn;
-    map_tile((int)blockIdx.x, tiles_m, tiles_n, tm, tn);
+    map_tile(wg, a.tiles_m, a.tiles_n, tm, tn);
     const int m0 = tm * TBM, n0 = tn * TBN;
-    const int rows_x = (M - m0) < TBM ? (M - m0) : TBM;
-    const int rows_y = (N - n0) < TBN ? (N - n0) : TBN;
+    const int rows_x = (a.M - m0) < TBM ? (a.M - m0) : TBM;
+    const int rows_y = (a.N - n0) < TBN ? (a.N - n0) : TBN;
     f32x16 acc[T::MI][T::NJ];
-    mainloop_t<IN, LAY, TBM, TBN, S>(X, Y, K, ldx, ldy, m0, n0, rows_x, rows_y, smem, acc);
+    mainloop_t<IN, LAY, TBM, TBN, S>(a.X, a.Y, a.K, a.ldx, a.ldy, m0, n0, rows_x, rows_y, smem, acc);
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int row0 = m0 + (wave >> 1) * (TBM / 2), col0 = n0 + (wave & 1) * (TBN / 2);
     if constexpr (EPI == EPI_FULL) {
         static_assert(4 * full_lds<T::NJ> <= T::LDS, "LDS for the full epilogue");
         __syncthreads();  // every wave is done with the operand ring
-        store_tile_full<OUT, T::MI, T::NJ>(acc, C, M, N, ldc, row0, col0, lane, epi,
+        store_tile_full<OUT, T::MI, T::NJ>(acc, a.C, a.M, a.N, a.ldc, row0, col0, lane, epi,
                                            smem + wave * full_lds<T::NJ>);
     } else {
-        store_tile<OUT, T::MI, T::NJ, EPI, false>(acc, C, M, N, ldc, row0, col0, lane >> 5,
+        store_tile<OUT, T::MI, T::NJ, EPI, false>(acc, a.C, a.M, a.N, a.ldc, row0, col0, lane >> 5,
                                                   lane & 31, epi);
     }
+}
+
+// One macro-tile per workgroup and K split, as gemm16_kernel.
+template <int IN, int LAY, int OUT, int TBM, int TBN, int EPI, int S>
+__global__ __launch_bounds__(256) void gemmt_kernel(GridArgs a, int kchunk, int64_t c_zstride,
+                                                    EpiArgs epi) {
+    using T = TileT<IN, LAY, TBM, TBN, S>;
+    __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
+    const int z = (int)blockIdx.y;
+    const int kbeg = z * kchunk;
+    a.X += (T::KC ? (int64_t)kbeg : (int64_t)kbeg * a.ldx) * T::ES;
+    a.Y += (T::KC ? (int64_t)kbeg : (int64_t)kbeg * a.ldy) * T::ES;
+    a.C += z * c_zstride;
+    a.K = (a.K - kbeg) < kchunk ? (a.K - kbeg) : kchunk;
+    grid_tile<IN, LAY, OUT, TBM, TBN, EPI, S>(a, (int)blockIdx.x, epi, smem);
+}
+
+// Both products of a backward pass and its column sums in one launch: the CUs that
+// one product's last round leaves idle take the other's tiles.  Tiles counted from
+// `first` on as in slicet.hip's pair.
+template <int IN, int TB>
+__global__ __launch_bounds__(256) void gemmt_pair_kernel(GridArgs nt, GridArgs tn, int first,
+                                                         ColReduceArgs r) {
+    constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
+    constexpr int L1 = TileT<IN, LAY_NT, TB, TB, 2>::LDS, L2 = TileT<IN, LAY_TN, TB, TB, 2>::LDS;
+    __shared__ __attribute__((aligned(1024))) char smem[L1 > L2 ? L1 : L2];
+    const int n_nt = nt.tiles_m * nt.tiles_n, n_tn = tn.tiles_m * tn.tiles_n;
+    int wg = (int)blockIdx.x;
+    if (wg < n_nt + n_tn) {
+        wg += first;
+        if (wg >= n_nt + n_tn) wg -= n_nt + n_tn;
+    }
+    EpiArgs e{};
+    if (wg < n_nt) grid_tile<IN, LAY_NT, OUT, TB, TB, EPI_FULL, 2>(nt, wg, e, smem);
+    else if (wg < n_nt + n_tn) grid_tile<IN, LAY_TN, OUT, TB, TB, EPI_FULL, 2>(tn, wg - n_nt, e, smem);
+    else col_reduce(wg - n_nt - n_tn, r, (float*)smem);
+}
+
+GridArgs grid_args(const GemmLaunch& L) {
+    return GridArgs{L.A, L.B, L.C, L.M, L.N, L.K, L.lda, L.ldb, L.ldc, L.tiles_m, L.tiles_n};
+}
+
+template <int IN>
+hipError_t go_pair_t(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first, const ColReduceArgs& r) {
+    const void* fn = nt.tbm == 256 ? (const void*)gemmt_pair_kernel<IN, 256>
+                                   : (const void*)gemmt_pair_kernel<IN, 128>;
+    GridArgs a = grid_args(nt), b = grid_args(tn);
+    int first = tn_first ? nt.tiles_m * nt.tiles_n : 0;
+    ColReduceArgs c = r;
+    void* args[] = {&a, &b, &first, &c};
+    const int blocks =
+        nt.tiles_m * nt.tiles_n + tn.tiles_m * tn.tiles_n + (r.N > 0 ? col_reduce_blocks(r.N) : 0);
+    return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, nt.stream);
 }
 
 template <int IN, int LAY, int OUT, int EPI>
@@ -366,15 +416,12 @@ hipError_t go_t(const GemmLaunch& L) {
         fn = L.stages == 4 ? (const void*)gemmt_kernel<IN, LAY, OUT, 128, 128, EPI, 4>
                            : (const void*)gemmt_kernel<IN, LAY, OUT, 128, 128, EPI, 2>;
     if (!fn) return hipErrorInvalidValue;
-    const char* a = L.A;
-    const char* b = L.B;
-    char* c = L.C;
-    int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc;
-    int tiles_m = L.tiles_m, tiles_n = L.tiles_n, kchunk = L.kchunk;
+    GridArgs a = grid_args(L);
+    int kchunk = L.kchunk;
     int64_t zs = L.c_zstride;
     EpiArgs e = L.e;
-    void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &tiles_m, &tiles_n, &kchunk, &zs, &e};
-    return hipLaunchKernel(fn, dim3((unsigned)(tiles_m * tiles_n), (unsigned)L.splits), dim3(256),
+    void* args[] = {&a, &kchunk, &zs, &e};
+    return hipLaunchKernel(fn, dim3((unsigned)(L.tiles_m * L.tiles_n), (unsigned)L.splits), dim3(256),
                            args, 0, L.stream);
 }
 
@@ -404,6 +451,17 @@ hipError_t launch_gemmt(const GemmLaunch& L) {
     if (L.in == IN_BF16 && L.layout == LAY_TN) return by_out<IN_BF16, LAY_TN>(L);
     if (L.in == IN_F16 && L.layout == LAY_NT) return by_out<IN_F16, LAY_NT>(L);
     if (L.in == IN_F16 && L.layout == LAY_TN) return by_out<IN_F16, LAY_TN>(L);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gemmt_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
+                             const ColReduceArgs& r) {
+    for (const GemmLaunch* L : {&nt, &tn})
+        if (L->splits != 1 || L->tbm != nt.tbm || L->tbn != nt.tbm || (nt.tbm != 128 && nt.tbm != 256) ||
+            L->in != nt.in)
+            return hipErrorInvalidValue;
+    if (nt.in == IN_BF16) return go_pair_t<IN_BF16>(nt, tn, tn_first, r);
+    if (nt.in == IN_F16) return go_pair_t<IN_F16>(nt, tn, tn_first, r);
     return hipErrorInvalidValue;
 }
 

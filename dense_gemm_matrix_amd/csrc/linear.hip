@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cmath>
 
 #include "dgemm.h"
 #include "dgemm_internal.h"
@@ -120,7 +121,8 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     // Against a slice-K tile a split also pays its second launch's gap on a stream:
     // 27 x 165 with 3571 k in 8 bits took 9.1 us in 14 pieces, 5.0 in slices, where
     // the estimates are 5.2 and 7.3.
-    best_us *= slice ? 0.65 : SPLIT_MARGIN;
+    const double margin = slice ? 0.65 : SPLIT_MARGIN;
+    best_us *= margin;
     for (const TileCand& t : TILES_T)
         for (int s = 2; s <= MAX_SPLITS && s <= nk; ++s) {
             const Plan p = plan_pieces(t, bk, M, N, K, s, ws_avail);
@@ -132,7 +134,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
             }
         }
     best.layout = layout;
-    if (us_out) *us_out = slice && best.splits == 1 ? best_us / 0.65 : best_us;
+    if (us_out) *us_out = best.splits == 1 ? best_us / margin : best_us;
     return best;
 }
 
@@ -358,25 +360,49 @@ double pair_us(int64_t ta, double wa, int64_t tb, double wb) {
     return t;
 }
 
+// `ta` grid tiles of ka terms and `tb` of kb, one workgroup of 256 x 256 per CU or
+// two of 128 x 128, in estimate_us's terms.  256 x 256: the schedule above, faster
+// where it leaves CUs idle (a half-filled chip clocks higher: a step 1.2 us, not
+// 1.7).  128 x 128: the work at the rate of shared CUs, and a tail where the last
+// round is not full, or the longest tile.  Within 15 % of 18 layers from 600 x 800 x 3000 to 5000^3.
+double pair_grid_us(const TileCand& t, int in, int64_t ta, int ka, int64_t tb, int kb, bool& b_first) {
+    const double step = step_us(in) * t.bm * t.bn / 65536.0 / t.eff;
+    const double wa = (double)ceil_div(ka, t_step(in)) * step + 1.0;
+    const double wb = (double)ceil_div(kb, t_step(in)) * step + 1.0;
+    const double work = ((double)ta * wa + (double)tb * wb) / NUM_CU;
+    b_first = wb > wa;
+    if (t.pair2 > 0.0) {
+        const double rounds = (double)(ta + tb) / (2 * NUM_CU);
+        const double tail = (std::ceil(rounds) - rounds) * std::min(wa, wb);
+        return std::max((work * 1.05 + tail) * t.pair2 / 2, std::max(wa, wb) * 1.05);
+    }
+    const double us = b_first ? pair_us(tb, wb, ta, wa) : pair_us(ta, wa, tb, wb);
+    return us * (0.7 + 0.3 * work / us);
+}
+
 // One launch saves the other launches' time (2.4 us of host time each, 1.5 to 2 us
 // of a graph) and fills the CUs that one product's tiles leave idle; the longer
-// tiles go first where that ends earlier.  In us, bf16, M x N x K, apart / together:
-//   256 x 256 x 256     14.7 /  6.8    1000 x 512 x  512   19.9 / 12.6
-//   917 x 415 x 1035    24.4 / 15.1    2000 x 300 x  600   25.7 / 18.1
-//   600 x 800 x 3000    29.4 / 33.2 (not taken)
-// and in fp32 256^3 20.6 / 8.0, 917 x 415 x 1035 47.0 / 30.8, 1024^3 69 / 51.
+// tiles go first.  The whole backward pass in us, M x N x K, apart / together:
+//   bf16   256 x  256 x  256    14.7 /   6.8   (slice-K tiles)
+//          917 x  415 x 1035    24.4 /  15.1   (slice-K)
+//          600 x  800 x 3000    29.5 /  20.4   (128 x 128)
+//         1024 x 2048 x 2048    43.1 /  33.6   (128 x 128)
+//         2048 x 4096 x 4096     140 /   123   (256 x 256)
+//         4096 x 4096 x 4096     235 /   226   (256 x 256)
+//         5000 x 5000 x 5000     532 /   511   (256 x 256)
+//   fp32   256^3 20.6 / 8.0, 917 x 415 x 1035 47.0 / 30.8, 1024^3 69 / 51
 PairPlan plan_pair(int in, int M, int N, int K, bool dA, bool dB, bool sums, uint64_t ws) {
     PairPlan r{};
     const int f = in_esize(in) == 4 ? IN_F32 : IN_BF16;  // 3 x bf16 in fp32 arithmetic here
     int fm, fn, fs;
     const bool forced = forced_grid(fm, fn, fs);
-    const bool tile = forced && fm == fn && (fm == 32 || fm == 64);
-    if (tile && fs != 1 && fs != 4) return r;
-    if (forced && !tile) return r;
+    const bool tile = forced && fm == fn && (fm == 32 || fm == 64) && (fs == 1 || fs == 4);
+    const bool grid = forced && fm == fn && (fm == 128 || fm == 256) && fs == 1 && f == IN_BF16 && dA && dB;
+    if (forced && !tile && !grid) return r;
     double best = (double)((dA ? 1 : 0) + (dB ? 1 : 0) + (sums ? 1 : 0) - 1) * PAIR_GAP_US;
     if (dA) best += alone_us(in, LAY_NT, M, K, N, ws);
     if (dB) best += alone_us(in, LAY_TN, K, N, M, ws);
-    for (int a = 32; a <= 64; a += 32)
+    for (int a = 32; a <= 64 && !grid; a += 32)
         for (int b = 32; b <= 64; b += 32) {
             if ((!dA && a > 32) || (!dB && b > 32) || (tile && ((dA && a != fm) || (dB && b != fm)))) continue;
             const int64_t ta = dA ? ceil_div(M, a) * ceil_div(K, a) : 0;
@@ -391,10 +417,26 @@ PairPlan plan_pair(int in, int M, int N, int K, bool dA, bool dB, bool sums, uin
             r.nt = slice4(LAY_NT, a, N);
             r.tn = slice4(LAY_TN, b, M);
         }
+    if (f == IN_F32 || !dA || !dB || tile) return r;
+    for (const TileCand& t : TILES_T) {
+        if (grid && t.bm != fm) continue;
+        const int64_t ta = ceil_div(M, t.bm) * ceil_div(K, t.bn), tb = ceil_div(K, t.bm) * ceil_div(N, t.bn);
+        if (ta + tb > INT32_MAX / 2) continue;
+        bool tn_first;
+        const double us = pair_grid_us(t, in, ta, N, tb, M, tn_first);
+        if (!grid && us >= best) continue;
+        best = us;
+        r.use = true;
+        r.tn_first = tn_first;
+        r.nt = Plan{t.bm, t.bn, 1, N, 0, 0};
+        r.tn = Plan{t.bm, t.bn, 1, M, 0, 0};
+        r.nt.layout = LAY_NT;
+        r.tn.layout = LAY_TN;
+    }
     return r;
 }
 
-GemmLaunch slice_launch(int in, const Plan& p, int M, int N, int K, const void* X, int ldx, const void* Y,
+GemmLaunch pair_launch(int in, const Plan& p, int M, int N, int K, const void* X, int ldx, const void* Y,
                         int ldy, void* C, int ldc, hipStream_t stream) {
     GemmLaunch L{};
     L.in = in == IN_F32X3 ? IN_F32 : in;
@@ -402,7 +444,7 @@ GemmLaunch slice_launch(int in, const Plan& p, int M, int N, int K, const void* 
     L.tbm = p.bm;
     L.tbn = p.bn;
     L.layout = p.layout;
-    L.slice_waves = 4;
+    L.slice_waves = p.waves;
     L.splits = 1;
     L.epi = EPI_FULL;
     L.A = (const char*)X;
@@ -517,14 +559,14 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
     }
     ColReduceArgs sums{(const float*)w_part, dbias, b.chunks, b.ldp, dbias && b.chunks != 1 ? N : 0};
     if ((dA || dB) && M > SKINNY_M && N > 0 && K > 0) {
-        // A small layer: the products and the column sums in one launch.
+        // The products and the column sums in one launch where that is faster.
         const PairPlan p = plan_pair(in, M, N, K, dA, dB, sums.N > 0, (uint64_t)gemm_bytes);
         if (p.use) {
-            GemmLaunch nt = slice_launch(in, p.nt, M, K, N, dz, lddz, B, ldb, dA, ldda, s);
-            GemmLaunch tn = slice_launch(in, p.tn, K, N, M, A, lda, dz, lddz, dB, lddb, s);
+            GemmLaunch nt = pair_launch(in, p.nt, M, K, N, dz, lddz, B, ldb, dA, ldda, s);
+            GemmLaunch tn = pair_launch(in, p.tn, K, N, M, A, lda, dz, lddz, dB, lddb, s);
             if (!dA) nt.tiles_m = 0;
             if (!dB) tn.tiles_m = 0;
-            return launched(launch_slicet_pair(nt, tn, p.tn_first, sums));
+            return launched((p.nt.waves > 0 ? launch_slicet_pair : launch_gemmt_pair)(nt, tn, p.tn_first, sums));
         }
     }
     if (sums.N > 0 && launch_col_reduce(sums, s) != hipSuccess) return DGEMM_ERR_LAUNCH;

@@ -281,6 +281,8 @@ def test_backward_grid_tiles(grid_plan, tile, splits, fmt):
     grid_plan(*tile, splits)
     run_bwd(fmt, "same", 300, 270, 261, "silu", seed=8)
     run_bwd(fmt, "same", 520, 136, 390, "none", seed=9)
+    for want in (("dA",), ("dB",), ("dB", "dbias")):
+        run_bwd(fmt, "same", 390, 300, 136, "silu", seed=10, want=want)
 
 
 @pytest.mark.parametrize("tile, waves", [(32, 4), (32, 8), (64, 4)])
@@ -295,10 +297,11 @@ def test_backward_slice_tiles(grid_plan, tile, waves, fmt):
 
 @pytest.mark.parametrize("fmt", ["bf16", "f16", "f32", "f32x3"])
 @pytest.mark.parametrize("shape", [(50, 30, 20), (400, 70, 500), (90, 700, 150), (917, 415, 1035), (240, 1501, 430),
-                                   (2000, 300, 200), (33, 2000, 1000)], ids=lambda s: "x".join(map(str, s)))
+                                   (2000, 300, 200), (33, 2000, 1000),
+                                   (600, 801, 1500), (1030, 1100, 520)], ids=lambda s: "x".join(map(str, s)))
 def test_backward_products_together(fmt, shape):
-    """Small layers, whose products share a launch: tiles of 32 and 64 in both
-    orders, with fewer and more workgroups than CUs."""
+    """Layers whose products share a launch: small tiles in both orders, with fewer
+    and more workgroups than CUs, and grid tiles."""
     run_bwd(fmt, "same", *shape, "silu", seed=60)
     run_bwd(fmt, "f32", *shape, "none", seed=61, want=("dA", "dB"))
     run_bwd(fmt, "same", *shape, "relu", seed=62, want=("dB", "dbias"))
