@@ -282,8 +282,8 @@ int gemm_ex_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
  * errors and execution as gemm_ex; a workspace allows split plans as in gemm_ex
  * (gemm_act_plan tells the bytes), never a Stream-K plan.
  *
- * At most 16 rows of bf16 / fp16 run a kernel of their own that streams B
- * through registers (tokens being generated: bound by reading B once).
+ * At most 16 rows of bf16, fp16 and fp32 run a kernel of their own that streams
+ * B through registers (tokens being generated: bound by reading B once).
  */
 int gemm_act(int in, int out, int M, int N, int K,
              const void* A, int lda,
@@ -311,8 +311,10 @@ int gemm_act_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
  * (not wanted); A is read only for dB, B only for dA, and with act =
  * DGEMM_ACT_NONE Z is not read.  relu'(0) = 0.  dZ is rounded once to the input
  * format for the products (unless it is dC itself); dbias sums unrounded fp32
- * values, in an order that depends on the shape only: results are
- * deterministic.  Empty sums are zero: M == 0 writes dB = 0 and dbias = 0, N == 0
+ * values, in an order that depends on the shape only.  Results are
+ * deterministic; the products' order of sums follows the plan, which depends on
+ * the sizes, formats, workspace and which of dA and dB are wanted (small
+ * DGEMM_IN_F32X3 layers run in fp32 arithmetic).  Empty sums are zero: M == 0 writes dB = 0 and dbias = 0, N == 0
  * writes dA = 0.  Outputs overlap no input and no other output.
  *
  * The workspace (16-byte aligned) holds dZ, partial column sums, transposes
