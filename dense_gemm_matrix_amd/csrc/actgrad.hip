@@ -4,8 +4,11 @@
 //
 // dZ is written in the products' input format: the matrix instructions take
 // 16-bit operands, so for 16-bit layers this is the one rounding between dC and
-// the gradients (half a step, 2^-9 relative for bf16, below the rounding of the
+// the gradients (half a step, 2^-8 relative for bf16, as the rounding of the
 // gradients it feeds).  dbias sums the unrounded fp32 values.
+//
+// Bound by memory: 4096 x 4096 bf16, dC and Z read and dZ written once, 22-26 us
+// (100 MB at 3.9 to 4.6 TB/s), beside 205 us of products.
 
 #include "kern_common.h"
 

@@ -32,6 +32,11 @@
 // outputs use it, and fp32 outputs (IN_F8W) widen the e4m3 values to bf16 in
 // registers, exactly, and take the bf16 instruction, whose sums are fp32.
 //
+// At 4096^3, one launch of 256 workgroups: 16-bit NT 111 us, TN 113 (1.2 PFLOP/s,
+// at the power cap); e4m3 with bias, gelu_tanh and a bf16 C 59-61 us (2.3 PFLOP/s):
+// a step takes 1.35 us, the matrix pipe busy 57 % of it, LDS near its rate, and the
+// epilogue of the single round is not hidden.
+//
 // Edges: rows past the output read zeros or feed unstored outputs; k-rows past K
 // fall outside the descriptors and read zeros; K-contiguous rows' bytes past K
 // (row padding) are zeroed in LDS for both operands, since 0 * NaN is a NaN.

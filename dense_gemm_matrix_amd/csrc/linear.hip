@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cmath>
 
 #include "dgemm.h"
 #include "dgemm_internal.h"

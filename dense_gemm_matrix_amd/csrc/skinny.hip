@@ -26,6 +26,9 @@
 // kernel waits for memory, and the sums are fp32 (the 8-bit instruction's are not
 // quite: gemmt.hip).
 //
+// Measured: 1 x 4096 x 4096 bf16 11.5 us (2.9 TB/s; 128 workgroups, each with all
+// the requests that a CU keeps in flight), 16 x 4096 x 4096 e4m3 7.1 us (2.4 TB/s).
+//
 // Rows past M come as zeros from A's resource.
 
 #include <type_traits>

@@ -205,3 +205,19 @@ def test_backward_in_place_empty_and_without_dweight():
     e = torch.empty(0, 300, dtype=torch.bfloat16, device="cuda")
     _, dw = dg.rms_norm_backward(e, e, w, torch.empty(0, device="cuda"))
     assert bool((dw == 0).all())
+
+
+@pytest.mark.parametrize("f8", [False, True])
+def test_more_rows_than_a_launch_holds(f8):
+    """2^25 + 5 rows of 8 columns (16 lanes each): two launches; the rows behind the
+    second one's start are those of a call on them alone."""
+    M, N, cut = (1 << 25) + 5, 8, 1 << 25
+    X = torch.randn(4096, N, generator=torch.Generator().manual_seed(70)).bfloat16().cuda().repeat(M // 4096 + 1, 1)[:M]
+    w = torch.linspace(0.5, 1.5, N, device="cuda")
+    out = dg.rms_norm(X, w, residual=X, f8=f8, keep=True, eps=EPS)
+    some = dg.rms_norm(X[:4096], w, residual=X[:4096], f8=f8, keep=True, eps=EPS)
+    for name, t in out.items():
+        t, want = (t.view(torch.uint8), some[name].view(torch.uint8)) if name == "Y" and f8 else (t, some[name])
+        for at in (0, cut - 4096):
+            assert torch.equal(t[at:at + 4096], want), (name, at)
+        assert torch.equal(t[cut:], want[:M - cut]), name
