@@ -50,70 +50,85 @@ __device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[
 constexpr int AG_COLS = 512;     // columns per workgroup: 64 lanes x 8
 
 // One workgroup of W waves: columns blockIdx.x * 512 .., rows blockIdx.y *
-// rows_per ...  Wave w takes every W-th row; the waves' column sums are added in
-// LDS in wave order and go to the workspace, one row of partial sums per
+// rows_per ...  T lanes share a row, so narrow layers put 64 / T rows into a wave
+// (64 columns, 300000 rows: 497 us with a wave per row, 38.5 with 16 lanes,
+// the column sums' second step included); the
+// W 64 / T rows of a pass interleave.  The column sums of a workgroup's lanes are
+// added in LDS in order and go to the workspace, one row of partial sums per
 // blockIdx.y.  Sixteen waves where one workgroup takes all the rows.
-template <int CF, int DF, int W>
+template <int CF, int DF, int W, int T>
 __global__ __launch_bounds__(64 * W) void act_grad_kernel(ActGradArgs a) {
-    __shared__ float sums[W][AG_COLS];
+    constexpr int RP = 64 / T;  // rows per wave and pass
+    __shared__ float sums[W * AG_COLS];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int c = (int)blockIdx.x * AG_COLS + lane * 8;
+    const int lr = lane / T;
+    const int c = (int)blockIdx.x * AG_COLS + (lane % T) * 8;
     const int nvalid = a.N - c;
     const int64_t r0 = (int64_t)blockIdx.y * a.rows_per;
     const int64_t r1 = r0 + a.rows_per < a.M ? r0 + a.rows_per : a.M;
     float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (nvalid > 0) {
 #pragma unroll 2
-        for (int64_t row = r0 + wave; row < r1; row += W) {
-            Row8<CF> x, zz;
-            const auto rc = make_rsrc(a.dC + row * a.lddc * fmt_es<CF>, (int64_t)a.N * fmt_es<CF>);
-            x.load(rc, (uint32_t)c * fmt_es<CF>, nvalid);
-            float d[8];
-            if (a.Z) {
-                const auto rz = make_rsrc(a.Z + row * a.ldz * fmt_es<CF>, (int64_t)a.N * fmt_es<CF>);
-                zz.load(rz, (uint32_t)c * fmt_es<CF>, nvalid);
-                float z[8];
-                x.get(d);
-                zz.get(z);
-                apply_act_grad(d, z, a.act);
-            } else {
-                x.get(d);
-            }
+    for (int64_t row = r0 + wave * RP; row < r1; row += W * RP) {
+        const int n = r1 - row < RP ? (int)(r1 - row) : RP;  // this wave's rows
+        auto rows = [&](const char* p, int ld, int es) {
+            return make_rsrc(p + row * ld * es, ((int64_t)(n - 1) * ld + a.N) * es);
+        };
+        // Rows and columns outside load as 0 and are not stored.
+        auto at = [&](int ld, int es) {
+            return lr < n && nvalid > 0 ? (uint32_t)((lr * ld + c) * es) : OOB_LANE;
+        };
+        Row8<CF> x, zz;
+        x.load(rows(a.dC, a.lddc, fmt_es<CF>), at(a.lddc, fmt_es<CF>), nvalid);
+        float d[8];
+        if (a.Z) {
+            zz.load(rows(a.Z, a.ldz, fmt_es<CF>), at(a.ldz, fmt_es<CF>), nvalid);
+            float z[8];
+            x.get(d);
+            zz.get(z);
+            apply_act_grad(d, z, a.act);
+        } else {
+            x.get(d);
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += d[j];
-            if (a.dZ) {
-                const auto rd = make_rsrc(a.dZ + row * a.lddz * fmt_es<DF>, (int64_t)a.N * fmt_es<DF>);
-                Row8<DF> o;
-                o.set(d);
-                o.store(rd, (uint32_t)c * fmt_es<DF>, nvalid);
-            }
+        for (int j = 0; j < 8; ++j) sum[j] += d[j];
+        if (a.dZ) {
+            Row8<DF> o;
+            o.set(d);
+            o.store(rows(a.dZ, a.lddz, fmt_es<DF>), at(a.lddz, fmt_es<DF>), nvalid);
         }
     }
     if (!a.part) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sums[wave][lane * 8 + j] = sum[j];
+    for (int j = 0; j < 8; ++j) sums[wave * AG_COLS + lane * 8 + j] = sum[j];
     __syncthreads();
-    for (int j = threadIdx.x; j < AG_COLS; j += 64 * W) {
+    for (int j = threadIdx.x; j < T * 8; j += 64 * W) {
         const int col = (int)blockIdx.x * AG_COLS + j;
         if (col >= a.N) break;
-        float v = sums[0][j];
+        float v = sums[j];
 #pragma unroll
-        for (int w = 1; w < W; ++w) v += sums[w][j];
+        for (int q = 1; q < W * RP; ++q) v += sums[q * T * 8 + j];
         a.part[(int64_t)blockIdx.y * a.ldp + col] = v;
     }
 }
 
-template <int CF, int DF>
+template <int CF, int DF, int T>
 hipError_t go_ag(const ActGradArgs& a, hipStream_t stream) {
     ActGradArgs b = a;
     void* args[] = {&b};
     const bool one = a.M > 16 && a.M <= a.rows_per;
-    const void* fn = one ? (const void*)act_grad_kernel<CF, DF, 16> : (const void*)act_grad_kernel<CF, DF, 4>;
+    const void* fn = one ? (const void*)act_grad_kernel<CF, DF, 16, T> : (const void*)act_grad_kernel<CF, DF, 4, T>;
     return hipLaunchKernel(fn,
                            dim3((unsigned)((a.N + AG_COLS - 1) / AG_COLS),
                                 (unsigned)((a.M + a.rows_per - 1) / a.rows_per)),
                            dim3(one ? 1024 : 256), args, 0, stream);
+}
+
+template <int CF, int DF>
+hipError_t ag_by_size(const ActGradArgs& a, hipStream_t stream) {
+    if (a.N <= 128) return go_ag<CF, DF, 16>(a, stream);
+    if (a.N <= 256) return go_ag<CF, DF, 32>(a, stream);
+    return go_ag<CF, DF, 64>(a, stream);
 }
 
 __global__ __launch_bounds__(256) void col_reduce_kernel(ColReduceArgs a) {
@@ -143,18 +158,27 @@ __global__ __launch_bounds__(256) void transpose32_kernel(const float* X, int ld
 // fewer than 8 rows each, and up to 64 rows in one chunk, whose sums are dbias
 // without a second launch (4 rows for each of 16 waves; 16 rows each measured
 // 16-35 us where two launches take 10).
-int act_grad_rows(int M) {
+// Up to 64 rows: one workgroup's.  Else 16 rows or more per workgroup from 4096 rows
+// on (4096 x 4096, column sums alone: 20.5 us with 8 rows, 19.1 with 16), and 512 to
+// 2048 workgroups.
+int act_grad_rows(int M, int N) {
     if (M <= 64) return 64;
-    const int64_t r = ((int64_t)M + 255) / 256;
-    return (int)(r < 8 ? 8 : (r + 3) / 4 * 4);
+    const int blocks = (N + AG_COLS - 1) / AG_COLS;
+    const int most = blocks >= 4 ? 512 : 2048 / (blocks > 0 ? blocks : 1);
+    const int unit = N <= 128 ? 16 : N <= 256 ? 8 : 4;  // rows of a pass of four waves
+    const int64_t share = ((int64_t)M + 255) / 256;
+    int64_t r = ((int64_t)M + most - 1) / most;
+    if (r < (share < 16 ? share : 16)) r = share < 16 ? share : 16;
+    if (r < 8) r = 8;
+    return (int)((r + unit - 1) / unit * unit);
 }
 
 hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream) {
-    if (cf == OUT_F32 && df == OUT_F32) return go_ag<OUT_F32, OUT_F32>(a, stream);
-    if (cf == OUT_F32 && df == OUT_BF16) return go_ag<OUT_F32, OUT_BF16>(a, stream);
-    if (cf == OUT_F32 && df == OUT_F16) return go_ag<OUT_F32, OUT_F16>(a, stream);
-    if (cf == OUT_BF16 && df == OUT_BF16) return go_ag<OUT_BF16, OUT_BF16>(a, stream);
-    if (cf == OUT_F16 && df == OUT_F16) return go_ag<OUT_F16, OUT_F16>(a, stream);
+    if (cf == OUT_F32 && df == OUT_F32) return ag_by_size<OUT_F32, OUT_F32>(a, stream);
+    if (cf == OUT_F32 && df == OUT_BF16) return ag_by_size<OUT_F32, OUT_BF16>(a, stream);
+    if (cf == OUT_F32 && df == OUT_F16) return ag_by_size<OUT_F32, OUT_F16>(a, stream);
+    if (cf == OUT_BF16 && df == OUT_BF16) return ag_by_size<OUT_BF16, OUT_BF16>(a, stream);
+    if (cf == OUT_F16 && df == OUT_F16) return ag_by_size<OUT_F16, OUT_F16>(a, stream);
     return hipErrorInvalidValue;
 }
 

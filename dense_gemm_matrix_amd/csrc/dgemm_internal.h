@@ -287,7 +287,7 @@ struct ActGradArgs {
     float* part;
     int M, N, lddc, ldz, lddz, ldp, rows_per, act;
 };
-int act_grad_rows(int M);
+int act_grad_rows(int M, int N);
 hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream);
 hipError_t launch_col_reduce(const ColReduceArgs& a, hipStream_t stream);
 hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,

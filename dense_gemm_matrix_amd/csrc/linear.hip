@@ -269,7 +269,7 @@ BwdParts bwd_parts(int in, int cfmt, int M, int N, int K, int act, bool products
     b.own_dz = products && (act != DGEMM_ACT_NONE || cfmt != dfmt);
     b.lddz = (int)up(N, 16 / es);
     b.ldp = (int)up(N, 4);
-    b.chunks = (int)ceil_div(M, act_grad_rows(M));
+    b.chunks = (int)ceil_div(M, act_grad_rows(M, N));
     b.dz = b.own_dz ? up((int64_t)M * b.lddz * es, WS_ALIGN) : 0;
     // One chunk's column sums are dbias itself.
     b.part = dbias && b.chunks != 1 ? up((int64_t)b.chunks * b.ldp * 4, WS_ALIGN) : 0;
@@ -552,7 +552,7 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
     if (M > 0 && N > 0 && (b.own_dz || dbias)) {
         const ActGradArgs a{(const char*)dC, (const char*)mZ.p, b.own_dz ? w : nullptr,
                             !dbias ? nullptr : b.chunks == 1 ? dbias : (float*)w_part, M, N, lddc, ldz, b.lddz, b.ldp,
-                            act_grad_rows(M), act};
+                            act_grad_rows(M, N), act};
         if (launch_act_grad(a, cf, out_format(in, DGEMM_OUT_SAME), s) != hipSuccess)
             return DGEMM_ERR_LAUNCH;
     }

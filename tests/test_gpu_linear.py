@@ -314,6 +314,15 @@ def test_backward_parts(want):
         run_bwd("f32", "f32", 70, 36, 90, act, seed=10, want=want)
 
 
+@pytest.mark.parametrize("N", [1, 8, 64, 65, 128, 130, 256, 257, 513, 1100])
+@pytest.mark.parametrize("M", [17, 64, 65, 131, 1003])
+def test_backward_widths(M, N):
+    """Several rows per wave of narrow layers, whole and part passes, one and many
+    workgroups per column block."""
+    run_bwd("bf16", "same", M, N, 24, "silu", seed=M + N)
+    run_bwd("bf16", "f32", M, N, 24, "gelu", seed=M + N + 1, want=("dbias",))
+
+
 def test_backward_against_differences():
     """The gradient of sum(w o C) by central differences of the plain 64-bit
     forward, along random directions.  The fp32 kernel's own error is within
