@@ -142,23 +142,28 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 // K-contiguous B: strips of 16 columns, 16 waves, never split (a strip of 16
 // outputs already reads whole lines).
 //
-// B stored along the output: strips of 32 columns with 16 waves, or from 160 strips of 64 columns on
-// (enough to fill the CUs) 64 with 8 waves: 1 x 12288 x 4096 36 us with 32, 23 with
-// 64; 1 x 8192 x 4096 14.5 with 32, 15.7 with 64.  Deep K leaves a wave many steps
-// one after another, each a round of memory latency; given a workspace, K is then
-// split over workgroups, in wider strips (longer pieces of B's rows), for a second
-// launch of about 2.7 us in a graph and 3 us more on a stream: from K = 8192 on,
-// up to 8 pieces of at least 512 k (16 from K = 16384 on) and 256 workgroups.  One
-// row in a replayed graph, B in the last-level cache / from HBM, in us:
-//                      unsplit        split
-//   2048 x 8192      18.5 / 30.5   11.9 / 14.6  (128 columns, 8 pieces)
-//   1024 x 16384     30.3 / 54.3   14.0 / 17.4  (128, 16)
-//   4096 x 4096      12.0 / 18.1   11.4 / 13.2  (128, 8; on a stream 12.0 / 14.6
-//                                  from the cache, so kept unsplit)
-//   512 x 4104        6.3 /  9.6    7.8 /  8.8  (128, 8; kept unsplit)
-// More rows make the partial products bigger and the wide strips' sums longer: 16
-// rows of 4096 x 4096 take 14.9 / 16.1 in 128 columns and 8 pieces, 13.0 / 14.6 in
-// 64 columns and 4.
+// B stored along the output: strips of 32 columns with 16 waves, or from 160 strips of
+// 64 columns on (enough to fill the CUs) 64 with 8 waves: 1 x 12288 x 4096 36 us with
+// 32, 23 with 64; 1 x 8192 x 4096 14.5 with 32, 15.7 with 64.  Deep K leaves a wave many
+// steps one after another, each a round of memory latency, and half-line strips waste
+// what HBM delivers.  Given a workspace, K is then split over workgroups, in strips of
+// 128 columns (fp32 64), for a second launch: up to 8 pieces of at least 512 k (16
+// from K = 16384 on) and 256 workgroups.  A piece has an odd number of 32-k steps:
+// with an even one and a power-of-two pitch, all pieces start on the same memory
+// channels (1 x 4096 x 14336 in 8 pieces of 56 steps 32.6 us, of 57 steps 24.0).
+// In us, B in the last-level cache / from HBM (twelve weights in turn):
+//                         unsplit        split
+//    1 x 4096 x  4096    8.9 / 17.7    8.9 / 12.3
+//   16 x 4096 x  4096   12.4 / 20.6   11.3 / 13.7
+//    4 x 6144 x  4096   12.4 / 20.1   13.2 / 15.7
+//    1 x 5120 x  5120   18.3 / 29.8   13.2 / 15.3
+//    1 x 4096 x  6144   15.3 / 24.2   13.7 / 15.8
+//   16 x 3000 x  5000   14.7 / 22.4   11.9 / 15.3
+//    1 x 2048 x  8192   18.5 / 30.5    9.5 / 13.9
+//    1 x 2048 x  4096    6.9 / 10.0    8.2 /  9.2   (kept unsplit)
+//    1 x 8192 x  4096   14.4 / 19.4   16.6 / 19.8   (kept unsplit: 256 strips of 32)
+//    1 x  512 x  4104    6.3 /  9.6    7.8 /  8.8   (kept unsplit)
+//   fp32 1 x 5120 x 5120 21.0 / 33.1   22.1 / 26.0
 Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     Plan p{SKINNY_M, 16, 1, K, 0, 0};
     p.waves = 16;
@@ -169,6 +174,11 @@ Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     }
     auto strips = [&](int cols, int splits) {  // splits = 0 if it does not fit
         Plan q = plan_pieces(TileCand{SKINNY_M, cols, 1, 0, 0, 1, 1}, 32, M, N, K, splits, ws_avail);
+        if (q.splits > 1 && q.kchunk % 64 == 0) {  // an odd number of steps
+            q.kchunk += 32;
+            q.splits = (int)ceil_div(K, q.kchunk);
+            q.ws_bytes = (int64_t)q.splits * M * q.ldw * 4;
+        }
         q.waves = cols == 32 ? 16 : 8;
         q.kind = PLAN_SKINNY;
         return q;
@@ -179,10 +189,10 @@ Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
         const Plan q = strips(fn, fs);
         if (q.splits > 0) return q;
     }
-    if (K >= 8192) {
-        const int cols = M <= 4 && !f32 ? 128 : 64, most = K >= 16384 ? 16 : 8;
-        const int wgs = (int)ceil_div(N, cols);
-        const int s = (int)std::min<int64_t>(std::min(most, K / (M <= 4 ? 512 : 1024)), 256 / wgs);
+    if (K >= 8192 || (K > 4096 && N >= 2048) || (K == 4096 && N >= 4096 && N < 8192)) {
+        const int cols = f32 ? 64 : 128, most = K >= 16384 ? 16 : 8;
+        const int64_t wgs = ceil_div(N, cols);
+        const int s = (int)std::min<int64_t>(std::min(most, K / 512), 256 / wgs);
         if (s >= 2) {
             const Plan q = strips(cols, s);
             if (q.splits > 1) return q;

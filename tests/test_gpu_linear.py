@@ -104,6 +104,15 @@ def test_forward_few_row_strips(grid_plan, cols, splits, fmt):
         run_act(fmt, "f32", M, N, K, "none", seed=30 + i, ws_bytes=ws, preact=False)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 4100, 4096), (16, 2050, 4130), (5, 130, 8200), (3, 70, 16500)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_forward_few_rows_deep(fmt, shape):
+    """The planner's own splits of few-row products, K a multiple of their step and not."""
+    assert dg.gemm_act_plan(fmt, *shape, 1 << 24, fmt != "f32")["splits"] > 1
+    run_act(fmt, "same", *shape, "silu", seed=20, ws_bytes=1 << 24)
+
+
 def test_integers_are_exact():
     """Small integers: every sum is exact, so the output is its one rounding."""
     for M, N, K in [(1, 70, 100), (16, 40, 64), (40, 72, 96), (300, 264, 200)]:
