@@ -139,8 +139,12 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 
 // At most SKINNY_M rows.
 //
-// K-contiguous B: strips of 16 columns, 16 waves, never split (a strip of 16
-// outputs already reads whole lines).
+// K-contiguous B: strips of 16 columns, never split (a strip of 16 outputs already
+// reads whole lines).  16 waves while each strip has a CU to itself; of more strips
+// a CU holds several, with 8 waves, or 4 where K is at most 16 steps of 128 bytes
+// (e4m3 from HBM, 16 / 8 / 4 waves in us: 1 x 4096 x 4096 5.7 / 5.8 / -, 1 x 14336 x
+// 4096 18.1 / 14.0 / 13.6, 1 x 8192 x 8192 17.7 / 15.2 / 15.7, 1 x 60000 x 2048
+// - / 29.7 / 22.8).
 //
 // B stored along the output: strips of 32 columns with 16 waves, or from 160 strips of
 // 64 columns on (enough to fill the CUs) 64 with 8 waves: 1 x 12288 x 4096 36 us with
@@ -170,6 +174,7 @@ Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     p.kind = PLAN_SKINNY;
     if (layout == LAY_NT) {
         p.layout = LAY_NT;
+        if (ceil_div(N, 16) > NUM_CU) p.waves = (int64_t)K * in_esize(in) <= 16 * 128 ? 4 : 8;
         return p;
     }
     auto strips = [&](int cols, int splits) {  // splits = 0 if it does not fit

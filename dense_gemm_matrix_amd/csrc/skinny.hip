@@ -38,7 +38,6 @@
 namespace dgemm {
 namespace {
 
-constexpr int NT_WAVES = 16;  // waves that share a strip's K in the NT kernel
 
 template <int IN>
 __device__ __forceinline__ f32x4 mfma_16(u32x4 a, u32x4 b, f32x4 c) {
@@ -390,18 +389,25 @@ hipError_t nn_by_out(const GemmLaunch& L) {
     return hipErrorInvalidValue;
 }
 
-template <int IN, int OUT>
-hipError_t go_nt(const GemmLaunch& L) {
-    if (L.tbn != 16 || L.slice_waves != NT_WAVES || L.splits != 1 || L.epi != EPI_FULL)
-        return hipErrorInvalidValue;
+template <int IN, int OUT, int W>
+hipError_t go_nt_w(const GemmLaunch& L) {
     const char* a = L.A;
     const char* b = L.B;
     char* c = L.C;
     int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc, strips = L.tiles_n;
     EpiArgs e = L.e;
     void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &strips, &e};
-    return hipLaunchKernel((const void*)skinny_nt_kernel<IN, OUT, NT_WAVES>, dim3((unsigned)strips),
-                           dim3(64 * NT_WAVES), args, 0, L.stream);
+    return hipLaunchKernel((const void*)skinny_nt_kernel<IN, OUT, W>, dim3((unsigned)strips), dim3(64 * W),
+                           args, 0, L.stream);
+}
+
+template <int IN, int OUT>
+hipError_t go_nt(const GemmLaunch& L) {
+    if (L.tbn != 16 || L.splits != 1 || L.epi != EPI_FULL) return hipErrorInvalidValue;
+    if (L.slice_waves == 16) return go_nt_w<IN, OUT, 16>(L);
+    if (L.slice_waves == 8) return go_nt_w<IN, OUT, 8>(L);
+    if (L.slice_waves == 4) return go_nt_w<IN, OUT, 4>(L);
+    return hipErrorInvalidValue;
 }
 
 template <int FMT>

@@ -416,6 +416,18 @@ def test_f8(od, shape):
     run_f8(*shape, od, acts[(i + 3) % 5], seed=i, bias=i % 2 == 0, residual=i % 2 == 1)
 
 
+@pytest.mark.parametrize("shape", [(3, 4109, 40), (16, 4200, 2050), (1, 4100, 5000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_few_rows_of_wide_outputs(shape):
+    """More strips than CUs: fewer waves each, short and long K; the same strips for
+    the 16-bit and fp32 gradients of A."""
+    M, N, K = shape
+    run_f8(M, N, K, torch.bfloat16, "silu", seed=31)
+    run_f8(M, N, K, torch.float32, "none", seed=32)
+    run_bwd("bf16", "same", M, K, N, "silu", seed=33, want=("dA",))
+    run_bwd("f32", "f32", M, K, N, "silu", seed=34, want=("dA",))
+
+
 @pytest.mark.parametrize("tile, splits", [((256, 256), 1), ((128, 128), 1), ((256, 256), 2), ((128, 128), 3)])
 def test_f8_grid_tiles(grid_plan, tile, splits):
     grid_plan(*tile, splits)
