@@ -664,16 +664,16 @@ __device__ __forceinline__ void col_reduce(int block, const ColReduceArgs& a, fl
     float v = 0.0f;
     if (col < a.N) {
         const float* p = a.part + col;
-        int g = q;
-        for (; g + 16 * 15 < a.G; g += 16 * 16) {
+        for (int g = q; g < a.G; g += 16 * 16) {
             float x[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = p[(int64_t)(g + 16 * i) * a.ldp];
+            for (int i = 0; i < 16; ++i) {  // rows past G: the last one's value, not added
+                const int r = g + 16 * i < a.G ? g + 16 * i : a.G - 1;
+                x[i] = p[(int64_t)r * a.ldp];
+            }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v += x[i];
+            for (int i = 0; i < 16; ++i) v += g + 16 * i < a.G ? x[i] : 0.0f;
         }
-#pragma unroll 4
-        for (; g < a.G; g += 16) v += p[(int64_t)g * a.ldp];
     }
     lds[threadIdx.x] = v;
     __syncthreads();
