@@ -26,8 +26,9 @@
 // kernel waits for memory, and the sums are fp32 (the 8-bit instruction's are not
 // quite: gemmt.hip).
 //
-// Measured: 1 x 4096 x 4096 bf16 11.5 us (2.9 TB/s; 128 workgroups, each with all
-// the requests that a CU keeps in flight), 16 x 4096 x 4096 e4m3 7.1 us (2.4 TB/s).
+// Measured, weights from HBM: 1 x 4096 x 4096 bf16 12.3 us (2.7 TB/s, its second
+// launch included), 1 x 4096 x 14336 28.0 (4.2), 16 x 4096 x 4096 e4m3 7.2 (2.3),
+// 1 x 8192 x 8192 e4m3 15.3 (4.4).  Small ones are bound by latency.
 //
 // Rows past M come as zeros from A's resource.
 
