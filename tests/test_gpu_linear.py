@@ -627,3 +627,41 @@ def test_long_pitch_offsets_past_32_bits():
                      residual=padded(R, torch.bfloat16))
     dg.gemm_act(Ad, padded(B, torch.bfloat16), Cd, bias=b.cuda(), act="silu", residual=Rd)
     assert torch.equal(Cd, want)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=str)
+def test_long_pitch_backward_and_norm(dt):
+    """The same for the gradients (products apart and together) and the norm: equal,
+    bit for bit, to the calls on compact rows."""
+    M, N, K, pitch = 1100, 24, 40, 4000 * 1000 * 2 // dt.itemsize
+    A, B, _, dC = inputs(M, N, K, dt, 15)
+    Z = torch.randn(M, N, generator=gen(16)).to(dt)
+    big = torch.empty(M * pitch, dtype=dt, device="cuda")  # 8.8 GB
+    view = lambda cols, at: torch.as_strided(big, (M, cols), (pitch, 1), at)  # noqa: E731
+    Ad, dCd, Zd, dAd, Sd = view(K, 0), view(N, 64), view(N, 128), view(K, 192), view(K, 256)
+    for d, s in ((Ad, A), (dCd, dC), (Zd, Z)):
+        d.copy_(s)
+    Ac, dCc, Zc, Bd = (padded(t, dt) for t in (A, dC, Z, B))
+    fmt = "f32" if dt == torch.float32 else "bf16"
+    work = torch.empty(dg.gemm_act_bwd_workspace(fmt, M, N, K, "silu", dt != torch.float32)[1], dtype=torch.uint8,
+                       device="cuda")
+    for act in ("silu", "none"):
+        for want in ((True, True), (True, False), (False, True)):
+            got, ref = [], []
+            for a, c, z, da, out in ((Ad, dCd, Zd, dAd, got), (Ac, dCc, Zc, sentinel(M, K, dt), ref)):
+                dB = sentinel(K, N, dt) if want[1] else None
+                db = torch.full((N,), float("nan"), device="cuda")
+                dg.gemm_act_bwd(a, Bd, c, dA=da if want[0] else None, dB=dB, dbias=db, preact=z, act=act,
+                                workspace=work)
+                out += [t.clone() for t in (da if want[0] else None, dB, db) if t is not None]
+            assert all(torch.equal(g, r) for g, r in zip(got, ref)), (act, want)
+    w = torch.linspace(0.5, 1.5, K, device="cuda")
+    rstd = torch.empty(M, device="cuda")
+    dg.rmsnorm(Ad, w, dAd, residual=Ad, total=Sd, rstd=rstd)
+    ref = dg.rms_norm(Ac, w, residual=Ac, keep=True)
+    assert torch.equal(dAd, ref["Y"]) and torch.equal(Sd, ref["total"]) and torch.equal(rstd, ref["rstd"])
+    wsn = torch.empty(dg.rmsnorm_bwd_workspace(M, K), dtype=torch.uint8, device="cuda")
+    dw = torch.empty(K, device="cuda")
+    dg.rmsnorm_bwd(Ad, Sd, w, rstd, dAd, dtotal=Ad, dweight=dw, workspace=wsn)
+    dX, dwr = dg.rms_norm_backward(Ac, ref["total"], w, ref["rstd"], dtotal=Ac)
+    assert torch.equal(dAd, dX) and torch.equal(dw, dwr)
