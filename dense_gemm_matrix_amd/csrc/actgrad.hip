@@ -20,14 +20,14 @@ namespace {
 //   z Phi(z):                       Phi(z) + z phi(z)
 //   relu:                           z > 0
 // Far out, s (1 - s) is 0 while z^3 stays finite, so the product is 0; where
-// z^2 itself overflows, the factor is taken as 0 or 1 by z's sign.
+// z^2 itself overflows or z is infinite, the factor is taken as 0 or 1 by z's sign.
 template <int NE>
 __device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[NE], int act) {
     if (act >= ACT_GELU_TANH) {
-        const float a = gate_a(act), b = gate_b(act);
+        const float a = act == ACT_SILU ? 1.0f : GELU_A, b = act == ACT_SILU ? 0.0f : GELU_B;
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            const float s = gate(z[i], a, b);
+            const float s = sigmoid(z[i] * (a + b * z[i] * z[i]));
             const float f = s + z[i] * (s * (1.0f - s)) * (a + 3.0f * b * z[i] * z[i]);
             const float far = z[i] > 0.0f ? 1.0f : 0.0f;
             d[i] *= __builtin_fabsf(z[i]) > 1e4f ? far : f;

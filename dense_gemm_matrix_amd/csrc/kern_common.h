@@ -353,19 +353,22 @@ __device__ __forceinline__ void run_steps(int n, Load load, Use use) {
 //   gelu(z) = z Phi(z) = z (1 + erf(z / sqrt 2)) / 2
 //   gelu_tanh(z) = z (1 + tanh(t)) / 2 = z / (1 + exp(-2 t)),
 //     t = sqrt(2 / pi) (z + 0.044715 z^3)
-// so gelu_tanh and silu(z) = z / (1 + exp(-z)) are one form z / (1 + exp(-p(z)))
-// with p(z) = z (a + b z^2), evaluated with the hardware's exp2 and reciprocal
-// (1 ulp each).  As z falls, exp overflows to infinity and its reciprocal to 0:
-// the limit -0.  Infinite z gives infinity or, at -infinity, NaN (-inf * 0), as
-// the formula itself does in floating point; a NaN stays a NaN.
+// so gelu_tanh and silu(z) = z / (1 + exp(-z)) are one form z / (1 + exp(-p)), with
+// p = 2 t or z, evaluated with the hardware's exp2 and reciprocal (1 ulp each).  As p
+// falls, exp overflows to infinity and its reciprocal to 0: the limit -0.  Infinite z
+// gives infinity or, at -infinity, NaN (-inf * 0), as the formula itself does in
+// floating point; a NaN stays a NaN.  silu's p is z itself, not a cubic with a zero
+// coefficient: 0 * inf would make a NaN of silu(+inf).
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SQRT_2_PI = 0.7978845608028654f;
 constexpr float GELU_C = 0.044715f;
+constexpr float GELU_A = 2.0f * SQRT_2_PI;           // 2 t = z (GELU_A + GELU_B z^2)
+constexpr float GELU_B = 2.0f * SQRT_2_PI * GELU_C;
 
-// The sigmoid of p(z) = z (a + b z^2).
-__device__ __forceinline__ float gate(float z, float a, float b) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * (z * (a + b * z * z))));
+__device__ __forceinline__ float sigmoid(float p) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-LOG2E * p));
 }
+__device__ __forceinline__ float gelu_2t(float z) { return z * (GELU_A + GELU_B * z * z); }
 
 // Phi(z), the normal distribution's integral, from Abramowitz and Stegun's
 // 7.1.26: for x >= 0, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2) within 1.5e-7,
@@ -382,18 +385,15 @@ __device__ __forceinline__ float normal_cdf(float z) {
     return z < 0.0f ? q : 1.0f - q;
 }
 
-__device__ __forceinline__ float gate_a(int act) { return act == ACT_SILU ? 1.0f : 2.0f * SQRT_2_PI; }
-__device__ __forceinline__ float gate_b(int act) {
-    return act == ACT_SILU ? 0.0f : 2.0f * SQRT_2_PI * GELU_C;
-}
-
 // act applied to NE values; `act` is wave-uniform, so one branch serves them all.
 template <int NE>
 __device__ __forceinline__ void apply_act(float (&v)[NE], int act) {
-    if (act >= ACT_GELU_TANH) {
-        const float a = gate_a(act), b = gate_b(act);
+    if (act == ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) v[i] *= gate(v[i], a, b);
+        for (int i = 0; i < NE; ++i) v[i] *= sigmoid(v[i]);
+    } else if (act == ACT_GELU_TANH) {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) v[i] *= sigmoid(gelu_2t(v[i]));
     } else if (act == ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < NE; ++i) v[i] *= normal_cdf(v[i]);
