@@ -146,28 +146,46 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 // 4096 18.1 / 14.0 / 13.6, 1 x 8192 x 8192 17.7 / 15.2 / 15.7, 1 x 60000 x 2048
 // - / 29.7 / 22.8).
 //
-// B stored along the output: strips of 32 columns with 16 waves, or from 160 strips of
-// 64 columns on (enough to fill the CUs) 64 with 8 waves: 1 x 12288 x 4096 36 us with
-// 32, 23 with 64; 1 x 8192 x 4096 14.5 with 32, 15.7 with 64.  Deep K leaves a wave many
-// steps one after another, each a round of memory latency, and half-line strips waste
-// what HBM delivers.  Given a workspace, K is then split over workgroups, in strips of
-// 128 columns (fp32 64), for a second launch: up to 8 pieces of at least 512 k (16
-// from K = 16384 on) and 256 workgroups.  A piece has an odd number of 32-k steps:
-// with an even one and a power-of-two pitch, all pieces start on the same memory
+// B stored along the output, unsplit: strips of 32 columns with 16 waves, one to a CU,
+// or from more such strips than CUs on 64 with 8 waves (from HBM, us, 32 / 64: 1 x 8192 x
+// 2048 11.8 / 12.2, 1 x 9216 x 2048 16.5 / 13.0, 1 x 12288 x 4096 35.0 / 25.2).
+//
+// Deep K leaves a wave of an unsplit strip many steps one after another, each a round
+// of memory latency (1.6 us per 1024 k from HBM where the strips have a CU each), and
+// half-line strips waste what HBM delivers.  Given a workspace, K is split over
+// workgroups, for a second launch (2.5 us and the partial sums): from K = 2048 on (fp32,
+// whose steps are longer, 1536), unless N is more than 2.5 K, where the strips alone keep
+// HBM busy.  Strips of 64 columns, or 128 (16-bit) from N = 4096 on, up to 16 pieces of
+// at least 256 k and up to 256 workgroups (a few more than that, and some CUs hold two:
+// 1 x 5120 x 4096 in 6 / 8 pieces 13.8 / 17.3 us).  A piece has an odd number of 32-k
+// steps: with an even one and a power-of-two pitch, all pieces start on the same memory
 // channels (1 x 4096 x 14336 in 8 pieces of 56 steps 32.6 us, of 57 steps 24.0).
-// In us, B in the last-level cache / from HBM (twelve weights in turn):
+// The three thresholds are where both plans take the same time.  From a sweep of 18 K
+// (512 to 28672), 19 N (100 to 28672) and 1, 4 and 16 rows, in us, B from HBM (enough
+// weights in turn) / the same B again, from the last-level cache:
 //                         unsplit        split
-//    1 x 4096 x  4096    8.9 / 17.7    8.9 / 12.3
-//   16 x 4096 x  4096   12.4 / 20.6   11.3 / 13.7
-//    4 x 6144 x  4096   12.4 / 20.1   13.2 / 15.7
-//    1 x 5120 x  5120   18.3 / 29.8   13.2 / 15.3
-//    1 x 4096 x  6144   15.3 / 24.2   13.7 / 15.8
-//   16 x 3000 x  5000   14.7 / 22.4   11.9 / 15.3
-//    1 x 2048 x  8192   18.5 / 30.5    9.5 / 13.9
-//    1 x 2048 x  4096    6.9 / 10.0    8.2 /  9.2   (kept unsplit)
-//    1 x 8192 x  4096   14.4 / 19.4   16.6 / 19.8   (kept unsplit: 256 strips of 32)
-//    1 x  512 x  4104    6.3 /  9.6    7.8 /  8.8   (kept unsplit)
-//   fp32 1 x 5120 x 5120 21.0 / 33.1   22.1 / 26.0
+//    1 x  512 x  2048    9.3 /  4.5     7.6 /  6.2
+//    1 x  512 x  4104   15.7 /  6.2     8.0 /  6.5
+//   16 x 1024 x  3500   16.6 /  6.5     8.2 /  6.5
+//    1 x 2048 x  2048    9.9 /  4.6     7.9 /  6.2
+//    1 x 2048 x  4096   16.8 /  6.3     9.3 /  6.8
+//    1 x 2048 x  8192   30.1 / 15.2    12.4 /  8.4
+//   16 x 3000 x  5000   22.4 / 14.4    12.8 /  9.7
+//    1 x 4096 x  2048   10.2 /  4.5     9.6 /  6.5
+//    1 x 4096 x  4096   17.5 /  8.7    12.2 /  8.1
+//   16 x 4096 x  4096   20.3 / 12.5    13.3 / 10.2
+//    1 x 5120 x  5120   29.9 / 18.2    15.0 / 12.8
+//    1 x 4096 x 14336   53.2 / 34.0    28.6 / 22.8
+//    1 x 8192 x  4096   20.2 / 14.3    19.0 / 15.0
+//   16 x 9216 x  4096   25.7 / 16.1    21.0 / 17.4
+//   16 x 11008 x 8192   44.4 / 30.6    39.4 / 32.0
+//    1 x 14336 x 8192   48.8 / 36.6    49.2 / 37.8
+//    1 x 4096 x  1024    6.5 /  3.8     7.5 /  5.6   (unsplit)
+//    1 x 11008 x 4096   20.3 / 15.6    21.1 / 18.5   (unsplit)
+//   fp32, 16 x 1024 x 1536 11.7 / 8.6, 8.4 / 6.9; 1 x 4096 x 4096 23.2 / 15.8, 19.3 / 15.9;
+//    1 x 5120 x 5120 33.5 / 20.8, 25.9 / 21.7; 16 x 8192 x 4096 33.9 / 23.9, 29.7 / 25.7
+// Over the sweep (from HBM) the chosen plan takes 1 % more than the fastest one on average,
+// 6 % at the 90th percentile, 23 % at most (N = 28672, where three or more rows would split).
 Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     Plan p{SKINNY_M, 16, 1, K, 0, 0};
     p.waves = 16;
@@ -194,16 +212,15 @@ Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
         const Plan q = strips(fn, fs);
         if (q.splits > 0) return q;
     }
-    if (K >= 8192 || (K > 4096 && N >= 2048) || (K == 4096 && N >= 4096 && N < 8192)) {
-        const int cols = f32 ? 64 : 128, most = K >= 16384 ? 16 : 8;
-        const int64_t wgs = ceil_div(N, cols);
-        const int s = (int)std::min<int64_t>(std::min(most, K / 512), 256 / wgs);
+    if (K >= (f32 ? 1536 : 2048) && 2 * (int64_t)N <= 5 * (int64_t)K) {
+        const int cols = f32 || N < 4096 ? 64 : 128;
+        const int s = (int)std::min<int64_t>(std::min(MAX_SPLITS, K / 256), NUM_CU / ceil_div(N, cols));
         if (s >= 2) {
             const Plan q = strips(cols, s);
             if (q.splits > 1) return q;
         }
     }
-    return strips(ceil_div(N, 64) >= 160 ? 64 : 32, 1);
+    return strips(ceil_div(N, 32) > NUM_CU ? 64 : 32, 1);
 }
 
 Plan plan_act(int in, int es_out, int M, int N, int K, uint64_t ws_avail) {
