@@ -6,6 +6,8 @@ the host queries go through ctypes; `linear`, `linear_backward`,
 `matmul_f8`, `rms_norm`, `rms_norm_backward` and `quantize_f8` allocate their
 results and workspaces the way `matmul` does."""
 import ctypes
+import functools
+import inspect
 
 import torch
 
@@ -113,14 +115,21 @@ def _bytes(n: int, device):
 
 
 def _on_stream(fn):
-    """Runs fn with `stream` current, so that its results and workspaces come from
-    the allocator's pool of the stream the kernels run on (as matmul does)."""
-    def wrapped(X, *args, stream=None, **kw):
-        if stream is not None and stream != torch.cuda.current_stream(X.device):
-            with torch.cuda.stream(stream):
-                return fn(X, *args, **kw)
-        return fn(X, *args, **kw)
-    wrapped.__name__, wrapped.__doc__ = fn.__name__, fn.__doc__
+    """Adds `stream=None`: runs fn with it current, so that its results and workspaces
+    come from the allocator's pool of the stream the kernels run on (as matmul does)."""
+    sig = inspect.signature(fn)
+    first = next(iter(sig.parameters))
+
+    @functools.wraps(fn)
+    def wrapped(*args, stream=None, **kw):
+        if stream is not None and (args or first in kw):
+            device = (args[0] if args else kw[first]).device
+            if stream != torch.cuda.current_stream(device):
+                with torch.cuda.stream(stream):
+                    return fn(*args, **kw)
+        return fn(*args, **kw)
+    wrapped.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(), inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return wrapped
 
 
