@@ -185,7 +185,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 //   fp32, 16 x 1024 x 1536 11.7 / 8.6, 8.4 / 6.9; 1 x 4096 x 4096 23.2 / 15.8, 19.3 / 15.9;
 //    1 x 5120 x 5120 33.5 / 20.8, 25.9 / 21.7; 16 x 8192 x 4096 33.9 / 23.9, 29.7 / 25.7
 // Over the sweep (from HBM) the chosen plan takes 1 % more than the fastest one on average,
-// 6 % at the 90th percentile, 23 % at most (N = 28672, where three or more rows would split).
+// 6 % at the 90th percentile, 23 % at most (16 x 28672 x 16384).
 Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     Plan p{SKINNY_M, 16, 1, K, 0, 0};
     p.waves = 16;
