@@ -15,13 +15,13 @@
 namespace dgemm {
 namespace {
 
-// act'(z) times d, with the forward's own forms (kern_common.h):
+// act'(z) times d, with the forward's own forms for Z's format CF (kern_common.h):
 //   z sigmoid(p), p = a z + b z^3:  s (1 + z (1 - s)(a + 3 b z^2)), s = sigmoid(p)
 //   z Phi(z):                       Phi(z) + z phi(z)
 //   relu:                           z > 0
 // Far out, s (1 - s) is 0 while z^3 stays finite, so the product is 0; where
 // z^2 itself overflows or z is infinite, the factor is taken as 0 or 1 by z's sign.
-template <int NE>
+template <int CF, int NE>
 __device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[NE], int act) {
     if (act >= ACT_GELU_TANH) {
         const float a = act == ACT_SILU ? 1.0f : GELU_A, b = act == ACT_SILU ? 0.0f : GELU_B;
@@ -36,9 +36,10 @@ __device__ __forceinline__ void apply_act_grad(float (&d)[NE], const float (&z)[
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             const float x = z[i];
-            const float phi = 0.3989422804014327f * __builtin_amdgcn_exp2f(-0.5f * LOG2E * x * x);
+            float e;
             const float far = x > 0.0f ? 1.0f : 0.0f;
-            const float f = normal_cdf(x) + x * phi;
+            const float cdf = normal_cdf<CF>(x, e);
+            const float f = cdf + x * (0.3989422804014327f * e);
             d[i] *= __builtin_fabsf(x) > 1e4f ? far : f;
         }
     } else if (act == ACT_RELU) {
@@ -86,7 +87,7 @@ __global__ __launch_bounds__(64 * W) void act_grad_kernel(ActGradArgs a) {
             float z[8];
             x.get(d);
             zz.get(z);
-            apply_act_grad(d, z, a.act);
+            apply_act_grad<CF>(d, z, a.act);
         } else {
             x.get(d);
         }

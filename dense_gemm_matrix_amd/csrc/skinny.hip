@@ -127,7 +127,7 @@ struct Strip {
                     store_c<OUT>(e.pre, (int64_t)row[q] * e.ldz + col[q], v[q]);
             }
         }
-        if constexpr (EPI == EPI_FULL) apply_act(v, e.act);
+        if constexpr (EPI == EPI_FULL) apply_act<OUT>(v, e.act);
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
             if constexpr (EPI == EPI_FULL) {

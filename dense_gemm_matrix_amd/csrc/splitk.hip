@@ -81,7 +81,7 @@ __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
                 if (e.bias) f[j] += e.bias[col0 + j];
             }
             if (e.pre) store4<OUT>(e.pre, (int64_t)row * e.ldz + col0, f);
-            apply_act(f, e.act);
+            apply_act<OUT>(f, e.act);
             if (e.res) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f[j] += res[j];
