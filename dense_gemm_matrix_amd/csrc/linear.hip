@@ -770,7 +770,8 @@ int quant_f8(int in, int transpose, int M, int N, const void* X, int ldx, void* 
     const Mat mQ{Q, transpose ? N : M, transpose ? M : N, ldq, 1};
     int st;
     if ((st = check_mat(mX)) != DGEMM_OK || (st = check_mat(mQ)) != DGEMM_OK) return st;
-    if (M == 0 || N == 0) return DGEMM_OK;
+    // Rows (columns) without elements still have a scale, that of an empty maximum.
+    if ((transpose ? N : M) == 0) return DGEMM_OK;
     if (!scale) return DGEMM_ERR_INVALID_VALUE;
     if (!transpose && N > ROW_MAX) return DGEMM_ERR_TOO_LARGE;
     if (check_vec(scale, 4) != DGEMM_OK) return DGEMM_ERR_MISALIGNED;

@@ -429,8 +429,9 @@ int rmsnorm_bwd_workspace(int M, int N, size_t* required);
  * e4m3(X[i][j] / scale[i]), the exact quotient rounded to nearest even.  With
  * transpose = 1 by columns: scale[j] from column j, Q (N x M, row pitch ldq)
  * [j][i] := e4m3(X[i][j] / scale[j]): a K x N weight becomes gemm_f8's N x K
- * operand.  A row (column) holding an infinity or a NaN gets scale NaN.  in: X's
- * format (DGEMM_IN_F32, _BF16 or _F16).  Without transpose N <= 32768.
+ * operand.  A row (column) holding an infinity or a NaN gets scale NaN, one without
+ * elements 2^-100.  in: X's format (DGEMM_IN_F32, _BF16 or _F16).  Without transpose
+ * N <= 32768.
  */
 int quant_f8(int in, int transpose, int M, int N,
              const void* X, int ldx,
