@@ -560,9 +560,10 @@ int gemm_act_bwd(int in, int out, int M, int N, int K, const void* A, int lda, c
     if (check_vec(dbias, 4) != DGEMM_OK || check_vec(workspace, 16) != DGEMM_OK) return DGEMM_ERR_MISALIGNED;
     const BwdParts b = bwd_parts(in, cf, M, N, K, act, dA || dB, dbias != nullptr);
     if ((uint64_t)b.required > workspace_bytes) return DGEMM_ERR_WORKSPACE;
-    // The products address the workspace's matrices in panels too: dZ, and for fp32
-    // the transposes, whose rows are as long as M or K.
-    if ((int64_t)PANEL_ROWS * up(es == 4 ? std::max(std::max(M, N), K) : N, 16) * es >= DESC_LIMIT)
+    // The products address the workspace's matrices in panels too.  dZ's rows are no longer
+    // than dC's and those of B's transpose (fp32) no longer than dA's, which are checked; those
+    // of A's transpose, for dB, are as long as M.
+    if (es == 4 && dB && M > SKINNY_M && (int64_t)PANEL_ROWS * up(M, 4) * 4 >= DESC_LIMIT)
         return DGEMM_ERR_TOO_LARGE;
     const Mat ws = bytes_of(workspace, (int64_t)std::min<uint64_t>(workspace_bytes, INT64_MAX));
     const Mat ins[] = {mA, mB, mdC, mZ}, outs[] = {mdA, mdB, vec(dbias, N), ws};

@@ -314,8 +314,10 @@ int gemm_act_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
  * values, in an order that depends on the shape only.  Results are
  * deterministic; the products' order of sums follows the plan, which depends on
  * the sizes, formats, workspace and which of dA and dB are wanted (small
- * DGEMM_IN_F32X3 layers run in fp32 arithmetic).  Empty sums are zero: M == 0 writes dB = 0 and dbias = 0, N == 0
- * writes dA = 0.  Outputs overlap no input and no other output.
+ * DGEMM_IN_F32_3XBF16 layers run in fp32 arithmetic).  Empty sums are zero: M == 0
+ * writes dB = 0 and dbias = 0, N == 0 writes dA = 0.  Outputs overlap no input and no
+ * other output.  dB of fp32 inputs takes M <= 2^21 - 4 (DGEMM_ERR_TOO_LARGE above: the
+ * rows of A's transpose are that long).
  *
  * The workspace (16-byte aligned) holds dZ, partial column sums, transposes
  * (fp32) and split plans' partial products; its contents before and after are
