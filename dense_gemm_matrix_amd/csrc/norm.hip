@@ -73,11 +73,12 @@ __device__ __forceinline__ float f8_scale(uint32_t bits) {
 // v / scale, correctly rounded: the product with the rounded reciprocal and one
 // correction by the exact remainder (Markstein's division), three operations where
 // the compiler's general division takes a dozen and made the quantizer wait for
-// arithmetic.  The quotient has to be exact: e4m3 rounding has ties (the 16-bit
+// arithmetic.  The quotient has to be fp32's own: e4m3 rounding has ties (the 16-bit
 // inputs meet them often), and a product with the reciprocal falls on their wrong
 // side.  Equal to the fp32 quotient on every pair of 16-bit significands and on 5e7
-// fp32 pairs, half of them next to a tie.  No intermediate leaves the normal range:
-// scale is in [2^-100, 2^120], the quotient below 449 in magnitude.
+// fp32 pairs, half of them next to a tie.  scale is in [2^-100, 2^120] and the quotient
+// below 449 in magnitude, so only the remainder of the smallest scales leaves the normal
+// range, by less than the correction's own rounding (equal down to rows of 2^-126).
 __device__ __forceinline__ float quotient(float v, float scale, float inv) {
     const float q = v * inv;
     return __builtin_fmaf(__builtin_fmaf(-q, scale, v), inv, q);

@@ -428,7 +428,8 @@ int rmsnorm_bwd_workspace(int M, int N, size_t* required);
 
 /*
  * Rows to 8 bits: scale[i] := max(max_j |X[i][j]| / 448, 2^-100), Q[i][j] :=
- * e4m3(X[i][j] / scale[i]), the exact quotient rounded to nearest even.  With
+ * e4m3(X[i][j] / scale[i]): the quotient is rounded to fp32 and then to e4m3, both to
+ * nearest even (one that fp32 rounds to a tie of e4m3 goes to the even code).  With
  * transpose = 1 by columns: scale[j] from column j, Q (N x M, row pitch ldq)
  * [j][i] := e4m3(X[i][j] / scale[j]): a K x N weight becomes gemm_f8's N x K
  * operand.  A row (column) holding an infinity or a NaN gets scale NaN, one without
