@@ -4,7 +4,11 @@ and quantizers.  As in _binding, the functions named like the C entry points
 (in _marshal, csrc/marshal.cpp) only marshal tensors the caller has allocated;
 the host queries go through ctypes; `linear`, `linear_backward`,
 `matmul_f8`, `rms_norm`, `rms_norm_backward` and `quantize_f8` allocate their
-results and workspaces the way `matmul` does."""
+results and workspaces the way `matmul` does.
+
+Nothing is recorded for autograd (nor by `matmul`): results never require
+gradients, whatever the inputs do, and a training program calls
+`linear_backward` and `rms_norm_backward` itself."""
 import ctypes
 import functools
 import inspect

@@ -8,7 +8,7 @@
 // gradients it feeds).  dbias sums the unrounded fp32 values.
 //
 // Bound by memory: 4096 x 4096 bf16, dC and Z read and dZ written once, 22-26 us
-// (100 MB at 3.9 to 4.6 TB/s), beside 205 us of products.
+// (100 MB at 3.9 to 4.6 TB/s), beside 223 us of products.
 
 #include "kern_common.h"
 
@@ -155,13 +155,12 @@ __global__ __launch_bounds__(256) void transpose32_kernel(const float* X, int ld
 
 }  // namespace
 
-// Rows per workgroup of act_grad_kernel: at most 256 rows of partial sums, no
-// fewer than 8 rows each, and up to 64 rows in one chunk, whose sums are dbias
-// without a second launch (4 rows for each of 16 waves; 16 rows each measured
-// 16-35 us where two launches take 10).
-// Up to 64 rows: one workgroup's.  Else 16 rows or more per workgroup from 4096 rows
-// on (4096 x 4096, column sums alone: 20.5 us with 8 rows, 19.1 with 16), and 512 to
-// 2048 workgroups.
+// Rows per workgroup of act_grad_kernel, one row of partial sums each.  Up to 64 rows: one
+// workgroup's, whose sums are dbias without a second launch (4 rows for each of 16 waves;
+// 16 rows each measured 16-35 us where two launches take 10).  More: as many rows as
+// leave at most 512 workgroups per column block, or 2048 in all where there are fewer than
+// four blocks, but at least 16, or an M / 256th if that is fewer, and never below 8 (4096 x
+// 4096, column sums alone: 20.5 us with 8 rows, 19.1 with 16), in whole passes of four waves.
 int act_grad_rows(int M, int N) {
     if (M <= 64) return 64;
     const int blocks = (N + AG_COLS - 1) / AG_COLS;

@@ -414,14 +414,14 @@ double pair_grid_us(const TileCand& t, int in, int64_t ta, int ka, int64_t tb, i
 // One launch saves the other launches' time (2.4 us of host time each, 1.5 to 2 us
 // of a graph) and fills the CUs that one product's tiles leave idle; the longer
 // tiles go first.  The whole backward pass in us, M x N x K, apart / together:
-//   bf16   256 x  256 x  256    14.7 /   6.8   (slice-K tiles)
+//   bf16   256 x  256 x  256    14.9 /   8.2   (slice-K tiles)
 //          917 x  415 x 1035    24.4 /  15.1   (slice-K)
-//          600 x  800 x 3000    29.5 /  20.4   (128 x 128)
-//         1024 x 2048 x 2048    43.1 /  33.6   (128 x 128)
-//         2048 x 4096 x 4096     140 /   123   (256 x 256)
-//         4096 x 4096 x 4096     235 /   226   (256 x 256)
-//         5000 x 5000 x 5000     532 /   511   (256 x 256)
-//   fp32   256^3 20.6 / 8.0, 917 x 415 x 1035 47.0 / 30.8, 1024^3 69 / 51
+//          600 x  800 x 3000    29.8 /  19.7   (128 x 128)
+//         1024 x 2048 x 2048    43.8 /  33.2   (128 x 128)
+//         2048 x 4096 x 4096     154 /   129   (256 x 256)
+//         4096 x 4096 x 4096     251 /   241   (256 x 256)
+//         5000 x 5000 x 5000     551 /   541   (256 x 256)
+//   fp32   256^3 20.9 / 7.7, 917 x 415 x 1035 47.0 / 30.8, 1024^3 69 / 51
 PairPlan plan_pair(int in, int M, int N, int K, bool dA, bool dB, bool sums, uint64_t ws) {
     PairPlan r{};
     const int f = in_esize(in) == 4 ? IN_F32 : IN_BF16;  // 3 x bf16 in fp32 arithmetic here

@@ -283,7 +283,9 @@ hipError_t row_by_mode(const RowArgs& a, bool norm, bool f8, hipStream_t s) {
 // per output.  One workgroup of 512 threads per 64 columns, two passes over
 // them: the columns' maxima, then 64 x 64 tiles quantized and transposed in LDS
 // (byte rows padded to 68 so that the eight columns a lane writes fall in
-// different banks).  Done once per weight.
+// different banks).  Done once per weight: 4096 x 4096 bf16 90 us (its bytes 10), 4096 x
+// 14336 (K x N) 115 (34), 14336 x 4096 372 (34), bound by the latency of a workgroup's loads,
+// one per thread in flight, and by CUs without one of the few workgroups.
 
 constexpr int QT_THREADS = 512;
 
