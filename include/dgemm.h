@@ -465,7 +465,7 @@ typedef enum {
  * workspace too small, Stream-K for fp32 inputs or under graph capture) falls
  * back to the cost model's choice, which gemm_ex_plan then reports.
  * gemm_act, gemm_act_bwd and gemm_f8 follow DGEMM_PLAN_GRID too: gemm_act the
- * tiles above and, for at most 16 rows of 16-bit inputs, 16 x 32, 16 x 64 and
+ * tiles above and, for at most 16 rows, 16 x 32, 16 x 64 and (16-bit inputs)
  * 16 x 128; the other two's 16-bit and 8-bit products 256 x 256, 128 x 128 and
  * the slice-K tiles (more than 16 rows).
  * DGEMM_PLAN_AUTO clears the override.  Not synchronised with calls running
