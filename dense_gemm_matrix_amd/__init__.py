@@ -1,6 +1,6 @@
 """Dense GEMM C = A*B for AMD MI355X (gfx950): hand-written HIP kernels behind a
 C ABI (include/dgemm.h), with a thin ctypes binding of the same names; and the
-linear layer's operators around it (_linear)."""
+linear layer's operators around it (_linear) and a feed-forward block's (_feedforward)."""
 from ._binding import (  # noqa: F401
     DGEMM_ACT_NONE, DGEMM_ACT_RELU, DGEMM_ERR_ALIAS, DGEMM_ERR_DEVICE, DGEMM_ERR_INVALID_VALUE, DGEMM_ERR_LAUNCH,
     DGEMM_ERR_LEADING_DIM, DGEMM_ERR_MISALIGNED, DGEMM_ERR_SCRATCH_SIZE, DGEMM_ERR_TOO_LARGE, DGEMM_ERR_WORKSPACE,
@@ -16,4 +16,8 @@ from ._linear import (  # noqa: F401
     ACT_CODES, gemm_act, gemm_act_bwd, gemm_act_bwd_workspace, gemm_act_plan, gemm_f8, gemm_f8_plan,
     linear, linear_backward, matmul_f8, quant_f8, quantize_f8, rms_norm, rms_norm_backward, rmsnorm,
     rmsnorm_bwd, rmsnorm_bwd_workspace,
+)
+from ._feedforward import (  # noqa: F401
+    gemm_f8_block, gemm_f8_block_plan, layer_norm, layer_norm_backward, layernorm, layernorm_bwd,
+    layernorm_bwd_workspace, matmul_f8_block, quant_f8_block, quantize_f8_block,
 )

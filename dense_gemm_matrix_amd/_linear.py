@@ -40,6 +40,7 @@ for _name, _types in _ARGTYPES.items():
 
 ACT_CODES = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 F8 = torch.float8_e4m3fn
+F8_BLOCK = 128  # columns that share a scale in gemm_f8_block's operands
 _ANY = 1 << 40  # a workspace size that no plan exceeds
 
 
@@ -112,6 +113,15 @@ def _empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
     """A matrix whose row pitch is a multiple of 16 bytes."""
     per16 = 16 // torch.empty((), dtype=dtype).element_size()
     return torch.empty((rows, (cols + per16 - 1) // per16 * per16), dtype=dtype, device=device)[:, :cols]
+
+
+def _blocks(n: int) -> int:
+    return (n + F8_BLOCK - 1) // F8_BLOCK
+
+
+def _block_scales(rows: int, cols: int, device) -> torch.Tensor:
+    """Scales [rows, blocks of cols], those of neighbouring rows next to each other."""
+    return torch.empty((_blocks(cols), rows), dtype=torch.float32, device=device).t()
 
 
 def _bytes(n: int, device):
@@ -188,19 +198,30 @@ def matmul_f8(A, B, scale_a, scale_b, *, bias=None, act: str = "none", residual=
     return C
 
 
-@_on_stream
-def rms_norm(X, weight, *, residual=None, f8: bool = False, keep: bool = False, eps: float = 1e-6):
-    """A dict of rmsnorm's results: "Y"; "scale" with f8; "total" with a residual;
-    "rstd" with keep (for rms_norm_backward)."""
+def _norm_results(X, residual, f8):
+    """What a norm's allocating form returns first: "Y", "scale" with f8, "total" with a residual."""
+    if f8 not in (False, True, "row", "block"):
+        raise ValueError("f8 must be False, True (a scale per row), 'row' or 'block'")
     _device_tensor(X, "X")
     M, N = X.shape
     out = {"Y": _empty(M, N, F8 if f8 else X.dtype, X.device)}
-    if f8:
+    if f8 == "block":
+        out["scale"] = _block_scales(M, N, X.device)
+    elif f8:
         out["scale"] = torch.empty(M, dtype=torch.float32, device=X.device)
     if residual is not None:
         out["total"] = _empty(M, N, X.dtype, X.device)
+    return out
+
+
+@_on_stream
+def rms_norm(X, weight, *, residual=None, f8=False, keep: bool = False, eps: float = 1e-6):
+    """A dict of rmsnorm's results: "Y"; "scale" with f8 (True or "row": a scale per row;
+    "block": per row and 128 columns); "total" with a residual; "rstd" with keep (for
+    rms_norm_backward)."""
+    out = _norm_results(X, residual, f8)
     if keep:
-        out["rstd"] = torch.empty(M, dtype=torch.float32, device=X.device)
+        out["rstd"] = torch.empty(X.shape[0], dtype=torch.float32, device=X.device)
     rmsnorm(X, weight, out["Y"], residual=residual, total=out.get("total"), scale=out.get("scale"),
             rstd=out.get("rstd"), eps=eps)
     return out

@@ -144,6 +144,12 @@ __global__ __launch_bounds__(256) void col_reduce_kernel(ColReduceArgs a) {
     col_reduce((int)blockIdx.x, a, lds);
 }
 
+__global__ __launch_bounds__(256) void col_reduce2_kernel(ColReduceArgs a, ColReduceArgs b, int blocks_a) {
+    __shared__ float lds[COL_REDUCE_LDS];
+    if ((int)blockIdx.x < blocks_a) col_reduce((int)blockIdx.x, a, lds);
+    else col_reduce((int)blockIdx.x - blocks_a, b, lds);
+}
+
 // Y[n][m] = X[m][n], fp32, in 32 x 32 tiles through LDS (rows padded to 33 words):
 // small enough that the backward pass of a small layer still fills the CUs.
 __global__ __launch_bounds__(256) void transpose32_kernel(const float* X, int ldx, int M, int N,
@@ -194,6 +200,16 @@ hipError_t launch_col_reduce(const ColReduceArgs& a, hipStream_t stream) {
     void* args[] = {&b};
     return hipLaunchKernel((const void*)col_reduce_kernel, dim3((unsigned)col_reduce_blocks(a.N)),
                            dim3(256), args, 0, stream);
+}
+
+hipError_t launch_col_reduce2(const ColReduceArgs& a, const ColReduceArgs& b, hipStream_t stream) {
+    ColReduceArgs x = a, y = b;
+    int na = a.N > 0 ? col_reduce_blocks(a.N) : 0;
+    const int nb = b.N > 0 ? col_reduce_blocks(b.N) : 0;
+    if (na + nb == 0) return hipSuccess;
+    void* args[] = {&x, &y, &na};
+    return hipLaunchKernel((const void*)col_reduce2_kernel, dim3((unsigned)(na + nb)), dim3(256), args, 0,
+                           stream);
 }
 
 hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,

@@ -235,6 +235,19 @@ hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_
 constexpr int SKINNY_M = 16;
 hipError_t launch_skinny(const GemmLaunch& L);
 
+// Products of e4m3 operands with a scale per block (blockf8.hip): A[M x K] B[N x K]^T, block b
+// of K being [F8_BLOCK b, F8_BLOCK (b + 1)), row i of A scaled by sa[i sa_row + b sa_blk], row j
+// of B by sb[(j / rows_b) sb_row + b sb_blk], rows_b 1 or F8_BLOCK.  g describes the launch as
+// for launch_gemmt / launch_slicet / launch_skinny (in: IN_F8, or IN_F8W for the widened
+// products); a split's kchunk is a multiple of F8_BLOCK.
+struct BlockScales {
+    const float* sa;
+    const float* sb;
+    int sa_row, sa_blk, sb_row, sb_blk, rows_b;
+};
+hipError_t launch_blockf8(const GemmLaunch& g, const BlockScales& s);
+hipError_t launch_blockf8_skinny(const GemmLaunch& g, const BlockScales& s);
+
 // Split-K reduction: C[i][j] = epilogue(sum_{z < splits} W[z][i][j]) with W
 // fp32, row pitch ldw (a multiple of 4) and split stride zstride elements.
 hipError_t launch_splitk_reduce(const float* W, int splits, int64_t zstride, int ldw, char* C,
@@ -246,9 +259,15 @@ hipError_t launch_splitk_reduce(const float* W, int splits, int64_t zstride, int
 constexpr int ROW_MAX = 32768;       // longest row of the norm and the row quantizer
 constexpr int NORM_BWD_MAX = 16384;  // of the norm's backward pass
 
-// A pass over the rows of X (norm.hip).  R, S, rstd may be NULL; Y is in X's
+// Output rows (dgemm_rows): X's format, e4m3 with a scale per row, or per block of
+// F8_BLOCK columns.
+enum Rows { ROWS_SAME = 0, ROWS_F8 = 1, ROWS_F8_BLOCK = 2 };
+constexpr int F8_BLOCK = 128;
+
+// A pass over the rows of X (norm.hip, layernorm.hip).  R, S, rstd may be NULL; Y is in X's
 // format, or e4m3 with `scale` (per row; per column for launch_quant_cols,
-// which writes Y transposed and uses X, Y and scale only).
+// which writes Y transposed and uses X, Y and scale only; per row and block, at row *
+// s_row + block * s_blk).  Layer norm also: bias, mean (each may be NULL).
 struct RowArgs {
     const char* X;
     const char* R;
@@ -259,8 +278,12 @@ struct RowArgs {
     float* rstd;
     float eps;
     int M, N, ldx, ldr, lds, ldy;
+    const float* bias;
+    float* mean;
+    int64_t s_row, s_blk;
 };
-hipError_t launch_rows(const RowArgs& a, int fmt, bool norm, bool f8, hipStream_t stream);
+hipError_t launch_rows(const RowArgs& a, int fmt, bool norm, int rows, hipStream_t stream);
+hipError_t launch_layernorm(const RowArgs& a, int fmt, int rows, hipStream_t stream);
 hipError_t launch_quant_cols(const RowArgs& a, int fmt, hipStream_t stream);
 
 // The norm's backward pass; part: norm_bwd_grid(M, N) rows of ldp fp32 partial
@@ -274,9 +297,22 @@ struct NormBwdArgs {
     char* dX;
     float* part;
     int M, N, lddy, lds, ldds, lddx, ldp;
+    const float* mean;  // layer norm, whose partial sums are two rows of ldp each: dweight's, dbias'
 };
 int norm_bwd_grid(int M, int N);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream);
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream);
+
+// X or its transpose in 8 bits with a scale per block of `rows` x F8_BLOCK (quantblock.hip):
+// block (i, b) of Q at scale[i s_row + b s_blk].
+struct QuantBlockArgs {
+    const char* X;
+    char* Q;
+    float* scale;
+    int M, N, ldx, ldq;
+    int64_t s_row, s_blk;
+};
+hipError_t launch_quant_block(const QuantBlockArgs& a, int fmt, int rows, bool transpose, hipStream_t stream);
 
 // dZ = dC act'(Z) (actgrad.hip).  Z NULL: dZ = dC.  dZ may be NULL; part: one row
 // of ldp fp32 column sums per rows_per rows, or NULL.
@@ -290,6 +326,8 @@ struct ActGradArgs {
 int act_grad_rows(int M, int N);
 hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream);
 hipError_t launch_col_reduce(const ColReduceArgs& a, hipStream_t stream);
+// Two of them in one launch (N = 0: none).
+hipError_t launch_col_reduce2(const ColReduceArgs& a, const ColReduceArgs& b, hipStream_t stream);
 hipError_t launch_transpose32(const float* X, int ldx, int M, int N, float* Y, int ldy,
                               hipStream_t stream);
 

@@ -66,6 +66,13 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds,
                  : "s"(lds), "v"(voffset), "s"(rsrc)
                  : "memory", "m0");
 }
+// The same of 4 bytes per lane: lane l's land at LDS byte lds + 4 l.
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rsrc, uint32_t lds, int voffset) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voffset), "s"(rsrc)
+                 : "memory", "m0");
+}
 #pragma clang diagnostic pop
 
 // s_waitcnt immediate: wait until at most vm vector-memory and lgkm LDS/scalar
@@ -557,7 +564,9 @@ constexpr int full_lds = 32 * full_pitch<NJ> * 4;
 // soon as this one's is used.  The strips themselves are a loop (only the
 // accumulators' copy to LDS is written out per strip), which keeps the code in
 // the instruction cache.
-template <int OUT, int MI, int NJ>
+// TR: the accumulators hold the transpose, row li and, in register r, column 8 (r / 4) +
+// 4 g + r % 4 of their block.
+template <int OUT, int MI, int NJ, bool TR = false>
 __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], char* C, int M, int N,
                                                 int ldc, int row0, int col0, int lane,
                                                 const EpiArgs& e, char* lds) {
@@ -606,10 +615,19 @@ __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], cha
         for (int k = 0; k < MI; ++k) {
             if (k != mi) continue;
 #pragma unroll
-            for (int nj = 0; nj < NJ; ++nj)
+            for (int nj = 0; nj < NJ; ++nj) {
+                if constexpr (TR) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    buf[(8 * (r >> 2) + 4 * g + (r & 3)) * P + nj * 32 + li] = acc[k][nj][r];
+                    for (int q = 0; q < 4; ++q)
+                        *(f32x4*)(buf + li * P + nj * 32 + 8 * q + 4 * g) =
+                            f32x4{acc[k][nj][4 * q], acc[k][nj][4 * q + 1], acc[k][nj][4 * q + 2],
+                                  acc[k][nj][4 * q + 3]};
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r)
+                        buf[(8 * (r >> 2) + 4 * g + (r & 3)) * P + nj * 32 + li] = acc[k][nj][r];
+                }
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();

@@ -1,0 +1,226 @@
+// layernorm.hip -- layer norm with the residual's addition, forward and backward, for
+// gfx950 (MI355X).
+//
+// The forward pass is the row pass of rows.h.  Bound by HBM, as the root-mean-square
+// norm's: each row is read once, held in registers over its two reductions (mean, then
+// the squared deviations) and written once.
+//
+// Backward: with xh = (s - mean) rstd and g = dy w,
+//   dx = rstd (g - mean(g) - xh mean(g xh)) + ds,  dw = sum over rows of dy xh,
+//   db = sum over rows of dy.
+// As the root-mean-square norm's (norm.hip): each workgroup walks rows blockIdx, blockIdx
+// + grid, ..., the next row's loads in flight over this one's reduction, whose two sums
+// share one barrier; a thread's columns are the same in every row, so dw and db are running
+// fp32 sums in registers, written once per workgroup and added over workgroups in a fixed
+// order by one more launch for both.
+
+#include "rows.h"
+
+namespace dgemm {
+namespace {
+
+// Two sums over the T threads that share a row, with one barrier; red: T / 64 words each.
+template <int T>
+__device__ __forceinline__ void row_sum2(float& x, float& y, float (*red)[Place<T>::WG / 64]) {
+#pragma unroll
+    for (int m = (T < 64 ? T : 64) / 2; m > 0; m >>= 1) {
+        x += __shfl_xor(x, m);
+        y += __shfl_xor(y, m);
+    }
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0) {
+            red[0][threadIdx.x >> 6] = x;
+            red[1][threadIdx.x >> 6] = y;
+        }
+        __syncthreads();
+        x = red[0][0];
+        y = red[1][0];
+#pragma unroll
+        for (int i = 1; i < T / 64; ++i) {
+            x += red[0][i];
+            y += red[1][i];
+        }
+    }
+}
+
+template <int FMT>
+hipError_t ln_by_rows(const RowArgs& a, int rows, hipStream_t s) {
+    if (rows == ROWS_F8_BLOCK) return row_by_size<FMT, LN_F8B>(a, s);
+    return rows == ROWS_F8 ? row_by_size<FMT, LN_F8>(a, s) : row_by_size<FMT, LN>(a, s);
+}
+
+template <int FMT, int T, int NV>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a) {
+    using P = Place<T>;
+    constexpr int ES = fmt_es<FMT>;
+    __shared__ float red[2][2][P::WG / 64];
+    __shared__ float dwl[P::RPW > 1 ? P::WG * NV * 8 : 1];
+    const P pl;
+    const int t = pl.t;
+    const int64_t step = (int64_t)gridDim.x * P::RPW;
+    auto col = [&](int i) { return (i * T + t) * 8; };
+    // 1024 threads have 128 registers each: no room for the next row's loads, nor
+    // to keep the weights over the rows.
+    constexpr bool PRE = T < 1024;
+    float w[PRE ? NV : 1][8], dw[NV][8], db[NV][8];
+    const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
+    auto load_w = [&](int i, float (&to)[8]) {
+        Row8<OUT_F32> w8;
+        w8.load(rw, (uint32_t)col(i) * 4, a.N - col(i));
+        w8.get(to);
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if constexpr (PRE) load_w(i, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+    }
+    Row8<FMT> y[NV], s[NV], d[NV];
+    float next_rstd = 0.0f, next_mean = 0.0f;
+    // The rows of this wave from row0 on; rows past M and columns past N load as 0.
+    auto load = [&](int64_t row0) {
+        next_rstd = row0 + pl.lr < a.M ? a.rstd[row0 + pl.lr] : 0.0f;
+        next_mean = row0 + pl.lr < a.M ? a.mean[row0 + pl.lr] : 0.0f;
+        const auto ry = P::rows(a.dY, row0, a.M, a.N, a.lddy, ES);
+        const auto rs = P::rows(a.S, row0, a.M, a.N, a.lds, ES);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            y[i].load(ry, pl.at(row0, a.M, a.N, col(i), a.lddy, ES), a.N - col(i));
+            s[i].load(rs, pl.at(row0, a.M, a.N, col(i), a.lds, ES), a.N - col(i));
+        }
+        if (a.dS) {
+            const auto rd = P::rows(a.dS, row0, a.M, a.N, a.ldds, ES);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                d[i].load(rd, pl.at(row0, a.M, a.N, col(i), a.ldds, ES), a.N - col(i));
+        }
+    };
+    int64_t row0 = (int64_t)blockIdx.x * P::RPW + P::first();
+    if (PRE && row0 < a.M) load(row0);
+    int par = 0;
+    for (; row0 < a.M; row0 += step, par ^= 1) {
+        if (!PRE) load(row0);
+        const float rstd = next_rstd, mean = next_mean;
+        // The row stays in its storage format (half the registers of fp32 for
+        // 16-bit rows); the few products are formed again after the reduction.
+        Row8<FMT> cy[NV], cs[NV], cd[NV];
+        float dot = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            cy[i] = y[i];
+            cs[i] = s[i];
+            cd[i] = d[i];
+            float dy[8], x[8];
+            cy[i].get(dy);
+            cs[i].get(x);
+            float wt[8];
+            if constexpr (!PRE) load_w(i, wt);
+            const float(&wi)[8] = PRE ? w[PRE ? i : 0] : wt;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float xh = (x[j] - mean) * rstd, gj = dy[j] * wi[j];
+                sum += gj;
+                dot += gj * xh;
+                dw[i][j] += dy[j] * xh;
+                db[i][j] += dy[j];
+            }
+        }
+        if (PRE && row0 + step < a.M) load(row0 + step);
+        // The reduction's words alternate between rows, so one barrier per row
+        // is enough: a wave reaches the next but one row's write only after
+        // every wave has passed the next row's barrier.
+        row_sum2<T>(sum, dot, red[par]);
+        const float mg = sum / (float)a.N, mgx = dot / (float)a.N;
+        const auto ro = P::rows(a.dX, row0, a.M, a.N, a.lddx, ES);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float dy[8], x[8], o[8], e[8];
+            cy[i].get(dy);
+            cs[i].get(x);
+            if (a.dS) cd[i].get(e);
+            float wt[8];
+            if constexpr (!PRE) load_w(i, wt);
+            const float(&wi)[8] = PRE ? w[PRE ? i : 0] : wt;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                o[j] = rstd * (dy[j] * wi[j] - mg - (x[j] - mean) * rstd * mgx);
+                if (a.dS) o[j] += e[j];
+            }
+            Row8<FMT> out;
+            out.set(o);
+            out.store(ro, pl.at(row0, a.M, a.N, col(i), a.lddx, ES), a.N - col(i));
+        }
+    }
+    if (!a.part) return;
+    // dw's partial sums, then db's, a row of ldp each per workgroup.
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        auto& v = which ? db : dw;
+        if constexpr (P::RPW > 1) {
+            // The workgroup's groups of T lanes hold the same columns: add them in order.
+            const int sub = (int)threadIdx.x / T;
+            if (which) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) dwl[(sub * NV * 8 + i * 8 + j) * T + t] = v[i][j];
+            __syncthreads();
+            if (sub == 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        for (int q = 1; q < P::RPW; ++q) v[i][j] += dwl[(q * NV * 8 + i * 8 + j) * T + t];
+            }
+        }
+        if (P::RPW > 1 && (int)threadIdx.x >= T) continue;
+        const auto rp = make_rsrc((const char*)(a.part + ((int64_t)blockIdx.x * 2 + which) * a.ldp),
+                                  (int64_t)a.N * 4);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            Row8<OUT_F32> out;
+            out.set(v[i]);
+            out.store(rp, (uint32_t)col(i) * 4, a.N - col(i));
+        }
+    }
+}
+
+template <int FMT, int T, int NV>
+hipError_t go_bwd(const NormBwdArgs& a, int grid, hipStream_t stream) {
+    NormBwdArgs b = a;
+    void* args[] = {&b};
+    return hipLaunchKernel((const void*)ln_bwd_kernel<FMT, T, NV>, dim3((unsigned)grid),
+                           dim3(T < 256 ? 256 : T), args, 0, stream);
+}
+
+template <int FMT>
+hipError_t bwd_by_size(const NormBwdArgs& a, int grid, hipStream_t s) {
+    if (a.N <= 128) return go_bwd<FMT, 16, 1>(a, grid, s);
+    if (a.N <= 256) return go_bwd<FMT, 32, 1>(a, grid, s);
+    if (a.N <= 512) return go_bwd<FMT, 64, 1>(a, grid, s);
+    if (a.N <= 1024) return go_bwd<FMT, 64, 2>(a, grid, s);
+    if (a.N <= 2048) return go_bwd<FMT, 256, 1>(a, grid, s);
+    if (a.N <= 4096) return go_bwd<FMT, 256, 2>(a, grid, s);
+    if (a.N <= 8192) return go_bwd<FMT, 512, 2>(a, grid, s);
+    if (a.N <= NORM_BWD_MAX) return go_bwd<FMT, 1024, 2>(a, grid, s);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+hipError_t launch_layernorm(const RowArgs& a, int fmt, int rows, hipStream_t stream) {
+    if (fmt == OUT_F32) return ln_by_rows<OUT_F32>(a, rows, stream);
+    if (fmt == OUT_BF16) return ln_by_rows<OUT_BF16>(a, rows, stream);
+    if (fmt == OUT_F16) return ln_by_rows<OUT_F16>(a, rows, stream);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream) {
+    const int grid = norm_bwd_grid(a.M, a.N);
+    if (fmt == OUT_F32) return bwd_by_size<OUT_F32>(a, grid, stream);
+    if (fmt == OUT_BF16) return bwd_by_size<OUT_BF16>(a, grid, stream);
+    if (fmt == OUT_F16) return bwd_by_size<OUT_F16>(a, grid, stream);
+    return hipErrorInvalidValue;
+}
+
+}  // namespace dgemm

@@ -6,67 +6,18 @@
 #include <algorithm>
 #include <cmath>
 
-#include "dgemm.h"
-#include "dgemm_internal.h"
-#include "plan.h"
+#include "host.h"
 
 namespace dgemm {
-namespace {
-
-constexpr int64_t WS_ALIGN = 256;  // pieces of a workspace start on this
-
-int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
-
-// A row-major matrix operand of a call.
-struct Mat {
-    const void* p;
-    int64_t rows, cols, ld, es;
-    Span span() const { return matrix_span(p, rows, cols, ld, es); }
-    bool empty() const { return rows <= 0 || cols <= 0; }
-};
-
-// Pitch, pointer, alignment and the 32-bit panel limit of one matrix.
-int check_mat(const Mat& m) {
-    if (m.ld < std::max<int64_t>(m.cols, 1)) return DGEMM_ERR_LEADING_DIM;
-    if (!m.empty()) {
-        if (!m.p) return DGEMM_ERR_INVALID_VALUE;
-        if (((uintptr_t)m.p & 15) || (m.ld * m.es) % 16) return DGEMM_ERR_MISALIGNED;
-    }
-    if ((int64_t)PANEL_ROWS * m.ld * m.es >= DESC_LIMIT) return DGEMM_ERR_TOO_LARGE;
-    return DGEMM_OK;
-}
-
-// An fp32 vector operand (NULL: absent).
-Mat vec(const void* p, int64_t n) { return Mat{p, p ? 1 : 0, n, n, 4}; }
-
-int check_vec(const void* p, int align) {
-    return ((uintptr_t)p & (uintptr_t)(align - 1)) ? DGEMM_ERR_MISALIGNED : DGEMM_OK;
-}
-
-// Whether any of `outs` shares a byte with another of them or with any of `ins`.
-bool any_overlap(const Mat* outs, int n_out, const Mat* ins, int n_in) {
-    for (int i = 0; i < n_out; ++i) {
-        if (!outs[i].p) continue;
-        for (int j = 0; j < n_in; ++j)
-            if (ins[j].p && spans_overlap(outs[i].span(), ins[j].span())) return true;
-        for (int j = 0; j < i; ++j)
-            if (outs[j].p && spans_overlap(outs[i].span(), outs[j].span())) return true;
-    }
-    return false;
-}
-
-Mat bytes_of(void* p, int64_t n) { return Mat{p, n > 0 ? 1 : 0, n, n, 1}; }
-
-bool valid_act(int act) { return act >= DGEMM_ACT_NONE && act <= DGEMM_ACT_SILU; }
 
 // -------------------------------------------------------------------- plans
 
 // Tiles of gemmt.hip: gemm16's constants, whose schedule and bytes per step it
 // shares (an 8-bit step is 128 k in the same time).
-constexpr TileCand TILES_T[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6},
+static constexpr TileCand TILES_T[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6},
                                 {128, 128, 0.6, 1.26, 1.35, 0.8, 1.0}};
 
-int t_step(int in) { return in >= IN_F8 ? 128 : 64; }
+static int t_step(int in) { return in >= IN_F8 ? 128 : 64; }
 
 // Plan of one tile at `splits` K pieces (1: unsplit); splits = 0 if it does not fit.
 Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uint64_t ws_avail) {
@@ -88,7 +39,7 @@ Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uin
 // The transposed layouts' plan: the estimate's choice among the slice-K tiles
 // (slicet.hip; slicek16's constants, an 8-bit block being 128 k), the two grid
 // tiles and 1 to 16 splits, by the same terms and margin as the other plans.
-Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail, double* us_out = nullptr) {
+Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail, double* us_out, bool big) {
     const int bk = t_step(in);
     int fm, fn, fs;
     if (forced_grid(fm, fn, fs) && fm == fn && (fm == 32 || fm == 64)) {
@@ -99,7 +50,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     }
     if (forced_grid(fm, fn, fs))
         for (const TileCand& t : TILES_T)
-            if (t.bm == fm && t.bn == fn) {
+            if (t.bm == fm && t.bn == fn && (big || t.bm < 256)) {
                 Plan p = plan_pieces(t, bk, M, N, K, fs, ws_avail);
                 p.layout = layout;
                 if (p.splits > 0) return p;
@@ -110,6 +61,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     const bool slice = slice_plan_t(M, N, std::min(K, nk * 64), best, best_us);
     best.kchunk = K;
     for (const TileCand& t : TILES_T) {
+        if (t.bm == 256 && !big) continue;
         if (slice) break;  // as for A[M x K] B[K x N]: unsplit small outputs are the slice-K kernel's
         const double us = estimate_us(in, es_out, M, N, t, 1, nk, 0);
         if (best_us < 0.0 || us < best_us) {
@@ -124,6 +76,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     best_us *= margin;
     for (const TileCand& t : TILES_T)
         for (int s = 2; s <= MAX_SPLITS && s <= nk; ++s) {
+            if (t.bm == 256 && !big) break;
             const Plan p = plan_pieces(t, bk, M, N, K, s, ws_avail);
             if (p.splits != s) continue;
             const double us = estimate_us(in, es_out, M, N, t, s, p.kchunk / bk, p.ldw);
@@ -223,6 +176,8 @@ Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
     return strips(ceil_div(N, 32) > NUM_CU ? 64 : 32, 1);
 }
 
+namespace {
+
 Plan plan_act(int in, int es_out, int M, int N, int K, uint64_t ws_avail) {
     if (in != IN_F32X3 && M > 0 && M <= SKINNY_M && N > 0)
         return plan_skinny(in, LAY_NN, M, N, K, ws_avail);
@@ -236,14 +191,6 @@ Plan plan_f8(int of, int M, int N, int K, uint64_t ws_avail) {
     const int in = f8_in(of, M);
     if (M > 0 && M <= SKINNY_M && N > 0) return plan_skinny(in, LAY_NT, M, N, K, ws_avail);
     return plan_t(in, LAY_NT, out_esize(of), M, N, K, ws_avail);
-}
-
-int report(const Plan& p, int* tile_rows, int* tile_cols, int* splits, size_t* used) {
-    if (tile_rows) *tile_rows = p.bm;
-    if (tile_cols) *tile_cols = p.bn;
-    if (splits) *splits = p.splits;
-    if (used) *used = (size_t)p.ws_bytes;
-    return DGEMM_OK;
 }
 
 // ------------------------------------------------- the forward products' call
@@ -493,13 +440,6 @@ GemmLaunch pair_launch(int in, const Plan& p, int M, int N, int K, const void* X
     return L;
 }
 
-int launched(hipError_t e) { return e == hipSuccess ? DGEMM_OK : DGEMM_ERR_LAUNCH; }
-
-// Format codes DGEMM_IN_F32 / _BF16 / _F16 of an elementwise operator.
-int row_fmt(int in) {
-    return in == DGEMM_IN_F32 ? OUT_F32 : in == DGEMM_IN_BF16 ? OUT_BF16 : in == DGEMM_IN_F16 ? OUT_F16 : -1;
-}
-
 }  // namespace
 }  // namespace dgemm
 
@@ -683,9 +623,10 @@ int rmsnorm(int in, int out, int M, int N, const void* X, int ldx, const void* R
             int lds, const float* weight, float eps, void* Y, int ldy, float* scale, float* rstd,
             void* stream) {
     const int fmt = row_fmt(in);
-    if (fmt < 0 || M < 0 || N < 0 || !(eps >= 0.0f) || (out != DGEMM_ROWS_SAME && out != DGEMM_ROWS_F8))
+    if (fmt < 0 || M < 0 || N < 0 || !(eps >= 0.0f) || out < DGEMM_ROWS_SAME || out > DGEMM_ROWS_F8_BLOCK)
         return DGEMM_ERR_INVALID_VALUE;
-    const bool f8 = out == DGEMM_ROWS_F8;
+    const bool f8 = out != DGEMM_ROWS_SAME;
+    const int64_t scales = (int64_t)M * (out == DGEMM_ROWS_F8_BLOCK ? ceil_div(N, F8_BLOCK) : 1);
     const int es = out_esize(fmt);
     const Mat mX{X, M, N, ldx, es}, mR{R, M, N, ldr, es}, mS{S, M, N, lds, es}, mY{Y, M, N, ldy, f8 ? 1 : es};
     int st;
@@ -703,7 +644,7 @@ int rmsnorm(int in, int out, int M, int N, const void* X, int ldx, const void* R
         return o.p == i.p && o.es == i.es && (o.ld == i.ld || M == 1);
     };
     const Mat none{nullptr, 0, 0, 0, 0};
-    const Mat outs[] = {mS, mY, vec(scale, M), vec(rstd, M)};
+    const Mat outs[] = {mS, mY, vec(scale, scales), vec(rstd, M)};
     if (any_overlap(outs, 4, nullptr, 0)) return DGEMM_ERR_ALIAS;
     for (const Mat& o : outs) {
         const bool whole = o.p && o.cols == N && o.rows == M && (o.p == S || o.p == Y);
@@ -713,8 +654,8 @@ int rmsnorm(int in, int out, int M, int N, const void* X, int ldx, const void* R
     }
     if ((st = check_device()) != DGEMM_OK) return st;
     const RowArgs a{(const char*)X, (const char*)R, (char*)S, weight, (char*)Y, scale, rstd, eps, M, N,
-                    ldx, ldr, lds, ldy};
-    return launched(launch_rows(a, fmt, true, f8, (hipStream_t)stream));
+                    ldx, ldr, lds, ldy, nullptr, nullptr, 1, M};
+    return launched(launch_rows(a, fmt, true, out, (hipStream_t)stream));
 }
 
 int rmsnorm_bwd(int in, int M, int N, const void* dY, int lddy, const void* S, int lds,
@@ -788,7 +729,7 @@ int quant_f8(int in, int transpose, int M, int N, const void* X, int ldx, void* 
     a.ldx = ldx;
     a.ldy = ldq;
     if (transpose) return launched(launch_quant_cols(a, fmt, (hipStream_t)stream));
-    return launched(launch_rows(a, fmt, false, true, (hipStream_t)stream));
+    return launched(launch_rows(a, fmt, false, ROWS_F8, (hipStream_t)stream));
 }
 
 }  // extern "C"

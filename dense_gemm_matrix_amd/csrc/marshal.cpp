@@ -120,6 +120,28 @@ float* need_vec(PyObject* o, const char* name, int n, int dev) {
     return vec(o, name, n, dev);
 }
 
+// A float32 matrix of block scales with any strides: block (i, b) at p[i * row + b * blk].
+struct Scales {
+    float* p = nullptr;
+    int rows = 0, row = 0, blk = 0;
+};
+
+Scales scales(PyObject* o, const char* name, int blocks, int dev) {
+    const at::Tensor& t = tensor(o, name);
+    if (t.scalar_type() != ScalarType::Float || t.dim() != 2 || t.size(1) != blocks || !t.is_cuda() ||
+        t.get_device() != dev)
+        fail(PyExc_ValueError, "%s must be a float32 device matrix with %d columns", name, blocks);
+    Scales s;
+    s.p = (float*)t.data_ptr();
+    s.rows = to_int(t.size(0));
+    // A stride that is never stepped is free.
+    s.row = s.rows > 1 ? to_int(t.stride(0)) : 1;
+    s.blk = blocks > 1 ? to_int(t.stride(1)) : 1;
+    return s;
+}
+
+int blocks_of(int n) { return (int)(((int64_t)n + DGEMM_F8_BLOCK - 1) / DGEMM_F8_BLOCK); }
+
 struct Bytes {
     void* p = nullptr;
     size_t n = 0;
@@ -139,6 +161,13 @@ int act_code(PyObject* o) {
     for (int i = 0; PyUnicode_Check(o) && i < 5; ++i)
         if (PyUnicode_CompareWithASCIIString(o, names[i]) == 0) return i;
     fail(PyExc_ValueError, "act must be one of none, relu, gelu, gelu_tanh, silu");
+}
+
+double number(PyObject* o, double otherwise) {
+    if (!o) return otherwise;
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return v;
 }
 
 // DGEMM_IN_F32 / _BF16 / _F16 of a type, -1 for any other.
@@ -323,16 +352,22 @@ PyObject* py_rmsnorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         const Mat Y = matrix_like(o[2], "Y", M, N, f8 ? ScalarType::Float8_e4m3fn : X.type, dev);
         const Mat R = matrix_like(o[3], "residual", M, N, X.type, dev);
         const Mat S = matrix_like(o[4], "total", M, N, X.type, dev);
-        float* scale = vec(o[5], "scale", M, dev);
-        float* rstd = vec(o[6], "rstd", M, dev);
-        double eps = 1e-6;
-        if (o[7]) {
-            eps = PyFloat_AsDouble(o[7]);
-            if (eps == -1.0 && PyErr_Occurred()) throw Raised{};
+        int out = f8 ? DGEMM_ROWS_F8 : DGEMM_ROWS_SAME;
+        float* scale = nullptr;
+        if (f8 && tensor(o[5], "scale").dim() == 2) {
+            out = DGEMM_ROWS_F8_BLOCK;
+            const Scales sc = scales(o[5], "scale", blocks_of(N), dev);
+            if (sc.rows != M || (M > 1 && sc.row != 1) || (N > DGEMM_F8_BLOCK && sc.blk != M))
+                fail(PyExc_ValueError, "scale must be the transpose of a contiguous (%d, %d) matrix", blocks_of(N), M);
+            scale = sc.p;
+        } else {
+            scale = vec(o[5], "scale", M, dev);
         }
+        float* rstd = vec(o[6], "rstd", M, dev);
+        const double eps = number(o[7], 1e-6);
         void* s = stream_of(o[8], dev);
         return call(dev, [&] {
-            return rmsnorm(fmt, f8 ? DGEMM_ROWS_F8 : DGEMM_ROWS_SAME, M, N, X.p, X.ld, R.p, R.ld, S.p, S.ld,
+            return rmsnorm(fmt, out, M, N, X.p, X.ld, R.p, R.ld, S.p, S.ld,
                            w, (float)eps, Y.p, Y.ld, scale, rstd, s);
         });
     });
@@ -381,6 +416,122 @@ PyObject* py_quant_f8(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObje
     });
 }
 
+PyObject* py_gemm_f8_block(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+    static const char* const names[] = {"A", "B", "C", "scale_a", "scale_b", "bias", "act", "residual",
+                                        "workspace", "stream"};
+    return guarded([&] {
+        PyObject* o[10];
+        parse("gemm_f8_block", names, 5, 5, args, nargs, kw, o);
+        const Mat A = matrix(o[0], "A"), B = matrix(o[1], "B"), C = matrix(o[2], "C");
+        if (A.cols != B.cols || C.rows != A.rows || C.cols != B.rows)
+            fail(PyExc_ValueError, "shapes (%d, %d) x (%d, %d)^T -> (%d, %d)", A.rows, A.cols, B.rows,
+                 B.cols, C.rows, C.cols);
+        if (A.dev != C.dev || B.dev != C.dev)
+            fail(PyExc_ValueError, "operands on different devices: %d, %d, %d", A.dev, B.dev, C.dev);
+        if (A.type != ScalarType::Float8_e4m3fn || B.type != ScalarType::Float8_e4m3fn)
+            fail(PyExc_TypeError, "A and B must be float8_e4m3fn");
+        const int fmt = need_fmt(C.type, "C"), kb = blocks_of(A.cols);
+        const Scales sa = scales(o[3], "scale_a", kb, C.dev), sb = scales(o[4], "scale_b", kb, C.dev);
+        if (sa.rows != C.rows) fail(PyExc_ValueError, "scale_a must have a row per row of A");
+        const bool each = sb.rows == C.cols;
+        if (!each && sb.rows != blocks_of(C.cols))
+            fail(PyExc_ValueError, "scale_b must have a row per row of B, or per %d of them", DGEMM_F8_BLOCK);
+        const float* bias = vec(o[5], "bias", C.cols, C.dev);
+        const int act = act_code(o[6]);
+        const Mat R = matrix_like(o[7], "residual", C.rows, C.cols, C.type, C.dev);
+        const Bytes ws = workspace(o[8], C.dev);
+        void* s = stream_of(o[9], C.dev);
+        return call(C.dev, [&] {
+            return gemm_f8_block(fmt, each ? 1 : DGEMM_F8_BLOCK, C.rows, C.cols, A.cols, A.p, A.ld, B.p, B.ld,
+                                 C.p, C.ld, sa.p, sa.row, sa.blk, sb.p, sb.row, sb.blk, bias, act, R.p, R.ld,
+                                 ws.p, ws.n, s);
+        });
+    });
+}
+
+PyObject* py_quant_f8_block(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+    static const char* const names[] = {"X", "Q", "scale", "transpose", "stream"};
+    return guarded([&] {
+        PyObject* o[5];
+        parse("quant_f8_block", names, 3, 3, args, nargs, kw, o);
+        const Mat X = matrix(o[0], "X");
+        const int fmt = need_fmt(X.type, "X");
+        const int tr = o[3] ? PyObject_IsTrue(o[3]) : 0;
+        if (tr < 0) throw Raised{};
+        const int rows = tr ? X.cols : X.rows, cols = tr ? X.rows : X.cols;
+        if (!given(o[1])) fail(PyExc_ValueError, "Q is required");
+        const Mat Q = matrix_like(o[1], "Q", rows, cols, ScalarType::Float8_e4m3fn, X.dev);
+        const Scales sc = scales(o[2], "scale", blocks_of(cols), X.dev);
+        if (sc.rows != rows && sc.rows != blocks_of(rows))
+            fail(PyExc_ValueError, "scale must have a row per row of Q, or per %d of them", DGEMM_F8_BLOCK);
+        void* s = stream_of(o[4], X.dev);
+        return call(X.dev, [&] {
+            return quant_f8_block(fmt, sc.rows == rows ? 1 : DGEMM_F8_BLOCK, tr, X.rows, X.cols, X.p, X.ld, Q.p,
+                                  Q.ld, sc.p, sc.row, sc.blk, s);
+        });
+    });
+}
+
+PyObject* py_layernorm(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+    static const char* const names[] = {"X", "weight", "bias", "Y", "residual", "total", "scale", "mean", "rstd",
+                                        "eps", "stream"};
+    return guarded([&] {
+        PyObject* o[11];
+        parse("layernorm", names, 4, 4, args, nargs, kw, o);
+        const Mat X = matrix(o[0], "X");
+        const int M = X.rows, N = X.cols, dev = X.dev, fmt = need_fmt(X.type, "X");
+        const float* w = need_vec(o[1], "weight", N, dev);
+        const float* b = vec(o[2], "bias", N, dev);
+        const bool f8 = tensor(o[3], "Y").scalar_type() == ScalarType::Float8_e4m3fn;
+        if (f8 != given(o[6])) fail(PyExc_ValueError, "a float8_e4m3fn Y takes a scale, and only that");
+        const Mat Y = matrix_like(o[3], "Y", M, N, f8 ? ScalarType::Float8_e4m3fn : X.type, dev);
+        const Mat R = matrix_like(o[4], "residual", M, N, X.type, dev);
+        const Mat S = matrix_like(o[5], "total", M, N, X.type, dev);
+        int out = f8 ? DGEMM_ROWS_F8 : DGEMM_ROWS_SAME;
+        Scales sc;
+        if (f8 && tensor(o[6], "scale").dim() == 2) {
+            out = DGEMM_ROWS_F8_BLOCK;
+            sc = scales(o[6], "scale", blocks_of(N), dev);
+            if (sc.rows != M) fail(PyExc_ValueError, "scale must have a row per row of Y");
+        } else {
+            sc.p = vec(o[6], "scale", M, dev);
+        }
+        float* mean = vec(o[7], "mean", M, dev);
+        float* rstd = vec(o[8], "rstd", M, dev);
+        const double eps = number(o[9], 1e-5);
+        void* s = stream_of(o[10], dev);
+        return call(dev, [&] {
+            return layernorm(fmt, out, M, N, X.p, X.ld, R.p, R.ld, S.p, S.ld, w, b, (float)eps, Y.p, Y.ld, sc.p,
+                             sc.row, sc.blk, mean, rstd, s);
+        });
+    });
+}
+
+PyObject* py_layernorm_bwd(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+    static const char* const names[] = {"dY", "total", "weight", "mean", "rstd", "dX", "dtotal", "dweight",
+                                        "dbias", "workspace", "stream"};
+    return guarded([&] {
+        PyObject* o[11];
+        parse("layernorm_bwd", names, 6, 6, args, nargs, kw, o);
+        const Mat dY = matrix(o[0], "dY");
+        const int M = dY.rows, N = dY.cols, dev = dY.dev, fmt = need_fmt(dY.type, "dY");
+        const Mat S = matrix_like(o[1], "total", M, N, dY.type, dev);
+        const float* w = need_vec(o[2], "weight", N, dev);
+        const float* mean = need_vec(o[3], "mean", M, dev);
+        const float* rstd = need_vec(o[4], "rstd", M, dev);
+        const Mat dX = matrix_like(o[5], "dX", M, N, dY.type, dev);
+        const Mat dS = matrix_like(o[6], "dtotal", M, N, dY.type, dev);
+        float* dw = vec(o[7], "dweight", N, dev);
+        float* db = vec(o[8], "dbias", N, dev);
+        const Bytes ws = workspace(o[9], dev);
+        void* s = stream_of(o[10], dev);
+        return call(dev, [&] {
+            return layernorm_bwd(fmt, M, N, dY.p, dY.ld, S.p, S.ld, w, mean, rstd, dS.p, dS.ld, dX.p, dX.ld, dw,
+                                 db, ws.p, ws.n, s);
+        });
+    });
+}
+
 #define FN(name, doc) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL | METH_KEYWORDS, doc}
 PyMethodDef methods[] = {
     FN(gemm_act,
@@ -405,7 +556,8 @@ PyMethodDef methods[] = {
        "        stream=None)\n\n"
        "Y = s * rstd * weight row by row, s = X + residual, rstd = (mean s^2 + eps)^-1/2.\n\n"
        "Y has X's dtype, or is float8_e4m3fn with a float32 `scale` per row (gemm_f8's A and\n"
-       "scale_a).  `total` (X's dtype) receives s and `rstd` (float32, one per row) its root\n"
+       "scale_a), or per row and block of 128 columns (gemm_f8_block's: the transpose of a\n"
+       "contiguous (blocks, rows) tensor).  `total` (X's dtype) receives s and `rstd` (float32, one per row) its root\n"
        "where given: what rmsnorm_bwd reads.  `total` and Y may be X or residual themselves."),
     FN(rmsnorm_bwd,
        "rmsnorm_bwd(dY, total, weight, rstd, dX, *, dtotal=None, dweight=None, workspace=None,\n"
@@ -418,6 +570,32 @@ PyMethodDef methods[] = {
        "quant_f8(X, Q, scale, *, transpose=False, stream=None)\n\n"
        "Q, scale = X's rows in 8 bits (float8_e4m3fn, one float32 scale per row); with transpose\n"
        "its columns, Q being X.T's shape: gemm_f8's B from a [K, N] weight."),
+    FN(gemm_f8_block,
+       "gemm_f8_block(A, B, C, scale_a, scale_b, *, bias=None, act='none', residual=None,\n"
+       "              workspace=None, stream=None)\n\n"
+       "C = act(a @ b.T + bias) + residual, a and b being float8_e4m3fn A [M, K] and B [N, K] with\n"
+       "each block of 128 columns scaled: scale_a [M, blocks] by row, scale_b [N, blocks] by row or\n"
+       "[ceil(N / 128), blocks] by 128 rows (float32, any strides).  C (and residual) float32,\n"
+       "bfloat16 or float16; `residual` may be C itself."),
+    FN(quant_f8_block,
+       "quant_f8_block(X, Q, scale, *, transpose=False, stream=None)\n\n"
+       "Q, scale = X (with transpose X.T) in 8 bits, float8_e4m3fn, with a float32 scale per block of\n"
+       "128 columns of Q and one or 128 of its rows, as scale's shape says: gemm_f8_block's operands."),
+    FN(layernorm,
+       "layernorm(X, weight, bias, Y, *, residual=None, total=None, scale=None, mean=None, rstd=None,\n"
+       "          eps=1e-5, stream=None)\n\n"
+       "Y = (s - mean) * rstd * weight + bias row by row, s = X + residual; bias may be None.\n\n"
+       "Y has X's dtype, or is float8_e4m3fn with a float32 `scale` per row (gemm_f8's A and scale_a)\n"
+       "or per row and block of 128 columns (gemm_f8_block's; any strides).  `total` (X's dtype)\n"
+       "receives s, `mean` and `rstd` (float32, one per row) its moments where given: what\n"
+       "layernorm_bwd reads.  `total` and Y may be X or residual themselves."),
+    FN(layernorm_bwd,
+       "layernorm_bwd(dY, total, weight, mean, rstd, dX, *, dtotal=None, dweight=None, dbias=None,\n"
+       "              workspace=None, stream=None)\n\n"
+       "Gradients of layernorm: dX (the residual's too) and, where given, dweight and dbias (float32;\n"
+       "either needs layernorm_bwd_workspace's bytes).  `total`, `mean` and `rstd` as layernorm stored\n"
+       "them (total is X where there was no residual); `dtotal` is the gradient that reaches total by\n"
+       "other ways.  dX may be dY or dtotal itself."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal",

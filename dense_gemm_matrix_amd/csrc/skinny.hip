@@ -53,9 +53,11 @@ __device__ __forceinline__ f32x4 mfma_16(u32x4 a, u32x4 b, f32x4 c) {
 // The elements of a strip that a lane finishes, and what the epilogue reads for
 // them, loaded before the K loop (at its end they would wait for memory once
 // more).  CPL accumulators of 16 x 16 per wave: value idx = 4 j + r of lane (g, c)
-// is row 4 g + r, column n0 + CPL c + j; wave w finishes idx in [w PER, ..).
-template <int OUT, int EPI, int CPL, int W>
+// is row 4 g + r, column n0 + CPL c + j (TR: row c, column n0 + 4 g + r); wave w finishes
+// idx in [w PER, ..).
+template <int OUT, int EPI, int CPL, int W, bool TR = false>
 struct Strip {
+    static_assert(!TR || CPL == 1, "one block of 16 x 16");
     static constexpr int NV = CPL * 4;            // values per lane
     static constexpr int PER = (NV + W - 1) / W;  // of them, finished by one wave
     int row[PER], col[PER];
@@ -67,8 +69,8 @@ struct Strip {
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
             const int idx = wave * PER + q;
-            row[q] = 4 * (lane >> 4) + idx % 4;
-            col[q] = n0 + CPL * (lane & 15) + idx / 4;
+            row[q] = TR ? lane & 15 : 4 * (lane >> 4) + idx % 4;
+            col[q] = TR ? n0 + 4 * (lane >> 4) + idx % 4 : n0 + CPL * (lane & 15) + idx / 4;
             if (idx >= NV) row[q] = M;  // W larger than the values: none
         }
         if constexpr (EPI == EPI_FULL) {
@@ -303,6 +305,75 @@ __global__ __launch_bounds__(64 * W) void skinny_nt_kernel(
     strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
 }
 
+// e4m3 operands with a scale per block of 128 k, which is a step: a step's products are summed
+// apart and added scaled.  The operands trade places, so that a lane's four sums are of one
+// row of A and their factor, but for B's share with a scale per row of B, one value per lane.
+// NB: B's scales are per row.
+template <int OUT, int W, bool NB>
+__global__ __launch_bounds__(64 * W) void skinny_block_kernel(
+    const char* __restrict__ A, const char* __restrict__ B, char* C, int M, int N, int K, int lda,
+    int ldb, int ldc, int strips, BlockScales sc, EpiArgs epi) {
+    __shared__ float red[W * 4 * 64];
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int n0 = strip_of((int)blockIdx.x, strips) * 16;
+    const int rows_b = (N - n0) < 16 ? (N - n0) : 16;
+    const int nstep = (K + F8_BLOCK - 1) / F8_BLOCK;
+    Strip<OUT, EPI_FULL, 1, W, true> strip;
+    strip.prefetch(M, N, n0, wave, lane, epi);
+    constexpr int D = 2;           // steps per chunk; two chunks in registers
+    constexpr int NS = NB ? 4 : 1;  // of B's scales per lane
+    u32x4 a[2 * D][2], b[2 * D][2];
+    float sa[2 * D], sb[2 * D][NS];
+    // Rows past the edges take the last one's scale: what it feeds is not stored.
+    const float* const pa = sc.sa + (int64_t)(c < M ? c : M - 1) * sc.sa_row;
+    const float* pb[NS];
+#pragma unroll
+    for (int r = 0; r < NS; ++r) {
+        const int j = n0 + 4 * g + r < N ? n0 + 4 * g + r : N - 1;
+        pb[r] = sc.sb + (int64_t)(NB ? j : n0 / F8_BLOCK) * sc.sb_row;
+    }
+    auto load = [&](int t, int S) {  // S: a constant once unrolled
+        const int k0 = t * F8_BLOCK;
+        const int krem = (K - k0) < F8_BLOCK ? (K - k0) : F8_BLOCK;
+        const auto ra = make_rsrc(A + k0, krem > 0 ? (int64_t)(M - 1) * lda + krem : 0);
+        const auto rb = make_rsrc(B + (int64_t)n0 * ldb + k0, krem > 0 ? (int64_t)(rows_b - 1) * ldb + krem : 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            a[S][h] = load16(ra, c * lda + 64 * h + 16 * g);
+            b[S][h] = load16(rb, c * ldb + 64 * h + 16 * g);
+        }
+        sa[S] = pa[(int64_t)t * sc.sa_blk];
+#pragma unroll
+        for (int r = 0; r < NS; ++r) sb[S][r] = pb[r][(int64_t)t * sc.sb_blk];
+    };
+    f32x4 acc[1] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+    auto use = [&](int t, int S) {
+        const int k0 = t * F8_BLOCK;
+        f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4 x = a[S][h], y = b[S][h];
+            if (k0 + F8_BLOCK > K) {  // the rows' padding: 0 * NaN would be a NaN, so both
+                const int valid = K - k0 - (64 * h + 16 * g);
+                x = mask_bytes(x, valid);
+                y = mask_bytes(y, valid);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; q += 2)
+                part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen_f8(y[q], y[q + 1]),
+                                                               widen_f8(x[q], x[q + 1]), part, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            acc[0][r] = __builtin_fmaf(part[r], sa[S] * sb[S][NB ? r : 0], acc[0][r]);
+    };
+    run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
+                 [&](int i, int slot, auto) { use(wave + i * W, slot); });
+    strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
+}
+
 // The rank-M update: C[k][n] = sum over m < M <= 16 of A[m][k] D[m][n], a weight's
 // gradient from a few tokens.  Its floor is writing C; at 16 rows the fp32 multiply-adds,
 // 1024 per lane, bound it (4096 x 4096 bf16 16 us, floor 6.5).  A wave owns 8 rows of 512
@@ -412,6 +483,28 @@ hipError_t go_nt(const GemmLaunch& L) {
     return hipErrorInvalidValue;
 }
 
+template <int OUT, int W>
+hipError_t go_block_w(const GemmLaunch& L, const BlockScales& s) {
+    const char* a = L.A;
+    const char* b = L.B;
+    char* c = L.C;
+    int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc, strips = L.tiles_n;
+    BlockScales sc = s;
+    EpiArgs e = L.e;
+    void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &strips, &sc, &e};
+    return hipLaunchKernel(s.rows_b == 1 ? (const void*)skinny_block_kernel<OUT, W, true>
+                                         : (const void*)skinny_block_kernel<OUT, W, false>,
+                           dim3((unsigned)strips), dim3(64 * W), args, 0, L.stream);
+}
+
+template <int OUT>
+hipError_t go_block(const GemmLaunch& L, const BlockScales& s) {
+    if (L.slice_waves == 16) return go_block_w<OUT, 16>(L, s);
+    if (L.slice_waves == 8) return go_block_w<OUT, 8>(L, s);
+    if (L.slice_waves == 4) return go_block_w<OUT, 4>(L, s);
+    return hipErrorInvalidValue;
+}
+
 template <int FMT>
 hipError_t go_outer(const GemmLaunch& L) {
     const char* a = L.A;
@@ -427,6 +520,14 @@ hipError_t go_outer(const GemmLaunch& L) {
 }
 
 }  // namespace
+
+hipError_t launch_blockf8_skinny(const GemmLaunch& L, const BlockScales& s) {
+    if (L.M < 1 || L.M > SKINNY_M || L.tbn != 16 || L.splits != 1 || L.epi != EPI_FULL) return hipErrorInvalidValue;
+    if (L.out == OUT_F32) return go_block<OUT_F32>(L, s);
+    if (L.out == OUT_BF16) return go_block<OUT_BF16>(L, s);
+    if (L.out == OUT_F16) return go_block<OUT_F16>(L, s);
+    return hipErrorInvalidValue;
+}
 
 hipError_t launch_skinny(const GemmLaunch& L) {
     if (L.layout == LAY_TN) {

@@ -147,7 +147,7 @@ typedef enum {
 } dgemm_in;
 
 /* Activations.  gemm_ex takes the first two; gemm_act, gemm_act_bwd and gemm_f8
-   take all.  Phi is the normal distribution's integral. */
+   take all, as do gemm_f8_block, gemm_gated and gemm_gated_bwd.  Phi is the normal distribution's integral. */
 typedef enum {
     DGEMM_ACT_NONE = 0,
     DGEMM_ACT_RELU = 1,       /* x < 0 -> 0; NaN passes through                              */
@@ -370,8 +370,69 @@ int gemm_f8(int out, int M, int N, int K,
 int gemm_f8_plan(int out, int M, int N, int K, size_t workspace_bytes,
                  int* tile_rows, int* tile_cols, int* splits, size_t* workspace_used);
 
-/* Output of rmsnorm: X's format, or gemm_f8's 8-bit rows and their scales. */
-typedef enum { DGEMM_ROWS_SAME = 0, DGEMM_ROWS_F8 = 1 } dgemm_rows;
+/* Columns (along K) that share a scale in gemm_f8_block's operands. */
+#define DGEMM_F8_BLOCK 128
+
+/*
+ * The product of 8-bit operands (e4m3) with a scale per block of 128 along K, in
+ * fp32 between the blocks:
+ *
+ *     C[i][j] := act(sum over blocks b of sa(i, b) * sb(j, b)
+ *                    * sum_{128 b <= k < 128 (b + 1)} A[i][k] * B[j][k] + bias[j]) + R[i][j]
+ *
+ *     sa(i, b) = scale_a[i * sa_row + b * sa_block]
+ *     sb(j, b) = scale_b[(j / rows_b) * sb_row + b * sb_block],   rows_b = 128 or 1
+ *
+ * rows_b = 128: a weight, with a scale per 128 x 128 (quant_f8_block); with A's rows quantized
+ * along K this is a layer's forward product, and with dZ's along N and the weight's 8-bit
+ * transpose (whose scales are the transposed ones) the gradient of its input.  rows_b = 1: a
+ * scale per row and block on both sides, the gradient of a weight from A and dZ quantized
+ * along the batch.  A: M x K, B: N x K, both K-contiguous, as in gemm_f8; the last block may be
+ * short.  Strides of the scales are in elements, >= 0; scales of neighbouring rows next to
+ * each other (sa_row = 1) load fastest.  256 rows' scales span less than 2 GiB.
+ *
+ * Sums between blocks are fp32.  Within a block: exactly fp32 for fp32 C and for at most 16
+ * rows; for 16-bit C the 8-bit matrix instruction, which drops bits below 2^-13 of the largest
+ * of neighbouring products.  out, bias, act, R, workspace, errors and execution as gemm_f8.
+ */
+int gemm_f8_block(int out, int rows_b, int M, int N, int K,
+                  const void* A, int lda,
+                  const void* B, int ldb,
+                  void* C, int ldc,
+                  const float* scale_a, int sa_row, int sa_block,
+                  const float* scale_b, int sb_row, int sb_block,
+                  const float* bias, int act,
+                  const void* R, int ldr,
+                  void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/* As gemm_ex_plan, for gemm_f8_block. */
+int gemm_f8_block_plan(int out, int rows_b, int M, int N, int K, size_t workspace_bytes,
+                       int* tile_rows, int* tile_cols, int* splits, size_t* workspace_used);
+
+/*
+ * An M x N matrix to 8 bits with a scale per block of `rows` x 128 of the result Q, which is
+ * X (transpose = 0) or X transposed (transpose = 1, Q is N x M):
+ *
+ *     s = max(max over the block |x| / 448, 2^-100)      scale[(i / rows) * scale_row + b * scale_block] := s
+ *     Q[i][j] := e4m3(x / s), the exact quotient rounded once, to nearest even
+ *
+ * rows = 1 (gemm_f8_block's A; with transpose, both operands of a weight's gradient) or 128 (its
+ * B: transpose = 1 for a K x N weight, 0 for its N x K transpose).  s is fp32 and the quotient
+ * by that value (exact rounding for s above 2^-84).  A block holding an infinity or a NaN gets
+ * scale NaN.  in: X's format (DGEMM_IN_F32, _BF16 or _F16).  The scales' strides, in elements, keep
+ * them apart from each other (DGEMM_ERR_LEADING_DIM otherwise).  With rows = 128 or transpose
+ * fewer than 2^23 blocks of 128 x 128 (DGEMM_ERR_TOO_LARGE).  M == 0 or N == 0 is a no-op.
+ */
+int quant_f8_block(int in, int rows, int transpose, int M, int N,
+                   const void* X, int ldx,
+                   void* Q, int ldq,
+                   float* scale, int scale_row, int scale_block,
+                   void* stream);
+
+/* Output of rmsnorm and layernorm: X's format; gemm_f8's 8-bit rows and a scale per row;
+   gemm_f8_block's, a scale per row and block of 128 columns. */
+typedef enum { DGEMM_ROWS_SAME = 0, DGEMM_ROWS_F8 = 1, DGEMM_ROWS_F8_BLOCK = 2 } dgemm_rows;
 
 /*
  * Root-mean-square norm of rows, with the residual's addition and an output in
@@ -425,6 +486,53 @@ int rmsnorm_bwd(int in, int M, int N,
                 void* stream);
 
 int rmsnorm_bwd_workspace(int M, int N, size_t* required);
+
+/*
+ * Layer norm of rows, with the residual's addition and an output in 8 bits:
+ *
+ *     s = X[i] + R[i]                                S[i] := s
+ *     mean[i] := mean_j s_j,  rstd[i] := (mean_j (s_j - mean[i])^2 + eps)^-1/2
+ *     y = (s - mean[i]) * rstd[i] * weight + bias    Y[i] := y,  or in 8 bits as rmsnorm
+ *
+ * bias: NULL (none) or N fp32 values, 16-byte aligned.  mean, rstd (NULL: not wanted): M fp32
+ * values each.  The deviations are squared after the mean is known, from registers: rows with a
+ * mean far from zero lose nothing.  DGEMM_ROWS_F8: scale[i] per row (its strides are not looked
+ * at); DGEMM_ROWS_F8_BLOCK: block b of row i at scale[i * scale_row + b * scale_block], kept apart
+ * from each other (DGEMM_ERR_LEADING_DIM otherwise).  Otherwise as rmsnorm.
+ */
+int layernorm(int in, int out, int M, int N,
+              const void* X, int ldx,
+              const void* R, int ldr,
+              void* S, int lds,
+              const float* weight, const float* bias, float eps,
+              void* Y, int ldy,
+              float* scale, int scale_row, int scale_block,
+              float* mean, float* rstd,
+              void* stream);
+
+/*
+ * layernorm's backward pass.  Given dY, dS (or NULL), S (X where there was no residual), mean
+ * and rstd as for rmsnorm_bwd:
+ *
+ *     h = (S[i] - mean[i]) * rstd[i],  g = dY[i] * weight
+ *     dX[i] := rstd[i] * (g - mean_j g_j - h * mean_j(g_j h_j)) + dS[i]   (R's gradient too)
+ *     dweight := sum_i dY[i] * h,  dbias := sum_i dY[i]                    (fp32)
+ *
+ * dX may be dY or dS itself.  dweight and dbias may each be NULL; with either, a workspace of
+ * layernorm_bwd_workspace's bytes holds partial sums, added in a fixed order.  N <= 16384
+ * (DGEMM_ERR_TOO_LARGE above); M == 0 writes zeros to them.  Otherwise as rmsnorm.
+ */
+int layernorm_bwd(int in, int M, int N,
+                  const void* dY, int lddy,
+                  const void* S, int lds,
+                  const float* weight, const float* mean, const float* rstd,
+                  const void* dS, int ldds,
+                  void* dX, int lddx,
+                  float* dweight, float* dbias,
+                  void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+int layernorm_bwd_workspace(int M, int N, size_t* required);
 
 /*
  * Rows to 8 bits: scale[i] := max(max_j |X[i][j]| / 448, 2^-100), Q[i][j] :=
