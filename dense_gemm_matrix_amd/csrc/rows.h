@@ -83,9 +83,10 @@ __device__ __forceinline__ float quotient(float v, float scale, float inv) {
 }
 // The same, as what rounds to e4m3 once: where fp32's quotient is inexact and its last bit
 // is even, moved by that bit towards the remainder's side, so that a quotient which fp32
-// rounds to a border between two codes still falls on its own side of it (one value in a
-// million does, and an fp32 sum over such rows would show it).  The remainder is exact
-// while the scale is above 2^-84.
+// rounds to a border between two codes still falls on its own side of it (one 16-bit value
+// in a thousand does, the ratio to the block's largest being one of small integers; fp32 sums
+// over such rows would show the other code).  The remainder is exact while the scale is
+// above 2^-84.
 __device__ __forceinline__ float quotient_odd(float v, float scale, float inv) {
     const float q = quotient(v, scale, inv);
     const float r = __builtin_fmaf(-q, scale, v);

@@ -184,7 +184,12 @@ def test_plain_quantizer_against_torch():
     x = torch.randn(50, 300, generator=torch.Generator().manual_seed(1)).bfloat16()
     q, s = quant_block64(x, 1)
     v = x.double() / s.double().repeat_interleave(128, 1)[:, :300]
-    # torch rounds the 64-bit quotient through fp32, which moves none of these
-    assert torch.equal(q, v.float().to(F8).double())
+    # torch rounds through fp32, whose quotient may lie on the border between two codes where the exact one does not:
+    # either code is then within half a step of it
+    through = v.float().to(F8).double()
+    moved = q != through
+    assert moved.float().mean() < 0.01
+    assert torch.equal((q - v.float().double()).abs()[moved], (through - v.float().double()).abs()[moved])
+    assert ((q - v).abs() <= (through - v).abs()).all()
     q, s = quant_block64(torch.zeros(3, 4), 128)
     assert torch.equal(q, torch.zeros(3, 4, dtype=torch.float64)) and float(s) == 2.0 ** -100
