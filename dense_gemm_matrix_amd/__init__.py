@@ -18,6 +18,7 @@ from ._linear import (  # noqa: F401
     rmsnorm_bwd, rmsnorm_bwd_workspace,
 )
 from ._feedforward import (  # noqa: F401
-    gemm_f8_block, gemm_f8_block_plan, layer_norm, layer_norm_backward, layernorm, layernorm_bwd,
-    layernorm_bwd_workspace, matmul_f8_block, quant_f8_block, quantize_f8_block,
+    gemm_f8_block, gemm_f8_block_plan, gemm_gated, gemm_gated_bwd, gemm_gated_bwd_workspace, gemm_gated_plan,
+    layer_norm, layer_norm_backward, layernorm, layernorm_bwd, layernorm_bwd_workspace, linear_gated,
+    linear_gated_backward, matmul_f8_block, quant_f8_block, quantize_f8_block,
 )

@@ -1,20 +1,28 @@
 """Binding of a feed-forward block's operators (include/dgemm.h) beside _linear's:
-layer norms and their gradients, and products of 8-bit operands with a scale per
-block of 128.  As there, the functions named like the C entry points (in _marshal)
+gated projections and layer norms with their gradients, and products of 8-bit
+operands with a scale per block of 128.  As there, the functions named like the C entry points (in _marshal)
 marshal tensors that the caller has allocated, the others allocate their results
 and workspaces, and nothing is recorded for autograd."""
 import ctypes
 
 import torch
 
-from ._binding import IN_CODES, _TORCH_IN, _check, _lib
-from ._linear import F8, F8_BLOCK, _ANY, _blocks, _block_scales, _bytes, _device_tensor, _empty, _norm_results, \
-    _on_stream, _plan
-from ._marshal import gemm_f8_block, layernorm, layernorm_bwd, quant_f8_block  # noqa: F401
+from ._binding import DGEMM_OUT_F32, DGEMM_OUT_SAME, IN_CODES, _TORCH_IN, _check, _lib, _shapes
+from ._linear import (
+    F8, F8_BLOCK, _ANY, _block_scales, _blocks, _bytes, _device_tensor, _empty, _formats, _norm_results, _on_stream,
+    _plan,
+)
+from ._marshal import (  # noqa: F401
+    gemm_f8_block, gemm_gated, gemm_gated_bwd, layernorm, layernorm_bwd, quant_f8_block,
+)
 
 _i, _p, _sz, _f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 _P, _PS = ctypes.POINTER(_i), ctypes.POINTER(_sz)
 _ARGTYPES = {
+    "gemm_gated": [_i] * 5 + [_p, _i] * 4 + [_p, _p, _i] + [_p, _i] * 2 + [_p, _sz, _p],
+    "gemm_gated_plan": [_i] * 5 + [_sz, _P, _P, _P, _PS],
+    "gemm_gated_bwd": [_i] * 5 + [_p, _i] * 6 + [_i] + [_p, _i] * 3 + [_p, _p, _p, _sz, _p],
+    "gemm_gated_bwd_workspace": [_i] * 5 + [_PS, _PS],
     "gemm_f8_block": [_i] * 5 + [_p, _i] * 3 + [_p, _i, _i] * 2 + [_p, _i, _p, _i, _p, _sz, _p],
     "gemm_f8_block_plan": [_i] * 5 + [_sz, _P, _P, _P, _PS],
     "quant_f8_block": [_i] * 5 + [_p, _i] * 2 + [_p, _i, _i, _p],
@@ -25,6 +33,20 @@ _ARGTYPES = {
 for _name, _types in _ARGTYPES.items():
     getattr(_lib, _name).argtypes = _types
     getattr(_lib, _name).restype = _i
+
+
+def gemm_gated_plan(in_fmt: str, M: int, N: int, K: int, workspace_bytes: int, out_same: bool = False) -> dict:
+    """Host query of the plan gemm_gated uses with `workspace_bytes` available."""
+    return _plan(_lib.gemm_gated_plan, IN_CODES[in_fmt], DGEMM_OUT_SAME if out_same else DGEMM_OUT_F32,
+                 M, N, K, int(workspace_bytes))
+
+
+def gemm_gated_bwd_workspace(in_fmt: str, M: int, N: int, K: int, out_same: bool = True):
+    """(required, best) workspace bytes of gemm_gated_bwd."""
+    req, best = _sz(0), _sz(0)
+    _check(_lib.gemm_gated_bwd_workspace(IN_CODES[in_fmt], DGEMM_OUT_SAME if out_same else DGEMM_OUT_F32, M, N, K,
+                                         ctypes.byref(req), ctypes.byref(best)))
+    return req.value, best.value
 
 
 def gemm_f8_block_plan(out_fmt: str, M: int, N: int, K: int, workspace_bytes: int, rows_b: int = F8_BLOCK) -> dict:
@@ -41,6 +63,40 @@ def layernorm_bwd_workspace(M: int, N: int) -> int:
 
 
 # ------------------------------------------------------------ allocating forms
+
+@_on_stream
+def linear_gated(A, Bg, Bu, *, bias_g=None, bias_u=None, act: str = "silu", out_dtype=None,
+                 keep_preact: bool = False):
+    """act(A @ Bg + bias_g) * (A @ Bu + bias_u), and with keep_preact also both factors before the
+    activation (for linear_gated_backward): C or (C, gate, up).  out_dtype: A's (default) or float32."""
+    _device_tensor(A, "A")
+    _device_tensor(Bg, "Bg")
+    out_dtype = A.dtype if out_dtype is None else out_dtype
+    code, out = _formats(A, Bg, out_dtype, None)
+    M, N, K = A.shape[0], Bg.shape[1], A.shape[1]
+    C = _empty(M, N, out_dtype, A.device)
+    G, U = (_empty(M, N, out_dtype, A.device) if keep_preact else None for _ in range(2))
+    plan = _plan(_lib.gemm_gated_plan, code, out, M, N, K, _ANY)
+    gemm_gated(A, Bg, Bu, C, bias_g=bias_g, bias_u=bias_u, act=act, gate=G, up=U,
+               workspace=_bytes(plan["workspace_bytes"], A.device))
+    return (C, G, U) if keep_preact else C
+
+
+@_on_stream
+def linear_gated_backward(A, Bg, Bu, dC, gate, up, *, act: str = "silu", bias: bool = False):
+    """(dA, dBg, dBu, dbias_g, dbias_u) of linear_gated; the biases' are None unless `bias`."""
+    _device_tensor(A, "A")
+    M, N, K = _shapes(A, Bg, dC)
+    code, out = _formats(A, Bg, dC.dtype, None)
+    dA = _empty(M, K, A.dtype, A.device)
+    dBg, dBu = (_empty(K, N, A.dtype, A.device) for _ in range(2))
+    dbg, dbu = (torch.empty(N, dtype=torch.float32, device=A.device) if bias else None for _ in range(2))
+    best = _sz(0)
+    _check(_lib.gemm_gated_bwd_workspace(code, out, M, N, K, None, ctypes.byref(best)))
+    gemm_gated_bwd(A, Bg, Bu, dC, gate, up, act=act, dA=dA, dBg=dBg, dBu=dBu, dbias_g=dbg, dbias_u=dbu,
+                   workspace=_bytes(best.value, A.device))
+    return dA, dBg, dBu, dbg, dbu
+
 
 @_on_stream
 def quantize_f8_block(X, *, rows: int = 1, transpose: bool = False):

@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("dgemm.hip", "linear.hip", "feedforward.hip", "gemm16.hip", "gemm32.hip", "gemmt.hip",
                      "slicek16.hip", "slicet.hip", "skinny.hip", "splitk.hip", "norm.hip", "layernorm.hip",
-                     "quantblock.hip", "blockf8.hip", "actgrad.hip")]
+                     "quantblock.hip", "blockf8.hip", "gated.hip", "actgrad.hip")]
 LIB = os.path.join(PKG, "libdgemm.so")
 # The benchmark's matrix-instruction ceiling kernel: a library of its own,
 # loaded only by bench.py, never by the package.

@@ -120,6 +120,95 @@ __global__ __launch_bounds__(64 * W) void act_grad_kernel(ActGradArgs a) {
     }
 }
 
+// The same for a gated layer: dG = dC U act'(G) and dU = dC act(G), with both column sums.  Bound by
+// memory too, five arrays instead of three.
+template <int CF, int DF, int W, int T>
+__global__ __launch_bounds__(64 * W) void gated_grad_kernel(GatedGradArgs a) {
+    constexpr int RP = 64 / T;  // rows per wave and pass
+    __shared__ float sums[2][W * AG_COLS];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int lr = lane / T;
+    const int c = (int)blockIdx.x * AG_COLS + (lane % T) * 8;
+    const int nvalid = a.N - c;
+    const int64_t r0 = (int64_t)blockIdx.y * a.rows_per;
+    const int64_t r1 = r0 + a.rows_per < a.M ? r0 + a.rows_per : a.M;
+    float sg[8] = {0, 0, 0, 0, 0, 0, 0, 0}, su[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 2
+    for (int64_t row = r0 + wave * RP; row < r1; row += W * RP) {
+        const int n = r1 - row < RP ? (int)(r1 - row) : RP;  // this wave's rows
+        auto rows = [&](const char* p, int ld, int es) {
+            return make_rsrc(p + row * ld * es, ((int64_t)(n - 1) * ld + a.N) * es);
+        };
+        auto at = [&](int ld, int es) {
+            return lr < n && nvalid > 0 ? (uint32_t)((lr * ld + c) * es) : OOB_LANE;
+        };
+        Row8<CF> x, y, z;
+        x.load(rows(a.dC, a.lddc, fmt_es<CF>), at(a.lddc, fmt_es<CF>), nvalid);
+        y.load(rows(a.G, a.ldg, fmt_es<CF>), at(a.ldg, fmt_es<CF>), nvalid);
+        z.load(rows(a.U, a.ldu, fmt_es<CF>), at(a.ldu, fmt_es<CF>), nvalid);
+        float d[8], g[8], u[8], dg[8], du[8];
+        x.get(d);
+        y.get(g);
+        z.get(u);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dg[j] = d[j] * u[j];
+            du[j] = g[j];
+        }
+        apply_act_grad<CF>(dg, g, a.act);
+        apply_act<CF>(du, a.act);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            du[j] *= d[j];
+            sg[j] += dg[j];
+            su[j] += du[j];
+        }
+        if (a.dG) {
+            Row8<DF> o;
+            o.set(dg);
+            o.store(rows(a.dG, a.lddz, fmt_es<DF>), at(a.lddz, fmt_es<DF>), nvalid);
+            o.set(du);
+            o.store(rows(a.dU, a.lddz, fmt_es<DF>), at(a.lddz, fmt_es<DF>), nvalid);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sums[0][wave * AG_COLS + lane * 8 + j] = sg[j];
+        sums[1][wave * AG_COLS + lane * 8 + j] = su[j];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * T * 8; i += 64 * W) {
+        const int which = i / (T * 8), j = i % (T * 8);
+        const int col = (int)blockIdx.x * AG_COLS + j;
+        if (col >= a.N) continue;
+        float v = sums[which][j];
+#pragma unroll
+        for (int q = 1; q < W * RP; ++q) v += sums[which][q * T * 8 + j];
+        a.part[((int64_t)blockIdx.y * 2 + which) * a.ldp + col] = v;
+    }
+}
+
+template <int CF, int DF, int T>
+hipError_t go_gg(const GatedGradArgs& a, hipStream_t stream) {
+    GatedGradArgs b = a;
+    void* args[] = {&b};
+    const bool one = a.M > 16 && a.M <= a.rows_per;
+    const void* fn = one ? (const void*)gated_grad_kernel<CF, DF, 16, T> : (const void*)gated_grad_kernel<CF, DF, 4, T>;
+    return hipLaunchKernel(fn,
+                           dim3((unsigned)((a.N + AG_COLS - 1) / AG_COLS),
+                                (unsigned)((a.M + a.rows_per - 1) / a.rows_per)),
+                           dim3(one ? 1024 : 256), args, 0, stream);
+}
+
+template <int CF, int DF>
+hipError_t gg_by_size(const GatedGradArgs& a, hipStream_t stream) {
+    if (a.N <= 128) return go_gg<CF, DF, 16>(a, stream);
+    if (a.N <= 256) return go_gg<CF, DF, 32>(a, stream);
+    return go_gg<CF, DF, 64>(a, stream);
+}
+
 template <int CF, int DF, int T>
 hipError_t go_ag(const ActGradArgs& a, hipStream_t stream) {
     ActGradArgs b = a;
@@ -192,6 +281,15 @@ hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t str
     if (cf == OUT_F32 && df == OUT_F16) return ag_by_size<OUT_F32, OUT_F16>(a, stream);
     if (cf == OUT_BF16 && df == OUT_BF16) return ag_by_size<OUT_BF16, OUT_BF16>(a, stream);
     if (cf == OUT_F16 && df == OUT_F16) return ag_by_size<OUT_F16, OUT_F16>(a, stream);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gated_grad(const GatedGradArgs& a, int cf, int df, hipStream_t stream) {
+    if (cf == OUT_F32 && df == OUT_F32) return gg_by_size<OUT_F32, OUT_F32>(a, stream);
+    if (cf == OUT_F32 && df == OUT_BF16) return gg_by_size<OUT_F32, OUT_BF16>(a, stream);
+    if (cf == OUT_F32 && df == OUT_F16) return gg_by_size<OUT_F32, OUT_F16>(a, stream);
+    if (cf == OUT_BF16 && df == OUT_BF16) return gg_by_size<OUT_BF16, OUT_BF16>(a, stream);
+    if (cf == OUT_F16 && df == OUT_F16) return gg_by_size<OUT_F16, OUT_F16>(a, stream);
     return hipErrorInvalidValue;
 }
 

@@ -225,6 +225,20 @@ hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool t
 // The same of 16-bit grid tiles, 128 x 128 or 256 x 256 for both.
 hipError_t launch_gemmt_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first,
                              const ColReduceArgs& r);
+// The products of a gated layer's backward pass and its column sums in one kernel: nt (LAY_NT) is
+// nt.A nt.B^T + A2 B2^T (A2 with nt.A's row pitch), tn the weights' gradients (LAY_TN); tiles_m = 0
+// or N = 0: none.  One tile size for all (launch_gemmt_gated, 16-bit) or one for nt and one for
+// tn (launch_slicet_gated, 4 waves); the TN tiles first if tn_first.
+struct GatedBwdLaunch {
+    GemmLaunch nt, tn[2];
+    const char* A2;
+    const char* B2;
+    int ldb2;
+    bool tn_first;
+    ColReduceArgs sums[2];
+};
+hipError_t launch_gemmt_gated(const GatedBwdLaunch& L);
+hipError_t launch_slicet_gated(const GatedBwdLaunch& L);
 hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_waves > 0
 
 // Products of at most SKINNY_M rows (skinny.hip): LAY_NN of 16-bit and fp32
@@ -234,6 +248,8 @@ hipError_t launch_slicek16(const GemmLaunch& L);  // IN_BF16, IN_F16 with slice_
 // the partials' C as for a grid launch.
 constexpr int SKINNY_M = 16;
 hipError_t launch_skinny(const GemmLaunch& L);
+// C = A B^T + A2 B2^T of few rows (A2 with A's row pitch), LAY_NT of 16-bit and fp32 operands.
+hipError_t launch_skinny_two(const GemmLaunch& L, const char* A2, const char* B2, int ldb2);
 
 // Products of e4m3 operands with a scale per block (blockf8.hip): A[M x K] B[N x K]^T, block b
 // of K being [F8_BLOCK b, F8_BLOCK (b + 1)), row i of A scaled by sa[i sa_row + b sa_blk], row j
@@ -247,6 +263,35 @@ struct BlockScales {
 };
 hipError_t launch_blockf8(const GemmLaunch& g, const BlockScales& s);
 hipError_t launch_blockf8_skinny(const GemmLaunch& g, const BlockScales& s);
+
+// Gated projections (gated.hip, skinny.hip): C := act(G) U, G := A Bg + bias_g, U := A Bu + bias_u.
+// biases, G and U may be NULL, and C for a split's partial products.
+struct GatedEpi {
+    const float* bias_g;
+    const float* bias_u;
+    int act;
+    char* G;
+    char* U;
+    int ldg, ldu;
+};
+// tbm x tbp tiles (tbp columns of G and of U); split z, of kchunk k, writes G and U at z zstride
+// bytes.  Few rows: strips of tbp columns, `waves` waves each (launch_gated_skinny).
+struct GatedLaunch {
+    int in, out, tbm, tbp, stages, waves;
+    const char* A;
+    const char* Bg;
+    const char* Bu;
+    char* C;
+    int M, N, K, lda, ldbg, ldbu, ldc, tiles_m, tiles_n, splits, kchunk;
+    int64_t zstride;
+    GatedEpi e;
+    hipStream_t stream;
+};
+hipError_t launch_gated(const GatedLaunch& L);
+hipError_t launch_gated_skinny(const GatedLaunch& L);
+// W[z]: M x 2 ldw fp32 partial products of G and, from column ldw on, of U.
+hipError_t launch_gated_reduce(const float* W, int splits, int64_t zstride, int ldw, char* C, int ldc, int M, int N,
+                               int out, const GatedEpi& e, hipStream_t stream);
 
 // Split-K reduction: C[i][j] = epilogue(sum_{z < splits} W[z][i][j]) with W
 // fp32, row pitch ldw (a multiple of 4) and split stride zstride elements.
@@ -323,6 +368,18 @@ struct ActGradArgs {
     float* part;
     int M, N, lddc, ldz, lddz, ldp, rows_per, act;
 };
+// The gated layer's: dG = dC U act'(G), dU = dC act(G); part: two rows of ldp sums per rows_per
+// rows, dG's and dU's, or NULL.
+struct GatedGradArgs {
+    const char* dC;
+    const char* G;
+    const char* U;
+    char* dG;
+    char* dU;
+    float* part;
+    int M, N, lddc, ldg, ldu, lddz, ldp, rows_per, act;
+};
+hipError_t launch_gated_grad(const GatedGradArgs& a, int cf, int df, hipStream_t stream);
 int act_grad_rows(int M, int N);
 hipError_t launch_act_grad(const ActGradArgs& a, int cf, int df, hipStream_t stream);
 hipError_t launch_col_reduce(const ColReduceArgs& a, hipStream_t stream);

@@ -1,7 +1,8 @@
-// feedforward.hip -- the C ABI of a feed-forward block's operators beside linear.hip's:
-// layer norms and their gradients (layernorm, layernorm_bwd), products of 8-bit operands with
-// a scale per block and the quantizer of those (gemm_f8_block, quant_f8_block).  Host code
-// only: validation, plans and launches.
+// feedforward.hip -- the C ABI of a feed-forward block's operators beside linear.hip's: gated
+// projections and their gradients (gemm_gated, gemm_gated_bwd), layer norms and theirs
+// (layernorm, layernorm_bwd), products of 8-bit operands with a scale per block and the
+// quantizer of those (gemm_f8_block, quant_f8_block).  Host code only: validation, plans and
+// launches.
 
 #include <algorithm>
 
@@ -77,6 +78,254 @@ int run_block(int of, int M, int N, int K, const void* A, int lda, const void* B
     if (launch_blockf8(L, s) != hipSuccess) return DGEMM_ERR_LAUNCH;
     return launched(launch_splitk_reduce((const float*)ws, p.splits, (int64_t)M * p.ldw, p.ldw, (char*)C, ldc, M,
                                          N, of, EPI_FULL, e, stream));
+}
+
+// ------------------------------------------------------------- gated projections
+
+// Tiles of gated.hip, their columns of G and U counted together: the estimates of the grid
+// kernels with the same accumulators and steps.
+constexpr TileCand TILES_G16[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6}, {128, 128, 0.6, 1.26, 1.35, 0.8, 1.0}};
+constexpr TileCand TILES_G32[] = {{128, 128, 0.85, 1.5, 1.5, 0.85, 1.0}};
+
+struct GatedPlan {
+    int bm, bn;     // bn: columns of G (and of U)
+    int splits, kchunk, ldw, waves;
+    int64_t ws_bytes;
+    bool skinny;
+};
+
+// A plan at `splits` K pieces of whole steps of bk; splits = 0 if it does not fit.
+GatedPlan gated_pieces(int bm, int bn, int bk, int M, int N, int K, int splits, uint64_t ws) {
+    const Plan q = plan_pieces(TileCand{bm, bn, 1, 0, 0, 1, 1}, bk, M, N, K, splits, UINT64_MAX);
+    GatedPlan p{bm, bn, q.splits, q.kchunk, q.ldw, 0, 2 * q.ws_bytes, false};
+    if (p.splits > 1 && ((uint64_t)p.ws_bytes > ws || (int64_t)PANEL_ROWS * 2 * p.ldw * 4 >= DESC_LIMIT)) p.splits = 0;
+    return p;
+}
+
+// At most SKINNY_M rows: as plan_skinny's strips of B stored along the output, of both weights.
+GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
+    auto strips = [&](int cols, int waves, int splits) {
+        GatedPlan p = gated_pieces(SKINNY_M, cols, 32, M, N, K, splits, ws);
+        if (p.splits > 1 && p.kchunk % 64 == 0) {  // an odd number of steps, as plan_skinny's
+            p.kchunk += 32;
+            p.splits = (int)ceil_div(K, p.kchunk);
+            p.ws_bytes = (int64_t)p.splits * M * 2 * p.ldw * 4;
+        }
+        p.waves = waves;
+        p.skinny = true;
+        return p;
+    };
+    int fm, fn, fs;
+    if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || (fn == 128 && in != IN_F32))) {
+        const GatedPlan p = strips(fn, fn == 32 ? 16 : 8, fs);
+        if (p.splits > 0) return p;
+    }
+    if (K >= 2048 && 2 * (int64_t)N <= 5 * (int64_t)K) {
+        const int s = (int)std::min<int64_t>(std::min(MAX_SPLITS, K / 256), NUM_CU / ceil_div(N, 64));
+        if (s >= 2) {
+            const GatedPlan p = strips(64, 8, s);
+            if (p.splits > 1) return p;
+        }
+    }
+    return ceil_div(N, 32) > NUM_CU ? strips(64, 8, 1) : strips(32, 16, 1);
+}
+
+GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
+    if (M > 0 && M <= SKINNY_M && N > 0) return plan_gated_skinny(in, M, N, K, ws);
+    const TileCand* tiles = in == IN_F32 ? TILES_G32 : TILES_G16;
+    const int n = in == IN_F32 ? 1 : 2, bk = in == IN_F32 ? 32 : 64;
+    const int nk = (int)ceil_div(std::max(K, 1), bk);
+    int fm, fn, fs;
+    if (forced_grid(fm, fn, fs))
+        for (int i = 0; i < n; ++i)
+            if (tiles[i].bm == fm && tiles[i].bn == fn) {
+                const GatedPlan p = gated_pieces(fm, fn / 2, bk, M, N, K, fs, ws);
+                if (p.splits > 0) return p;
+            }
+    GatedPlan best{};
+    double best_us = -1.0;
+    const int N2 = (int)std::min<int64_t>(2 * up(N, 32), INT32_MAX);
+    for (int s = 1; s <= MAX_SPLITS && s <= nk; ++s)
+        for (int i = 0; i < n; ++i) {
+            const TileCand& t = tiles[i];
+            const GatedPlan p = gated_pieces(t.bm, t.bn / 2, bk, M, N, K, s, ws);
+            if (p.splits != s) continue;
+            double us = estimate_us(in, es_out, M, N2, t, s, s == 1 ? nk : p.kchunk / bk, s == 1 ? 0 : 2 * p.ldw);
+            if (s > 1) us /= SPLIT_MARGIN;
+            if (best_us < 0.0 || us < best_us) {
+                best_us = us;
+                best = p;
+            }
+        }
+    return best;
+}
+
+int run_gated(int in, int of, int M, int N, int K, const void* A, int lda, const void* Bg, int ldbg, const void* Bu,
+              int ldbu, void* C, int ldc, const GatedEpi& e, const GatedPlan& p, void* ws, hipStream_t stream) {
+    GatedLaunch L{};
+    L.in = in;
+    L.out = of;
+    L.tbm = p.bm;
+    L.tbp = p.bn;
+    L.A = (const char*)A;
+    L.Bg = (const char*)Bg;
+    L.Bu = (const char*)Bu;
+    L.C = (char*)C;
+    L.M = M;
+    L.N = N;
+    L.K = K;
+    L.lda = lda;
+    L.ldbg = ldbg;
+    L.ldbu = ldbu;
+    L.ldc = ldc;
+    L.tiles_m = (int)ceil_div(M, p.bm);
+    L.tiles_n = (int)ceil_div(N, p.bn);
+    L.splits = p.splits;
+    L.kchunk = p.splits > 1 ? p.kchunk : std::max(K, 1);
+    L.waves = p.waves;
+    L.e = e;
+    L.stream = stream;
+    const int64_t wgs = (int64_t)L.tiles_m * L.tiles_n * p.splits;
+    if (wgs > INT32_MAX) return DGEMM_ERR_TOO_LARGE;
+    // Alone on its CU the 128 x 64 tile has room for a ring of four stages (as gemm16's).
+    L.stages = p.bm == 128 && wgs <= NUM_CU ? 4 : 2;
+    const auto launch = p.skinny ? launch_gated_skinny : launch_gated;
+    if (p.splits == 1) return launched(launch(L));
+    L.out = OUT_F32;
+    L.C = nullptr;
+    L.zstride = (int64_t)M * 2 * p.ldw * 4;
+    L.e = GatedEpi{};
+    L.e.G = (char*)ws;
+    L.e.U = (char*)ws + (int64_t)p.ldw * 4;
+    L.e.ldg = L.e.ldu = 2 * p.ldw;
+    if (launch(L) != hipSuccess) return DGEMM_ERR_LAUNCH;
+    return launched(launch_gated_reduce((const float*)ws, p.splits, (int64_t)M * 2 * p.ldw, p.ldw, (char*)C, ldc, M, N,
+                                        of, e, stream));
+}
+
+// The pieces of gemm_gated_bwd's workspace, in order: dG, dU, the column sums of the biases, an
+// operand's transpose (fp32), then what fp32 products' plans may use.
+struct GatedBwdParts {
+    int lddz, ldp, chunks;
+    int64_t dz, part, trans, required;  // dz: of one of the two
+};
+
+GatedBwdParts gated_bwd_parts(int in, int M, int N, int K, bool products, bool dbias) {
+    GatedBwdParts b{};
+    const int es = in_esize(in);
+    b.lddz = (int)up(N, 16 / es);
+    b.ldp = (int)up(N, 4);
+    b.chunks = (int)ceil_div(M, act_grad_rows(M, N));
+    b.dz = products ? up((int64_t)M * b.lddz * es, WS_ALIGN) : 0;
+    b.part = dbias ? up((int64_t)b.chunks * 2 * b.ldp * 4, WS_ALIGN) : 0;
+    if (products && es == 4 && M > SKINNY_M)
+        b.trans = up(std::max((int64_t)N * up(K, 4), (int64_t)K * up(M, 4)) * 4, WS_ALIGN);
+    b.required = 2 * b.dz + b.part + b.trans;
+    return b;
+}
+
+// How the products of a gated layer's backward pass run: tile sizes of the input's gradient (nt)
+// and of the weights' (tn), 0 where it is not wanted; slices: slicet.hip's tiles, else gemmt.hip's.
+struct GatedBwdPlan {
+    int nt, tn;
+    bool nt_slices, tn_slices, together, tn_first, transposes;  // transposes: fp32 by the grid kernels
+};
+
+// M rows, K inputs, N gated outputs: nt has M x K outputs of 2 N terms, tn two of K x N of M.
+GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint64_t ws) {
+    const int f = in == IN_F32 ? IN_F32 : IN_BF16;
+    const int kn = (int)std::min<int64_t>(2 * up(N, 64), INT32_MAX);
+    GatedBwdPlan best{};
+    double best_us = -1.0;
+    auto consider = [&](double us, const GatedBwdPlan& p) {
+        if (best_us >= 0.0 && us >= best_us) return;
+        best_us = us;
+        best = p;
+    };
+    auto nt_tiles = [&](int t) { return dA ? ceil_div(M, t) * ceil_div(K, t) : 0; };
+    auto tn_tiles = [&](int t) { return dB ? 2 * ceil_div(K, t) * ceil_div(N, t) : 0; };
+    int fm, fn, fs;
+    const bool forced = forced_grid(fm, fn, fs) && fm == fn && (fm == 32 || fm == 64 || (f != IN_F32 && fm >= 128));
+    auto allowed = [&](int t) { return !forced || t == fm; };
+    // One product alone: us, tile and kind.
+    struct Alone { double us; int tile; bool slices; };
+    auto alone = [&](bool nt) {
+        Alone a{-1.0, 0, false};
+        for (int t = 32; t <= 64; t += 32) {
+            const int64_t n = nt ? nt_tiles(t) : tn_tiles(t);
+            if (!allowed(t) || n > INT32_MAX / 2) continue;
+            const double us = pair_us(n, slice_tile_us(f, t, nt ? kn : M), 0, 0.0);
+            if (a.us < 0.0 || us < a.us) a = Alone{us, t, true};
+        }
+        for (const TileCand& t : TILES_T) {
+            const int64_t n = nt ? nt_tiles(t.bm) : tn_tiles(t.bm);
+            if (f == IN_F32 || !allowed(t.bm) || n > INT32_MAX / 2) continue;
+            bool first;
+            const double us = pair_grid_us(t, in, n, nt ? kn : M, 0, 0, first);
+            if (a.us < 0.0 || us < a.us) a = Alone{us, t.bm, false};
+        }
+        return a;
+    };
+    for (int a = 32; a <= 64; a += 32)
+        for (int b = 32; b <= 64; b += 32) {
+            if ((!dA && a > 32) || (!dB && b > 32) || !allowed(a) || !allowed(b)) continue;
+            const int64_t ta = nt_tiles(a), tb = tn_tiles(b);
+            if (ta + tb > (forced ? (int64_t)INT32_MAX / 2 : f == IN_F32 ? PAIR_TILES_32 : PAIR_TILES_16)) continue;
+            const double wa = slice_tile_us(f, a, kn), wb = slice_tile_us(f, b, M);
+            const double fwd = pair_us(ta, wa, tb, wb), rev = pair_us(tb, wb, ta, wa);
+            consider(std::min(fwd, rev), GatedBwdPlan{a, b, true, true, true, rev < fwd, false});
+        }
+    if (f != IN_F32)
+        for (const TileCand& t : TILES_T) {
+            const int64_t ta = nt_tiles(t.bm), tb = tn_tiles(t.bm);
+            if (!allowed(t.bm) || ta + tb > INT32_MAX / 2) continue;
+            bool tn_first;
+            const double us = pair_grid_us(t, in, ta, kn, tb, M, tn_first);
+            consider(us, GatedBwdPlan{t.bm, t.bm, false, false, true, tn_first, false});
+        }
+    if (f == IN_F32 && !forced) {
+        double us = 0.0;
+        if (dA)
+            us += 2 * (PAIR_GAP_US + (double)K * N * 8.0 / 4e6 + PAIR_GAP_US +
+                       plan_us(in, 4, make_plan(in, 4, M, K, N, ws, false), M, K, N));
+        if (dB)
+            us += PAIR_GAP_US + (double)K * M * 8.0 / 4e6 +
+                  2 * (PAIR_GAP_US + plan_us(in, 4, make_plan(in, 4, K, N, M, ws, false), K, N, M));
+        consider(us, GatedBwdPlan{0, 0, false, false, false, false, true});
+    }
+    if (dA && dB && !forced) {
+        const Alone a = alone(true), b = alone(false);
+        if (a.us >= 0.0 && b.us >= 0.0)
+            consider(a.us + b.us + PAIR_GAP_US, GatedBwdPlan{a.tile, b.tile, a.slices, b.slices, false, false, false});
+    }
+    return best;
+}
+
+GemmLaunch bwd_launch(int in, int layout, int tile, bool slices, int M, int N, int K, const void* X, int ldx,
+                      const void* Y, int ldy, void* C, int ldc, hipStream_t stream) {
+    GemmLaunch L{};
+    L.in = in;
+    L.out = out_format(in, DGEMM_OUT_SAME);
+    L.tbm = L.tbn = tile;
+    L.layout = layout;
+    L.slice_waves = slices ? 4 : 0;
+    L.splits = 1;
+    L.kchunk = K;
+    L.epi = EPI_FULL;
+    L.e.alpha = 1.0f;
+    L.A = (const char*)X;
+    L.B = (const char*)Y;
+    L.C = (char*)C;
+    L.M = M;
+    L.N = N;
+    L.K = K;
+    L.lda = ldx;
+    L.ldb = ldy;
+    L.ldc = ldc;
+    L.tiles_m = (int)ceil_div(M, tile);
+    L.tiles_n = (int)ceil_div(N, tile);
+    L.stream = stream;
+    return L;
 }
 
 }  // namespace
@@ -243,6 +492,193 @@ int layernorm_bwd_workspace(int M, int N, size_t* required) {
     if (M < 0 || N < 0) return DGEMM_ERR_INVALID_VALUE;
     if (N > NORM_BWD_MAX) return DGEMM_ERR_TOO_LARGE;
     if (required) *required = (size_t)norm_bwd_grid(M, N) * 2 * (size_t)up(N, 4) * 4;
+    return DGEMM_OK;
+}
+
+int gemm_gated(int in, int out, int M, int N, int K, const void* A, int lda, const void* Bg, int ldbg, const void* Bu,
+               int ldbu, void* C, int ldc, const float* bias_g, const float* bias_u, int act, void* G, int ldg,
+               void* U, int ldu, void* workspace, size_t workspace_bytes, void* stream) {
+    if (in < IN_F32 || in > IN_F16 || M < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_VALUE;
+    const int of = out_format(in, out);
+    if (of < 0 || !valid_act(act) || (workspace_bytes > 0 && !workspace)) return DGEMM_ERR_INVALID_VALUE;
+    const int eo = out_esize(of), es = in_esize(in);
+    const bool reads = M > 0 && N > 0;
+    const Mat mA{A, reads ? M : 0, K, lda, es}, mBg{Bg, reads ? K : 0, N, ldbg, es}, mBu{Bu, reads ? K : 0, N, ldbu, es};
+    const Mat mC{C, M, N, ldc, eo}, mG{G, G ? M : 0, N, ldg, eo}, mU{U, U ? M : 0, N, ldu, eo};
+    int st;
+    if ((st = check_mat(mA)) != DGEMM_OK || (st = check_mat(mBg)) != DGEMM_OK || (st = check_mat(mBu)) != DGEMM_OK ||
+        (st = check_mat(mC)) != DGEMM_OK || (G && (st = check_mat(mG)) != DGEMM_OK) ||
+        (U && (st = check_mat(mU)) != DGEMM_OK))
+        return st;
+    if (!reads) return DGEMM_OK;
+    const GatedPlan p = plan_gated(in, eo, M, N, K, workspace ? workspace_bytes : 0);
+    const Mat ws = bytes_of(workspace, p.ws_bytes);
+    if (check_vec(bias_g, 4) != DGEMM_OK || check_vec(bias_u, 4) != DGEMM_OK || check_vec(ws.p, 16) != DGEMM_OK)
+        return DGEMM_ERR_MISALIGNED;
+    const Mat ins[] = {mA, mBg, mBu, vec(bias_g, N), vec(bias_u, N)}, outs[] = {mC, mG, mU, ws};
+    if (any_overlap(outs, 4, ins, 5)) return DGEMM_ERR_ALIAS;
+    if ((st = check_device()) != DGEMM_OK) return st;
+    return run_gated(in, of, M, N, K, A, lda, Bg, ldbg, Bu, ldbu, C, ldc,
+                     GatedEpi{bias_g, bias_u, act, (char*)G, (char*)U, ldg, ldu}, p, workspace, (hipStream_t)stream);
+}
+
+int gemm_gated_plan(int in, int out, int M, int N, int K, size_t workspace_bytes, int* tile_rows, int* tile_cols,
+                    int* splits, size_t* workspace_used) {
+    if (in < IN_F32 || in > IN_F16 || M < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_VALUE;
+    const int of = out_format(in, out);
+    if (of < 0) return DGEMM_ERR_INVALID_VALUE;
+    if (ceil_div(M, 128) * ceil_div(N, 64) > INT32_MAX) return DGEMM_ERR_TOO_LARGE;
+    const GatedPlan p = plan_gated(in, out_esize(of), M, N, K, workspace_bytes);
+    Plan q{};
+    q.bm = p.bm;
+    q.bn = p.bn;
+    q.splits = p.splits;
+    q.ws_bytes = p.ws_bytes;
+    return report(q, tile_rows, tile_cols, splits, workspace_used);
+}
+
+int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda, const void* Bg, int ldbg,
+                   const void* Bu, int ldbu, const void* dC, int lddc, const void* G, int ldg, const void* U, int ldu,
+                   int act, void* dA, int ldda, void* dBg, int lddbg, void* dBu, int lddbu, float* dbias_g,
+                   float* dbias_u, void* workspace, size_t workspace_bytes, void* stream) {
+    if (in < IN_F32 || in > IN_F16 || M < 0 || N < 0 || K < 0) return DGEMM_ERR_INVALID_VALUE;
+    const int cf = out_format(in, out);
+    if (cf < 0 || !valid_act(act) || (workspace_bytes > 0 && !workspace)) return DGEMM_ERR_INVALID_VALUE;
+    const int es = in_esize(in), ec = out_esize(cf);
+    const bool dB = dBg || dBu, bias = dbias_g || dbias_u;
+    const Mat mA{A, dB ? M : 0, K, lda, es}, mBg{Bg, dA ? K : 0, N, ldbg, es}, mBu{Bu, dA ? K : 0, N, ldbu, es};
+    const Mat mdC{dC, M, N, lddc, ec}, mG{G, M, N, ldg, ec}, mU{U, M, N, ldu, ec};
+    const Mat mdA{dA, dA ? M : 0, K, ldda, es}, mdBg{dBg, dBg ? K : 0, N, lddbg, es}, mdBu{dBu, dBu ? K : 0, N, lddbu, es};
+    int st;
+    if (dB && (st = check_mat(mA)) != DGEMM_OK) return st;
+    if (dA && ((st = check_mat(mBg)) != DGEMM_OK || (st = check_mat(mBu)) != DGEMM_OK)) return st;
+    if ((st = check_mat(mdC)) != DGEMM_OK || (st = check_mat(mG)) != DGEMM_OK || (st = check_mat(mU)) != DGEMM_OK)
+        return st;
+    if ((dA && (st = check_mat(mdA)) != DGEMM_OK) || (dBg && (st = check_mat(mdBg)) != DGEMM_OK) ||
+        (dBu && (st = check_mat(mdBu)) != DGEMM_OK))
+        return st;
+    if (check_vec(dbias_g, 4) != DGEMM_OK || check_vec(dbias_u, 4) != DGEMM_OK || check_vec(workspace, 16) != DGEMM_OK)
+        return DGEMM_ERR_MISALIGNED;
+    const GatedBwdParts b = gated_bwd_parts(in, M, N, K, dA || dB, bias);
+    if ((uint64_t)b.required > workspace_bytes) return DGEMM_ERR_WORKSPACE;
+    // The rows of A's transpose (fp32), for the weights' gradients, are as long as M.
+    if (es == 4 && dB && M > SKINNY_M && (int64_t)PANEL_ROWS * up(M, 4) * 4 >= DESC_LIMIT) return DGEMM_ERR_TOO_LARGE;
+    const Mat ws = bytes_of(workspace, (int64_t)std::min<uint64_t>(workspace_bytes, INT64_MAX));
+    const Mat ins[] = {mA, mBg, mBu, mdC, mG, mU};
+    const Mat outs[] = {mdA, mdBg, mdBu, vec(dbias_g, N), vec(dbias_u, N), ws};
+    if (any_overlap(outs, 6, ins, 6)) return DGEMM_ERR_ALIAS;
+    if ((st = check_device()) != DGEMM_OK) return st;
+
+    char* const w = (char*)workspace;
+    char* const dG = w;
+    char* const dU = w + b.dz;
+    float* const part = (float*)(w + 2 * b.dz);
+    float* const w_trans = (float*)(w + 2 * b.dz + b.part);
+    char* const w_gemm = w + b.required;
+    const int64_t gemm_bytes = (int64_t)std::min<uint64_t>(workspace_bytes, INT64_MAX) - b.required;
+    hipStream_t s = (hipStream_t)stream;
+    if (M > 0 && N > 0 && (dA || dB || bias)) {
+        const bool products = (dA || dB) && K > 0;
+        const GatedGradArgs a{(const char*)dC, (const char*)G, (const char*)U, products ? dG : nullptr,
+                              products ? dU : nullptr, bias ? part : nullptr, M, N, lddc, ldg, ldu, b.lddz, b.ldp,
+                              act_grad_rows(M, N), act};
+        if (launch_gated_grad(a, cf, out_format(in, DGEMM_OUT_SAME), s) != hipSuccess) return DGEMM_ERR_LAUNCH;
+    }
+    const int G2 = M > 0 ? b.chunks : 0;
+    const ColReduceArgs sg{part, dbias_g, G2, 2 * b.ldp, dbias_g ? N : 0};
+    const ColReduceArgs su{part + b.ldp, dbias_u, G2, 2 * b.ldp, dbias_u ? N : 0};
+    const bool want_a = dA && M > 0 && K > 0, want_b = dB && K > 0 && N > 0;
+    void* const dW[2] = {dBg, dBu};
+    const int lddw[2] = {lddbg, lddbu};
+    char* const dz[2] = {dG, dU};
+
+    if (M <= SKINNY_M) {
+        // Few rows: the weights once through registers for dA, rank-M updates for theirs.
+        if (want_a) {
+            const Plan p = plan_skinny(in, LAY_NT, M, K, (int)std::min<int64_t>(2 * (int64_t)N, INT32_MAX), 0);
+            GemmLaunch L = bwd_launch(in, LAY_NT, p.bn, true, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);
+            L.tiles_m = 1;
+            L.slice_waves = p.waves;
+            if (launch_skinny_two(L, dU, (const char*)Bu, ldbu) != hipSuccess) return DGEMM_ERR_LAUNCH;
+        }
+        for (int i = 0; i < 2; ++i)
+            if (want_b && dW[i]) {
+                const GemmLaunch L = bwd_launch(in, LAY_TN, 32, true, K, N, M, A, lda, dz[i], b.lddz, dW[i], lddw[i], s);
+                if (launch_skinny(L) != hipSuccess) return DGEMM_ERR_LAUNCH;
+            }
+        return launched(launch_col_reduce2(sg, su, s));
+    }
+    if (!want_a && !want_b) return launched(launch_col_reduce2(sg, su, s));
+    const GatedBwdPlan p = plan_gated_bwd(in, M, N, K, want_a, want_b, (uint64_t)gemm_bytes);
+    if (!p.transposes) {
+        GatedBwdLaunch L{};
+        const int tt = p.tn ? p.tn : p.nt, ta = p.nt ? p.nt : p.tn;
+        L.nt = bwd_launch(in, LAY_NT, ta, p.nt_slices, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);
+        for (int i = 0; i < 2; ++i) {
+            L.tn[i] = bwd_launch(in, LAY_TN, tt, p.tn_slices, K, N, M, A, lda, dz[i], b.lddz, dW[i], lddw[i], s);
+            if (!want_b || !dW[i]) L.tn[i].tiles_m = 0;
+        }
+        if (!want_a) L.nt.tiles_m = 0;
+        L.A2 = dU;
+        L.B2 = (const char*)Bu;
+        L.ldb2 = ldbu;
+        L.tn_first = p.tn_first;
+        L.sums[0] = sg;
+        L.sums[1] = su;
+        if (p.together) return launched((p.nt_slices ? launch_slicet_gated : launch_gemmt_gated)(L));
+        // Apart: the input's gradient, then the weights' with the sums.
+        GatedBwdLaunch first = L;
+        first.tn[0] = first.tn[1] = L.nt;
+        first.tn[0].tiles_m = first.tn[1].tiles_m = 0;
+        first.sums[0].N = first.sums[1].N = 0;
+        first.tn_first = false;
+        if ((p.nt_slices ? launch_slicet_gated : launch_gemmt_gated)(first) != hipSuccess) return DGEMM_ERR_LAUNCH;
+        L.nt = L.tn[0];
+        L.nt.tiles_m = 0;
+        L.tn_first = false;
+        return launched((p.tn_slices ? launch_slicet_gated : launch_gemmt_gated)(L));
+    }
+    // fp32 of large layers: the grid kernels, which take A[M x K] B[K x N].
+    if (launch_col_reduce2(sg, su, s) != hipSuccess) return DGEMM_ERR_LAUNCH;
+    const void* const W[2] = {Bg, Bu};
+    const int ldw[2] = {ldbg, ldbu};
+    for (int i = 0; i < 2 && want_a; ++i) {
+        const int ldt = (int)up(K, 4);
+        if (N > 0 && launch_transpose32((const float*)W[i], ldw[i], K, N, w_trans, ldt, s) != hipSuccess)
+            return DGEMM_ERR_LAUNCH;
+        EpiArgs e{};
+        e.alpha = 1.0f;
+        e.beta = i ? 1.0f : 0.0f;
+        st = run(in, OUT_F32, M, K, N, dz[i], b.lddz, w_trans, ldt, dA, ldda, e, i ? EPI_BASIC : EPI_NONE,
+                 make_plan(in, 4, M, K, N, (uint64_t)gemm_bytes, false), w_gemm, s);
+        if (st != DGEMM_OK) return st;
+    }
+    if (!want_b) return DGEMM_OK;
+    const int ldt = (int)up(M, 4);
+    if (launch_transpose32((const float*)A, lda, M, K, w_trans, ldt, s) != hipSuccess) return DGEMM_ERR_LAUNCH;
+    for (int i = 0; i < 2; ++i) {
+        if (!dW[i]) continue;
+        EpiArgs e{};
+        e.alpha = 1.0f;
+        st = run(in, OUT_F32, K, N, M, w_trans, ldt, dz[i], b.lddz, dW[i], lddw[i], e, EPI_NONE,
+                 make_plan(in, 4, K, N, M, (uint64_t)gemm_bytes, false), w_gemm, s);
+        if (st != DGEMM_OK) return st;
+    }
+    return DGEMM_OK;
+}
+
+int gemm_gated_bwd_workspace(int in, int out, int M, int N, int K, size_t* required, size_t* best) {
+    if (in < IN_F32 || in > IN_F16 || M < 0 || N < 0 || K < 0 || out_format(in, out) < 0)
+        return DGEMM_ERR_INVALID_VALUE;
+    const GatedBwdParts b = gated_bwd_parts(in, M, N, K, true, true);
+    int64_t more = 0;
+    const uint64_t any = (uint64_t)1 << 40;
+    if (in == IN_F32 && M > SKINNY_M && K > 0 && plan_gated_bwd(in, M, N, K, true, true, any).transposes) {
+        more = make_plan(in, 4, M, K, N, any, false).ws_bytes;
+        more = std::max(more, make_plan(in, 4, K, N, M, any, false).ws_bytes);
+    }
+    if (required) *required = (size_t)b.required;
+    if (best) *best = (size_t)(b.required + more);
     return DGEMM_OK;
 }
 

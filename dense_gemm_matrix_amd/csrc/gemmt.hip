@@ -90,12 +90,22 @@ struct Frag {
     u32x4 w[F8 ? 2 : 1];
 };
 
-template <int IN, int LAY, int TBM, int TBN, int S>
+// A second pair of operands of the same sizes, whose product is added (the gradient of a gated
+// layer's input: dG Bg^T + dU Bu^T); X2 has X's row pitch.
+struct Second {
+    const char* X2;
+    const char* Y2;
+    int ldy2;
+};
+
+// SEG: the K loop runs on over the second pair's k.
+template <int IN, int LAY, int TBM, int TBN, int S, bool SEG = false>
 __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const char* __restrict__ Y,
                                            int K, int ldx, int ldy, int m0, int n0, int rows_x,
                                            int rows_y, char* smem,
-                                           f32x16 (&acc)[TBM / 64][TBN / 64]) {
+                                           f32x16 (&acc)[TBM / 64][TBN / 64], const Second& two = Second{}) {
     using T = TileT<IN, LAY, TBM, TBN, S>;
+    static_assert(!SEG || LAY == LAY_NT, "a second pair");
     constexpr int MI = T::MI, NJ = T::NJ, ES = T::ES;
     constexpr bool KC = T::KC, F8 = T::F8;
     char* const smA = smem;
@@ -103,7 +113,8 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
     const int tid = (int)threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int nk = (K + T::STEPK - 1) / T::STEPK;
+    const int nk1 = (K + T::STEPK - 1) / T::STEPK;  // steps of one pair
+    const int nk = SEG ? 2 * nk1 : nk1;
 
     // Global byte offset of the 16 bytes that belong in this lane's slot of load
     // block `blk` (1 KiB, filled lane-linearly) of an operand with `TB` rows: the
@@ -118,15 +129,18 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
             return k * ld * 2 + (((lane % ch) ^ b16_swz(k)) << 4);
         }
     };
-    int vx[T::A_DMA], vy[T::B_DMA];
+    int vx[T::A_DMA], vy[T::B_DMA], vy2[SEG ? T::B_DMA : 1];
 #pragma unroll
     for (int j = 0; j < T::A_DMA; ++j) vx[j] = voff(wave * T::A_DMA + j, ldx, TBM);
 #pragma unroll
-    for (int j = 0; j < T::B_DMA; ++j) vy[j] = voff(wave * T::B_DMA + j, ldy, TBN);
+    for (int j = 0; j < T::B_DMA; ++j) {
+        vy[j] = voff(wave * T::B_DMA + j, ldy, TBN);
+        if constexpr (SEG) vy2[j] = voff(wave * T::B_DMA + j, two.ldy2, TBN);
+    }
 
     // Step kt's two resources; steps past the end get empty ones, whose loads
     // fill zeros and keep the count per step uniform.
-    struct Desc { __amdgpu_buffer_rsrc_t a, b; int s; };
+    struct Desc { __amdgpu_buffer_rsrc_t a, b; int s; bool second; };
     auto operand = [&](const char* p, int ld, int o0, int rows, int kt) {
         const int k0 = kt * T::STEPK;
         const int krem = (K - k0) < T::STEPK ? (K - k0) : T::STEPK;
@@ -138,14 +152,20 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
                              krem > 0 ? ((int64_t)(krem - 1) * ld + rows) * ES : 0);
     };
     auto desc = [&](int kt) {
-        return Desc{operand(X, ldx, m0, rows_x, kt), operand(Y, ldy, n0, rows_y, kt), kt % S};
+        if constexpr (SEG) {
+            const bool q = kt >= nk1;
+            const int k = q ? kt - nk1 : kt;
+            return Desc{operand(q ? two.X2 : X, ldx, m0, rows_x, k),
+                        operand(q ? two.Y2 : Y, q ? two.ldy2 : ldy, n0, rows_y, k), kt % S, q};
+        }
+        return Desc{operand(X, ldx, m0, rows_x, kt), operand(Y, ldy, n0, rows_y, kt), kt % S, false};
     };
     auto dma_one = [&](const Desc& d, int j) {
         if (j < T::A_DMA)
             dma16(d.a, lds_addr(smA + d.s * T::A_STAGE + (wave * T::A_DMA + j) * 1024), vx[j]);
         else
             dma16(d.b, lds_addr(smB + d.s * T::B_STAGE + (wave * T::B_DMA + j - T::A_DMA) * 1024),
-                  vy[j - T::A_DMA]);
+                  SEG && d.second ? vy2[SEG ? j - T::A_DMA : 0] : vy[j - T::A_DMA]);
     };
 
     // K-contiguous operands: zero the last step's bytes at and past K in LDS.
@@ -162,8 +182,8 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
         for (int c = chunk0 + ((valid & 15) ? 1 : 0); c < A16_CH; ++c)
             *(u32x4*)(stage + a16_off(row, c)) = u32x4{0u, 0u, 0u, 0u};
     };
-    auto fix_tail = [&]() {
-        const int valid = (K - (nk - 1) * T::STEPK) * ES, s = (nk - 1) % S;
+    auto fix_tail = [&](int kt) {  // of step kt, the last of a pair
+        const int valid = (K - (nk1 - 1) * T::STEPK) * ES, s = kt % S;
         if (tid < TBM) fix_row(smA + s * T::A_STAGE, tid, valid);
         if (tid < TBN) fix_row(smB + s * T::B_STAGE, tid, valid);
     };
@@ -279,7 +299,7 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
             for (int j = 0; j < T::LOADS; ++j) dma_one(d, j);
         }
         sync(FirstIn{});
-        if (ragged && nk == 1) { fix_tail(); sync(FirstIn{}); }
+        if (ragged && nk1 == 1) { fix_tail(0); sync(FirstIn{}); }
 #pragma unroll
         for (int o = 0; o < T::NREAD; ++o) {
             read_piece(0, 0, o);
@@ -298,7 +318,7 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
                 if (i == BAR) {
                     d = desc(kt + S);
                     sync(NextIn{});
-                    if (ragged && kt + 2 == nk) { fix_tail(); sync(NextIn{}); }
+                    if (ragged && (kt + 2 == nk || (SEG && kt + 2 == nk1))) { fix_tail(kt + 1); sync(NextIn{}); }
                 }
                 mfma_one(i / T::NMFMA, i % T::NMFMA);
                 __builtin_amdgcn_sched_barrier(0);
@@ -337,8 +357,9 @@ struct GridArgs {
 };
 
 // Macro-tile `wg` of a product (of one K split of it).
-template <int IN, int LAY, int OUT, int TBM, int TBN, int EPI, int S>
-__device__ __forceinline__ void grid_tile(const GridArgs& a, int wg, const EpiArgs& epi, char* smem) {
+template <int IN, int LAY, int OUT, int TBM, int TBN, int EPI, int S, bool SEG = false>
+__device__ __forceinline__ void grid_tile(const GridArgs& a, int wg, const EpiArgs& epi, char* smem,
+                                          const Second& two = Second{}) {
     using T = TileT<IN, LAY, TBM, TBN, S>;
     int tm, tn;
     map_tile(wg, a.tiles_m, a.tiles_n, tm, tn);
@@ -346,7 +367,7 @@ __device__ __forceinline__ void grid_tile(const GridArgs& a, int wg, const EpiAr
     const int rows_x = (a.M - m0) < TBM ? (a.M - m0) : TBM;
     const int rows_y = (a.N - n0) < TBN ? (a.N - n0) : TBN;
     f32x16 acc[T::MI][T::NJ];
-    mainloop_t<IN, LAY, TBM, TBN, S>(a.X, a.Y, a.K, a.ldx, a.ldy, m0, n0, rows_x, rows_y, smem, acc);
+    mainloop_t<IN, LAY, TBM, TBN, S, SEG>(a.X, a.Y, a.K, a.ldx, a.ldy, m0, n0, rows_x, rows_y, smem, acc, two);
     const int lane = (int)threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int row0 = m0 + (wave >> 1) * (TBM / 2), col0 = n0 + (wave & 1) * (TBN / 2);
@@ -397,6 +418,33 @@ __global__ __launch_bounds__(256) void gemmt_pair_kernel(GridArgs nt, GridArgs t
     else col_reduce(wg - n_nt - n_tn, r, (float*)smem);
 }
 
+// A gated layer's: dA = X Y^T + X2 Y2^T (nt), both weights' gradients (tn, and with Y2 and C2 in
+// place of Y and C), both biases' column sums.  Any of the products may have no tiles.
+template <int IN, int TB>
+__global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second two, GridArgs tn, GridArgs tn2,
+                                                          int first, ColReduceArgs r, ColReduceArgs r2) {
+    constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
+    constexpr int L1 = TileT<IN, LAY_NT, TB, TB, 2>::LDS, L2 = TileT<IN, LAY_TN, TB, TB, 2>::LDS;
+    __shared__ __attribute__((aligned(1024))) char smem[L1 > L2 ? L1 : L2];
+    const int n_nt = nt.tiles_m * nt.tiles_n, n_tn = tn.tiles_m * tn.tiles_n;
+    const int n_all = n_nt + n_tn + tn2.tiles_m * tn2.tiles_n;
+    int wg = (int)blockIdx.x;
+    if (wg < n_all) {
+        wg += first;
+        if (wg >= n_all) wg -= n_all;
+    }
+    EpiArgs e{};
+    if (wg < n_nt) {
+        grid_tile<IN, LAY_NT, OUT, TB, TB, EPI_FULL, 2, true>(nt, wg, e, smem, two);
+    } else if (wg < n_all) {
+        const bool b = wg >= n_nt + n_tn;
+        grid_tile<IN, LAY_TN, OUT, TB, TB, EPI_FULL, 2>(b ? tn2 : tn, wg - n_nt - (b ? n_tn : 0), e, smem);
+    } else {
+        const int c = wg - n_all, n1 = r.N > 0 ? (r.N + 15) / 16 : 0;
+        col_reduce(c < n1 ? c : c - n1, c < n1 ? r : r2, (float*)smem);
+    }
+}
+
 GridArgs grid_args(const GemmLaunch& L) {
     return GridArgs{L.A, L.B, L.C, L.M, L.N, L.K, L.lda, L.ldb, L.ldc, L.tiles_m, L.tiles_n};
 }
@@ -412,6 +460,21 @@ hipError_t go_pair_t(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first, 
     const int blocks =
         nt.tiles_m * nt.tiles_n + tn.tiles_m * tn.tiles_n + (r.N > 0 ? col_reduce_blocks(r.N) : 0);
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, nt.stream);
+}
+
+template <int IN>
+hipError_t go_gated_t(const GatedBwdLaunch& L) {
+    const void* fn = L.nt.tbm == 256 ? (const void*)gemmt_gated_kernel<IN, 256>
+                                     : (const void*)gemmt_gated_kernel<IN, 128>;
+    GridArgs a = grid_args(L.nt), b = grid_args(L.tn[0]), c = grid_args(L.tn[1]);
+    Second two{L.A2, L.B2, L.ldb2};
+    const int tiles = a.tiles_m * a.tiles_n, tns = b.tiles_m * b.tiles_n + c.tiles_m * c.tiles_n;
+    int first = L.tn_first ? tiles : 0;
+    ColReduceArgs r = L.sums[0], r2 = L.sums[1];
+    const int blocks = tiles + tns + (r.N > 0 ? col_reduce_blocks(r.N) : 0) + (r2.N > 0 ? col_reduce_blocks(r2.N) : 0);
+    if (blocks == 0) return hipSuccess;
+    void* args[] = {&a, &two, &b, &c, &first, &r, &r2};
+    return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, L.nt.stream);
 }
 
 template <int IN, int LAY, int OUT, int EPI>
@@ -469,6 +532,14 @@ hipError_t launch_gemmt_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn
             return hipErrorInvalidValue;
     if (nt.in == IN_BF16) return go_pair_t<IN_BF16>(nt, tn, tn_first, r);
     if (nt.in == IN_F16) return go_pair_t<IN_F16>(nt, tn, tn_first, r);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gemmt_gated(const GatedBwdLaunch& L) {
+    for (const GemmLaunch* p : {&L.nt, &L.tn[0], &L.tn[1]})
+        if (p->tbm != L.nt.tbm || p->tbn != L.nt.tbm || (p->tbm != 128 && p->tbm != 256)) return hipErrorInvalidValue;
+    if (L.nt.in == IN_BF16) return go_gated_t<IN_BF16>(L);
+    if (L.nt.in == IN_F16) return go_gated_t<IN_F16>(L);
     return hipErrorInvalidValue;
 }
 

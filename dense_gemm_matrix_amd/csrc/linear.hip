@@ -12,13 +12,6 @@ namespace dgemm {
 
 // -------------------------------------------------------------------- plans
 
-// Tiles of gemmt.hip: gemm16's constants, whose schedule and bytes per step it
-// shares (an 8-bit step is 128 k in the same time).
-static constexpr TileCand TILES_T[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6},
-                                {128, 128, 0.6, 1.26, 1.35, 0.8, 1.0}};
-
-static int t_step(int in) { return in >= IN_F8 ? 128 : 64; }
-
 // Plan of one tile at `splits` K pieces (1: unsplit); splits = 0 if it does not fit.
 Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uint64_t ws_avail) {
     Plan p{t.bm, t.bn, 1, K, 0, 0};
@@ -285,12 +278,6 @@ int run_bwd_product(int in, int layout, int rows, int M, int N, int K, const voi
                p.layout != LAY_NN ? EPI_FULL : EPI_NONE, p, ws, stream);
 }
 
-constexpr double PAIR_GAP_US = 2.0;          // another launch
-// Most tiles: more are the 16-bit grid's (1500^3: 45 us, together 50); fp32's
-// grid kernels are slower than the pair's 64 x 64 tiles at many odd sizes
-// (1500^3 181 / 155 us, 3500^3 1748 / 1487), so there the estimate decides.
-constexpr int64_t PAIR_TILES_16 = 4 * NUM_CU, PAIR_TILES_32 = 32 * NUM_CU;
-
 // A product of the backward pass by itself, M x N with K terms; in fp32 with the
 // launch that transposes an operand.
 double alone_us(int in, int layout, int M, int N, int K, uint64_t ws) {
@@ -317,6 +304,8 @@ struct PairPlan {
     Plan nt, tn;
     bool use, tn_first;
 };
+
+}  // namespace
 
 // A CU holds one of these workgroups (128 KB of LDS), and each starts where one
 // ended.  `ta` tiles of `wa` us, then `tb` of `wb`: after the first product
@@ -357,6 +346,8 @@ double pair_grid_us(const TileCand& t, int in, int64_t ta, int ka, int64_t tb, i
     const double us = b_first ? pair_us(tb, wb, ta, wa) : pair_us(ta, wa, tb, wb);
     return us * (0.7 + 0.3 * work / us);
 }
+
+namespace {
 
 // One launch saves the other launches' time (2.4 us of host time each, 1.5 to 2 us
 // of a graph) and fills the CUs that one product's tiles leave idle; the longer

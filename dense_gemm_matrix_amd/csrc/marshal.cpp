@@ -532,6 +532,64 @@ PyObject* py_layernorm_bwd(PyObject*, PyObject* const* args, Py_ssize_t nargs, P
     });
 }
 
+// The second weight of a gated layer, like the first; a row pitch of its own.
+Mat second_weight(PyObject* o, const Mat& first) {
+    if (!given(o)) fail(PyExc_ValueError, "Bu is required");
+    return matrix_like(o, "Bu", first.rows, first.cols, first.type, first.dev);
+}
+
+PyObject* py_gemm_gated(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+    static const char* const names[] = {"A", "Bg", "Bu", "C", "bias_g", "bias_u", "act", "gate", "up", "workspace",
+                                        "stream"};
+    return guarded([&] {
+        PyObject* o[11];
+        parse("gemm_gated", names, 4, 4, args, nargs, kw, o);
+        const Mat A = matrix(o[0], "A"), Bg = matrix(o[1], "Bg"), Bu = second_weight(o[2], Bg), C = matrix(o[3], "C");
+        conform(A, Bg, C);
+        int in, out;
+        formats(A, Bg, C.type, nullptr, in, out);
+        const float* bg = vec(o[4], "bias_g", C.cols, C.dev);
+        const float* bu = vec(o[5], "bias_u", C.cols, C.dev);
+        const int act = o[6] ? act_code(o[6]) : DGEMM_ACT_SILU;
+        const Mat G = matrix_like(o[7], "gate", C.rows, C.cols, C.type, C.dev);
+        const Mat U = matrix_like(o[8], "up", C.rows, C.cols, C.type, C.dev);
+        const Bytes ws = workspace(o[9], C.dev);
+        void* s = stream_of(o[10], C.dev);
+        return call(C.dev, [&] {
+            return gemm_gated(in, out, C.rows, C.cols, A.cols, A.p, A.ld, Bg.p, Bg.ld, Bu.p, Bu.ld, C.p, C.ld, bg, bu,
+                              act, G.p, G.ld, U.p, U.ld, ws.p, ws.n, s);
+        });
+    });
+}
+
+PyObject* py_gemm_gated_bwd(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
+    static const char* const names[] = {"A", "Bg", "Bu", "dC", "gate", "up", "act", "dA", "dBg", "dBu", "dbias_g",
+                                        "dbias_u", "workspace", "stream"};
+    return guarded([&] {
+        PyObject* o[14];
+        parse("gemm_gated_bwd", names, 6, 6, args, nargs, kw, o);
+        const Mat A = matrix(o[0], "A"), Bg = matrix(o[1], "Bg"), Bu = second_weight(o[2], Bg);
+        const Mat dC = matrix(o[3], "dC");
+        conform(A, Bg, dC);
+        const int M = dC.rows, N = dC.cols, K = A.cols, dev = dC.dev;
+        int in, out;
+        formats(A, Bg, dC.type, nullptr, in, out);
+        if (!given(o[4]) || !given(o[5])) fail(PyExc_ValueError, "gate and up are required");
+        const Mat G = matrix_like(o[4], "gate", M, N, dC.type, dev), U = matrix_like(o[5], "up", M, N, dC.type, dev);
+        const int act = o[6] ? act_code(o[6]) : DGEMM_ACT_SILU;
+        const Mat dA = matrix_like(o[7], "dA", M, K, A.type, dev);
+        const Mat dBg = matrix_like(o[8], "dBg", K, N, A.type, dev), dBu = matrix_like(o[9], "dBu", K, N, A.type, dev);
+        float* dbg = vec(o[10], "dbias_g", N, dev);
+        float* dbu = vec(o[11], "dbias_u", N, dev);
+        const Bytes ws = workspace(o[12], dev);
+        void* s = stream_of(o[13], dev);
+        return call(dev, [&] {
+            return gemm_gated_bwd(in, out, M, N, K, A.p, A.ld, Bg.p, Bg.ld, Bu.p, Bu.ld, dC.p, dC.ld, G.p, G.ld, U.p,
+                                  U.ld, act, dA.p, dA.ld, dBg.p, dBg.ld, dBu.p, dBu.ld, dbg, dbu, ws.p, ws.n, s);
+        });
+    });
+}
+
 #define FN(name, doc) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL | METH_KEYWORDS, doc}
 PyMethodDef methods[] = {
     FN(gemm_act,
@@ -570,6 +628,18 @@ PyMethodDef methods[] = {
        "quant_f8(X, Q, scale, *, transpose=False, stream=None)\n\n"
        "Q, scale = X's rows in 8 bits (float8_e4m3fn, one float32 scale per row); with transpose\n"
        "its columns, Q being X.T's shape: gemm_f8's B from a [K, N] weight."),
+    FN(gemm_gated,
+       "gemm_gated(A, Bg, Bu, C, *, bias_g=None, bias_u=None, act='silu', gate=None, up=None,\n"
+       "           workspace=None, stream=None)\n\n"
+       "C = act(G) * U with G = A @ Bg + bias_g and U = A @ Bu + bias_u, stored in `gate` and `up`\n"
+       "(C's shape and dtype) where given.  float32, bfloat16 or float16; C has A's dtype or is\n"
+       "float32.  `act` is silu, gelu, gelu_tanh, relu or none; `workspace` as in gemm_ex."),
+    FN(gemm_gated_bwd,
+       "gemm_gated_bwd(A, Bg, Bu, dC, gate, up, *, act='silu', dA=None, dBg=None, dBu=None,\n"
+       "               dbias_g=None, dbias_u=None, workspace=None, stream=None)\n\n"
+       "Gradients of gemm_gated: dA, dBg and dBu (shapes and dtype of A, Bg and Bu), dbias_g and\n"
+       "dbias_u (float32), each written if given; `gate` and `up` as gemm_gated stored them.  The\n"
+       "workspace holds at least gemm_gated_bwd_workspace's required bytes."),
     FN(gemm_f8_block,
        "gemm_f8_block(A, B, C, scale_a, scale_b, *, bias=None, act='none', residual=None,\n"
        "              workspace=None, stream=None)\n\n"

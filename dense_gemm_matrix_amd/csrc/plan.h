@@ -83,6 +83,23 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
 // The plan of a product of at most SKINNY_M rows (linear.hip).
 Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail);
 
+// The estimated time of `ta` workgroups of wa us and then `tb` of wb, one at a time on a CU, and of
+// that many grid tiles t of ka and kb terms (b_first: whether the second kind should go first)
+// (linear.hip).
+double pair_us(int64_t ta, double wa, int64_t tb, double wb);
+double pair_grid_us(const TileCand& t, int in, int64_t ta, int ka, int64_t tb, int kb, bool& b_first);
+constexpr double PAIR_GAP_US = 2.0;          // another launch
+// Most tiles: more are the 16-bit grid's (1500^3: 45 us, together 50); fp32's
+// grid kernels are slower than the pair's 64 x 64 tiles at many odd sizes
+// (1500^3 181 / 155 us, 3500^3 1748 / 1487), so there the estimate decides.
+constexpr int64_t PAIR_TILES_16 = 4 * NUM_CU, PAIR_TILES_32 = 32 * NUM_CU;
+
+// Tiles of gemmt.hip: gemm16's constants, whose schedule and bytes per step it
+// shares (an 8-bit step is 128 k in the same time).
+constexpr TileCand TILES_T[] = {{256, 256, 1.0, 0.0, 0.0, 1.0, 0.6},
+                                {128, 128, 0.6, 1.26, 1.35, 0.8, 1.0}};
+inline int t_step(int in) { return in >= IN_F8 ? 128 : 64; }
+
 // Validated arguments and a plan -> its launches, with epilogue e at level epi.
 int run(int in, int outfmt, int M, int N, int K, const void* A, int lda, const void* B, int ldb,
         void* C, int ldc, const EpiArgs& e, int epi, const Plan& p, void* ws, hipStream_t stream);

@@ -244,10 +244,12 @@ __global__ __launch_bounds__(64 * W) void skinny_nn_kernel(
     strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
 }
 
-template <int IN, int OUT, int W>
+// SEG: A B^T + A2 B2^T, the waves taking the steps of both in turn.
+template <int IN, int OUT, int W, bool SEG = false>
 __global__ __launch_bounds__(64 * W) void skinny_nt_kernel(
     const char* __restrict__ A, const char* __restrict__ B, char* C, int M, int N, int K, int lda,
-    int ldb, int ldc, int strips, EpiArgs epi) {
+    int ldb, int ldc, int strips, EpiArgs epi, const char* __restrict__ A2, const char* __restrict__ B2,
+    int ldb2) {
     constexpr int ES = IN == IN_F32 ? 4 : IN == IN_F8W ? 1 : 2;
     __shared__ float red[W * 4 * 64];
     const int lane = (int)threadIdx.x & 63;
@@ -256,27 +258,30 @@ __global__ __launch_bounds__(64 * W) void skinny_nt_kernel(
     const int n0 = strip_of((int)blockIdx.x, strips) * 16;
     const int rows_b = (N - n0) < 16 ? (N - n0) : 16;
     constexpr int SK = 128 / ES;  // k per step
-    const int nstep = (K + SK - 1) / SK;
+    const int nstep1 = (K + SK - 1) / SK, nstep = SEG ? 2 * nstep1 : nstep1;
+    auto k_of = [&](int t) { return (SEG && t >= nstep1 ? t - nstep1 : t) * SK; };
     Strip<OUT, EPI_FULL, 1, W> strip;
     strip.prefetch(M, N, n0, wave, lane, epi);
     constexpr int D = 2;  // steps per chunk; two chunks in registers
     u32x4 a[2 * D][2], b[2 * D][2];
     auto load = [&](int t, int S) {  // S: a constant once unrolled
-        const int k0 = t * SK;
+        const int k0 = k_of(t);
+        const bool sec = SEG && t >= nstep1;
+        const int lb = sec ? ldb2 : ldb;
         const int krem = (K - k0) < SK ? (K - k0) : SK;
-        const auto ra = make_rsrc(A + (int64_t)k0 * ES,
+        const auto ra = make_rsrc((sec ? A2 : A) + (int64_t)k0 * ES,
                                   krem > 0 ? ((int64_t)(M - 1) * lda + krem) * ES : 0);
-        const auto rb = make_rsrc(B + ((int64_t)n0 * ldb + k0) * ES,
-                                  krem > 0 ? ((int64_t)(rows_b - 1) * ldb + krem) * ES : 0);
+        const auto rb = make_rsrc((sec ? B2 : B) + ((int64_t)n0 * lb + k0) * ES,
+                                  krem > 0 ? ((int64_t)(rows_b - 1) * lb + krem) * ES : 0);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             a[S][h] = load16(ra, c * lda * ES + 64 * h + 16 * g);
-            b[S][h] = load16(rb, c * ldb * ES + 64 * h + 16 * g);
+            b[S][h] = load16(rb, c * lb * ES + 64 * h + 16 * g);
         }
     };
     f32x4 acc[1] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
     auto use = [&](int t, int S) {
-        const int k0 = t * SK;
+        const int k0 = k_of(t);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             u32x4 x = a[S][h], y = b[S][h];
@@ -303,6 +308,148 @@ __global__ __launch_bounds__(64 * W) void skinny_nt_kernel(
     run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
                  [&](int i, int slot, auto) { use(wave + i * W, slot); });
     strip.finish(acc, red, C, M, N, ldc, wave, lane, epi);
+}
+
+// Gated projections: the products with both weights, a strip of 16 CPL columns of each per
+// workgroup, as skinny_nn_kernel; A's pieces serve both.  PARTIAL: the sums of a K split, fp32.
+template <int IN, int OUT, bool PARTIAL, int CPL, int W>
+__global__ __launch_bounds__(64 * W) void gated_skinny_kernel(
+    const char* __restrict__ A, const char* __restrict__ Bg, const char* __restrict__ Bu, char* C, int M, int N,
+    int K, int lda, int ldbg, int ldbu, int ldc, int strips, int kchunk, int64_t zstride, GatedEpi e) {
+    constexpr bool F32 = IN == IN_F32;
+    constexpr int ES = F32 ? 4 : 2;
+    constexpr int WD = CPL * ES / 4;    // words per lane, weight and k-row
+    constexpr int AW = ES / 2;          // 16-byte pieces of A per lane and step
+    // Steps per chunk; two chunks in registers, within 128 of them for 16 waves.
+    constexpr int D = WD >= 2 ? 1 : 2;
+    constexpr int NV = CPL * 4, PER = (NV + W - 1) / W;
+    __shared__ float red[2 * W * NV * 64];
+    {
+        const int kbeg = (int)blockIdx.y * kchunk;
+        A += (int64_t)kbeg * ES;
+        Bg += (int64_t)kbeg * ldbg * ES;
+        Bu += (int64_t)kbeg * ldbu * ES;
+        if (e.G) e.G += (int)blockIdx.y * zstride;
+        if (e.U) e.U += (int)blockIdx.y * zstride;
+        K = (K - kbeg) < kchunk ? (K - kbeg) : kchunk;
+    }
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int n0 = strip_of((int)blockIdx.x, strips) * 16 * CPL;
+    const int cols = (N - n0) < 16 * CPL ? (N - n0) : 16 * CPL;
+    const int nstep = (K + 31) / 32;
+    // The values this lane finishes, idx = wave PER + q as in Strip, and their biases.
+    int row[PER], col[PER];
+    float bias[2][PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int idx = wave * PER + q;
+        row[q] = idx < NV ? 4 * g + idx % 4 : M;
+        col[q] = n0 + CPL * c + idx / 4;
+        const bool in = row[q] < M && col[q] < N;
+        bias[0][q] = e.bias_g && in ? e.bias_g[col[q]] : 0.0f;
+        bias[1][q] = e.bias_u && in ? e.bias_u[col[q]] : 0.0f;
+    }
+    uint32_t b[2 * D][2][8][WD];
+    u32x4 a[2 * D][AW];
+    auto load = [&](int t, int S) {  // S: a constant once unrolled
+        const int k0 = t * 32;
+        const int rows = (K - k0) < 32 ? (K - k0) : 32;
+        const auto ra = make_rsrc(A + (int64_t)k0 * ES,
+                                  rows > 0 ? ((int64_t)(M - 1) * lda + rows) * ES : 0);
+#pragma unroll
+        for (int h = 0; h < AW; ++h) a[S][h] = load16(ra, (c * lda + 8 * g) * ES + 16 * h);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int ldb = u ? ldbu : ldbg;
+            const auto rb = make_rsrc((u ? Bu : Bg) + ((int64_t)k0 * ldb + n0) * ES,
+                                      rows > 0 ? ((int64_t)(rows - 1) * ldb + cols) * ES : 0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int off = ((8 * g + j) * ldb + CPL * c) * ES;
+                if constexpr (WD == 4) {
+                    const u32x4 v = load16(rb, off);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) b[S][u][j][w] = v[w];
+                } else if constexpr (WD == 2) {
+                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                    const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rb, off, 0, 0);
+                    b[S][u][j][0] = v[0];
+                    b[S][u][j][1] = v[1];
+                } else {
+                    b[S][u][j][0] = __builtin_amdgcn_raw_buffer_load_b32(rb, off, 0, 0);
+                }
+            }
+        }
+    };
+    f32x4 acc[2][CPL];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) acc[u][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto use = [&](int t, int S) {
+        const int k0 = t * 32;
+        u32x4 av[AW];
+#pragma unroll
+        for (int h = 0; h < AW; ++h) {
+            av[h] = a[S][h];
+            if (k0 + 32 > K) av[h] = mask_bytes(av[h], (K - k0 - 8 * g) * ES - 16 * h);  // row padding
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (F32) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int w = 0; w < WD; ++w)
+                        acc[u][w] = __builtin_amdgcn_mfma_f32_16x16x4f32(
+                            as_float(av[j >> 2][j & 3]), as_float(b[S][u][j][w]), acc[u][w], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int w = 0; w < WD; ++w)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        u32x4 bv;
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            bv[p] = __builtin_amdgcn_perm(b[S][u][2 * p + 1][w], b[S][u][2 * p][w],
+                                                          h ? 0x07060302u : 0x05040100u);
+                        acc[u][2 * w + h] = mfma_16<IN>(av[0], bv, acc[u][2 * w + h]);
+                    }
+            }
+        }
+    };
+    run_steps<D>((nstep - wave + W - 1) / W, [&](int i, int slot) { load(wave + i * W, slot); },
+                 [&](int i, int slot, auto) { use(wave + i * W, slot); });
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[((u * W + wave) * NV + j * 4 + r) * 64 + lane] = acc[u][j][r];
+    __syncthreads();
+    if (wave * PER >= NV) return;
+    float v[2][PER];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {  // the waves' sums in wave order
+            const int idx = wave * PER + q;
+            float s = red[(u * W * NV + idx) * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) s += red[((u * W + w) * NV + idx) * 64 + lane];
+            v[u][q] = s + bias[u][q];
+            char* const to = u ? e.U : e.G;
+            if (to && row[q] < M && col[q] < N)
+                store_c<OUT>(to, (int64_t)row[q] * (u ? e.ldu : e.ldg) + col[q], v[u][q]);
+        }
+    if constexpr (!PARTIAL) {
+        apply_act<OUT>(v[0], e.act);
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (row[q] < M && col[q] < N) store_c<OUT>(C, (int64_t)row[q] * ldc + col[q], v[0][q] * v[1][q]);
+    }
 }
 
 // e4m3 operands with a scale per block of 128 k, which is a step: a step's products are summed
@@ -462,25 +609,54 @@ hipError_t nn_by_out(const GemmLaunch& L) {
     return hipErrorInvalidValue;
 }
 
-template <int IN, int OUT, int W>
-hipError_t go_nt_w(const GemmLaunch& L) {
+struct Two {
+    const char* A;
+    const char* B;
+    int ldb;
+};
+
+template <int IN, int OUT, int W, bool SEG>
+hipError_t go_nt_w(const GemmLaunch& L, const Two& two) {
     const char* a = L.A;
     const char* b = L.B;
     char* c = L.C;
     int M = L.M, N = L.N, K = L.K, lda = L.lda, ldb = L.ldb, ldc = L.ldc, strips = L.tiles_n;
     EpiArgs e = L.e;
-    void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &strips, &e};
-    return hipLaunchKernel((const void*)skinny_nt_kernel<IN, OUT, W>, dim3((unsigned)strips), dim3(64 * W),
+    Two t = two;
+    void* args[] = {&a, &b, &c, &M, &N, &K, &lda, &ldb, &ldc, &strips, &e, &t.A, &t.B, &t.ldb};
+    return hipLaunchKernel((const void*)skinny_nt_kernel<IN, OUT, W, SEG>, dim3((unsigned)strips), dim3(64 * W),
                            args, 0, L.stream);
 }
 
-template <int IN, int OUT>
-hipError_t go_nt(const GemmLaunch& L) {
+template <int IN, int OUT, bool SEG = false>
+hipError_t go_nt(const GemmLaunch& L, const Two& two = Two{}) {
     if (L.tbn != 16 || L.splits != 1 || L.epi != EPI_FULL) return hipErrorInvalidValue;
-    if (L.slice_waves == 16) return go_nt_w<IN, OUT, 16>(L);
-    if (L.slice_waves == 8) return go_nt_w<IN, OUT, 8>(L);
-    if (L.slice_waves == 4) return go_nt_w<IN, OUT, 4>(L);
+    if (L.slice_waves == 16) return go_nt_w<IN, OUT, 16, SEG>(L, two);
+    if (L.slice_waves == 8) return go_nt_w<IN, OUT, 8, SEG>(L, two);
+    if (L.slice_waves == 4) return go_nt_w<IN, OUT, 4, SEG>(L, two);
     return hipErrorInvalidValue;
+}
+
+template <int IN, int OUT, bool PARTIAL>
+hipError_t go_gated(const GatedLaunch& L) {
+    const void* fn = nullptr;
+    if constexpr (IN != IN_F32) {
+        if (L.tbp == 128 && L.waves == 8) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 8, 8>;
+    }
+    if (L.tbp == 64 && L.waves == 8) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 4, 8>;
+    if (L.tbp == 32 && L.waves == 16) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 2, 16>;
+    if (L.tbp == 32 && L.waves == 8) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 2, 8>;
+    if (!fn) return hipErrorInvalidValue;
+    const char* a = L.A;
+    const char* bg = L.Bg;
+    const char* bu = L.Bu;
+    char* c = L.C;
+    int M = L.M, N = L.N, K = L.K, lda = L.lda, ldbg = L.ldbg, ldbu = L.ldbu, ldc = L.ldc, strips = L.tiles_n;
+    int kchunk = L.kchunk;
+    int64_t zs = L.zstride;
+    GatedEpi e = L.e;
+    void* args[] = {&a, &bg, &bu, &c, &M, &N, &K, &lda, &ldbg, &ldbu, &ldc, &strips, &kchunk, &zs, &e};
+    return hipLaunchKernel(fn, dim3((unsigned)strips, (unsigned)L.splits), dim3(64 * L.waves), args, 0, L.stream);
 }
 
 template <int OUT, int W>
@@ -520,6 +696,32 @@ hipError_t go_outer(const GemmLaunch& L) {
 }
 
 }  // namespace
+
+hipError_t launch_skinny_two(const GemmLaunch& L, const char* A2, const char* B2, int ldb2) {
+    if (L.M < 1 || L.M > SKINNY_M) return hipErrorInvalidValue;
+    const Two two{A2, B2, ldb2};
+    if (L.in == IN_F32 && L.out == OUT_F32) return go_nt<IN_F32, OUT_F32, true>(L, two);
+    if (L.in == IN_BF16 && L.out == OUT_BF16) return go_nt<IN_BF16, OUT_BF16, true>(L, two);
+    if (L.in == IN_F16 && L.out == OUT_F16) return go_nt<IN_F16, OUT_F16, true>(L, two);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gated_skinny(const GatedLaunch& L) {
+    if (L.M < 1 || L.M > SKINNY_M || L.splits < 1) return hipErrorInvalidValue;
+    if (!L.C) {  // partial products
+        if (L.out != OUT_F32) return hipErrorInvalidValue;
+        if (L.in == IN_F32) return go_gated<IN_F32, OUT_F32, true>(L);
+        if (L.in == IN_BF16) return go_gated<IN_BF16, OUT_F32, true>(L);
+        if (L.in == IN_F16) return go_gated<IN_F16, OUT_F32, true>(L);
+        return hipErrorInvalidValue;
+    }
+    if (L.in == IN_F32 && L.out == OUT_F32) return go_gated<IN_F32, OUT_F32, false>(L);
+    if (L.in == IN_BF16 && L.out == OUT_F32) return go_gated<IN_BF16, OUT_F32, false>(L);
+    if (L.in == IN_BF16 && L.out == OUT_BF16) return go_gated<IN_BF16, OUT_BF16, false>(L);
+    if (L.in == IN_F16 && L.out == OUT_F32) return go_gated<IN_F16, OUT_F32, false>(L);
+    if (L.in == IN_F16 && L.out == OUT_F16) return go_gated<IN_F16, OUT_F16, false>(L);
+    return hipErrorInvalidValue;
+}
 
 hipError_t launch_blockf8_skinny(const GemmLaunch& L, const BlockScales& s) {
     if (L.M < 1 || L.M > SKINNY_M || L.tbn != 16 || L.splits != 1 || L.epi != EPI_FULL) return hipErrorInvalidValue;

@@ -56,9 +56,17 @@ struct SliceTile {
     static constexpr int LDS = cmax(STAGES, RED);
 };
 
-// Tile `wg` of a product.
-template <int IN, int LAY, int OUT, int MI, int W>
-__device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const EpiArgs& epi, char* smem) {
+// A second pair of operands of the same sizes, whose product is added; X2 has X's row pitch.
+struct Second {
+    const char* X2;
+    const char* Y2;
+    int ldy2;
+};
+
+// Tile `wg` of a product.  SEG: of the sum of two, the waves dividing the blocks of both.
+template <int IN, int LAY, int OUT, int MI, int W, bool SEG = false>
+__device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const EpiArgs& epi, char* smem,
+                                           const Second& two = Second{}) {
     const char* __restrict__ X = a.X;
     const char* __restrict__ Y = a.Y;
     char* const C = a.C;
@@ -81,7 +89,7 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
     const int m0 = tm * TS, n0 = tn * TS;
     const int rows_x = (M - m0) < TS ? (M - m0) : TS;
     const int rows_y = (N - n0) < TS ? (N - n0) : TS;
-    const int nblk = (K + BK - 1) / BK;
+    const int nblk1 = (K + BK - 1) / BK, nblk = SEG ? 2 * nblk1 : nblk1;
     const int kb0 = (int)((int64_t)wave * nblk / W);
     const int nb = (int)((int64_t)(wave + 1) * nblk / W) - kb0;
 
@@ -148,7 +156,7 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
 
     char* const mine = smem + wave * 2 * D * 2 * BLKB;
     // Load j's 16 bytes of this lane belong at bytes 1024 j + 16 lane of the stage.
-    int vx[NDB], vy[NDB];
+    int vx[NDB], vy[NDB], vy2[SEG ? NDB : 1];
 #pragma unroll
     for (int j = 0; j < NDB; ++j) {
         const int row = A16_RPB * j + lane / A16_CH;
@@ -157,7 +165,9 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
         constexpr int RB = ES * TS;
         vx[j] = KC ? row * ldx * ES + 16 * c : (q / RB) * ldx * ES + q % RB;
         vy[j] = KC ? row * ldy * ES + 16 * c : (q / RB) * ldy * ES + q % RB;
+        if constexpr (SEG) vy2[j] = row * two.ldy2 * ES + 16 * c;
     }
+    static_assert(!SEG || KC, "a second pair");
     // The transpose read's slot: lane 16 G + 4 a + q reads k-row 8 (G / 2) + a,
     // columns 16 (G & 1) + 4 q ...
     const int grp = lane >> 4;
@@ -170,15 +180,21 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
         else
             return make_rsrc(p + ((int64_t)k0 * ld + o0) * ES, ((int64_t)(krem - 1) * ld + rows) * ES);
     };
+    auto k_of = [&](int i) {  // the first k of block i of this wave
+        const int kb = kb0 + i;
+        return (SEG && kb >= nblk1 ? kb - nblk1 : kb) * BK;
+    };
     auto load = [&](int i, int s) {
-        const int k0 = (kb0 + i) * BK;
-        const auto rx = operand(X, ldx, m0, rows_x, k0);
-        const auto ry = operand(Y, ldy, n0, rows_y, k0);
+        const int k0 = k_of(i);
+        const bool sec = SEG && kb0 + i >= nblk1;
+        const auto rx = operand(sec ? two.X2 : X, ldx, m0, rows_x, k0);
+        const auto ry = operand(sec ? two.Y2 : Y, sec ? two.ldy2 : ldy, n0, rows_y, k0);
         char* st = mine + s * 2 * BLKB;
 #pragma unroll
         for (int j = 0; j < NDB; ++j) dma16(rx, lds_addr(st + 1024 * j), vx[j]);
 #pragma unroll
-        for (int j = 0; j < NDB; ++j) dma16(ry, lds_addr(st + BLKB + 1024 * j), vy[j]);
+        for (int j = 0; j < NDB; ++j)
+            dma16(ry, lds_addr(st + BLKB + 1024 * j), SEG && sec ? vy2[SEG ? j : 0] : vy[j]);
     };
     run_steps<D>(nb, load, [&](int i, int s, auto newer) {
         // This step's loads have landed; at most the newer steps' are in flight.
@@ -221,7 +237,7 @@ __device__ __forceinline__ void slice_tile(const SliceArgs& a, int wg, const Epi
         // The reads are done before the slot's next loads are issued.
         __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
         __builtin_amdgcn_sched_barrier(0);
-        const int k0 = (kb0 + i) * BK;
+        const int k0 = k_of(i);
         if (KC && k0 + BK > K) {  // the rows' padding: 0 * NaN would be a NaN, so both operands
 #pragma unroll
             for (int h = 0; h < 4; ++h)
@@ -290,6 +306,32 @@ __global__ __launch_bounds__(256) void slicet_pair_kernel(SliceArgs nt, SliceArg
     else col_reduce(wg - n_nt - n_tn, r, (float*)smem);
 }
 
+// A gated layer's: dA = X Y^T + X2 Y2^T (nt), both weights' gradients, both biases' column sums.
+template <int IN, int MI_NT, int MI_TN>
+__global__ __launch_bounds__(256) void slicet_gated_kernel(SliceArgs nt, Second two, SliceArgs tn, SliceArgs tn2,
+                                                           int first, ColReduceArgs r, ColReduceArgs r2) {
+    constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : IN == IN_F16 ? OUT_F16 : OUT_F32;
+    __shared__ __attribute__((
+        aligned(1024))) char smem[cmax(SliceTile<MI_NT, 4>::LDS, SliceTile<MI_TN, 4>::LDS)];
+    const int n_nt = nt.tiles_m * nt.tiles_n, n_tn = tn.tiles_m * tn.tiles_n;
+    const int n_all = n_nt + n_tn + tn2.tiles_m * tn2.tiles_n;
+    int wg = (int)blockIdx.x;
+    if (wg < n_all) {
+        wg += first;
+        if (wg >= n_all) wg -= n_all;
+    }
+    EpiArgs e{};
+    if (wg < n_nt) {
+        slice_tile<IN, LAY_NT, OUT, MI_NT, 4, true>(nt, wg, e, smem, two);
+    } else if (wg < n_all) {
+        const bool b = wg >= n_nt + n_tn;
+        slice_tile<IN, LAY_TN, OUT, MI_TN, 4>(b ? tn2 : tn, wg - n_nt - (b ? n_tn : 0), e, smem);
+    } else {
+        const int c = wg - n_all, n1 = r.N > 0 ? (r.N + 15) / 16 : 0;
+        col_reduce(c < n1 ? c : c - n1, c < n1 ? r : r2, (float*)smem);
+    }
+}
+
 SliceArgs args_of(const GemmLaunch& L) {
     return SliceArgs{L.A, L.B, L.C, L.M, L.N, L.K, L.lda, L.ldb, L.ldc, L.tiles_m, L.tiles_n};
 }
@@ -315,6 +357,22 @@ hipError_t go_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn_first, co
     const int blocks = nt.tiles_m * nt.tiles_n + tn.tiles_m * tn.tiles_n + (r.N > 0 ? col_reduce_blocks(r.N) : 0);
     if (blocks == 0) return hipSuccess;
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, nt.stream);
+}
+
+template <int IN>
+hipError_t go_gated(const GatedBwdLaunch& L) {
+    const bool m2 = L.nt.tbm == 64, n2 = L.tn[0].tbm == 64;
+    const void* fn = m2 ? (n2 ? (const void*)slicet_gated_kernel<IN, 2, 2> : (const void*)slicet_gated_kernel<IN, 2, 1>)
+                        : (n2 ? (const void*)slicet_gated_kernel<IN, 1, 2> : (const void*)slicet_gated_kernel<IN, 1, 1>);
+    SliceArgs a = args_of(L.nt), b = args_of(L.tn[0]), c = args_of(L.tn[1]);
+    Second two{L.A2, L.B2, L.ldb2};
+    const int tiles = a.tiles_m * a.tiles_n, tns = b.tiles_m * b.tiles_n + c.tiles_m * c.tiles_n;
+    int first = L.tn_first ? tiles : 0;
+    ColReduceArgs r = L.sums[0], r2 = L.sums[1];
+    const int blocks = tiles + tns + (r.N > 0 ? col_reduce_blocks(r.N) : 0) + (r2.N > 0 ? col_reduce_blocks(r2.N) : 0);
+    if (blocks == 0) return hipSuccess;
+    void* args[] = {&a, &two, &b, &c, &first, &r, &r2};
+    return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, L.nt.stream);
 }
 
 template <int IN, int LAY, int OUT>
@@ -350,6 +408,15 @@ hipError_t launch_slicet_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool t
     if (nt.in == IN_BF16) return go_pair<IN_BF16>(nt, tn, tn_first, r);
     if (nt.in == IN_F16) return go_pair<IN_F16>(nt, tn, tn_first, r);
     if (nt.in == IN_F32) return go_pair<IN_F32>(nt, tn, tn_first, r);
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_slicet_gated(const GatedBwdLaunch& L) {
+    for (const GemmLaunch* p : {&L.nt, &L.tn[0], &L.tn[1]})
+        if (p->tbm != p->tbn || (p->tbm != 32 && p->tbm != 64) || L.tn[0].tbm != L.tn[1].tbm) return hipErrorInvalidValue;
+    if (L.nt.in == IN_BF16) return go_gated<IN_BF16>(L);
+    if (L.nt.in == IN_F16) return go_gated<IN_F16>(L);
+    if (L.nt.in == IN_F32) return go_gated<IN_F32>(L);
     return hipErrorInvalidValue;
 }
 

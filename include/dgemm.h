@@ -550,6 +550,71 @@ int quant_f8(int in, int transpose, int M, int N,
              float* scale,
              void* stream);
 
+/*
+ * Gated projections, both products, the activation and the product of the two in one kernel:
+ *
+ *     G[i][j] := sum_k A[i][k] * Bg[k][j] + bias_g[j]
+ *     U[i][j] := sum_k A[i][k] * Bu[k][j] + bias_u[j]
+ *     C[i][j] := act(G[i][j]) * U[i][j]
+ *
+ * Evaluated in fp32 on the fp32 sums, each output rounded once (to nearest even) to C's format;
+ * C takes the unrounded G and U.  in: DGEMM_IN_F32, _BF16 or _F16; out as gemm_act.  Bg and Bu: K x
+ * N with row pitches of their own (two halves of one K x 2 N matrix, for instance).  bias_g,
+ * bias_u: NULL or N fp32 values (4-byte aligned).  G, U: NULL, or where to keep them for
+ * gemm_gated_bwd, in C's format (either may be asked for alone; the pitch is not looked at where
+ * the pointer is NULL).  C, G and U overlap no input and not each other.  Any dgemm_act
+ * (DGEMM_ACT_NONE: the plain product of both).  Alignment, pitches, panel size, errors and execution
+ * as gemm_ex; a workspace allows split plans, whose results differ in the order of fp32 sums only
+ * (gemm_gated_plan tells the bytes).  At most 16 rows run a kernel of their own that streams both
+ * weights through registers.
+ */
+int gemm_gated(int in, int out, int M, int N, int K,
+               const void* A, int lda,
+               const void* Bg, int ldbg,
+               const void* Bu, int ldbu,
+               void* C, int ldc,
+               const float* bias_g, const float* bias_u, int act,
+               void* G, int ldg,
+               void* U, int ldu,
+               void* workspace, size_t workspace_bytes,
+               void* stream);
+
+/* As gemm_ex_plan, for gemm_gated: tile_cols columns of G and the same of U. */
+int gemm_gated_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
+                    int* tile_rows, int* tile_cols, int* splits, size_t* workspace_used);
+
+/*
+ * gemm_gated's backward pass.  Given dC, the gradient of C (in C's format, which `out` names), and
+ * G and U as gemm_gated stored them:
+ *
+ *     dG = dC o U o act'(G),  dU = dC o act(G)
+ *     dA := dG * Bg^T + dU * Bu^T                        (M x K, input format)
+ *     dBg := A^T * dG,  dBu := A^T * dU                  (K x N, input format)
+ *     dbias_g, dbias_u := column sums of dG and dU        (fp32)
+ *
+ * Each output may be NULL (not wanted); A is read only for dBg and dBu, Bg and Bu only for dA.
+ * relu'(0) = 0.  dG and dU are rounded once to the input format for the products; dA's two products
+ * are one fp32 sum; the biases' sums take unrounded fp32 values.  Results are deterministic; the order
+ * of sums follows the plan, as for gemm_act_bwd, and so do empty sums, aliasing, limits of M for
+ * fp32 weights' gradients, and the workspace (`required` bytes of gemm_gated_bwd_workspace hold dG,
+ * dU, partial sums and an fp32 operand's transpose; with `best` the products take their fastest plans).
+ */
+int gemm_gated_bwd(int in, int out, int M, int N, int K,
+                   const void* A, int lda,
+                   const void* Bg, int ldbg,
+                   const void* Bu, int ldbu,
+                   const void* dC, int lddc,
+                   const void* G, int ldg,
+                   const void* U, int ldu, int act,
+                   void* dA, int ldda,
+                   void* dBg, int lddbg,
+                   void* dBu, int lddbu,
+                   float* dbias_g, float* dbias_u,
+                   void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+int gemm_gated_bwd_workspace(int in, int out, int M, int N, int K, size_t* required, size_t* best);
+
 /* Plan kinds of dgemm_set_plan_override. */
 typedef enum {
     DGEMM_PLAN_AUTO = 0,      /* the cost model's choice (the default)                */
@@ -575,7 +640,10 @@ typedef enum {
  * gemm_act, gemm_act_bwd and gemm_f8 follow DGEMM_PLAN_GRID too: gemm_act the
  * tiles above and, for at most 16 rows, 16 x 32, 16 x 64 and (16-bit inputs)
  * 16 x 128; the other two's 16-bit and 8-bit products 256 x 256, 128 x 128 and
- * the slice-K tiles (more than 16 rows).
+ * the slice-K tiles (more than 16 rows).  gemm_f8_block follows it as gemm_f8 does (256 x 256 for
+ * 16-bit C and rows_b = 128 only); gemm_gated takes 256 x 256 (16-bit inputs), 128 x 128 (its columns
+ * of G and U counted together) and the 16-row strips, gemm_gated_bwd 256 x 256, 128 x 128 (16-bit)
+ * and the slice-K tiles.
  * DGEMM_PLAN_AUTO clears the override.  Not synchronised with calls running
  * on other host threads.  Returns DGEMM_OK, or DGEMM_ERR_INVALID_VALUE for a
  * bad kind or splits < 1 with DGEMM_PLAN_GRID.

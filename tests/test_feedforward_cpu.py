@@ -193,3 +193,91 @@ def test_plain_quantizer_against_torch():
     assert ((q - v).abs() <= (through - v).abs()).all()
     q, s = quant_block64(torch.zeros(3, 4), 128)
     assert torch.equal(q, torch.zeros(3, 4, dtype=torch.float64)) and float(s) == 2.0 ** -100
+
+
+# ------------------------------------------------------------------ gated projections
+
+def gated_call(in_=1, out=1, M=8, N=8, K=8, A=PA, lda=64, Bg=PB, ldbg=64, Bu=PB + 4096, ldbu=64, C=PC, ldc=64, bg=None,
+               bu=None, act=4, G=None, ldg=64, U=None, ldu=64, ws=None, ws_bytes=0):
+    return lib.gemm_gated(in_, out, M, N, K, V(A), lda, V(Bg), ldbg, V(Bu), ldbu, V(C), ldc, V(bg), V(bu), act, V(G),
+                          ldg, V(U), ldu, V(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("want, kw", [
+    (INVALID, dict(in_=3)), (INVALID, dict(in_=4)), (INVALID, dict(out=2)), (INVALID, dict(act=5)),
+    (INVALID, dict(M=-1)), (INVALID, dict(A=0)), (INVALID, dict(Bg=0)), (INVALID, dict(Bu=0)), (INVALID, dict(C=0)),
+    (INVALID, dict(ws_bytes=64)), (LEADING, dict(ldbu=4)), (LEADING, dict(ldbg=4)), (LEADING, dict(G=PZ, ldg=4)),
+    (LEADING, dict(U=PZ, ldu=4)), (MISALIGNED, dict(Bu=PB + 4098)), (MISALIGNED, dict(ldbu=65)),
+    (MISALIGNED, dict(G=PZ + 2)), (MISALIGNED, dict(bu=PR + 2)), (MISALIGNED, dict(bg=PR + 1)),
+    (LARGE, dict(ldbu=1 << 22)), (LARGE, dict(U=FAR, ldu=1 << 22)), (ALIAS, dict(C=PA)), (ALIAS, dict(C=PB + 4096)),
+    (ALIAS, dict(G=PC)), (ALIAS, dict(U=PC + 128)), (ALIAS, dict(G=PZ, U=PZ)), (ALIAS, dict(U=PA)), (ALIAS, dict(bu=PC)),
+    (ALIAS, dict(M=64, N=64, K=16384, lda=16384, C=FAR, ws=FAR, ws_bytes=1 << 40, Bu=3 * FAR, Bg=4 * FAR, A=5 * FAR)),
+])
+def test_gemm_gated_refusals(want, kw):
+    assert gated_call(**kw) == want
+
+
+def test_gemm_gated_accepts_until_the_device():
+    without_gpu()
+    for kw in (dict(), dict(Bu=PB), dict(ldbu=72), dict(Bu=PB + 16, N=8, ldbg=64), dict(G=PZ, U=PZ + 4096, bg=PR, bu=PR),
+               dict(G=PZ), dict(U=PZ), dict(K=0, A=0, Bg=0, Bu=0), dict(G=PZ, U=PZ + 32)):
+        assert gated_call(**kw) == dg.DGEMM_ERR_DEVICE, kw
+    assert gated_call(M=0, A=0, Bg=0, Bu=0, C=0) == dg.DGEMM_OK and gated_call(N=0) == dg.DGEMM_OK
+
+
+def gated_bwd_call(in_=1, out=1, M=8, N=8, K=8, A=PA, lda=64, Bg=PB, ldbg=64, Bu=PB + 4096, ldbu=64, dC=PC, lddc=64,
+                   G=PZ, ldg=64, U=PZ + 4096, ldu=64, act=4, dA=FAR, ldda=64, dBg=2 * FAR, lddbg=64, dBu=3 * FAR,
+                   lddbu=64, dbg=None, dbu=None, ws=PW, ws_bytes=1 << 20):
+    return lib.gemm_gated_bwd(in_, out, M, N, K, V(A), lda, V(Bg), ldbg, V(Bu), ldbu, V(dC), lddc, V(G), ldg, V(U), ldu,
+                              act, V(dA), ldda, V(dBg), lddbg, V(dBu), lddbu, V(dbg), V(dbu), V(ws), ws_bytes, None)
+
+
+@pytest.mark.parametrize("want, kw", [
+    (INVALID, dict(in_=3)), (INVALID, dict(act=9)), (INVALID, dict(K=-1)), (INVALID, dict(G=0)), (INVALID, dict(U=0)),
+    (INVALID, dict(dC=0)), (INVALID, dict(A=0)), (INVALID, dict(Bg=0)), (INVALID, dict(Bu=0)), (INVALID, dict(ws=0)),
+    (LEADING, dict(lddc=4)), (LEADING, dict(ldg=4)), (LEADING, dict(ldu=4)), (LEADING, dict(ldda=4)),
+    (LEADING, dict(lddbg=4)), (LEADING, dict(lddbu=4)), (MISALIGNED, dict(dA=FAR + 8)),
+    (MISALIGNED, dict(dbg=PR + 1)), (MISALIGNED, dict(dbu=PR + 2)), (SPACE, dict(ws_bytes=0, ws=0)),
+    (SPACE, dict(ws_bytes=64)), (ALIAS, dict(dA=PA)), (ALIAS, dict(dBg=FAR)), (ALIAS, dict(dBu=2 * FAR)),
+    (ALIAS, dict(dBu=PZ)), (ALIAS, dict(dbg=PC)), (ALIAS, dict(dbg=PR, dbu=PR)), (ALIAS, dict(ws=PC)),
+    (ALIAS, dict(dA=PW)), (LARGE, dict(ldu=1 << 22, U=FAR * 4)),
+    (LARGE, dict(in_=0, out=0, M=1 << 21, ws_bytes=1 << 50)),
+])
+def test_gemm_gated_bwd_refusals(want, kw):
+    assert gated_bwd_call(**kw) == want
+
+
+def test_gemm_gated_bwd_accepts_until_the_device():
+    without_gpu()
+    for kw in (dict(), dict(dA=None, Bg=0, Bu=0), dict(dBg=None, dBu=None, A=0), dict(dBg=None), dict(U=PZ),
+               dict(dbg=PR, dbu=PR + 64), dict(dA=None, dBg=None, dBu=None, A=0, Bg=0, Bu=0, dbg=PR), dict(M=0)):
+        assert gated_bwd_call(**kw) == dg.DGEMM_ERR_DEVICE, kw
+
+
+def test_gated_plans():
+    p = dg.gemm_gated_plan("bf16", 8192, 8192, 4096, 0, True)
+    assert p == {"tile_rows": 256, "tile_cols": 128, "splits": 1, "workspace_bytes": 0}
+    assert dg.gemm_gated_plan("f32", 8192, 8192, 4096, 0)["tile_rows"] == 128
+    for M, N, K in [(1, 2048, 8192), (16, 1000, 8200), (64, 500, 4096), (512, 512, 512)]:
+        p = dg.gemm_gated_plan("bf16", M, N, K, 1 << 30, True)
+        if p["splits"] > 1:
+            assert p["workspace_bytes"] == p["splits"] * M * 2 * ((N + 3) // 4 * 4) * 4
+            assert dg.gemm_gated_plan("bf16", M, N, K, p["workspace_bytes"] - 1, True)["splits"] < p["splits"]
+        assert dg.gemm_gated_plan("bf16", M, N, K, 0, True)["splits"] == 1
+    for fmt in ("f32", "bf16", "f16"):
+        for M in (1, 16, 100, 3000):
+            req, best = dg.gemm_gated_bwd_workspace(fmt, M, 200, 300)
+            assert 2 * M * 200 * (4 if fmt == "f32" else 2) < req <= best
+    with pytest.raises(dg.DgemmError):
+        dg.gemm_gated_plan("f32x3", 8, 8, 8, 0)
+
+
+def test_gated_signatures_and_host_tensors():
+    forms = {"linear_gated": "A Bg Bu bias_g bias_u act out_dtype keep_preact",
+             "linear_gated_backward": "A Bg Bu dC gate up act bias"}
+    x, w, c = torch.ones(4, 16), torch.ones(16, 8), torch.ones(4, 8)
+    for name, params in forms.items():
+        fn = getattr(dg, name)
+        assert list(inspect.signature(fn).parameters) == params.split() + ["stream"] and fn.__doc__
+        with pytest.raises(ValueError, match="device tensor"):
+            fn(x, w, w, *((c, c, c) if name.endswith("backward") else ()))
