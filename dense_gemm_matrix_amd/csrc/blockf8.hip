@@ -6,18 +6,19 @@
 //
 // A: M x K, B: N x K, both K-contiguous.  A K step of the matrix kernels is 128 bytes of
 // every row, which is one block: a step's matrix instructions start from zero, and their
-// sums are added to the running ones scaled, in fp32.  That is one multiply-add per output
-// and block, 64 cycles of the vector unit for the 128 cycles that a 32 x 32 block's two
-// matrix instructions take.  To have one factor per lane for all of a block's 16 sums, the
+// sums are added to the running ones scaled, in fp32: one multiply-add per output and block,
+// half of the vector unit's time at the matrix units' full rate.  To have few factors per lane, the
 // operands trade places: the instruction's rows are B's, its columns (a lane each) A's,
-// and sb is the same for all of them where a weight has a scale per 128 x 128.  With a
-// scale per row of B a lane's 16 sums have 16 of them, a second multiplication each.
+// and sb is the same for all of a lane's sums where a weight has a scale per 128 x 128.  With a
+// scale per row of B they differ, a second multiplication each, and the vector unit is as busy
+// as the matrix units.
 //
 // The vector unit adds to ordinary registers only, not to the accumulation half of the
 // register file, so a wave cannot hold 256 running sums as gemmt.hip's do: a wave owns
 // 128 x 64 outputs (256 x 256 tile, 8 waves, two to a SIMD) or 64 x 64 (128 x 128 tile, 4
 // waves, two workgroups to a CU), and one wave's multiply-adds run beside the other's
-// matrix instructions.
+// matrix instructions.  4096^3, bf16 C: 64-69 us with a scale per 128 x 128 (2.0 PFLOP/s; gemm_f8 with
+// a scale per row 58-61), 73.7 with one per row and block.
 //
 // The scales of a step come with its operands, by 4-byte direct-to-LDS loads (one per
 // wave and step), and are read back one per lane.  Operands, LDS layout, tile map and
@@ -103,10 +104,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rsrc(const float* p, int
 // ------------------------------------------------------------------ small outputs
 
 // As slicet.hip: a TS x TS tile (TS = 32 MI) per workgroup of W waves, each with a run of
-// the blocks and its own LDS stages; the waves' sums are added in LDS in wave order.
-template <int MI, int W>
+// the blocks and its own LDS stages; the waves' sums are added in LDS in wave order.  32 x 32 with
+// eight waves, 64 x 64 with four (32 x 32 with four, more blocks in flight in each: 12 to 37 % slower).
+template <int MI>
 struct SliceTile {
-    static constexpr int D = MI == 1 && W == 4 ? 2 : 1;   // blocks per chunk, two chunks in LDS
+    static constexpr int W = MI == 1 ? 8 : 4;
+    static constexpr int D = 1;                           // blocks per chunk, two chunks in LDS
     static constexpr int BLKB = 128 * 32 * MI;            // bytes of one operand's block
     static constexpr int STAGE = 2 * BLKB + 512;          // and 64 scales of either
     static constexpr int RED = W * MI * MI * 16 * 64 * 4;
@@ -114,9 +117,10 @@ struct SliceTile {
 };
 
 // NB: B's scales are per row.
-template <int IN, int OUT, int MI, int W, bool NB>
-__global__ __launch_bounds__(64 * W) void block_slice_kernel(BlockArgs a, EpiArgs epi) {
-    using T = SliceTile<MI, W>;
+template <int IN, int OUT, int MI, bool NB>
+__global__ __launch_bounds__(64 * SliceTile<MI>::W) void block_slice_kernel(BlockArgs a, EpiArgs epi) {
+    using T = SliceTile<MI>;
+    constexpr int W = T::W;
     constexpr int TS = 32 * MI, NBLK = MI * MI, D = T::D, BLKB = T::BLKB;
     constexpr int NDB = BLKB / 1024;  // an operand block's direct-to-LDS loads
     __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
@@ -249,7 +253,7 @@ __global__ __launch_bounds__(64 * W) void block_slice_kernel(BlockArgs a, EpiArg
 template <int TBM, int TBN, int WM, int WN>
 struct GridTile {
     static constexpr int NW = WM * WN, S = 2;
-    static constexpr int MI = TBM / WM / 32, NJ = TBN / WN / 32;
+    static constexpr int MI = TBM / WM / 32, NJ = TBN / WN / 32;  // a wave's blocks of 32 x 32
     static constexpr int A_STAGE = TBM * 128, B_STAGE = TBN * 128, S_STAGE = (TBM + TBN) * 4;
     static constexpr int A_DMA = A_STAGE / 1024 / NW, B_DMA = B_STAGE / 1024 / NW;
     static constexpr int LOADS = A_DMA + B_DMA + 1;  // and the scales of 64 rows
@@ -258,11 +262,25 @@ struct GridTile {
     static_assert(NW * full_lds<NJ> <= LDS && LDS <= 160 * 1024, "LDS budget");
 };
 
+// IN_F8 (16-bit outputs, and the fp32 partial sums of their K splits): the 16 x 16 x 128 instruction
+// takes a whole block of K: its sums, rows 4 (lane / 16) .. of B and column lane % 16 of A, are four registers
+// that the next instruction's cycles scale and add, so that two sets of four do for the
+// products in flight; with a scale per row of B (NB) a lane needs four of them per 16 rows.  Two
+// waves to a SIMD, at 247 of their 256 registers on the large tile.
+//
+// Against 32 x 32 x 64 instructions, two to a block (4096^3: 69 us either way with a scale per 128 x
+// 128; with a scale per row, whose 32 factors per 64 rows leave no registers for the large tile,
+// 95 on the small one), it takes 73.7 us there, and the small tile 76 and 87 where it took 85 and 95.
+//
+// IN_F8W (fp32 outputs): four 16 x 16 x 32 bf16 instructions a block, on fragments widened once per
+// step (B's) and per 16 rows (A's).  4096^3 127 us, with a scale per row of B 140 (32 x 32
+// instructions whose fragments were widened per use 128 and 255).
 template <int IN, int OUT, int TBM, int TBN, int WM, int WN, bool NB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a, int kchunk, int64_t c_zstride,
                                                                      EpiArgs epi) {
     using T = GridTile<TBM, TBN, WM, WN>;
-    constexpr int MI = T::MI, NJ = T::NJ, S = T::S, NW = T::NW;
+    constexpr int S = T::S, NW = T::NW, MI = TBM / WM / 16, NJ = TBN / WN / 16;
+    constexpr bool WIDE = IN == IN_F8W;
     __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
     char* const smA = smem;
     char* const smB = smem + S * T::A_STAGE;
@@ -286,25 +304,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int g = lane >> 5, li = lane & 31;
+    const int g = lane >> 4, c = lane & 15;
     const int K = a.K, nk = (K + F8_BLOCK - 1) / F8_BLOCK;
-
-    // Load j of a wave fills the 8 rows of block j NW + wave: the rows' swizzle is then the
-    // same for every j (it has a period of 32 rows), and so is the lane's offset but for a
-    // wave-uniform number of rows.
-    static_assert(NW % 4 == 0, "the swizzle's period");
     const int row0 = wave * A16_RPB + lane / A16_CH;
     const int ch = ((lane % A16_CH) ^ a16_phi(row0)) << 4;
     const int va = row0 * a.lda + ch, vb = row0 * a.ldb + ch;
     const int ja = NW * A16_RPB * a.lda, jb = NW * A16_RPB * a.ldb;
-    // Scales: waves below TBM / 64 load A's, the others B's, 64 rows each.
-    const bool for_a = wave < TBM / 64;
-    const int srow = (for_a ? wave : wave - TBM / 64) * 64 + lane;
     const int64_t sb_row0 = NB ? n0 : n0 / F8_BLOCK;
     const int sb_rows = NB ? rows_b : (n0 + rows_b - 1) / F8_BLOCK - n0 / F8_BLOCK + 1;
+    const bool for_a = wave < TBM / 64;
+    const int srow = (for_a ? wave : wave - TBM / 64) * 64 + lane;
     const int vs = for_a ? scale_off(srow, rows_a, a.s.sa_row)
                          : scale_off(NB ? srow : srow / F8_BLOCK, sb_rows, a.s.sb_row);
-
     struct Desc { __amdgpu_buffer_rsrc_t a, b, s; int st; };
     auto desc = [&](int kt) {
         const int k0 = kt * F8_BLOCK;
@@ -326,29 +337,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
         else
             dma4(d.s, lds_addr(smS + d.st * T::S_STAGE + wave * 256), vs);
     };
-    // The last step's bytes at and past K are zeroed in LDS, in both operands.
     const bool ragged = K % F8_BLOCK != 0;
     auto fix_tail = [&]() {
         const int valid = K - (nk - 1) * F8_BLOCK, s = (nk - 1) % S;
         for (int r = tid; r < TBM + TBN; r += 64 * NW) {
             char* st = r < TBM ? smA + s * T::A_STAGE : smB + s * T::B_STAGE;
             const int row = r < TBM ? r : r - TBM;
-            for (int c = valid >> 4; c < A16_CH; ++c) {
-                u32x4* p = (u32x4*)(st + a16_off(row, c));
-                *p = mask_bytes(*p, valid - 16 * c);
+            for (int q = valid >> 4; q < A16_CH; ++q) {
+                u32x4* p = (u32x4*)(st + a16_off(row, q));
+                *p = mask_bytes(*p, valid - 16 * q);
             }
         }
     };
-    // This lane's chunks of a row: the swizzle depends on li alone, rows being counted from
-    // multiples of 32.
-    int off[4];
+    // Chunks 2 g and 2 g + 1 of row c of 16; the swizzle has a period of 32 rows.
+    int off[2][2];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) off[h] = a16_off(li, 4 * (h >> 1) + 2 * g + (h & 1));
-    auto read_a = [&](int kt, int mi, int h, RowFrag& f) {
-        f.w[h] = *(const u32x4*)(smA + (kt % S) * T::A_STAGE + (wm * (TBM / WM) + mi * 32) * 128 + off[h]);
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) off[o][h] = a16_off(16 * o + c, 2 * g + h);
+    struct Half { u32x4 w[2]; };
+    auto read = [&](const char* st, int strip, int h, Half& f) {  // of the wave's 16-row strips
+        f.w[h] = *(const u32x4*)(st + (strip >> 1) * 4096 + off[strip & 1][h]);
     };
-    auto read_b = [&](int kt, int nj, int h, RowFrag& f) {
-        f.w[h] = *(const u32x4*)(smB + (kt % S) * T::B_STAGE + (wn * (TBN / WN) + nj * 32) * 128 + off[h]);
+    auto read_a = [&](int kt, int mi, int h, Half& f) {
+        read(smA + (kt % S) * T::A_STAGE + wm * (TBM / WM) * 128, mi, h, f);
+    };
+    auto read_b = [&](int kt, int nj, int h, Half& f) {
+        read(smB + (kt % S) * T::B_STAGE + wn * (TBN / WN) * 128, nj, h, f);
     };
     auto sync = [&](auto vm_tag) {
         constexpr int VM = decltype(vm_tag)::value;
@@ -360,11 +375,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
     using FirstIn = std::integral_constant<int, T::LOADS>;
     using AllIn = std::integral_constant<int, 0>;
 
-    f32x16 acc[MI][NJ];
+    f32x4 acc[MI][NJ];
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int nj = 0; nj < NJ; ++nj) acc[mi][nj] = zero16();
+        for (int nj = 0; nj < NJ; ++nj) acc[mi][nj] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (nk > 0) {
 #pragma unroll
         for (int s = 0; s < S; ++s) {
@@ -374,98 +389,102 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
         }
         sync(FirstIn{});
         if (ragged && nk == 1) { fix_tail(); sync(FirstIn{}); }
-        RowFrag fa[2], fb[NJ];
-        float sa[MI], sb[NB ? NJ : 1][NB ? 16 : 1];
-        auto read_scales = [&](int kt) {
-            const float* p = (const float*)(smS + (kt % S) * T::S_STAGE);
+        Half fa[2], fb[NJ];
+        bf16x8 wa[WIDE ? 4 : 1], wb[WIDE ? NJ : 1][4];
+        auto widen = [&](const Half& f, bf16x8* to) {
 #pragma unroll
-            for (int mi = 0; mi < MI; ++mi) sa[mi] = p[wm * (TBM / WM) + mi * 32 + li];
-            if constexpr (NB) {
+            for (int q = 0; q < 4; ++q) to[q] = widen_f8(f.w[q >> 1][2 * (q & 1)], f.w[q >> 1][2 * (q & 1) + 1]);
+        };
+        constexpr int NS = NB ? NJ : 1;
+        float sa[MI];
+        f32x4 sb[NS];
+        auto read_sb = [&](int kt, int nj) {
+            const float* p = (const float*)(smS + (kt % S) * T::S_STAGE) + TBM + wn * (TBN / WN);
+            if constexpr (NB) sb[nj] = *(const f32x4*)(p + nj * 16 + 4 * g);
+            else if (nj == 0) sb[0][0] = p[0];
+        };
+        auto read_sa = [&](int kt) {
+            const float* p = (const float*)(smS + (kt % S) * T::S_STAGE) + wm * (TBM / WM) + c;
 #pragma unroll
-                for (int nj = 0; nj < NJ; ++nj)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        sb[nj][r] = p[TBM + wn * (TBN / WN) + nj * 32 + 8 * (r >> 2) + 4 * g + (r & 3)];
-            } else {
-                sb[0][0] = p[TBM + wn * (TBN / WN)];
-            }
+            for (int mi = 0; mi < MI; ++mi) sa[mi] = p[mi * 16];
         };
 #pragma unroll
-        for (int h = 0; h < 4; ++h) read_a(0, 0, h, fa[0]);
+        for (int h = 0; h < 2; ++h) read_a(0, 0, h, fa[0]);
 #pragma unroll
-        for (int nj = 0; nj < NJ; ++nj)
+        for (int nj = 0; nj < NJ; ++nj) {
 #pragma unroll
-            for (int h = 0; h < 4; ++h) read_b(0, nj, h, fb[nj]);
-        read_scales(0);
-        // Block i (A's rows i / NJ, B's i % NJ) of a step has two slots of a matrix instruction
-        // each, and carries the scaled addition of the block before it: the last block's of a
-        // step goes into the next step's first.
-        f32x16 part[2] = {zero16(), zero16()};
-        float f_prev[NB ? 16 : 1];
-#pragma unroll
-        for (int r = 0; r < (NB ? 16 : 1); ++r) f_prev[r] = 0.0f;
+            for (int h = 0; h < 2; ++h) read_b(0, nj, h, fb[nj]);
+            read_sb(0, nj);
+        }
+        read_sa(0);
+        f32x4 part[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
+        float a_prev = 0.0f;
+        f32x4 b_prev = {0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int NBLK = MI * NJ;
-        static_assert(NBLK % 2 == 0, "the sums alternate between two sets");
-        auto add = [&](int i, const float (&f)[NB ? 16 : 1], int half) {
+        // Block i's sums times its scales, added to the running ones.
+        auto add = [&](int i, float fa_, const f32x4& fb_) {
             const int mi = i / NJ, nj = i % NJ;
 #pragma unroll
-            for (int r = 8 * half; r < 8 * half + 8; ++r)
-                acc[mi][nj][r] = __builtin_fmaf(part[i & 1][r], f[NB ? r : 0], acc[mi][nj][r]);
+            for (int r = 0; r < 4; ++r) {
+                const float f = NB ? fa_ * fb_[r] : fa_;
+                acc[mi][nj][r] = __builtin_fmaf(part[i & 1][r], f, acc[mi][nj][r]);
+            }
             // Here, in program order: the scheduling barriers order only what has side effects,
             // and the compiler would otherwise leave a step's additions to its end.
             asm volatile("" : "+v"(acc[mi][nj]));
         };
         for (int kt = 0; kt < nk; ++kt) {
             Desc d;
+            if constexpr (!NB) {
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) sa[mi] *= sb[0][0];
+            }
 #pragma unroll
             for (int i = 0; i < NBLK; ++i) {
                 const int mi = i / NJ, nj = i % NJ;
-                // The next 32 rows of A while this one's products run; the last ones come
-                // from the next step, whose stage has landed by then.
                 if (mi == MI - 1 && nj == 0) {
                     d = desc(kt + S);
                     sync(AllIn{});
                     if (ragged && kt + 2 == nk) { fix_tail(); sync(AllIn{}); }
                 }
-                float f[NB ? 16 : 1];
+                const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (WIDE) {
+                    if (mi == 0) widen(fb[nj], wb[nj]);
+                    if (nj == 0) widen(fa[mi & 1], wa);
 #pragma unroll
-                for (int r = 0; r < (NB ? 16 : 1); ++r) f[r] = sa[mi] * sb[NB ? nj : 0][NB ? r : 0];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    part[i & 1] = half_product<IN>(fb[nj], fa[mi & 1], q, q == 0 ? zero16() : part[i & 1]);
-                    __builtin_amdgcn_sched_barrier(0);
-                    add(i == 0 ? NBLK - 1 : i - 1, f_prev, q);
-                    const int slot = 2 * nj + q;  // of 2 NJ
-#pragma unroll
-                    for (int h = (slot * 4) / (2 * NJ); h < ((slot + 1) * 4) / (2 * NJ); ++h) {
-                        if (mi + 1 < MI) read_a(kt, mi + 1, h, fa[(mi + 1) & 1]);
-                        else read_a(kt + 1, 0, h, fa[MI & 1]);
-                    }
-                    if (mi == MI - 1) {
-#pragma unroll
-                        for (int j = (slot * T::LOADS) / (2 * NJ); j < ((slot + 1) * T::LOADS) / (2 * NJ); ++j)
-                            dma_one(d, j);
-                        if (q == 1) {
-#pragma unroll
-                            for (int h = 0; h < 4; ++h) read_b(kt + 1, nj, h, fb[nj]);
-                        }
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int q = 0; q < 4; ++q)
+                        part[i & 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[nj][q], wa[q], q ? part[i & 1] : zero,
+                                                                              0, 0, 0);
+                } else {
+                    part[i & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        both(fb[nj].w[0], fb[nj].w[1]), both(fa[mi & 1].w[0], fa[mi & 1].w[1]), zero, 0, 0, 0, 0, 0, 0);
                 }
+                __builtin_amdgcn_sched_barrier(0);
+                add(i == 0 ? NBLK - 1 : i - 1, a_prev, b_prev);
+                a_prev = sa[mi];
+                b_prev = sb[NB ? nj : 0];
+                if (nj < 2) {
+                    if (mi + 1 < MI) read_a(kt, mi + 1, nj, fa[(mi + 1) & 1]);
+                    else read_a(kt + 1, 0, nj, fa[MI & 1]);
+                }
+                if (mi == MI - 1) {
 #pragma unroll
-                for (int r = 0; r < (NB ? 16 : 1); ++r) f_prev[r] = f[r];
+                    for (int j = (nj * T::LOADS) / NJ; j < ((nj + 1) * T::LOADS) / NJ; ++j) dma_one(d, j);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) read_b(kt + 1, nj, h, fb[nj]);
+                    read_sb(kt + 1, nj);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
-            static_assert(MI % 2 == 0, "A's fragments alternate between two sets");
-            read_scales(kt + 1);
+            read_sa(kt + 1);
         }
-        add(NBLK - 1, f_prev, 0);
-        add(NBLK - 1, f_prev, 1);
+        add(NBLK - 1, a_prev, b_prev);
     }
     // No direct-to-LDS write may still be in flight when the LDS is reused.
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
     __syncthreads();  // every wave is done with the operand ring
-    store_tile_full<OUT, MI, NJ, true>(acc, a.C, a.M, a.N, a.ldc, m0 + wm * (TBM / WM), n0 + wn * (TBN / WN),
-                                       lane, epi, smem + wave * full_lds<NJ>);
+    store_tile_full<OUT, MI / 2, NJ / 2, true>(acc, a.C, a.M, a.N, a.ldc, m0 + wm * (TBM / WM), n0 + wn * (TBN / WN),
+                                            lane, epi, smem + wave * full_lds<NJ / 2>);
 }
 
 // ------------------------------------------------------------------ launches
@@ -483,9 +502,8 @@ hipError_t go(const GemmLaunch& L, const BlockScales& s) {
     if (L.slice_waves > 0) {
         if (L.splits != 1) return hipErrorInvalidValue;
         const void* fn = nullptr;
-        if (L.tbm == 32 && L.slice_waves == 4) fn = (const void*)block_slice_kernel<IN, OUT, 1, 4, NB>;
-        if (L.tbm == 32 && L.slice_waves == 8) fn = (const void*)block_slice_kernel<IN, OUT, 1, 8, NB>;
-        if (L.tbm == 64 && L.slice_waves == 4) fn = (const void*)block_slice_kernel<IN, OUT, 2, 4, NB>;
+        if (L.tbm == 32 && L.slice_waves == 8) fn = (const void*)block_slice_kernel<IN, OUT, 1, NB>;
+        if (L.tbm == 64 && L.slice_waves == 4) fn = (const void*)block_slice_kernel<IN, OUT, 2, NB>;
         if (!fn || L.tbm != L.tbn) return hipErrorInvalidValue;
         void* args[] = {&a, &e};
         return hipLaunchKernel(fn, dim3((unsigned)(L.tiles_m * L.tiles_n)), dim3(64 * L.slice_waves), args, 0,
@@ -493,13 +511,13 @@ hipError_t go(const GemmLaunch& L, const BlockScales& s) {
     }
     const void* fn = nullptr;
     int threads = 256;
-    if (L.tbm == 128 && L.tbn == 128) fn = (const void*)block_grid_kernel<IN, OUT, 128, 128, 2, 2, NB>;
-    if constexpr (IN == IN_F8 && !NB) {
+    if constexpr (IN == IN_F8) {
         if (L.tbm == 256 && L.tbn == 256) {
             fn = (const void*)block_grid_kernel<IN, OUT, 256, 256, 2, 4, NB>;
             threads = 512;
         }
     }
+    if (L.tbm == 128 && L.tbn == 128) fn = (const void*)block_grid_kernel<IN, OUT, 128, 128, 2, 2, NB>;
     if (!fn) return hipErrorInvalidValue;
     void* args[] = {&a, &kchunk, &zs, &e};
     return hipLaunchKernel(fn, dim3((unsigned)(L.tiles_m * L.tiles_n), (unsigned)L.splits), dim3(threads), args,

@@ -228,7 +228,9 @@ hipError_t launch_gemmt_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn
 // The products of a gated layer's backward pass and its column sums in one kernel: nt (LAY_NT) is
 // nt.A nt.B^T + A2 B2^T (A2 with nt.A's row pitch), tn the weights' gradients (LAY_TN); tiles_m = 0
 // or N = 0: none.  One tile size for all (launch_gemmt_gated, 16-bit) or one for nt and one for
-// tn (launch_slicet_gated, 4 waves); the TN tiles first if tn_first.
+// tn (launch_slicet_gated, 4 waves); the TN tiles first if tn_first.  launch_gemmt_gated: nt's K
+// steps (of 64, of both pairs) in nt.splits runs of nt.kchunk steps, their fp32 sums at nt.C + z
+// nt.c_zstride.
 struct GatedBwdLaunch {
     GemmLaunch nt, tn[2];
     const char* A2;
@@ -275,7 +277,8 @@ struct GatedEpi {
     int ldg, ldu;
 };
 // tbm x tbp tiles (tbp columns of G and of U); split z, of kchunk k, writes G and U at z zstride
-// bytes.  Few rows: strips of tbp columns, `waves` waves each (launch_gated_skinny).
+// bytes.  waves = 4: a tile's K split over its waves (32 x 32, 64 x 32; unsplit).  Few rows: strips
+// of tbp columns, `waves` waves each (launch_gated_skinny).
 struct GatedLaunch {
     int in, out, tbm, tbp, stages, waves;
     const char* A;

@@ -32,13 +32,67 @@ int check_scales(const Scales& s, bool output) {
     return DGEMM_OK;
 }
 
+// Launch, first loads and last stores, which the grid kernels' estimate leaves out.
+constexpr double GRID_US = 2.5;
+
 // fp32 outputs and few rows: the widened products, whose sums are fp32.
 int block_in(int of, int M) { return of == OUT_F32 || M <= SKINNY_M ? IN_F8W : IN_F8; }
 
+// The tiles of blockf8.hip, in the terms of the other 8-bit products (the scaled additions cost some
+// of the rate, and an underfilled chip does not run the small one faster); `each`: a scale per
+// row of B.
+TileCand block_tile(int i, bool each) {
+    const double f = each ? 0.89 : 1.0;
+    return i == 0 ? TileCand{256, 256, 0.87 * f, 0.0, 0.0, 0.87 * f, 0.6}
+                  : TileCand{128, 128, 0.55 * f, 1.26, 1.35, 0.6 * f, 1.0};
+}
+
+// Tiles whose waves split K (32 x 32 with 8 waves, 64 x 64 with 4) by the time of a round of 256,
+// grid tiles and K splits by the common estimate.  us, slices of 32 / of 64 / best grid plan:
+// bf16 C, 64 x 4096 x 4096 5.8 / 12.0 / 14.5, 17 x 8192 x 1024 3.6 / 6.3 / 8.5, 300 x 1000 x 2000 8.5 /
+// 9.4 / 13.3, 1000^3 13.1 / 9.2 / 10.2, 512 x 4096 x 4096 38.5 / 25.1 / 25.3, 700 x 5000 x 3000 67.7 / 45.1 /
+// 26.6; fp32 C, 700 x 5000 x 3000 71 / 55 / 35.
 Plan plan_block(int of, int rows_b, int M, int N, int K, uint64_t ws) {
     const int in = block_in(of, M);
     if (M > 0 && M <= SKINNY_M && N > 0) return plan_skinny(in, LAY_NT, M, N, K, 0);
-    return plan_t(in, LAY_NT, out_esize(of), M, N, K, ws, nullptr, in == IN_F8 && rows_b != 1);
+    const int nk = (int)ceil_div(std::max(K, 1), F8_BLOCK);
+    const bool each = rows_b == 1;
+    auto slices = [&](int t) {
+        Plan p{t, t, 1, K, 0, 0};
+        p.waves = t == 32 ? 8 : 4;
+        return p;
+    };
+    int fm, fn, fs;
+    const bool forced = forced_grid(fm, fn, fs) && fm == fn;
+    if (forced && (fm == 32 || fm == 64)) return slices(fm);
+    Plan best{};
+    double best_us = -1.0;
+    for (int t = 32; t <= 64; t += 32) {
+        const int64_t n = ceil_div(M, t) * ceil_div(N, t);
+        if (n > INT32_MAX) continue;
+        const double wide = in == IN_F8 ? 1.0 : t == 32 ? 1.12 : 1.3;  // fp32 C, by the widened products
+        const double round =
+            (t == 32 ? 2.3 + 0.55 * (double)ceil_div(nk, 8) : 4.5 + 0.85 * (double)ceil_div(nk, 4)) * wide;
+        const double us = 1.1 + (double)ceil_div(n, NUM_CU) * round;
+        if (best_us < 0.0 || us < best_us) {
+            best_us = us;
+            best = slices(t);
+        }
+    }
+    for (int s = 1; s <= MAX_SPLITS && s <= nk; ++s)
+        for (int i = in == IN_F8 ? 0 : 1; i < 2; ++i) {
+            const TileCand t = block_tile(i, each);
+            const Plan p = plan_pieces(t, F8_BLOCK, M, N, K, s, ws);
+            if (p.splits != s || (forced && (t.bm != fm || s != fs))) continue;
+            const double us = estimate_us(in, out_esize(of), M, N, t, s, s == 1 ? nk : p.kchunk / F8_BLOCK, p.ldw) /
+                                  (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US;
+            if (us < best_us || forced) {
+                best_us = us;
+                best = p;
+                if (forced) return best;
+            }
+        }
+    return best;
 }
 
 int run_block(int of, int M, int N, int K, const void* A, int lda, const void* B, int ldb, void* C, int ldc,
@@ -102,7 +156,10 @@ GatedPlan gated_pieces(int bm, int bn, int bk, int M, int N, int K, int splits, 
     return p;
 }
 
-// At most SKINNY_M rows: as plan_skinny's strips of B stored along the output, of both weights.
+// At most SKINNY_M rows: as plan_skinny's strips of B stored along the output, of both weights,
+// but never of 128 columns (two weights' loads are as wide as one's twice: 1 x 14336 x 4096 bf16, weights
+// from the last-level cache, 32 / 64 / 128 columns 43.8 / 37.4 / 38.4 us), nor split from a fixed K on
+// in fp32.
 GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
     auto strips = [&](int cols, int waves, int splits) {
         GatedPlan p = gated_pieces(SKINNY_M, cols, 32, M, N, K, splits, ws);
@@ -116,7 +173,7 @@ GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
         return p;
     };
     int fm, fn, fs;
-    if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64 || (fn == 128 && in != IN_F32))) {
+    if (forced_grid(fm, fn, fs) && fm == SKINNY_M && (fn == 32 || fn == 64)) {
         const GatedPlan p = strips(fn, fn == 32 ? 16 : 8, fs);
         if (p.splits > 0) return p;
     }
@@ -136,6 +193,8 @@ GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
     const int n = in == IN_F32 ? 1 : 2, bk = in == IN_F32 ? 32 : 64;
     const int nk = (int)ceil_div(std::max(K, 1), bk);
     int fm, fn, fs;
+    auto slices = [&](int bm) { return GatedPlan{bm, 32, 1, K, 0, 4, 0, false}; };
+    if (forced_grid(fm, fn, fs) && fn == fm && (fm == 32 || fm == 64)) return slices(fm);
     if (forced_grid(fm, fn, fs))
         for (int i = 0; i < n; ++i)
             if (tiles[i].bm == fm && tiles[i].bn == fn) {
@@ -144,6 +203,24 @@ GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
             }
     GatedPlan best{};
     double best_us = -1.0;
+    // Small outputs: a round of 256 tiles whose waves split K, by its blocks of 128 bytes per wave,
+    // against the grid tiles.  Measured (us; 32 x 32 / 64 x 32 slices / best grid plan with a
+    // workspace): bf16 512^3 4.2 / 5.3 / 8.5, 64 x 2048 x 1024 5.0 / 6.5 / 11.4, 512 x 1024 x 512
+    // 7.1 / 5.4 / 8.6, 1024^3 20.9 / 12.5 / 12.0, 300 x 600 x 8192 35.0 / 37.5 / 22.9; fp32 512^3
+    // 8.0 / 12.5 / 20.1, 64 x 4096 x 4096 42.9 / 69.8 / 69.4, 1024^3 47.5 / 41.9 / 46.4, 256 x 256 x
+    // 4096 38.7 / 70.2 / 28.0.
+    const double nb = (double)ceil_div(nk, 4);
+    for (int t = 32; t <= 64; t += 32) {
+        const int64_t n = ceil_div(M, t) * ceil_div(N, 32);
+        if (n > INT32_MAX) continue;
+        const double round = in == IN_F32 ? (t == 32 ? 1.8 + 1.27 * nb : 3.6 + 2.05 * nb)
+                                          : (t == 32 ? 1.6 + 0.75 * nb : 2.6 + 0.9 * nb);
+        const double us = 1.1 + (double)ceil_div(n, NUM_CU) * round;
+        if (best_us < 0.0 || us < best_us) {
+            best_us = us;
+            best = slices(t);
+        }
+    }
     const int N2 = (int)std::min<int64_t>(2 * up(N, 32), INT32_MAX);
     for (int s = 1; s <= MAX_SPLITS && s <= nk; ++s)
         for (int i = 0; i < n; ++i) {
@@ -151,8 +228,8 @@ GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
             const GatedPlan p = gated_pieces(t.bm, t.bn / 2, bk, M, N, K, s, ws);
             if (p.splits != s) continue;
             double us = estimate_us(in, es_out, M, N2, t, s, s == 1 ? nk : p.kchunk / bk, s == 1 ? 0 : 2 * p.ldw);
-            if (s > 1) us /= SPLIT_MARGIN;
-            if (best_us < 0.0 || us < best_us) {
+            us = us / (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US;
+            if (us < best_us) {
                 best_us = us;
                 best = p;
             }
@@ -229,6 +306,8 @@ GatedBwdParts gated_bwd_parts(int in, int M, int N, int K, bool products, bool d
 struct GatedBwdPlan {
     int nt, tn;
     bool nt_slices, tn_slices, together, tn_first, transposes;  // transposes: fp32 by the grid kernels
+    int splits = 1, per = 0, ldw = 0;  // of nt's K steps, for grid tiles: runs of `per`, partial sums of pitch ldw
+    int64_t ws_bytes = 0;              // of those
 };
 
 // M rows, K inputs, N gated outputs: nt has M x K outputs of 2 N terms, tn two of K x N of M.
@@ -280,8 +359,35 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
             const int64_t ta = nt_tiles(t.bm), tb = tn_tiles(t.bm);
             if (!allowed(t.bm) || ta + tb > INT32_MAX / 2) continue;
             bool tn_first;
-            const double us = pair_grid_us(t, in, ta, kn, tb, M, tn_first);
+            // Three products on 128 x 128 tiles were slower than the estimate for two.
+            const double f128 = t.bm == 128 ? 1.15 : 1.0;
+            const double us = pair_grid_us(t, in, ta, kn, tb, M, tn_first) * f128;
             consider(us, GatedBwdPlan{t.bm, t.bm, false, false, true, tn_first, false});
+            // dA's sums are twice as long as a plain layer's: where its tiles are few they are the
+            // pass's longest, and in runs of their steps, to a workspace, fill the CUs that it leaves
+            // idle.  The whole pass in us, bf16, M x N x K, whole / in runs:
+            //    300 x 1500 x  900    43.0 /  21.9   (128 x 128, 5 runs)
+            //    100 x 3000 x 4000    85.3 /  35.5   (128 x 128, 4)
+            //   1000 x 2744 x 1032    93.7 /  50.4   (256 x 256, 6)
+            //    600 x 8000 x 1000     189 /  67.4   (256 x 256, 8)
+            //   2000 x 4000 x 2000     171 /   141   (256 x 256, 2)
+            //   3000 x 6000 x 1500     285 /   260   (256 x 256, 2)
+            // With these constants the plan chosen among 1 to 12 runs of either tile takes 3 % more
+            // than the fastest on average over ten such layers, 14 % at most.
+            const int steps = kn / 64;
+            for (int s = 2; s <= MAX_SPLITS && s <= steps && dA; ++s) {
+                GatedBwdPlan p{t.bm, t.bm, false, false, true, false, false};
+                p.per = (int)ceil_div(steps, s);
+                p.splits = (int)ceil_div(steps, p.per);
+                p.ldw = (int)up(K, 4);
+                p.ws_bytes = (int64_t)p.splits * M * p.ldw * 4;
+                if (p.splits != s || (uint64_t)p.ws_bytes > ws || (int64_t)PANEL_ROWS * p.ldw * 4 >= DESC_LIMIT ||
+                    ta * s + tb > INT32_MAX / 2 || (forced && fs != s))
+                    continue;
+                const double sum_us = 4.0 + (2.0 * (double)p.ws_bytes + (double)M * K * 2) / 8e6;
+                const double split_us = pair_grid_us(t, in, ta * s, p.per * 64, tb, M, p.tn_first) * f128 + sum_us;
+                consider(forced ? 0.0 : split_us, p);
+            }
         }
     if (f == IN_F32 && !forced) {
         double us = 0.0;
@@ -625,6 +731,19 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
         L.tn_first = p.tn_first;
         L.sums[0] = sg;
         L.sums[1] = su;
+        if (p.splits > 1) {
+            L.nt.splits = p.splits;
+            L.nt.kchunk = p.per;
+            L.nt.C = w_gemm;
+            L.nt.ldc = p.ldw;
+            L.nt.c_zstride = (int64_t)M * p.ldw * 4;
+            if (launch_gemmt_gated(L) != hipSuccess) return DGEMM_ERR_LAUNCH;
+            EpiArgs e{};
+            e.alpha = 1.0f;
+            return launched(launch_splitk_reduce((const float*)w_gemm, p.splits, (int64_t)M * p.ldw, p.ldw, (char*)dA,
+                                                 ldda, M, K, out_format(in, DGEMM_OUT_SAME), EPI_NONE, e, s));
+        }
+        L.nt.kchunk = 2 * (int)ceil_div(N, 64);
         if (p.together) return launched((p.nt_slices ? launch_slicet_gated : launch_gemmt_gated)(L));
         // Apart: the input's gradient, then the weights' with the sums.
         GatedBwdLaunch first = L;
@@ -673,9 +792,13 @@ int gemm_gated_bwd_workspace(int in, int out, int M, int N, int K, size_t* requi
     const GatedBwdParts b = gated_bwd_parts(in, M, N, K, true, true);
     int64_t more = 0;
     const uint64_t any = (uint64_t)1 << 40;
-    if (in == IN_F32 && M > SKINNY_M && K > 0 && plan_gated_bwd(in, M, N, K, true, true, any).transposes) {
-        more = make_plan(in, 4, M, K, N, any, false).ws_bytes;
-        more = std::max(more, make_plan(in, 4, K, N, M, any, false).ws_bytes);
+    if (M > SKINNY_M && K > 0) {
+        // dA is split more readily where it is wanted alone.
+        for (int i = 0; i < 2; ++i) more = std::max(more, plan_gated_bwd(in, M, N, K, true, i == 0, any).ws_bytes);
+        if (in == IN_F32) {
+            more = std::max(more, make_plan(in, 4, M, K, N, any, false).ws_bytes);
+            more = std::max(more, make_plan(in, 4, K, N, M, any, false).ws_bytes);
+        }
     }
     if (required) *required = (size_t)b.required;
     if (best) *best = (size_t)(b.required + more);

@@ -369,6 +369,188 @@ __global__ __launch_bounds__(256) void gated_kernel(GatedArgs a, int kchunk, int
                                     n0 + (wave & 1) * (TBP / 2), lane, e, smem + wave * full_lds<T::NJ>);
 }
 
+// ------------------------------------------------------------------ small outputs
+//
+// As slicet.hip: a workgroup of four waves owns 32 MI rows of 32 columns of G and U, each wave
+// takes an equal run of 128-byte K blocks (64 k, fp32 32) into its own LDS stages and holds the
+// whole tile's sums for its k; the four are added in LDS in wave order.  A's rows lie in LDS
+// K-contiguous (gemm16's swizzle), the weights' k-rows as in memory, read through the transpose
+// read or, fp32, one value at a time (the two lane halves 4 k-rows apart meet in the same banks,
+// which costs less than the matrix instructions they feed).  512^3 with nothing kept: fp32 8.0 us
+// where split grid tiles take 20, bf16 4.2 where unsplit ones take 8.5.
+template <int MI>
+struct SliceG {
+    static constexpr int W = 4;
+    static constexpr int A_BLK = 128 * 32 * MI, W_BLK = 128 * 32;  // bytes of a block of A, of a weight
+    static constexpr int STAGE = A_BLK + 2 * W_BLK;
+    static constexpr int NA = A_BLK / 1024, NW = W_BLK / 1024;     // direct-to-LDS loads
+    static constexpr int RED = W * MI * 2 * 16 * 64 * 4;
+    static constexpr int LDS = 2 * W * STAGE > RED ? 2 * W * STAGE : RED;
+};
+
+template <int IN, int OUT, int MI>
+__global__ __launch_bounds__(256) void gated_slice_kernel(GatedArgs a, GatedEpi e) {
+    using T = SliceG<MI>;
+    constexpr int W = T::W, ES = IN == IN_F32 ? 4 : 2, BK = 128 / ES, RB = 32 * ES;
+    __shared__ __attribute__((aligned(1024))) char smem[T::LDS];
+    int tm, tn;
+    map_tile((int)blockIdx.x, a.tiles_m, a.tiles_n, tm, tn);
+    const int lane = (int)threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 5, li = lane & 31;
+    const int m0 = tm * 32 * MI, n0 = tn * 32;
+    const int rows_a = (a.M - m0) < 32 * MI ? (a.M - m0) : 32 * MI;
+    const int cols = (a.N - n0) < 32 ? (a.N - n0) : 32;
+    const int nblk = (a.K + BK - 1) / BK;
+    const int kb0 = (int)((int64_t)wave * nblk / W);
+    const int nb = (int)((int64_t)(wave + 1) * nblk / W) - kb0;
+
+    f32x16 acc[2][MI];  // G's blocks, U's
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[u][mi][r] = 0.0f;
+
+    char* const mine = smem + wave * 2 * T::STAGE;
+    int va[T::NA], vw[2][T::NW];
+#pragma unroll
+    for (int j = 0; j < T::NA; ++j) {
+        const int row = A16_RPB * j + lane / A16_CH;
+        va[j] = row * a.lda * ES + (((lane % A16_CH) ^ a16_phi(row)) << 4);
+    }
+#pragma unroll
+    for (int j = 0; j < T::NW; ++j) {
+        const int q = 1024 * j + 16 * lane;  // k-row q / RB, byte q % RB of the row
+        vw[0][j] = (q / RB) * a.ldbg * ES + q % RB;
+        vw[1][j] = (q / RB) * a.ldbu * ES + q % RB;
+    }
+    auto load = [&](int i, int s) {
+        const int k0 = (kb0 + i) * BK;
+        const int krem = (a.K - k0) < BK ? (a.K - k0) : BK;
+        char* st = mine + s * T::STAGE;
+        const auto ra = make_rsrc(a.A + ((int64_t)m0 * a.lda + k0) * ES, ((int64_t)(rows_a - 1) * a.lda + krem) * ES);
+#pragma unroll
+        for (int j = 0; j < T::NA; ++j) dma16(ra, lds_addr(st + 1024 * j), va[j]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int ld = u ? a.ldbu : a.ldbg;
+            const auto rw = make_rsrc((u ? a.Bu : a.Bg) + ((int64_t)k0 * ld + n0) * ES,
+                                      ((int64_t)(krem - 1) * ld + cols) * ES);
+#pragma unroll
+            for (int j = 0; j < T::NW; ++j) dma16(rw, lds_addr(st + T::A_BLK + u * T::W_BLK + 1024 * j), vw[u][j]);
+        }
+    };
+    // The transpose read's slot, as in slicet.hip.
+    const int grp = lane >> 4;
+    const int slot = ((8 * (grp >> 1) + ((lane >> 2) & 3)) * 32 + 16 * (grp & 1) + 4 * (lane & 3)) * 2;
+    run_steps<1>(nb, load, [&](int i, int s, auto newer) {
+        // This step's loads have landed; at most the newer step's are in flight.
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(decltype(newer)::value * (T::NA + 2 * T::NW), 15));
+        __builtin_amdgcn_sched_barrier(0);
+        const char* st = mine + s * T::STAGE;
+        u32x4 fa[MI][4], fw[2][4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) fa[mi][h] = *(const u32x4*)(st + a16_off(mi * 32 + li, 2 * h + g));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const char* w = st + T::A_BLK + u * T::W_BLK;
+                if constexpr (IN == IN_F32) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        fw[u][h][q] = *(const uint32_t*)(w + ((8 * h + 4 * g + q) * 32 + li) * 4);
+                } else {
+                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const u32x2 p = __builtin_bit_cast(
+                            u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (lds_s16x4_t*)(w + slot + (16 * h + 4 * t) * 64)));
+                        fw[u][h][2 * t] = p[0];
+                        fw[u][h][2 * t + 1] = p[1];
+                    }
+                }
+            }
+        }
+        // The reads are done before the slot's next loads are issued.
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+        __builtin_amdgcn_sched_barrier(0);
+        const int k0 = (kb0 + i) * BK;
+        if (k0 + BK > a.K) {  // A's row padding (k-rows past K read zeros)
+#pragma unroll
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi)
+                    fa[mi][h] = mask_bytes(fa[mi][h], (a.K - k0) * ES - 16 * (2 * h + g));
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int mi = 0; mi < MI; ++mi) {
+                    if constexpr (IN == IN_F32) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            acc[u][mi] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+                                as_float(fa[mi][h][q]), as_float(fw[u][h][q]), acc[u][mi], 0, 0, 0);
+                    } else if constexpr (IN == IN_BF16) {
+                        acc[u][mi] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            __builtin_bit_cast(bf16x8, fa[mi][h]), __builtin_bit_cast(bf16x8, fw[u][h]), acc[u][mi],
+                            0, 0, 0);
+                    } else {
+                        acc[u][mi] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                            __builtin_bit_cast(f16x8, fa[mi][h]), __builtin_bit_cast(f16x8, fw[u][h]), acc[u][mi],
+                            0, 0, 0);
+                    }
+                }
+    });
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __syncthreads();  // every wave is done with its stages: the sums reuse them
+
+    // Value idx = 16 mi + r of either product, wave w finishing idx in [w PER, w PER + PER).
+    float* const red = (float*)smem;
+    constexpr int NV = MI * 16, PER = NV / W;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) red[((wave * 2 + u) * NV + i) * 64 + lane] = acc[u][i / 16][i % 16];
+    __syncthreads();
+    float v[2][PER];
+    const int col = n0 + li;
+    const bool in_n = col < a.N;
+    const float bias[2] = {e.bias_g && in_n ? e.bias_g[col] : 0.0f, e.bias_u && in_n ? e.bias_u[col] : 0.0f};
+    int row[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int idx = wave * PER + q;
+        row[q] = m0 + (idx / 16) * 32 + 8 * ((idx % 16) >> 2) + 4 * g + (idx & 3);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float s = red[(u * NV + idx) * 64 + lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) s += red[((w * 2 + u) * NV + idx) * 64 + lane];
+            v[u][q] = s + bias[u];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        char* const to = u ? e.U : e.G;
+        if (!to) continue;
+#pragma unroll
+        for (int q = 0; q < PER; ++q)
+            if (in_n && row[q] < a.M) store_c<OUT>(to, (int64_t)row[q] * (u ? e.ldu : e.ldg) + col, v[u][q]);
+    }
+    apply_act<OUT>(v[0], e.act);
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+        if (in_n && row[q] < a.M) store_c<OUT>(a.C, (int64_t)row[q] * a.ldc + col, v[0][q] * v[1][q]);
+}
+
 // Sums the splits' partial products in ascending order and finishes: four columns of one row
 // per thread.  W[z]: M x 2 ldw, G's columns from 0 and U's from ldw.
 template <int OUT>
@@ -429,8 +611,18 @@ hipError_t go_gated(const GatedLaunch& L) {
     if (L.tbm == 128 && L.tbp == 64)
         fn = L.stages == 4 ? (const void*)gated_kernel<IN, OUT, 128, 64, 4>
                            : (const void*)gated_kernel<IN, OUT, 128, 64, 2>;
+    if (L.waves == 4 && L.tbp == 32)
+        fn = L.tbm == 32   ? (const void*)gated_slice_kernel<IN, OUT, 1>
+             : L.tbm == 64 ? (const void*)gated_slice_kernel<IN, OUT, 2>
+                           : nullptr;
     if (!fn) return hipErrorInvalidValue;
     GatedArgs a{L.A, L.Bg, L.Bu, L.C, L.M, L.N, L.K, L.lda, L.ldbg, L.ldbu, L.ldc, L.tiles_m, L.tiles_n};
+    if (L.waves > 0) {
+        if (L.splits != 1 || !L.C) return hipErrorInvalidValue;
+        GatedEpi e = L.e;
+        void* args[] = {&a, &e};
+        return hipLaunchKernel(fn, dim3((unsigned)(L.tiles_m * L.tiles_n)), dim3(256), args, 0, L.stream);
+    }
     int kchunk = L.kchunk;
     int64_t zs = L.zstride;
     GatedEpi e = L.e;

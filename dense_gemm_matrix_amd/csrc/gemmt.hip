@@ -91,11 +91,13 @@ struct Frag {
 };
 
 // A second pair of operands of the same sizes, whose product is added (the gradient of a gated
-// layer's input: dG Bg^T + dU Bu^T); X2 has X's row pitch.
+// layer's input: dG Bg^T + dU Bu^T); X2 has X's row pitch.  Of the steps of both, one pair's
+// after the other's, the loop takes `count` from `first` on.
 struct Second {
     const char* X2;
     const char* Y2;
     int ldy2;
+    int first, count;
 };
 
 // SEG: the K loop runs on over the second pair's k.
@@ -114,7 +116,10 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nk1 = (K + T::STEPK - 1) / T::STEPK;  // steps of one pair
-    const int nk = SEG ? 2 * nk1 : nk1;
+    const int nk = SEG ? two.count : nk1;
+    const int g0 = SEG ? two.first : 0;
+    // Whether step kt is the last of a pair (or of the only one).
+    auto last = [&](int kt) { return kt + g0 == nk1 - 1 || (SEG && kt + g0 == 2 * nk1 - 1); };
 
     // Global byte offset of the 16 bytes that belong in this lane's slot of load
     // block `blk` (1 KiB, filled lane-linearly) of an operand with `TB` rows: the
@@ -153,8 +158,8 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
     };
     auto desc = [&](int kt) {
         if constexpr (SEG) {
-            const bool q = kt >= nk1;
-            const int k = q ? kt - nk1 : kt;
+            const bool q = kt + g0 >= nk1;
+            const int k = kt >= nk ? 2 * nk1 : q ? kt + g0 - nk1 : kt + g0;  // past the run: past K
             return Desc{operand(q ? two.X2 : X, ldx, m0, rows_x, k),
                         operand(q ? two.Y2 : Y, q ? two.ldy2 : ldy, n0, rows_y, k), kt % S, q};
         }
@@ -299,7 +304,7 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
             for (int j = 0; j < T::LOADS; ++j) dma_one(d, j);
         }
         sync(FirstIn{});
-        if (ragged && nk1 == 1) { fix_tail(0); sync(FirstIn{}); }
+        if (ragged && last(0)) { fix_tail(0); sync(FirstIn{}); }
 #pragma unroll
         for (int o = 0; o < T::NREAD; ++o) {
             read_piece(0, 0, o);
@@ -318,7 +323,7 @@ __device__ __forceinline__ void mainloop_t(const char* __restrict__ X, const cha
                 if (i == BAR) {
                     d = desc(kt + S);
                     sync(NextIn{});
-                    if (ragged && (kt + 2 == nk || (SEG && kt + 2 == nk1))) { fix_tail(kt + 1); sync(NextIn{}); }
+                    if (ragged && kt + 1 < nk && last(kt + 1)) { fix_tail(kt + 1); sync(NextIn{}); }
                 }
                 mfma_one(i / T::NMFMA, i % T::NMFMA);
                 __builtin_amdgcn_sched_barrier(0);
@@ -418,15 +423,18 @@ __global__ __launch_bounds__(256) void gemmt_pair_kernel(GridArgs nt, GridArgs t
     else col_reduce(wg - n_nt - n_tn, r, (float*)smem);
 }
 
-// A gated layer's: dA = X Y^T + X2 Y2^T (nt), both weights' gradients (tn, and with Y2 and C2 in
-// place of Y and C), both biases' column sums.  Any of the products may have no tiles.
+// A gated layer's: dA = X Y^T + X2 Y2^T (nt, its steps in `splits` runs of `per` at most, whose
+// fp32 sums go to part + z zstride, as nt's C otherwise), both weights' gradients (tn, tn2), both
+// biases' column sums.  Any of the products may have no tiles.
 template <int IN, int TB>
-__global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second two, GridArgs tn, GridArgs tn2,
+__global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second two, int splits, int per,
+                                                          int64_t zstride, GridArgs tn, GridArgs tn2,
                                                           int first, ColReduceArgs r, ColReduceArgs r2) {
     constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
     constexpr int L1 = TileT<IN, LAY_NT, TB, TB, 2>::LDS, L2 = TileT<IN, LAY_TN, TB, TB, 2>::LDS;
     __shared__ __attribute__((aligned(1024))) char smem[L1 > L2 ? L1 : L2];
-    const int n_nt = nt.tiles_m * nt.tiles_n, n_tn = tn.tiles_m * tn.tiles_n;
+    const int tiles = nt.tiles_m * nt.tiles_n;
+    const int n_nt = tiles * splits, n_tn = tn.tiles_m * tn.tiles_n;
     const int n_all = n_nt + n_tn + tn2.tiles_m * tn2.tiles_n;
     int wg = (int)blockIdx.x;
     if (wg < n_all) {
@@ -435,7 +443,16 @@ __global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second tw
     }
     EpiArgs e{};
     if (wg < n_nt) {
-        grid_tile<IN, LAY_NT, OUT, TB, TB, EPI_FULL, 2, true>(nt, wg, e, smem, two);
+        const int z = wg / tiles;
+        const int steps = 2 * ((nt.K + TileT<IN, LAY_NT, TB, TB, 2>::STEPK - 1) / TileT<IN, LAY_NT, TB, TB, 2>::STEPK);
+        two.first = z * per;
+        two.count = steps - two.first < per ? steps - two.first : per;
+        if (splits > 1) {
+            nt.C += z * zstride;
+            grid_tile<IN, LAY_NT, OUT_F32, TB, TB, EPI_NONE, 2, true>(nt, wg - z * tiles, e, smem, two);
+        } else {
+            grid_tile<IN, LAY_NT, OUT, TB, TB, EPI_FULL, 2, true>(nt, wg, e, smem, two);
+        }
     } else if (wg < n_all) {
         const bool b = wg >= n_nt + n_tn;
         grid_tile<IN, LAY_TN, OUT, TB, TB, EPI_FULL, 2>(b ? tn2 : tn, wg - n_nt - (b ? n_tn : 0), e, smem);
@@ -467,13 +484,15 @@ hipError_t go_gated_t(const GatedBwdLaunch& L) {
     const void* fn = L.nt.tbm == 256 ? (const void*)gemmt_gated_kernel<IN, 256>
                                      : (const void*)gemmt_gated_kernel<IN, 128>;
     GridArgs a = grid_args(L.nt), b = grid_args(L.tn[0]), c = grid_args(L.tn[1]);
-    Second two{L.A2, L.B2, L.ldb2};
-    const int tiles = a.tiles_m * a.tiles_n, tns = b.tiles_m * b.tiles_n + c.tiles_m * c.tiles_n;
+    Second two{L.A2, L.B2, L.ldb2, 0, 0};
+    int splits = L.nt.splits, per = L.nt.kchunk;
+    int64_t zs = L.nt.c_zstride;
+    const int tiles = a.tiles_m * a.tiles_n * splits, tns = b.tiles_m * b.tiles_n + c.tiles_m * c.tiles_n;
     int first = L.tn_first ? tiles : 0;
     ColReduceArgs r = L.sums[0], r2 = L.sums[1];
     const int blocks = tiles + tns + (r.N > 0 ? col_reduce_blocks(r.N) : 0) + (r2.N > 0 ? col_reduce_blocks(r2.N) : 0);
     if (blocks == 0) return hipSuccess;
-    void* args[] = {&a, &two, &b, &c, &first, &r, &r2};
+    void* args[] = {&a, &two, &splits, &per, &zs, &b, &c, &first, &r, &r2};
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, L.nt.stream);
 }
 

@@ -564,10 +564,10 @@ constexpr int full_lds = 32 * full_pitch<NJ> * 4;
 // soon as this one's is used.  The strips themselves are a loop (only the
 // accumulators' copy to LDS is written out per strip), which keeps the code in
 // the instruction cache.
-// TR: the accumulators hold the transpose, row li and, in register r, column 8 (r / 4) +
-// 4 g + r % 4 of their block.
-template <int OUT, int MI, int NJ, bool TR = false>
-__device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], char* C, int M, int N,
+// TR: the accumulators are blocks of 16 x 16, twice as many each way, and hold the transpose:
+// row lane % 16 and, in register r, column 4 (lane / 16) + r of their block.
+template <int OUT, int MI, int NJ, bool TR = false, class Acc>
+__device__ __forceinline__ void store_tile_full(const Acc& acc, char* C, int M, int N,
                                                 int ldc, int row0, int col0, int lane,
                                                 const EpiArgs& e, char* lds) {
     if (row0 >= M || col0 >= N) return;  // this wave's part of the tile lies outside C
@@ -619,9 +619,9 @@ __device__ __forceinline__ void store_tile_full(const f32x16 (&acc)[MI][NJ], cha
                 if constexpr (TR) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        *(f32x4*)(buf + li * P + nj * 32 + 8 * q + 4 * g) =
-                            f32x4{acc[k][nj][4 * q], acc[k][nj][4 * q + 1], acc[k][nj][4 * q + 2],
-                                  acc[k][nj][4 * q + 3]};
+                        *(f32x4*)(buf + (16 * (q >> 1) + (lane & 15)) * P + nj * 32 +
+                                  16 * (q & 1) + 4 * (lane >> 4)) =
+                            acc[2 * k + (q >> 1)][2 * nj + (q & 1)];
                 } else {
 #pragma unroll
                     for (int r = 0; r < 16; ++r)

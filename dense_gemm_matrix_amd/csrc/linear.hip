@@ -32,7 +32,8 @@ Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uin
 // The transposed layouts' plan: the estimate's choice among the slice-K tiles
 // (slicet.hip; slicek16's constants, an 8-bit block being 128 k), the two grid
 // tiles and 1 to 16 splits, by the same terms and margin as the other plans.
-Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail, double* us_out, bool big) {
+static Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail,
+                   double* us_out = nullptr) {
     const int bk = t_step(in);
     int fm, fn, fs;
     if (forced_grid(fm, fn, fs) && fm == fn && (fm == 32 || fm == 64)) {
@@ -43,7 +44,7 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     }
     if (forced_grid(fm, fn, fs))
         for (const TileCand& t : TILES_T)
-            if (t.bm == fm && t.bn == fn && (big || t.bm < 256)) {
+            if (t.bm == fm && t.bn == fn) {
                 Plan p = plan_pieces(t, bk, M, N, K, fs, ws_avail);
                 p.layout = layout;
                 if (p.splits > 0) return p;
@@ -54,7 +55,6 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     const bool slice = slice_plan_t(M, N, std::min(K, nk * 64), best, best_us);
     best.kchunk = K;
     for (const TileCand& t : TILES_T) {
-        if (t.bm == 256 && !big) continue;
         if (slice) break;  // as for A[M x K] B[K x N]: unsplit small outputs are the slice-K kernel's
         const double us = estimate_us(in, es_out, M, N, t, 1, nk, 0);
         if (best_us < 0.0 || us < best_us) {
@@ -69,7 +69,6 @@ Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_ava
     best_us *= margin;
     for (const TileCand& t : TILES_T)
         for (int s = 2; s <= MAX_SPLITS && s <= nk; ++s) {
-            if (t.bm == 256 && !big) break;
             const Plan p = plan_pieces(t, bk, M, N, K, s, ws_avail);
             if (p.splits != s) continue;
             const double us = estimate_us(in, es_out, M, N, t, s, p.kchunk / bk, p.ldw);

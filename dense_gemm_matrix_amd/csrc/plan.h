@@ -76,10 +76,6 @@ Plan make_plan(int in, int es_out, int M, int N, int K, uint64_t ws_avail, bool 
 // Plan of one tile at `splits` K pieces of whole steps of bk (1: unsplit); splits = 0 if it
 // does not fit (linear.hip).
 Plan plan_pieces(const TileCand& t, int bk, int M, int N, int K, int splits, uint64_t ws_avail);
-// The plan of a product in a transposed layout, or of 8-bit operands, and its estimate
-// (linear.hip); big: whether its kernels have the 256 x 256 tile.
-Plan plan_t(int in, int layout, int es_out, int M, int N, int K, uint64_t ws_avail, double* us_out = nullptr,
-            bool big = true);
 // The plan of a product of at most SKINNY_M rows (linear.hip).
 Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail);
 

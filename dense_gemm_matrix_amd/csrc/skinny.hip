@@ -322,6 +322,7 @@ __global__ __launch_bounds__(64 * W) void gated_skinny_kernel(
     constexpr int AW = ES / 2;          // 16-byte pieces of A per lane and step
     // Steps per chunk; two chunks in registers, within 128 of them for 16 waves.
     constexpr int D = WD >= 2 ? 1 : 2;
+    static_assert(WD == 1 || WD == 2 || WD == 4, "a load per k-row");
     constexpr int NV = CPL * 4, PER = (NV + W - 1) / W;
     __shared__ float red[2 * W * NV * 64];
     {
@@ -640,12 +641,8 @@ hipError_t go_nt(const GemmLaunch& L, const Two& two = Two{}) {
 template <int IN, int OUT, bool PARTIAL>
 hipError_t go_gated(const GatedLaunch& L) {
     const void* fn = nullptr;
-    if constexpr (IN != IN_F32) {
-        if (L.tbp == 128 && L.waves == 8) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 8, 8>;
-    }
     if (L.tbp == 64 && L.waves == 8) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 4, 8>;
     if (L.tbp == 32 && L.waves == 16) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 2, 16>;
-    if (L.tbp == 32 && L.waves == 8) fn = (const void*)gated_skinny_kernel<IN, OUT, PARTIAL, 2, 8>;
     if (!fn) return hipErrorInvalidValue;
     const char* a = L.A;
     const char* bg = L.Bg;

@@ -39,7 +39,7 @@ def block_call(out=1, rows=128, M=8, N=8, K=8, A=PA, lda=64, B=PB, ldb=64, C=PC,
     (LARGE, dict(lda=1 << 23)), (LARGE, dict(sar=1 << 21)), (LARGE, dict(rows=1, sbr=1 << 21)),
     (ALIAS, dict(C=PA)), (ALIAS, dict(C=PB)), (ALIAS, dict(sa=PC)), (ALIAS, dict(sa=PC - 4 * 7, sar=1)),
     (ALIAS, dict(R=PC + 128)), (ALIAS, dict(R=PC, ldr=72)), (ALIAS, dict(bias=PC)),
-    (ALIAS, dict(M=64, N=64, K=16384, lda=16384, ldb=16384, ldc=64, sab=64, sbb=4, B=FAR, C=2 * FAR, ws=FAR,
+    (ALIAS, dict(M=256, N=256, K=65536, lda=65536, ldb=65536, ldc=256, sab=256, sbb=4, B=FAR, C=2 * FAR, ws=FAR,
                  ws_bytes=1 << 40)),
 ])
 def test_gemm_f8_block_refusals(want, kw):
@@ -129,12 +129,12 @@ def test_plans():
     assert dg.gemm_f8_block_plan("bf16", 16, 4096, 4096, 0)["tile_rows"] == 16
     big = dg.gemm_f8_block_plan("bf16", 4096, 4096, 4096, 0)
     assert big == {"tile_rows": 256, "tile_cols": 256, "splits": 1, "workspace_bytes": 0}
-    # fp32 sums, and a scale per row on both sides, have the small tile only
+    # fp32 sums have the small tile only
     assert dg.gemm_f8_block_plan("f32", 4096, 4096, 4096, 0)["tile_rows"] == 128
-    assert dg.gemm_f8_block_plan("bf16", 4096, 4096, 4096, 0, rows_b=1)["tile_rows"] == 128
-    deep = dg.gemm_f8_block_plan("bf16", 64, 64, 16384, 1 << 30)
-    assert deep["splits"] > 1 and deep["workspace_bytes"] == deep["splits"] * 64 * 64 * 4
-    assert dg.gemm_f8_block_plan("bf16", 64, 64, 16384, deep["workspace_bytes"] - 1)["splits"] < deep["splits"]
+    assert dg.gemm_f8_block_plan("bf16", 4096, 4096, 4096, 0, rows_b=1)["tile_rows"] == 256
+    deep = dg.gemm_f8_block_plan("bf16", 256, 256, 65536, 1 << 30)
+    assert deep["splits"] > 1 and deep["workspace_bytes"] == deep["splits"] * 256 * 256 * 4
+    assert dg.gemm_f8_block_plan("bf16", 256, 256, 65536, deep["workspace_bytes"] - 1)["splits"] < deep["splits"]
     with pytest.raises(dg.DgemmError):
         dg.gemm_f8_block_plan("bf16", 64, 64, 64, 0, rows_b=3)
     assert dg.layernorm_bwd_workspace(16384, 4096) == 2 * dg.rmsnorm_bwd_workspace(16384, 4096)

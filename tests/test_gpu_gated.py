@@ -89,7 +89,16 @@ def test_forward_grid_tiles(plan, fmt, tile, splits):
     run(fmt, "same", 40, 1030, 1000, "relu", seed=14, ws_bytes=ws)
 
 
-@pytest.mark.parametrize("cols", [32, 64, 128])
+@pytest.mark.parametrize("fmt", list(DT))
+@pytest.mark.parametrize("tile", [32, 64])
+def test_forward_slice_tiles(plan, fmt, tile):
+    plan(tile, tile)
+    for i, (M, N, K) in enumerate([(40, 70, 600), (65, 33, 1290), (17, 200, 130), (100, 129, 64), (33, 31, 30)]):
+        run(fmt, "same", M, N, K, ACTS[i % 5], seed=i)
+        run(fmt, "f32", M, N, K, ACTS[(i + 2) % 5], seed=i, bias=False, keep=False)
+
+
+@pytest.mark.parametrize("cols", [32, 64])
 @pytest.mark.parametrize("splits", [1, 3])
 @pytest.mark.parametrize("fmt", list(DT))
 def test_forward_few_row_strips(plan, cols, splits, fmt):
@@ -101,7 +110,7 @@ def test_forward_few_row_strips(plan, cols, splits, fmt):
 
 
 @pytest.mark.parametrize("fmt", list(DT))
-@pytest.mark.parametrize("shape", [(1, 2050, 4130), (16, 500, 4096), (40, 300, 8200), (128, 1000, 4104)],
+@pytest.mark.parametrize("shape", [(1, 2050, 4130), (16, 500, 4096), (40, 300, 8200)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_forward_deep(fmt, shape):
     """The planner's own splits."""
@@ -227,6 +236,16 @@ def test_backward_tiles(plan, fmt, tile):
     plan(tile, tile)
     for i, (M, N, K) in enumerate([(300, 270, 200), (130, 515, 328), (65, 31, 64), (200, 40, 300)]):
         run_bwd(fmt, "same", M, N, K, ACTS[i], seed=i)
+
+
+@pytest.mark.parametrize("fmt, tile", [("bf16", 256), ("bf16", 128), ("f16", 256), ("f16", 128)])
+@pytest.mark.parametrize("splits", [2, 3, 7])
+def test_backward_with_the_inputs_gradient_split(plan, fmt, tile, splits):
+    """Runs of its steps that end inside the first pair, at its end and inside the second."""
+    for i, (M, N, K) in enumerate([(300, 270, 200), (130, 512, 328), (65, 1000, 64), (40, 449, 300)]):
+        plan(tile, tile, splits)
+        run_bwd(fmt, "same", M, N, K, ACTS[i], seed=i)
+        run_bwd(fmt, "f32", M, N, K, ACTS[i], seed=i, want=("dA", "dBu", "dbias_g"))
 
 
 def test_backward_of_fp32_by_the_grid():
