@@ -348,6 +348,7 @@ struct NormBwdArgs {
     const float* mean;  // layer norm, whose partial sums are two rows of ldp each: dweight's, dbias'
 };
 int norm_bwd_grid(int M, int N);
+int layernorm_bwd_grid(int M, int N, int fmt);
 hipError_t launch_norm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream);
 hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream);
 

@@ -570,9 +570,10 @@ int layernorm_bwd(int in, int M, int N, const void* dY, int lddy, const void* S,
     if (check_vec(weight, 16) != DGEMM_OK || check_vec(mean, 4) != DGEMM_OK || check_vec(rstd, 4) != DGEMM_OK ||
         check_vec(dweight, 4) != DGEMM_OK || check_vec(dbias, 4) != DGEMM_OK || check_vec(workspace, 16) != DGEMM_OK)
         return DGEMM_ERR_MISALIGNED;
-    const int grid = norm_bwd_grid(M, N), ldp = (int)up(N, 4);
-    const int64_t need = sums ? (int64_t)grid * 2 * ldp * 4 : 0;
-    if ((uint64_t)need > workspace_bytes) return DGEMM_ERR_WORKSPACE;
+    const int grid = layernorm_bwd_grid(M, N, fmt), ldp = (int)up(N, 4);
+    size_t need = 0;
+    if (sums) layernorm_bwd_workspace(M, N, &need);
+    if (need > workspace_bytes) return DGEMM_ERR_WORKSPACE;
     // dX may be dY or dS itself (a row is read before it is written).
     const auto same = [&](const Mat& i) { return mdX.p == i.p && (mdX.ld == i.ld || M == 1); };
     const Mat none{nullptr, 0, 0, 0, 0};
@@ -597,7 +598,8 @@ int layernorm_bwd(int in, int M, int N, const void* dY, int lddy, const void* S,
 int layernorm_bwd_workspace(int M, int N, size_t* required) {
     if (M < 0 || N < 0) return DGEMM_ERR_INVALID_VALUE;
     if (N > NORM_BWD_MAX) return DGEMM_ERR_TOO_LARGE;
-    if (required) *required = (size_t)norm_bwd_grid(M, N) * 2 * (size_t)up(N, 4) * 4;
+    // The 16-bit types' count, the larger.
+    if (required) *required = (size_t)layernorm_bwd_grid(M, N, OUT_BF16) * 2 * (size_t)up(N, 4) * 4;
     return DGEMM_OK;
 }
 

@@ -215,8 +215,23 @@ hipError_t launch_layernorm(const RowArgs& a, int fmt, int rows, hipStream_t str
     return hipErrorInvalidValue;
 }
 
+// Workgroups of the backward pass.  Each writes two rows of partial sums, which are read once
+// more, so every CU has one workgroup before any has two, and a second only from four passes
+// each on (1000 x 8192 bf16 24.0 us with 256, 32.8 with 500; 1000 x 3000 f16 17.1 and 18.7;
+// 8192 x 512 bf16 11.5 with 512, 13.5 with 256, 13.2 with 1024).  In fp32 a row takes twice as long
+// and one per CU is enough (16384 x 4096 194 us with 256, 206 with 512; 4096 x 1024 15.6 and 17.2;
+// 8192 x 512 15.1 and 15.7), as it is from 8192 columns on, with 16 waves each.
+int layernorm_bwd_grid(int M, int N, int fmt) {
+    const int per = N <= 128 ? 16 : N <= 256 ? 8 : N <= 1024 ? 4 : 1;  // rows per pass of a workgroup
+    const int64_t rows = ((int64_t)M + per - 1) / per;
+    if (rows <= NUM_CU) return (int)rows;
+    const int most = fmt == OUT_F32 || N > 8192 ? NUM_CU : 2 * NUM_CU;
+    const int64_t four = rows / 4;
+    return four < NUM_CU ? NUM_CU : four < most ? (int)four : most;
+}
+
 hipError_t launch_layernorm_bwd(const NormBwdArgs& a, int fmt, hipStream_t stream) {
-    const int grid = norm_bwd_grid(a.M, a.N);
+    const int grid = layernorm_bwd_grid(a.M, a.N, fmt);
     if (fmt == OUT_F32) return bwd_by_size<OUT_F32>(a, grid, stream);
     if (fmt == OUT_BF16) return bwd_by_size<OUT_BF16>(a, grid, stream);
     if (fmt == OUT_F16) return bwd_by_size<OUT_F16>(a, grid, stream);
