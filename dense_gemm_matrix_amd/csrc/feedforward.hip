@@ -304,7 +304,7 @@ GatedBwdParts gated_bwd_parts(int in, int M, int N, int K, bool products, bool d
 // How the products of a gated layer's backward pass run: tile sizes of the input's gradient (nt)
 // and of the weights' (tn), 0 where it is not wanted; slices: slicet.hip's tiles, else gemmt.hip's.
 struct GatedBwdPlan {
-    int nt, tn;
+    int nt, tn;  // 0: none fits
     bool nt_slices, tn_slices, together, tn_first, transposes;  // transposes: fp32 by the grid kernels
     int splits = 1, per = 0, ldw = 0;  // of nt's K steps, for grid tiles: runs of `per`, partial sums of pitch ldw
     int64_t ws_bytes = 0;              // of those
@@ -347,7 +347,7 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
     };
     for (int a = 32; a <= 64; a += 32)
         for (int b = 32; b <= 64; b += 32) {
-            if ((!dA && a > 32) || (!dB && b > 32) || !allowed(a) || !allowed(b)) continue;
+            if (((!dA || !dB) && a != b) || !allowed(a) || !allowed(b)) continue;
             const int64_t ta = nt_tiles(a), tb = tn_tiles(b);
             if (ta + tb > (forced ? (int64_t)INT32_MAX / 2 : f == IN_F32 ? PAIR_TILES_32 : PAIR_TILES_16)) continue;
             const double wa = slice_tile_us(f, a, kn), wb = slice_tile_us(f, b, M);
@@ -718,12 +718,12 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
     }
     if (!want_a && !want_b) return launched(launch_col_reduce2(sg, su, s));
     const GatedBwdPlan p = plan_gated_bwd(in, M, N, K, want_a, want_b, (uint64_t)gemm_bytes);
+    if (!p.transposes && p.nt == 0) return DGEMM_ERR_TOO_LARGE;
     if (!p.transposes) {
         GatedBwdLaunch L{};
-        const int tt = p.tn ? p.tn : p.nt, ta = p.nt ? p.nt : p.tn;
-        L.nt = bwd_launch(in, LAY_NT, ta, p.nt_slices, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);
+        L.nt = bwd_launch(in, LAY_NT, p.nt, p.nt_slices, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);
         for (int i = 0; i < 2; ++i) {
-            L.tn[i] = bwd_launch(in, LAY_TN, tt, p.tn_slices, K, N, M, A, lda, dz[i], b.lddz, dW[i], lddw[i], s);
+            L.tn[i] = bwd_launch(in, LAY_TN, p.tn, p.tn_slices, K, N, M, A, lda, dz[i], b.lddz, dW[i], lddw[i], s);
             if (!want_b || !dW[i]) L.tn[i].tiles_m = 0;
         }
         if (!want_a) L.nt.tiles_m = 0;
