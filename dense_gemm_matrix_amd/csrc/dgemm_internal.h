@@ -230,7 +230,7 @@ hipError_t launch_gemmt_pair(const GemmLaunch& nt, const GemmLaunch& tn, bool tn
 // or N = 0: none.  One tile size for all (launch_gemmt_gated, 16-bit) or one for nt and one for
 // tn (launch_slicet_gated, 4 waves); the TN tiles first if tn_first.  launch_gemmt_gated: nt's K
 // steps (of 64, of both pairs) in nt.splits runs of nt.kchunk steps, their fp32 sums at nt.C + z
-// nt.c_zstride.
+// nt.c_zstride; tn's rows of the batch in tn[0].splits runs of tn[0].kchunk, as far apart at both C.
 struct GatedBwdLaunch {
     GemmLaunch nt, tn[2];
     const char* A2;
@@ -301,6 +301,16 @@ hipError_t launch_gated_reduce(const float* W, int splits, int64_t zstride, int 
 hipError_t launch_splitk_reduce(const float* W, int splits, int64_t zstride, int ldw, char* C,
                                 int ldc, int M, int N, int out, int epi, const EpiArgs& e,
                                 hipStream_t stream);
+
+// C [M x N] (16-bit) = the sum of `splits` fp32 matrices of pitch ldw, zstride floats apart; up to
+// three such sums in one launch.
+struct SplitSum {
+    const float* W;
+    int64_t zstride;
+    char* C;
+    int splits, ldw, ldc, M, N;
+};
+hipError_t launch_splitk_reduce3(const SplitSum* sums, int count, int out, hipStream_t stream);
 
 // ------------------------------------------- norms, quantizers, activations
 

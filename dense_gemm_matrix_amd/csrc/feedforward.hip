@@ -306,8 +306,9 @@ GatedBwdParts gated_bwd_parts(int in, int M, int N, int K, bool products, bool d
 struct GatedBwdPlan {
     int nt, tn;  // 0: none fits
     bool nt_slices, tn_slices, together, tn_first, transposes;  // transposes: fp32 by the grid kernels
-    int splits = 1, per = 0, ldw = 0;  // of nt's K steps, for grid tiles: runs of `per`, partial sums of pitch ldw
-    int64_t ws_bytes = 0;              // of those
+    // Grid tiles: nt's K steps in runs of `per`, with partial sums of pitch ldw; tn's rows likewise.
+    int splits = 1, per = 0, ldw = 0, tn_splits = 1, tn_per = 0, tn_ldw = 0;
+    int64_t ws_bytes = 0;  // of those
 };
 
 // M rows, K inputs, N gated outputs: nt has M x K outputs of 2 N terms, tn two of K x N of M.
@@ -358,6 +359,10 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
         for (const TileCand& t : TILES_T) {
             const int64_t ta = nt_tiles(t.bm), tb = tn_tiles(t.bm);
             if (!allowed(t.bm) || ta + tb > INT32_MAX / 2) continue;
+            // Up to 64 rows the weights' tiles are one step and their stores, which two workgroups
+            // per CU overlap and one does not (4 x 2228 x 3330 bf16 23.2 us with 128 x 128, 28.5 with
+            // 256 x 256, 16 x 4096 x 4096 38.3 and 45.0).
+            if (M <= 64 && t.bm == 256 && !forced) continue;
             bool tn_first;
             // Three products on 128 x 128 tiles were slower than the estimate for two.
             const double f128 = t.bm == 128 ? 1.15 : 1.0;
@@ -374,22 +379,53 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
             //   3000 x 6000 x 1500     285 /   260   (256 x 256, 2)
             // With these constants the plan chosen among 1 to 12 runs of either tile takes 3 % more
             // than the fastest on average over ten such layers, 14 % at most.
-            const int steps = kn / 64;
-            for (int s = 2; s <= MAX_SPLITS && s <= steps && dA; ++s) {
+            // The weights' sums are as long as the batch, and a small layer's are split the same way,
+            // alone or with dA's (us, dA's sums alone in runs / these too):
+            //   4096 x  578 x  488    42.1 / 38.7   (128 x 128, 3 runs)
+            //   4096 x 1226 x  276    51.1 / 42.8   (128 x 128, 3)
+            //  16384 x  512 x  128    66.8 / 38.6   (128 x 128, 16 of the batch)
+            const int steps = kn / 64, tn_steps = (int)ceil_div(M, 64);
+            auto runs = [&](int sa, int sb) {
                 GatedBwdPlan p{t.bm, t.bm, false, false, true, false, false};
-                p.per = (int)ceil_div(steps, s);
-                p.splits = (int)ceil_div(steps, p.per);
+                if (dA && sa > 1) {
+                    p.per = (int)ceil_div(steps, sa);
+                    p.splits = (int)ceil_div(steps, p.per);
+                }
+                if (dB && sb > 1) {
+                    p.tn_per = (int)ceil_div(tn_steps, sb) * 64;
+                    p.tn_splits = (int)ceil_div(M, p.tn_per);
+                }
                 p.ldw = (int)up(K, 4);
-                p.ws_bytes = (int64_t)p.splits * M * p.ldw * 4;
-                if (p.splits != s || (uint64_t)p.ws_bytes > ws || (int64_t)PANEL_ROWS * p.ldw * 4 >= DESC_LIMIT ||
-                    ta * s + tb > INT32_MAX / 2 || (forced && fs != s))
-                    continue;
-                const double sum_us = 4.0 + (2.0 * (double)p.ws_bytes + (double)M * K * 2) / 8e6;
-                const double split_us = pair_grid_us(t, in, ta * s, p.per * 64, tb, M, p.tn_first) * f128 + sum_us;
+                p.tn_ldw = (int)up(N, 4);
+                int64_t out = 0;
+                if (p.splits > 1) p.ws_bytes = (int64_t)p.splits * M * p.ldw * 4, out = (int64_t)M * K * 2;
+                if (p.tn_splits > 1) {
+                    p.ws_bytes += (int64_t)p.tn_splits * 2 * K * p.tn_ldw * 4;
+                    out += (int64_t)K * N * 4;
+                }
+                const int64_t na = ta * p.splits, nb = tb * p.tn_splits;
+                if (p.ws_bytes == 0 || (uint64_t)p.ws_bytes > ws || na + nb > INT32_MAX / 2 ||
+                    (int64_t)PANEL_ROWS * std::max(p.ldw, p.tn_ldw) * 4 >= DESC_LIMIT)
+                    return;
+                const double sum_us = 4.0 + (2.0 * (double)p.ws_bytes + (double)out) / 8e6;
+                const int la = p.splits > 1 ? p.per * 64 : kn, lb = p.tn_splits > 1 ? p.tn_per : M;
+                const double split_us = pair_grid_us(t, in, na, la, nb, lb, p.tn_first) * f128 + sum_us;
                 consider(forced ? 0.0 : split_us, p);
+            };
+            if (forced) {
+                if (fs > 1) runs(std::min(fs, steps), std::min(fs, tn_steps));
+                continue;
+            }
+            for (int s = 2; s <= MAX_SPLITS && s <= steps && dA; ++s) runs(s, 1);
+            // Both in runs of about the same length, while they fit the CUs at once.
+            for (int s = 2; s <= MAX_SPLITS && s <= tn_steps && dB; ++s) {
+                const int sa = (int)std::min<int64_t>(MAX_SPLITS, (int64_t)steps * s / std::max(tn_steps, 1));
+                if (s > 2 && tb * s > 2 * NUM_CU) break;
+                runs(sa, s);
+                if (sa > 1) runs(1, s);
             }
         }
-    if (f == IN_F32 && !forced) {
+    if (f == IN_F32 && !forced && M > SKINNY_M) {
         double us = 0.0;
         if (dA)
             us += 2 * (PAIR_GAP_US + (double)K * N * 8.0 / 4e6 + PAIR_GAP_US +
@@ -405,6 +441,21 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
             consider(a.us + b.us + PAIR_GAP_US, GatedBwdPlan{a.tile, b.tile, a.slices, b.slices, false, false, false});
     }
     return best;
+}
+
+// Whether a backward pass of few rows is left to the kernels for few rows (skinny.hip): one launch
+// for dA and one for each weight, against one launch, or two, by the plan above.  The whole pass in
+// us, M x N x K, by them / by the plan:
+//   bf16   1 x   64 x   64   12.9 /  6.4     fp32   1 x   64 x   64   14.6 /  8.3
+//         16 x 1000 x 1000   24.5 / 15.5           16 x 1000 x 1000   31.0 / 26.5
+//         10 x 5121 x   64   31.3 / 18.5           10 x 5121 x   64   43.5 / 58.3
+//          4 x 2228 x 3330   27.9 / 23.9            4 x 2228 x 3330   42.4 / 96.0
+//         16 x 4096 x 4096   54.7 / 40            16 x 4096 x 1024   60.0 / 55.5
+//          8 x 8192 x 4096   70.9 / 66.5            8 x 8192 x 4096    177 /  298
+// (16-bit, from the fourth row on, with dA's sums in runs.)
+bool few_rows(int in, int M, int N, int K, const GatedBwdPlan& p) {
+    const bool small = N <= 1024 && (int64_t)N * K <= 1 << 20;
+    return M <= SKINNY_M && (M == 0 || (!small && (in == IN_F32 || p.ws_bytes == 0)));
 }
 
 GemmLaunch bwd_launch(int in, int layout, int tile, bool slices, int M, int N, int K, const void* X, int ldx,
@@ -700,13 +751,15 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
     const int lddw[2] = {lddbg, lddbu};
     char* const dz[2] = {dG, dU};
 
-    if (M <= SKINNY_M) {
+    GatedBwdPlan p{};
+    if (want_a || want_b) p = plan_gated_bwd(in, M, N, K, want_a, want_b, (uint64_t)gemm_bytes);
+    if (few_rows(in, M, N, K, p)) {
         // Few rows: the weights once through registers for dA, rank-M updates for theirs.
         if (want_a) {
-            const Plan p = plan_skinny(in, LAY_NT, M, K, (int)std::min<int64_t>(2 * (int64_t)N, INT32_MAX), 0);
-            GemmLaunch L = bwd_launch(in, LAY_NT, p.bn, true, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);
+            const Plan q = plan_skinny(in, LAY_NT, M, K, (int)std::min<int64_t>(2 * (int64_t)N, INT32_MAX), 0);
+            GemmLaunch L = bwd_launch(in, LAY_NT, q.bn, true, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);
             L.tiles_m = 1;
-            L.slice_waves = p.waves;
+            L.slice_waves = q.waves;
             if (launch_skinny_two(L, dU, (const char*)Bu, ldbu) != hipSuccess) return DGEMM_ERR_LAUNCH;
         }
         for (int i = 0; i < 2; ++i)
@@ -717,7 +770,6 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
         return launched(launch_col_reduce2(sg, su, s));
     }
     if (!want_a && !want_b) return launched(launch_col_reduce2(sg, su, s));
-    const GatedBwdPlan p = plan_gated_bwd(in, M, N, K, want_a, want_b, (uint64_t)gemm_bytes);
     if (!p.transposes && p.nt == 0) return DGEMM_ERR_TOO_LARGE;
     if (!p.transposes) {
         GatedBwdLaunch L{};
@@ -733,19 +785,30 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
         L.tn_first = p.tn_first;
         L.sums[0] = sg;
         L.sums[1] = su;
-        if (p.splits > 1) {
-            L.nt.splits = p.splits;
-            L.nt.kchunk = p.per;
-            L.nt.C = w_gemm;
-            L.nt.ldc = p.ldw;
-            L.nt.c_zstride = (int64_t)M * p.ldw * 4;
-            if (launch_gemmt_gated(L) != hipSuccess) return DGEMM_ERR_LAUNCH;
-            EpiArgs e{};
-            e.alpha = 1.0f;
-            return launched(launch_splitk_reduce((const float*)w_gemm, p.splits, (int64_t)M * p.ldw, p.ldw, (char*)dA,
-                                                 ldda, M, K, out_format(in, DGEMM_OUT_SAME), EPI_NONE, e, s));
-        }
         L.nt.kchunk = 2 * (int)ceil_div(N, 64);
+        if (p.ws_bytes > 0) {
+            // Sums in runs go to the workspace, dA's first, and are added by one more launch.
+            SplitSum sums[3];
+            int count = 0;
+            char* at = w_gemm;
+            auto to_workspace = [&](GemmLaunch& g, int splits, int per, int ldw) {
+                sums[count++] = SplitSum{(const float*)at, (int64_t)g.M * ldw, g.C, splits, ldw, g.ldc, g.M, g.N};
+                g.splits = splits;
+                g.kchunk = per;
+                g.C = at;
+                g.ldc = ldw;
+                g.c_zstride = (int64_t)g.M * ldw * 4;
+                at += splits * g.c_zstride;
+            };
+            if (p.splits > 1) to_workspace(L.nt, p.splits, p.per, p.ldw);
+            for (GemmLaunch& g : L.tn) {
+                if (p.tn_splits <= 1) continue;
+                if (g.tiles_m) to_workspace(g, p.tn_splits, p.tn_per, p.tn_ldw);
+                else g.splits = p.tn_splits, g.kchunk = p.tn_per, g.c_zstride = (int64_t)K * p.tn_ldw * 4;
+            }
+            if (launch_gemmt_gated(L) != hipSuccess) return DGEMM_ERR_LAUNCH;
+            return launched(launch_splitk_reduce3(sums, count, out_format(in, DGEMM_OUT_SAME), s));
+        }
         if (p.together) return launched((p.nt_slices ? launch_slicet_gated : launch_gemmt_gated)(L));
         // Apart: the input's gradient, then the weights' with the sums.
         GatedBwdLaunch first = L;
@@ -794,10 +857,10 @@ int gemm_gated_bwd_workspace(int in, int out, int M, int N, int K, size_t* requi
     const GatedBwdParts b = gated_bwd_parts(in, M, N, K, true, true);
     int64_t more = 0;
     const uint64_t any = (uint64_t)1 << 40;
-    if (M > SKINNY_M && K > 0) {
-        // dA is split more readily where it is wanted alone.
-        for (int i = 0; i < 2; ++i) more = std::max(more, plan_gated_bwd(in, M, N, K, true, i == 0, any).ws_bytes);
-        if (in == IN_F32) {
+    if (M > 0 && K > 0) {
+        // One gradient alone is split more readily than both.
+        for (int i = 0; i < 3; ++i) more = std::max(more, plan_gated_bwd(in, M, N, K, i < 2, i != 1, any).ws_bytes);
+        if (in == IN_F32 && M > SKINNY_M) {
             more = std::max(more, make_plan(in, 4, M, K, N, any, false).ws_bytes);
             more = std::max(more, make_plan(in, 4, K, N, M, any, false).ws_bytes);
         }

@@ -423,19 +423,24 @@ __global__ __launch_bounds__(256) void gemmt_pair_kernel(GridArgs nt, GridArgs t
     else col_reduce(wg - n_nt - n_tn, r, (float*)smem);
 }
 
-// A gated layer's: dA = X Y^T + X2 Y2^T (nt, its steps in `splits` runs of `per` at most, whose
-// fp32 sums go to part + z zstride, as nt's C otherwise), both weights' gradients (tn, tn2), both
-// biases' column sums.  Any of the products may have no tiles.
+// Sums in `splits` runs of `per` steps at most (nt) or rows (tn), run z's in fp32 at C + z zstride.
+struct Runs {
+    int splits, per;
+    int64_t zstride;
+};
+
+// A gated layer's: dA = X Y^T + X2 Y2^T (nt, in ra's runs), both weights' gradients (tn, tn2, in
+// rb's), both biases' column sums.  Any of the products may have no tiles.
 template <int IN, int TB>
-__global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second two, int splits, int per,
-                                                          int64_t zstride, GridArgs tn, GridArgs tn2,
-                                                          int first, ColReduceArgs r, ColReduceArgs r2) {
+__global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second two, Runs ra, GridArgs tn,
+                                                          GridArgs tn2, Runs rb, int first,
+                                                          ColReduceArgs r, ColReduceArgs r2) {
     constexpr int OUT = IN == IN_BF16 ? OUT_BF16 : OUT_F16;
     constexpr int L1 = TileT<IN, LAY_NT, TB, TB, 2>::LDS, L2 = TileT<IN, LAY_TN, TB, TB, 2>::LDS;
     __shared__ __attribute__((aligned(1024))) char smem[L1 > L2 ? L1 : L2];
     const int tiles = nt.tiles_m * nt.tiles_n;
-    const int n_nt = tiles * splits, n_tn = tn.tiles_m * tn.tiles_n;
-    const int n_all = n_nt + n_tn + tn2.tiles_m * tn2.tiles_n;
+    const int n_nt = tiles * ra.splits, n_tn = tn.tiles_m * tn.tiles_n * rb.splits;
+    const int n_all = n_nt + n_tn + tn2.tiles_m * tn2.tiles_n * rb.splits;
     int wg = (int)blockIdx.x;
     if (wg < n_all) {
         wg += first;
@@ -445,17 +450,29 @@ __global__ __launch_bounds__(256) void gemmt_gated_kernel(GridArgs nt, Second tw
     if (wg < n_nt) {
         const int z = wg / tiles;
         const int steps = 2 * ((nt.K + TileT<IN, LAY_NT, TB, TB, 2>::STEPK - 1) / TileT<IN, LAY_NT, TB, TB, 2>::STEPK);
-        two.first = z * per;
-        two.count = steps - two.first < per ? steps - two.first : per;
-        if (splits > 1) {
-            nt.C += z * zstride;
+        two.first = z * ra.per;
+        two.count = steps - two.first < ra.per ? steps - two.first : ra.per;
+        if (ra.splits > 1) {
+            nt.C += z * ra.zstride;
             grid_tile<IN, LAY_NT, OUT_F32, TB, TB, EPI_NONE, 2, true>(nt, wg - z * tiles, e, smem, two);
         } else {
             grid_tile<IN, LAY_NT, OUT, TB, TB, EPI_FULL, 2, true>(nt, wg, e, smem, two);
         }
     } else if (wg < n_all) {
         const bool b = wg >= n_nt + n_tn;
-        grid_tile<IN, LAY_TN, OUT, TB, TB, EPI_FULL, 2>(b ? tn2 : tn, wg - n_nt - (b ? n_tn : 0), e, smem);
+        GridArgs a = b ? tn2 : tn;
+        wg -= n_nt + (b ? n_tn : 0);
+        if (rb.splits > 1) {
+            const int t = a.tiles_m * a.tiles_n, z = wg / t;
+            const int64_t at = (int64_t)z * rb.per;
+            a.X += at * a.ldx * TileT<IN, LAY_TN, TB, TB, 2>::ES;
+            a.Y += at * a.ldy * TileT<IN, LAY_TN, TB, TB, 2>::ES;
+            a.C += z * rb.zstride;
+            a.K = a.K - at < rb.per ? (int)(a.K - at) : rb.per;
+            grid_tile<IN, LAY_TN, OUT_F32, TB, TB, EPI_NONE, 2>(a, wg - z * t, e, smem);
+        } else {
+            grid_tile<IN, LAY_TN, OUT, TB, TB, EPI_FULL, 2>(a, wg, e, smem);
+        }
     } else {
         const int c = wg - n_all, n1 = r.N > 0 ? (r.N + 15) / 16 : 0;
         col_reduce(c < n1 ? c : c - n1, c < n1 ? r : r2, (float*)smem);
@@ -485,14 +502,14 @@ hipError_t go_gated_t(const GatedBwdLaunch& L) {
                                      : (const void*)gemmt_gated_kernel<IN, 128>;
     GridArgs a = grid_args(L.nt), b = grid_args(L.tn[0]), c = grid_args(L.tn[1]);
     Second two{L.A2, L.B2, L.ldb2, 0, 0};
-    int splits = L.nt.splits, per = L.nt.kchunk;
-    int64_t zs = L.nt.c_zstride;
-    const int tiles = a.tiles_m * a.tiles_n * splits, tns = b.tiles_m * b.tiles_n + c.tiles_m * c.tiles_n;
+    Runs ra{L.nt.splits, L.nt.kchunk, L.nt.c_zstride}, rb{L.tn[0].splits, L.tn[0].kchunk, L.tn[0].c_zstride};
+    const int tiles = a.tiles_m * a.tiles_n * ra.splits;
+    const int tns = (b.tiles_m * b.tiles_n + c.tiles_m * c.tiles_n) * rb.splits;
     int first = L.tn_first ? tiles : 0;
     ColReduceArgs r = L.sums[0], r2 = L.sums[1];
     const int blocks = tiles + tns + (r.N > 0 ? col_reduce_blocks(r.N) : 0) + (r2.N > 0 ? col_reduce_blocks(r2.N) : 0);
     if (blocks == 0) return hipSuccess;
-    void* args[] = {&a, &two, &splits, &per, &zs, &b, &c, &first, &r, &r2};
+    void* args[] = {&a, &two, &ra, &b, &c, &rb, &first, &r, &r2};
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(256), args, 0, L.nt.stream);
 }
 

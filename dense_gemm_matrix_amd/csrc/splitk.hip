@@ -116,6 +116,37 @@ __global__ __launch_bounds__(RED_THREADS) void splitk_reduce_kernel(
     }
 }
 
+// The plain sums of up to three products in one launch.
+struct Reduce3 {
+    SplitSum s[3];
+    int64_t end[3];  // the blocks up to each product's last
+};
+
+template <int OUT>
+__global__ __launch_bounds__(RED_THREADS) void splitk_reduce3_kernel(Reduce3 r) {
+    const int64_t b = blockIdx.x;
+    const int i = b < r.end[0] ? 0 : b < r.end[1] ? 1 : 2;
+    const SplitSum a = i == 0 ? r.s[0] : i == 1 ? r.s[1] : r.s[2];
+    const int64_t t = (b - (i == 0 ? 0 : i == 1 ? r.end[0] : r.end[1])) * RED_THREADS + threadIdx.x;
+    const int nq = a.ldw >> 2;
+    if (t >= (int64_t)a.M * nq) return;
+    const int row = (int)(t / nq);
+    const int col0 = (int)(t - (int64_t)row * nq) * 4;
+    if (col0 >= a.N) return;
+    const float* p = a.W + (int64_t)row * a.ldw + col0;
+    f32x4 s = *(const f32x4*)p;
+#pragma unroll 4
+    for (int z = 1; z < a.splits; ++z) s += *(const f32x4*)(p + z * a.zstride);
+    const int64_t base = (int64_t)row * a.ldc + col0;
+    const float v[4] = {s[0], s[1], s[2], s[3]};
+    if (col0 + 4 <= a.N) {
+        store4<OUT>(a.C, base, v);
+    } else {
+        for (int j = 0; j < 4; ++j)
+            if (col0 + j < a.N) store_c<OUT>(a.C, base + j, v[j]);
+    }
+}
+
 template <int OUT, int EPI>
 hipError_t go(const float* W, int splits, int64_t zstride, int ldw, char* C, int ldc, int M, int N,
               const EpiArgs& e, hipStream_t stream) {
@@ -147,6 +178,26 @@ hipError_t launch_splitk_reduce(const float* W, int splits, int64_t zstride, int
     if (out == OUT_BF16) return by_epi<OUT_BF16>(epi, W, splits, zstride, ldw, C, ldc, M, N, e, stream);
     if (out == OUT_F16) return by_epi<OUT_F16>(epi, W, splits, zstride, ldw, C, ldc, M, N, e, stream);
     return hipErrorInvalidValue;
+}
+
+hipError_t launch_splitk_reduce3(const SplitSum* sums, int count, int out, hipStream_t stream) {
+    if (count < 1 || count > 3 || (out != OUT_BF16 && out != OUT_F16)) return hipErrorInvalidValue;
+    Reduce3 r{};
+    int64_t blocks = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (i < count) {
+            if (sums[i].ldw % 4 != 0 || sums[i].splits < 1) return hipErrorInvalidValue;
+            r.s[i] = sums[i];
+            blocks += ((int64_t)sums[i].M * (sums[i].ldw / 4) + RED_THREADS - 1) / RED_THREADS;
+        }
+        r.end[i] = blocks;
+    }
+    if (blocks <= 0) return hipSuccess;
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    void* args[] = {&r};
+    return hipLaunchKernel(out == OUT_BF16 ? (const void*)splitk_reduce3_kernel<OUT_BF16>
+                                           : (const void*)splitk_reduce3_kernel<OUT_F16>,
+                           dim3((unsigned)blocks), dim3(RED_THREADS), args, 0, stream);
 }
 
 }  // namespace dgemm

@@ -240,12 +240,35 @@ def test_backward_tiles(plan, fmt, tile):
 
 @pytest.mark.parametrize("fmt, tile", [("bf16", 256), ("bf16", 128), ("f16", 256), ("f16", 128)])
 @pytest.mark.parametrize("splits", [2, 3, 7])
-def test_backward_with_the_inputs_gradient_split(plan, fmt, tile, splits):
-    """Runs of its steps that end inside the first pair, at its end and inside the second."""
+def test_backward_in_runs(plan, fmt, tile, splits):
+    """Runs of dA's steps that end inside the first pair, at its end and inside the second, and of the batch."""
     for i, (M, N, K) in enumerate([(300, 270, 200), (130, 512, 328), (65, 1000, 64), (40, 449, 300)]):
         plan(tile, tile, splits)
         run_bwd(fmt, "same", M, N, K, ACTS[i], seed=i)
         run_bwd(fmt, "f32", M, N, K, ACTS[i], seed=i, want=("dA", "dBu", "dbias_g"))
+
+
+@pytest.mark.parametrize("fmt", list(DT))
+@pytest.mark.parametrize("shape", [(1, 1100, 40), (16, 1030, 72), (7, 2050, 33), (13, 1025, 1200), (3, 700, 1600)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_backward_of_few_rows(fmt, shape):
+    """By the kernels for few rows, with the least workspace, and in runs, with more."""
+    for least in (True, False):
+        run_bwd(fmt, "same", *shape, "silu", seed=5, least=least)
+        for want in (("dA",), ("dBg", "dBu"), ("dBu", "dbias_g")):
+            run_bwd(fmt, "same", *shape, "gelu", seed=6, least=least, want=want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(9000, 520, 136), (4096, 577, 323), (543, 5065, 103)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_backward_of_long_batches(fmt, shape):
+    """The planner's runs of the batch."""
+    req, best = dg.gemm_gated_bwd_workspace(fmt, *shape)
+    assert best > req
+    run_bwd(fmt, "same", *shape, "silu", seed=7)
+    run_bwd(fmt, "f32", *shape, "gelu_tanh", seed=8, want=("dBg",))
+    run_bwd(fmt, "same", *shape, "none", seed=9, want=("dBu", "dA"))
 
 
 def test_backward_of_fp32_by_the_grid():
