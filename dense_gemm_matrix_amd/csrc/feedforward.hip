@@ -158,7 +158,7 @@ GatedPlan gated_pieces(int bm, int bn, int bk, int M, int N, int K, int splits, 
 
 // At most SKINNY_M rows: as plan_skinny's strips of B stored along the output, of both weights,
 // but never of 128 columns (two weights' loads are as wide as one's twice: 1 x 14336 x 4096 bf16, weights
-// from the last-level cache, 32 / 64 / 128 columns 43.8 / 37.4 / 38.4 us), nor split from a fixed K on
+// from the last-level cache, 32 / 64 / 128 columns 43.8 / 37.4 / 38.4 us), and split from the same K on
 // in fp32.
 GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
     auto strips = [&](int cols, int waves, int splits) {
@@ -208,14 +208,18 @@ GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
     // workspace): bf16 512^3 4.2 / 5.3 / 8.5, 64 x 2048 x 1024 5.0 / 6.5 / 11.4, 512 x 1024 x 512
     // 7.1 / 5.4 / 8.6, 1024^3 20.9 / 12.5 / 12.0, 300 x 600 x 8192 35.0 / 37.5 / 22.9; fp32 512^3
     // 8.0 / 12.5 / 20.1, 64 x 4096 x 4096 42.9 / 69.8 / 69.4, 1024^3 47.5 / 41.9 / 46.4, 256 x 256 x
-    // 4096 38.7 / 70.2 / 28.0.
+    // 4096 38.7 / 70.2 / 28.0.  Slices draw on HBM unevenly, 4.6 TB/s of the weights at most (bf16,
+    // slices / grid: 64 x 14336 x 4096 50.7 / 41.8, 32 x 11008 x 4096 40.1 / 33.3), and a K split pays
+    // SPLIT_US for its second launch beside the estimate (261 x 76 x 2325 7.2 / 12.1 in 8 pieces).
+    constexpr double SPLIT_US = 2.0;
+    const double weights_us = 2.0 * (double)K * N * in_esize(in) / 4.6e6;
     const double nb = (double)ceil_div(nk, 4);
     for (int t = 32; t <= 64; t += 32) {
         const int64_t n = ceil_div(M, t) * ceil_div(N, 32);
         if (n > INT32_MAX) continue;
         const double round = in == IN_F32 ? (t == 32 ? 1.8 + 1.27 * nb : 3.6 + 2.05 * nb)
                                           : (t == 32 ? 1.6 + 0.75 * nb : 2.6 + 0.9 * nb);
-        const double us = 1.1 + (double)ceil_div(n, NUM_CU) * round;
+        const double us = std::max(1.1 + (double)ceil_div(n, NUM_CU) * round, weights_us);
         if (best_us < 0.0 || us < best_us) {
             best_us = us;
             best = slices(t);
@@ -228,7 +232,7 @@ GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
             const GatedPlan p = gated_pieces(t.bm, t.bn / 2, bk, M, N, K, s, ws);
             if (p.splits != s) continue;
             double us = estimate_us(in, es_out, M, N2, t, s, s == 1 ? nk : p.kchunk / bk, s == 1 ? 0 : 2 * p.ldw);
-            us = us / (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US;
+            us = us / (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US + (s > 1 ? SPLIT_US : 0.0);
             if (us < best_us) {
                 best_us = us;
                 best = p;
