@@ -17,8 +17,8 @@
 // register file, so a wave cannot hold 256 running sums as gemmt.hip's do: a wave owns
 // 128 x 64 outputs (256 x 256 tile, 8 waves, two to a SIMD) or 64 x 64 (128 x 128 tile, 4
 // waves, two workgroups to a CU), and one wave's multiply-adds run beside the other's
-// matrix instructions.  4096^3, bf16 C: 64-69 us with a scale per 128 x 128 (2.0 PFLOP/s; gemm_f8 with
-// a scale per row 58-61), 73.7 with one per row and block.
+// matrix instructions.  4096^3, bf16 C: 63-66 us with a scale per 128 x 128 (2.1 PFLOP/s; gemm_f8 with
+// a scale per row 58-61), 72 with one per row and block.
 //
 // The scales of a step come with its operands, by 4-byte direct-to-LDS loads (one per
 // wave and step), and are read back one per lane.  Operands, LDS layout, tile map and
@@ -268,12 +268,12 @@ struct GridTile {
 // products in flight; with a scale per row of B (NB) a lane needs four of them per 16 rows.  Two
 // waves to a SIMD, at 247 of their 256 registers on the large tile.
 //
-// Against 32 x 32 x 64 instructions, two to a block (4096^3: 69 us either way with a scale per 128 x
-// 128; with a scale per row, whose 32 factors per 64 rows leave no registers for the large tile,
-// 95 on the small one), it takes 73.7 us there, and the small tile 76 and 87 where it took 85 and 95.
+// Against 32 x 32 x 64 instructions, two to a block (4096^3: 69 us with a scale per 128 x 128; with
+// a scale per row, whose 32 factors per 64 rows leave no registers for the large tile, 95 on the
+// small one), it takes 65 and 72 us, and the small tile 83 and 85 where it took 85 and 95.
 //
 // IN_F8W (fp32 outputs): four 16 x 16 x 32 bf16 instructions a block, on fragments widened once per
-// step (B's) and per 16 rows (A's).  4096^3 127 us, with a scale per row of B 140 (32 x 32
+// step (B's) and per 16 rows (A's).  4096^3 122 us, with a scale per row of B 135 (32 x 32
 // instructions whose fragments were widened per use 128 and 255).
 template <int IN, int OUT, int TBM, int TBN, int WM, int WN, bool NB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a, int kchunk, int64_t c_zstride,
@@ -349,12 +349,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
             }
         }
     };
-    // Chunks 2 g and 2 g + 1 of row c of 16; the swizzle has a period of 32 rows.
+    // Chunks g and g + 4 of row c of 16 (both operands' k in the same order, which is any); the
+    // swizzle has a period of 32 rows.  An LDS read of 16 bytes serves lanes 0-3, 12-15, 20-23, 24-27
+    // at once, then the others likewise, from a 256-byte window: with chunks 2 g and 2 g + 1 the
+    // two lane groups of such a set met in the same banks.
     int off[2][2];
 #pragma unroll
     for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) off[o][h] = a16_off(16 * o + c, 2 * g + h);
+        for (int h = 0; h < 2; ++h) off[o][h] = a16_off(16 * o + c, g + 4 * h);
     struct Half { u32x4 w[2]; };
     auto read = [&](const char* st, int strip, int h, Half& f) {  // of the wave's 16-row strips
         f.w[h] = *(const u32x4*)(st + (strip >> 1) * 4096 + off[strip & 1][h]);

@@ -13,8 +13,9 @@
 // take the maxima of columns, to write rows of the transpose in whole lines.  A workgroup
 // of 256 threads holds it in registers, eight consecutive rows of eight columns per
 // thread, so that a thread's values of one column are eight neighbouring bytes of the
-// transpose: it goes through LDS as 8-byte pieces (rows of 136 bytes, so that the columns
-// a wave writes at once are spread over the banks).
+// transpose: it goes through LDS as 8-byte pieces, in rows of 128 bytes whose pieces trade
+// places by the column's eighth, so that the 16 columns that are written at once, eight apart,
+// and the 16 pieces of a row that are read at once each meet all banks.
 
 #include "rows.h"
 
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(QuantBlockArgs a, uint3
 template <int FMT, bool TR, int ROWS>
 __global__ __launch_bounds__(256) void quant_tile_kernel(QuantBlockArgs a, int tiles_n) {
     static_assert(TR || ROWS == F8_BLOCK, "rows as they lie are quant_rows_kernel's");
-    constexpr int P = F8_BLOCK + 8;
+    constexpr int P = F8_BLOCK;
     __shared__ uint32_t wmax[4][ROWS == 1 ? F8_BLOCK : 1];
     __shared__ __attribute__((aligned(16))) float cdiv[3][ROWS == 1 ? F8_BLOCK : 4];
     __shared__ __attribute__((aligned(16))) char tile[TR ? F8_BLOCK * P : 8];
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantBlockArgs a, int t
                 x[i].get(w);
                 v[i] = w[j];
             }
-            *(u32x2*)(tile + (c8 + j) * P + r8) = quantize8<FMT>(v, div[ROWS == 1 ? j : 0]);
+            *(u32x2*)(tile + (c8 + j) * P + (r8 ^ c8)) = quantize8<FMT>(v, div[ROWS == 1 ? j : 0]);
         }
         __syncthreads();
         // Row n0 + r of Q: bytes m0 + 8 (t % 16) .., 16 rows at a time.
@@ -188,7 +189,7 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(QuantBlockArgs a, int t
         for (int i = 0; i < 8; ++i) {
             const int r = i * 16 + (t >> 4), c = (t & 15) * 8;
             if (n0 + r < a.N && m0 + c < a.M)
-                put8(a.Q + (int64_t)(n0 + r) * a.ldq + m0 + c, *(const u32x2*)(tile + r * P + c), a.M - (m0 + c));
+                put8(a.Q + (int64_t)(n0 + r) * a.ldq + m0 + c, *(const u32x2*)(tile + r * P + (c ^ (r & ~7))), a.M - (m0 + c));
         }
     }
 }
