@@ -147,7 +147,8 @@ typedef enum {
 } dgemm_in;
 
 /* Activations.  gemm_ex takes the first two; gemm_act, gemm_act_bwd and gemm_f8
-   take all, as do gemm_f8_block, gemm_gated and gemm_gated_bwd.  Phi is the normal distribution's integral. */
+   take all, as do gemm_f8_block, gemm_gated and gemm_gated_bwd.  Phi is the normal
+   distribution's integral. */
 typedef enum {
     DGEMM_ACT_NONE = 0,
     DGEMM_ACT_RELU = 1,       /* x < 0 -> 0; NaN passes through                              */
@@ -640,11 +641,13 @@ typedef enum {
  * gemm_act, gemm_act_bwd and gemm_f8 follow DGEMM_PLAN_GRID too: gemm_act the
  * tiles above and, for at most 16 rows, 16 x 32, 16 x 64 and (16-bit inputs)
  * 16 x 128; the other two's 16-bit and 8-bit products 256 x 256, 128 x 128 and
- * the slice-K tiles (more than 16 rows).  gemm_f8_block follows it as gemm_f8 does (256 x 256 for
- * 16-bit C only, its slice-K tiles with 8 and 4 waves whatever `splits`); gemm_gated takes 256 x 256 (16-bit inputs), 128 x 128 and 64 x 64
- * (its columns of G and U counted together; 64 x 64 is a slice-K tile), 32 x 32 (32 columns of each)
- * and the 16-row strips of 32 and 64 columns, gemm_gated_bwd 256 x 256, 128 x 128 (16-bit; `splits` runs of dA's K
- * steps) and the slice-K tiles.
+ * the slice-K tiles (more than 16 rows).  gemm_f8_block follows it as gemm_f8
+ * does (256 x 256 for 16-bit C only, its slice-K tiles with 8 and 4 waves
+ * whatever `splits`); gemm_gated takes 256 x 256 (16-bit inputs), 128 x 128 and
+ * 64 x 64 (its columns of G and U counted together; 64 x 64 is a slice-K tile),
+ * 32 x 32 (32 columns of each) and the 16-row strips of 32 and 64 columns;
+ * gemm_gated_bwd 256 x 256 and 128 x 128 (16-bit inputs; dA's K steps and the
+ * weights' rows in `splits` runs) and the slice-K tiles.
  * DGEMM_PLAN_AUTO clears the override.  Not synchronised with calls running
  * on other host threads.  Returns DGEMM_OK, or DGEMM_ERR_INVALID_VALUE for a
  * bad kind or splits < 1 with DGEMM_PLAN_GRID.
