@@ -406,10 +406,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
             if constexpr (NB) sb[nj] = *(const f32x4*)(p + nj * 16 + 4 * g);
             else if (nj == 0) sb[0][0] = p[0];
         };
-        auto read_sa = [&](int kt) {
-            const float* p = (const float*)(smS + (kt % S) * T::S_STAGE) + wm * (TBM / WM) + c;
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) sa[mi] = p[mi * 16];
+        auto read_sa = [&](int kt, int mi) {
+            sa[mi] = ((const float*)(smS + (kt % S) * T::S_STAGE))[TBM / WM * wm + mi * 16 + c];
         };
 #pragma unroll
         for (int h = 0; h < 2; ++h) read_a(0, 0, h, fa[0]);
@@ -419,7 +417,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
             for (int h = 0; h < 2; ++h) read_b(0, nj, h, fb[nj]);
             read_sb(0, nj);
         }
-        read_sa(0);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) read_sa(0, mi);
         f32x4 part[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
         float a_prev = 0.0f;
         f32x4 b_prev = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -438,10 +437,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
         };
         for (int kt = 0; kt < nk; ++kt) {
             Desc d;
-            if constexpr (!NB) {
-#pragma unroll
-                for (int mi = 0; mi < MI; ++mi) sa[mi] *= sb[0][0];
-            }
 #pragma unroll
             for (int i = 0; i < NBLK; ++i) {
                 const int mi = i / NJ, nj = i % NJ;
@@ -450,6 +445,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
                     sync(AllIn{});
                     if (ragged && kt + 2 == nk) { fix_tail(); sync(AllIn{}); }
                 }
+                if (!NB && nj == 0) sa[mi] *= sb[0][0];
                 const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
                 if constexpr (WIDE) {
                     if (mi == 0) widen(fb[nj], wb[nj]);
@@ -476,10 +472,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
 #pragma unroll
                     for (int h = 0; h < 2; ++h) read_b(kt + 1, nj, h, fb[nj]);
                     read_sb(kt + 1, nj);
+                    // A's scales of the strips that are done, so that the next step's first factor, a
+                    // product with B's, does not wait for them (2 % of 16384 x 4096 x 4096; with a scale
+                    // per row of B the factors are formed later, and the step ends with these reads).
+                    if (!NB && nj == 1)
+#pragma unroll
+                        for (int m = 0; m + 1 < MI; ++m) read_sa(kt + 1, m);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
-            read_sa(kt + 1);
+#pragma unroll
+            for (int m = NB ? 0 : MI - 1; m < MI; ++m) read_sa(kt + 1, m);
         }
         add(NBLK - 1, a_prev, b_prev);
     }
