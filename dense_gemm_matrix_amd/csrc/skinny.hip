@@ -470,7 +470,8 @@ __global__ __launch_bounds__(64 * W) void skinny_block_kernel(
     const int nstep = (K + F8_BLOCK - 1) / F8_BLOCK;
     Strip<OUT, EPI_FULL, 1, W, true> strip;
     strip.prefetch(M, N, n0, wave, lane, epi);
-    constexpr int D = 2;           // steps per chunk; two chunks in registers
+    // Steps per chunk; two chunks in registers, of which 16 waves have 128 each.
+    constexpr int D = NB && W == 16 ? 1 : 2;
     constexpr int NS = NB ? 4 : 1;  // of B's scales per lane
     u32x4 a[2 * D][2], b[2 * D][2];
     float sa[2 * D], sb[2 * D][NS];
