@@ -11,7 +11,7 @@
 // As the root-mean-square norm's (norm.hip): each workgroup walks rows blockIdx, blockIdx
 // + grid, ..., the next row's loads in flight over this one's reduction, whose two sums
 // share one barrier; a thread's columns are the same in every row, so dw and db are running
-// fp32 sums in registers, written once per workgroup and added over workgroups in a fixed
+// fp32 sums in registers (from 8193 columns on in LDS), written once per workgroup and added over workgroups in a fixed
 // order by one more launch for both.
 
 #include "rows.h"
@@ -59,10 +59,30 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
     const int t = pl.t;
     const int64_t step = (int64_t)gridDim.x * P::RPW;
     auto col = [&](int i) { return (i * T + t) * 8; };
-    // 1024 threads have 128 registers each: no room for the next row's loads, nor
-    // to keep the weights over the rows.
-    constexpr bool PRE = T < 1024;
+    // 1024 threads have 128 registers each: no room for the next row's loads, nor to keep the
+    // weights over the rows, and the running sums are in LDS, a thread's own in its own words (4000 x
+    // 16384 bf16 130 us, fp32 218; with the sums in registers, 30 of them in scratch, 197 and 275).
+    constexpr bool PRE = T < 1024, IN_LDS = T == 1024;
+    __shared__ f32x4 lsum[IN_LDS ? 4 * NV : 1][IN_LDS ? T : 1];  // dw's halves of eight columns, then db's
     float w[PRE ? NV : 1][8], dw[NV][8], db[NV][8];
+    auto to_lds = [&](int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            lsum[2 * i + h][t] = f32x4{dw[i][4 * h], dw[i][4 * h + 1], dw[i][4 * h + 2], dw[i][4 * h + 3]};
+            lsum[2 * (NV + i) + h][t] = f32x4{db[i][4 * h], db[i][4 * h + 1], db[i][4 * h + 2], db[i][4 * h + 3]};
+        }
+    };
+    auto from_lds = [&](int i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f32x4 x = lsum[2 * i + h][t], y = lsum[2 * (NV + i) + h][t];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                dw[i][4 * h + j] = x[j];
+                db[i][4 * h + j] = y[j];
+            }
+        }
+    };
     const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
     auto load_w = [&](int i, float (&to)[8]) {
         Row8<OUT_F32> w8;
@@ -74,6 +94,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
         if constexpr (PRE) load_w(i, w[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
+        if (IN_LDS) to_lds(i);
     }
     Row8<FMT> y[NV], s[NV], d[NV];
     float next_rstd = 0.0f, next_mean = 0.0f;
@@ -116,6 +137,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
             float wt[8];
             if constexpr (!PRE) load_w(i, wt);
             const float(&wi)[8] = PRE ? w[PRE ? i : 0] : wt;
+            if (IN_LDS) from_lds(i);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float xh = (x[j] - mean) * rstd, gj = dy[j] * wi[j];
@@ -124,6 +146,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
                 dw[i][j] += dy[j] * xh;
                 db[i][j] += dy[j];
             }
+            if (IN_LDS) to_lds(i);
         }
         if (PRE && row0 + step < a.M) load(row0 + step);
         // The reduction's words alternate between rows, so one barrier per row
@@ -152,6 +175,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
         }
     }
     if (!a.part) return;
+    if (IN_LDS)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) from_lds(i);
     // dw's partial sums, then db's, a row of ldp each per workgroup.
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
