@@ -6,19 +6,20 @@
 //
 // A: M x K, B: N x K, both K-contiguous.  A K step of the matrix kernels is 128 bytes of
 // every row, which is one block: a step's matrix instructions start from zero, and their
-// sums are added to the running ones scaled, in fp32: one multiply-add per output and block,
-// half of the vector unit's time at the matrix units' full rate.  To have few factors per lane, the
+// sums are added to the running ones scaled, in fp32: one multiply-add per output and block.
+// Matrix and fp32 vector instructions hardly overlap on a SIMD (4096^3 on the large tile: 53 % of its
+// cycles the one, 35 % the other; with two vector instructions per output, on the small tile, 42 %
+// and 46 %), so what is left to save is vector instructions: the loop has next to none but these,
+// with the stages' addresses in the reads' offsets (two steps written out) and no copies of scales.  To have few factors per lane, the
 // operands trade places: the instruction's rows are B's, its columns (a lane each) A's,
 // and sb is the same for all of a lane's sums where a weight has a scale per 128 x 128.  With a
-// scale per row of B they differ, a second multiplication each, and the vector unit is as busy
-// as the matrix units.
+// scale per row of B they differ, a second multiplication each.
 //
 // The vector unit adds to ordinary registers only, not to the accumulation half of the
 // register file, so a wave cannot hold 256 running sums as gemmt.hip's do: a wave owns
 // 128 x 64 outputs (256 x 256 tile, 8 waves, two to a SIMD) or 64 x 64 (128 x 128 tile, 4
-// waves, two workgroups to a CU), and one wave's multiply-adds run beside the other's
-// matrix instructions.  4096^3, bf16 C: 63-66 us with a scale per 128 x 128 (2.1 PFLOP/s; gemm_f8 with
-// a scale per row 58-61), 72 with one per row and block.
+// waves, two workgroups to a CU), and one wave's instructions fill the other's waits.  4096^3, bf16 C: 63-66 us with a scale per 128 x 128 (2.1 PFLOP/s; gemm_f8 with
+// a scale per row 58-61), 70.5 with one per row and block.
 //
 // The scales of a step come with its operands, by 4-byte direct-to-LDS loads (one per
 // wave and step), and are read back one per lane.  Operands, LDS layout, tile map and
@@ -270,7 +271,7 @@ struct GridTile {
 //
 // Against 32 x 32 x 64 instructions, two to a block (4096^3: 69 us with a scale per 128 x 128; with
 // a scale per row, whose 32 factors per 64 rows leave no registers for the large tile, 95 on the
-// small one), it takes 65 and 72 us, and the small tile 83 and 85 where it took 85 and 95.
+// small one), it takes 65 and 70.5 us, and the small tile 78 and 82 where it took 85 and 95.
 //
 // IN_F8W (fp32 outputs): four 16 x 16 x 32 bf16 instructions a block, on fragments widened once per
 // step (B's) and per 16 rows (A's).  4096^3 122 us, with a scale per row of B 135 (32 x 32
@@ -362,11 +363,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
     auto read = [&](const char* st, int strip, int h, Half& f) {  // of the wave's 16-row strips
         f.w[h] = *(const u32x4*)(st + (strip >> 1) * 4096 + off[strip & 1][h]);
     };
-    auto read_a = [&](int kt, int mi, int h, Half& f) {
-        read(smA + (kt % S) * T::A_STAGE + wm * (TBM / WM) * 128, mi, h, f);
+    // st: the stage, a constant where it counts, so that it is part of the LDS reads' offsets.
+    auto read_a = [&](int st, int mi, int h, Half& f) {
+        read(smA + st * T::A_STAGE + wm * (TBM / WM) * 128, mi, h, f);
     };
-    auto read_b = [&](int kt, int nj, int h, Half& f) {
-        read(smB + (kt % S) * T::B_STAGE + wn * (TBN / WN) * 128, nj, h, f);
+    auto read_b = [&](int st, int nj, int h, Half& f) {
+        read(smB + st * T::B_STAGE + wn * (TBN / WN) * 128, nj, h, f);
     };
     auto sync = [&](auto vm_tag) {
         constexpr int VM = decltype(vm_tag)::value;
@@ -401,13 +403,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
         constexpr int NS = NB ? NJ : 1;
         float sa[MI];
         f32x4 sb[NS];
-        auto read_sb = [&](int kt, int nj) {
-            const float* p = (const float*)(smS + (kt % S) * T::S_STAGE) + TBM + wn * (TBN / WN);
+        auto read_sb = [&](int st, int nj) {
+            const float* p = (const float*)(smS + st * T::S_STAGE) + TBM + wn * (TBN / WN);
             if constexpr (NB) sb[nj] = *(const f32x4*)(p + nj * 16 + 4 * g);
             else if (nj == 0) sb[0][0] = p[0];
         };
-        auto read_sa = [&](int kt, int mi) {
-            sa[mi] = ((const float*)(smS + (kt % S) * T::S_STAGE))[TBM / WM * wm + mi * 16 + c];
+        auto read_sa = [&](int st, int mi) {
+            sa[mi] = ((const float*)(smS + st * T::S_STAGE))[TBM / WM * wm + mi * 16 + c];
         };
 #pragma unroll
         for (int h = 0; h < 2; ++h) read_a(0, 0, h, fa[0]);
@@ -421,21 +423,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
         for (int mi = 0; mi < MI; ++mi) read_sa(0, mi);
         f32x4 part[2] = {f32x4{0.0f, 0.0f, 0.0f, 0.0f}, f32x4{0.0f, 0.0f, 0.0f, 0.0f}};
         float a_prev = 0.0f;
-        f32x4 b_prev = {0.0f, 0.0f, 0.0f, 0.0f};
         constexpr int NBLK = MI * NJ;
         // Block i's sums times its scales, added to the running ones.
-        auto add = [&](int i, float fa_, const f32x4& fb_) {
+        auto add = [&](int i) {
             const int mi = i / NJ, nj = i % NJ;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float f = NB ? fa_ * fb_[r] : fa_;
+                const float f = NB ? a_prev * sb[NB ? nj : 0][r] : a_prev;
                 acc[mi][nj][r] = __builtin_fmaf(part[i & 1][r], f, acc[mi][nj][r]);
             }
             // Here, in program order: the scheduling barriers order only what has side effects,
             // and the compiler would otherwise leave a step's additions to its end.
             asm volatile("" : "+v"(acc[mi][nj]));
         };
-        for (int kt = 0; kt < nk; ++kt) {
+        auto step = [&](int kt, auto stage) {
+            constexpr int P = decltype(stage)::value, Q = (P + 1) % S;
             Desc d;
 #pragma unroll
             for (int i = 0; i < NBLK; ++i) {
@@ -459,32 +461,39 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void block_grid_kernel(BlockArgs a
                         both(fb[nj].w[0], fb[nj].w[1]), both(fa[mi & 1].w[0], fa[mi & 1].w[1]), zero, 0, 0, 0, 0, 0, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
-                add(i == 0 ? NBLK - 1 : i - 1, a_prev, b_prev);
+                add(i == 0 ? NBLK - 1 : i - 1);
                 a_prev = sa[mi];
-                b_prev = sb[NB ? nj : 0];
                 if (nj < 2) {
-                    if (mi + 1 < MI) read_a(kt, mi + 1, nj, fa[(mi + 1) & 1]);
-                    else read_a(kt + 1, 0, nj, fa[MI & 1]);
+                    if (mi + 1 < MI) read_a(P, mi + 1, nj, fa[(mi + 1) & 1]);
+                    else read_a(Q, 0, nj, fa[MI & 1]);
                 }
                 if (mi == MI - 1) {
 #pragma unroll
                     for (int j = (nj * T::LOADS) / NJ; j < ((nj + 1) * T::LOADS) / NJ; ++j) dma_one(d, j);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) read_b(kt + 1, nj, h, fb[nj]);
-                    read_sb(kt + 1, nj);
+                    for (int h = 0; h < 2; ++h) read_b(Q, nj, h, fb[nj]);
                     // A's scales of the strips that are done, so that the next step's first factor, a
                     // product with B's, does not wait for them (2 % of 16384 x 4096 x 4096; with a scale
                     // per row of B the factors are formed later, and the step ends with these reads).
                     if (!NB && nj == 1)
 #pragma unroll
-                        for (int m = 0; m + 1 < MI; ++m) read_sa(kt + 1, m);
+                        for (int m = 0; m + 1 < MI; ++m) read_sa(Q, m);
+                    // B's scales, each after its last use here.
+                    if (!NB && nj == 0) read_sb(Q, 0);
+                    if (NB && nj > 0) read_sb(Q, nj - 1);
                 }
+                if (NB && i == 0) read_sb(P, NJ - 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
-            for (int m = NB ? 0 : MI - 1; m < MI; ++m) read_sa(kt + 1, m);
+            for (int m = NB ? 0 : MI - 1; m < MI; ++m) read_sa(Q, m);
+        };
+        static_assert(S == 2, "the loop's two steps are the stages");
+        for (int kt = 0; kt < nk; kt += 2) {
+            step(kt, std::integral_constant<int, 0>{});
+            if (kt + 1 < nk) step(kt + 1, std::integral_constant<int, 1>{});
         }
-        add(NBLK - 1, a_prev, b_prev);
+        add(NBLK - 1);
     }
     // No direct-to-LDS write may still be in flight when the LDS is reused.
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
