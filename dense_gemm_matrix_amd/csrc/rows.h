@@ -328,6 +328,14 @@ hipError_t row_by_size(const RowArgs& a, hipStream_t s) {
     if (a.N <= 512) return go_row<FMT, MODE, 64, 1>(a, s);
     if (a.N <= 1024) return go_row<FMT, MODE, 64, 2>(a, s);
     if (a.N <= 2048) return go_row<FMT, MODE, 256, 1>(a, s);
+    // Rows that have a CU each: eight columns per thread, for the time of one row (8-bit blocks, bf16, 8
+    // and 16 columns per thread or more: 1 x 4096 3.8 and 4.4 us, 1 x 8192 4.7 and 6.4, 256 x 8192 6.1
+    // and 7.8; plain output 256 x 4096 4.0 and 4.05, 1000 x 4096 6.9 and 6.5).  The order of a row's sums
+    // differs, so the root-mean-square norm's other outputs keep one width.
+    if constexpr (MODE >= NORM_F8B) {
+        if (a.M <= NUM_CU && a.N > 2048 && a.N <= 4096) return go_row<FMT, MODE, 512, 1>(a, s);
+        if (a.M <= NUM_CU && a.N > 4096 && a.N <= 8192) return go_row<FMT, MODE, 1024, 1>(a, s);
+    }
     if (a.N <= 4096) return go_row<FMT, MODE, 256, 2>(a, s);
     if (a.N <= 8192) return go_row<FMT, MODE, 256, 4>(a, s);
     if (a.N <= 16384) return go_row<FMT, MODE, 1024, 2>(a, s);

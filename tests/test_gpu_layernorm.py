@@ -11,6 +11,7 @@ from tests.test_gpu_norm import DTS, SIZES, norm64, rows, rstd_err
 pytestmark = pytest.mark.gpu
 
 EPS = 1e-5
+WIDTHS = [(256, 2050), (257, 2050), (257, 4100), (256, 8190), (257, 8190)]  # either side of one row per CU
 
 
 def vector(n, seed, base=0.0):
@@ -22,7 +23,7 @@ def nans(*shape):
 
 
 @pytest.mark.parametrize("dt", DTS, ids=str)
-@pytest.mark.parametrize("size", SIZES + [(2, 20000), (2, 32768)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("size", SIZES + WIDTHS + [(2, 20000), (2, 32768)], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("res, bias, shift", [(False, True, 0.0), (True, False, 0.0), (True, True, 50.0)])
 def test_forward(dt, size, res, bias, shift):
     M, N = size
@@ -41,7 +42,7 @@ def test_forward(dt, size, res, bias, shift):
 
 
 @pytest.mark.parametrize("dt", DTS, ids=str)
-@pytest.mark.parametrize("size", SIZES + [(2, 32768)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("size", SIZES + WIDTHS + [(2, 32768)], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("kind", ["row", "block", "block rows apart", "rms block"])
 def test_forward_f8(dt, size, kind):
     M, N = size
