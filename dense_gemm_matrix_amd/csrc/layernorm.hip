@@ -96,41 +96,52 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
         for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.0f;
         if (IN_LDS) to_lds(i);
     }
-    Row8<FMT> y[NV], s[NV], d[NV];
-    float next_rstd = 0.0f, next_mean = 0.0f;
-    // The rows of this wave from row0 on; rows past M and columns past N load as 0.
-    auto load = [&](int64_t row0) {
-        next_rstd = row0 + pl.lr < a.M ? a.rstd[row0 + pl.lr] : 0.0f;
-        next_mean = row0 + pl.lr < a.M ? a.mean[row0 + pl.lr] : 0.0f;
+    // Rows in flight beside the one at work: its time is far below memory's latency, so two where eight
+    // 16-bit columns per thread leave them room (8192 x 2048 bf16 27.9 us, 31.2 with one; with 16 columns
+    // 16384 x 4096 112 us, 106 with one).
+    constexpr int D = PRE && FMT != OUT_F32 && NV == 1 ? 2 : 1;
+    const bool ragged = (a.N & 7) != 0;
+    Row8<FMT> y[D][NV], s[D][NV], d[D][NV];
+    float next_rstd[D], next_mean[D];
+    // The rows of this wave from row0 on; rows past M load as 0.  Columns past N are zeroed where the
+    // values are used: here that would wait for them (1000 x 2999 f16 17.0 us, 15.1 this way).
+    auto load = [&](int64_t row0, auto slot) {
+        constexpr int q = decltype(slot)::value;
+        next_rstd[q] = row0 + pl.lr < a.M ? a.rstd[row0 + pl.lr] : 0.0f;
+        next_mean[q] = row0 + pl.lr < a.M ? a.mean[row0 + pl.lr] : 0.0f;
         const auto ry = P::rows(a.dY, row0, a.M, a.N, a.lddy, ES);
         const auto rs = P::rows(a.S, row0, a.M, a.N, a.lds, ES);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            y[i].load(ry, pl.at(row0, a.M, a.N, col(i), a.lddy, ES), a.N - col(i));
-            s[i].load(rs, pl.at(row0, a.M, a.N, col(i), a.lds, ES), a.N - col(i));
+            y[q][i].load_whole(ry, pl.at(row0, a.M, a.N, col(i), a.lddy, ES));
+            s[q][i].load_whole(rs, pl.at(row0, a.M, a.N, col(i), a.lds, ES));
         }
         if (a.dS) {
             const auto rd = P::rows(a.dS, row0, a.M, a.N, a.ldds, ES);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                d[i].load(rd, pl.at(row0, a.M, a.N, col(i), a.ldds, ES), a.N - col(i));
+            for (int i = 0; i < NV; ++i) d[q][i].load_whole(rd, pl.at(row0, a.M, a.N, col(i), a.ldds, ES));
         }
     };
-    int64_t row0 = (int64_t)blockIdx.x * P::RPW + P::first();
-    if (PRE && row0 < a.M) load(row0);
+    using Slot0 = std::integral_constant<int, 0>;
+    using Slot1 = std::integral_constant<int, D - 1>;
     int par = 0;
-    for (; row0 < a.M; row0 += step, par ^= 1) {
-        if (!PRE) load(row0);
-        const float rstd = next_rstd, mean = next_mean;
+    auto pass = [&](int64_t row0, auto slot) {
+        constexpr int q = decltype(slot)::value;
+        if (!PRE) load(row0, slot);
+        const float rstd = next_rstd[q], mean = next_mean[q];
         // The row stays in its storage format (half the registers of fp32 for
         // 16-bit rows); the few products are formed again after the reduction.
         Row8<FMT> cy[NV], cs[NV], cd[NV];
         float dot = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            cy[i] = y[i];
-            cs[i] = s[i];
-            cd[i] = d[i];
+            cy[i] = y[q][i];
+            cs[i] = s[q][i];
+            cd[i] = d[q][i];
+            if (ragged && a.N - col(i) < 8) {
+                cy[i].mask(a.N - col(i));
+                cs[i].mask(a.N - col(i));
+            }
             float dy[8], x[8];
             cy[i].get(dy);
             cs[i].get(x);
@@ -148,7 +159,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
             }
             if (IN_LDS) to_lds(i);
         }
-        if (PRE && row0 + step < a.M) load(row0 + step);
+        if (PRE && row0 + D * step < a.M) load(row0 + D * step, slot);
         // The reduction's words alternate between rows, so one barrier per row
         // is enough: a wave reaches the next but one row's write only after
         // every wave has passed the next row's barrier.
@@ -173,6 +184,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void ln_bwd_kernel(NormBwdArgs a
             out.set(o);
             out.store(ro, pl.at(row0, a.M, a.N, col(i), a.lddx, ES), a.N - col(i));
         }
+        par ^= 1;
+    };
+    int64_t row0 = (int64_t)blockIdx.x * P::RPW + P::first();
+    if (PRE && row0 < a.M) load(row0, Slot0{});
+    if (D > 1 && row0 + step < a.M) load(row0 + step, Slot1{});
+    for (; row0 < a.M; row0 += D * step) {
+        pass(row0, Slot0{});
+        if (D > 1 && row0 + step < a.M) pass(row0 + step, Slot1{});
     }
     if (!a.part) return;
     if (IN_LDS)
