@@ -4,22 +4,24 @@
 //   C = act(sum over blocks b of sa[i][b] sb[j'][b] sum_{k in b} A[i][k] B[j][k] + bias) + R,
 //   j' = j / 128 (weights) or j (gradients: a scale per row and block on both sides)
 //
-// A: M x K, B: N x K, both K-contiguous.  A K step of the matrix kernels is 128 bytes of
-// every row, which is one block: a step's matrix instructions start from zero, and their
-// sums are added to the running ones scaled, in fp32: one multiply-add per output and block.
-// Matrix and fp32 vector instructions hardly overlap on a SIMD (4096^3 on the large tile: 53 % of its
-// cycles the one, 35 % the other; with two vector instructions per output, on the small tile, 42 %
-// and 46 %), so what is left to save is vector instructions: the loop has next to none but these,
-// with the stages' addresses in the reads' offsets (two steps written out) and no copies of scales.  To have few factors per lane, the
-// operands trade places: the instruction's rows are B's, its columns (a lane each) A's,
-// and sb is the same for all of a lane's sums where a weight has a scale per 128 x 128.  With a
-// scale per row of B they differ, a second multiplication each.
+// A: M x K, B: N x K, both K-contiguous.  A K step of the matrix kernels is 128 bytes of every
+// row, which is one block: a step's matrix instructions start from zero, and their sums are
+// added to the running ones scaled, in fp32: one multiply-add per output and block. Matrix and
+// fp32 vector instructions hardly overlap on a SIMD (4096^3 on the large tile: 53 % of its
+// cycles the one, 35 % the other; with two vector instructions per output, on the small tile,
+// 42 % and 46 %), so what is left to save is vector instructions: the loop has next to none but
+// these, with the stages' addresses in the reads' offsets (two steps written out) and no copies
+// of scales.  To have few factors per lane, the operands trade places: the instruction's rows
+// are B's, its columns (a lane each) A's, and sb is the same for all of a lane's sums where a
+// weight has a scale per 128 x 128.  With a scale per row of B they differ, a second
+// multiplication each.
 //
-// The vector unit adds to ordinary registers only, not to the accumulation half of the
-// register file, so a wave cannot hold 256 running sums as gemmt.hip's do: a wave owns
-// 128 x 64 outputs (256 x 256 tile, 8 waves, two to a SIMD) or 64 x 64 (128 x 128 tile, 4
-// waves, two workgroups to a CU), and one wave's instructions fill the other's waits.  4096^3, bf16 C: 63-66 us with a scale per 128 x 128 (2.1 PFLOP/s; gemm_f8 with
-// a scale per row 58-61), 70.5 with one per row and block.
+// The vector unit adds to ordinary registers only, not to the accumulation half of the register
+// file, so a wave cannot hold 256 running sums as gemmt.hip's do: a wave owns 128 x 64 outputs
+// (256 x 256 tile, 8 waves, two to a SIMD) or 64 x 64 (128 x 128 tile, 4 waves, two workgroups
+// to a CU), and one wave's instructions fill the other's waits.  4096^3, bf16 C: 63-66 us with
+// a scale per 128 x 128 (2.1 PFLOP/s; gemm_f8 with a scale per row 58-61), 70.5 with one per
+// row and block.
 //
 // The scales of a step come with its operands, by 4-byte direct-to-LDS loads (one per
 // wave and step), and are read back one per lane.  Operands, LDS layout, tile map and

@@ -8,11 +8,11 @@
 // Backward: with xh = (s - mean) rstd and g = dy w,
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + ds,  dw = sum over rows of dy xh,
 //   db = sum over rows of dy.
-// As the root-mean-square norm's (norm.hip): each workgroup walks rows blockIdx, blockIdx
-// + grid, ..., the next row's loads in flight over this one's reduction, whose two sums
-// share one barrier; a thread's columns are the same in every row, so dw and db are running
-// fp32 sums in registers (from 8193 columns on in LDS), written once per workgroup and added over workgroups in a fixed
-// order by one more launch for both.
+// As the root-mean-square norm's (norm.hip): each workgroup walks rows blockIdx, blockIdx +
+// grid, ..., the next row's loads in flight over this one's reduction, whose two sums share one
+// barrier; a thread's columns are the same in every row, so dw and db are running fp32 sums in
+// registers (from 8193 columns on in LDS), written once per workgroup and added over workgroups
+// in a fixed order by one more launch for both.
 
 #include "rows.h"
 
