@@ -161,13 +161,14 @@ GatedPlan gated_pieces(int bm, int bn, int bk, int M, int N, int K, int splits, 
 // from the last-level cache, 32 / 64 / 128 columns 43.8 / 37.4 / 38.4 us), and split from the same K on
 // in fp32.
 GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
-    auto strips = [&](int cols, int waves, int splits) {
-        GatedPlan p = gated_pieces(SKINNY_M, cols, 32, M, N, K, splits, ws);
+    auto strips = [&](int cols, int waves, int splits) {  // splits = 0 if it does not fit
+        GatedPlan p = gated_pieces(SKINNY_M, cols, 32, M, N, K, splits, UINT64_MAX);
         if (p.splits > 1 && p.kchunk % 64 == 0) {  // an odd number of steps, as plan_skinny's
             p.kchunk += 32;
             p.splits = (int)ceil_div(K, p.kchunk);
-            p.ws_bytes = (int64_t)p.splits * M * 2 * p.ldw * 4;
+            p.ws_bytes = p.splits > 1 ? (int64_t)p.splits * M * 2 * p.ldw * 4 : 0;
         }
+        if ((uint64_t)p.ws_bytes > ws) p.splits = 0;  // what the pieces need once they are final
         p.waves = waves;
         p.skinny = true;
         return p;

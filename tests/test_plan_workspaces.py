@@ -1,0 +1,65 @@
+"""A plan query's bytes are the bytes its plan takes: asked again with exactly those it answers the same plan,
+with fewer another one, and the allocating forms, which allocate what the query says, run the plan it names."""
+import random
+
+import pytest
+import torch
+
+import dense_gemm_matrix_amd as dg
+
+ANY = 1 << 40
+
+
+def sizes(seed, count=400):
+    """M up to 16, N and K spread over their logarithm, with the depths from which K is split among them."""
+    rng = random.Random(seed)
+    for _ in range(count):
+        yield rng.randint(1, 16), int(2 ** rng.uniform(0, 15)), int(2 ** rng.uniform(10, 15))
+
+
+def same_with_its_bytes(query, shapes):
+    split = 0
+    for shape in shapes:
+        p = query(*shape, ANY)
+        assert query(*shape, p["workspace_bytes"]) == p, shape
+        if p["splits"] > 1:
+            split += 1
+            assert query(*shape, p["workspace_bytes"] - 1)["workspace_bytes"] < p["workspace_bytes"], shape
+        else:
+            assert p["workspace_bytes"] == 0, shape
+    assert split > 20
+
+
+GATED = [(1, 1024, 4096), (1, 512, 4096), (1, 1024, 5120), (8, 512, 7168), (3, 298, 8002)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "f32"])
+def test_gated_rows_split_with_the_reported_bytes(fmt):
+    same_with_its_bytes(lambda M, N, K, ws: dg.gemm_gated_plan(fmt, M, N, K, ws, fmt != "f32"),
+                        GATED + list(sizes(1)))
+
+
+@pytest.mark.parametrize("cols", [32, 64])
+def test_forced_gated_strips_take_what_they_report(cols):
+    """Few steps of K: pieces of an odd number of steps may leave a single one, which takes no workspace."""
+    dg.dgemm_set_plan_override(dg.DGEMM_PLAN_GRID, 16, cols, 2)
+    try:
+        for K in (32, 64, 96, 100, 128, 160, 4096):
+            p = dg.gemm_gated_plan("bf16", 4, 40, K, ANY, True)
+            assert (p["workspace_bytes"] > 0) == (p["splits"] > 1), K
+            assert dg.gemm_gated_plan("bf16", 4, 40, K, p["workspace_bytes"], True) == p, K
+    finally:
+        dg.dgemm_set_plan_override(dg.DGEMM_PLAN_AUTO)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", GATED, ids=lambda s: "x".join(map(str, s)))
+def test_gated_with_its_bytes_as_with_more(shape):
+    """linear_gated runs the plan that a larger workspace gets: the same bits."""
+    M, N, K = shape
+    gen = torch.Generator(device="cuda").manual_seed(M + N + K)
+    A = torch.randn(M, (K + 7) // 8 * 8, generator=gen, device="cuda").bfloat16()[:, :K]
+    Bg, Bu = (torch.randn(K, (N + 7) // 8 * 8, generator=gen, device="cuda").bfloat16()[:, :N] for _ in range(2))
+    C = torch.empty(M, (N + 7) // 8 * 8, device="cuda", dtype=torch.bfloat16)[:, :N]
+    dg.gemm_gated(A, Bg, Bu, C, workspace=torch.empty(8 << 20, device="cuda", dtype=torch.uint8))
+    assert torch.equal(dg.linear_gated(A, Bg, Bu), C)
