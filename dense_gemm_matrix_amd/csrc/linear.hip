@@ -141,12 +141,13 @@ Plan plan_skinny(int in, int layout, int M, int N, int K, uint64_t ws_avail) {
         return p;
     }
     auto strips = [&](int cols, int splits) {  // splits = 0 if it does not fit
-        Plan q = plan_pieces(TileCand{SKINNY_M, cols, 1, 0, 0, 1, 1}, 32, M, N, K, splits, ws_avail);
+        Plan q = plan_pieces(TileCand{SKINNY_M, cols, 1, 0, 0, 1, 1}, 32, M, N, K, splits, UINT64_MAX);
         if (q.splits > 1 && q.kchunk % 64 == 0) {  // an odd number of steps
             q.kchunk += 32;
             q.splits = (int)ceil_div(K, q.kchunk);
-            q.ws_bytes = (int64_t)q.splits * M * q.ldw * 4;
+            q.ws_bytes = q.splits > 1 ? (int64_t)q.splits * M * q.ldw * 4 : 0;
         }
+        if ((uint64_t)q.ws_bytes > ws_avail) q.splits = 0;  // what the pieces need once they are final
         q.waves = cols == 32 ? 16 : 8;
         q.kind = PLAN_SKINNY;
         return q;

@@ -52,6 +52,39 @@ def test_forced_gated_strips_take_what_they_report(cols):
         dg.dgemm_set_plan_override(dg.DGEMM_PLAN_AUTO)
 
 
+ACT = [(1, 1024, 4096), (1, 512, 4096), (2, 336, 11856), (8, 512, 7168), (3, 298, 8002)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f16", "f32"])
+def test_rows_split_with_the_reported_bytes(fmt):
+    same_with_its_bytes(lambda M, N, K, ws: dg.gemm_act_plan(fmt, M, N, K, ws, fmt != "f32"), ACT + list(sizes(2)))
+
+
+@pytest.mark.parametrize("cols", [32, 64, 128])
+def test_forced_strips_take_what_they_report(cols):
+    dg.dgemm_set_plan_override(dg.DGEMM_PLAN_GRID, 16, cols, 2)
+    try:
+        for K in (32, 64, 96, 100, 128, 160, 4096):
+            p = dg.gemm_act_plan("bf16", 4, 40, K, ANY, True)
+            assert (p["workspace_bytes"] > 0) == (p["splits"] > 1), K
+            assert dg.gemm_act_plan("bf16", 4, 40, K, p["workspace_bytes"], True) == p, K
+    finally:
+        dg.dgemm_set_plan_override(dg.DGEMM_PLAN_AUTO)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", ACT, ids=lambda s: "x".join(map(str, s)))
+def test_rows_with_their_bytes_as_with_more(shape):
+    """linear runs the plan that a larger workspace gets: the same bits."""
+    M, N, K = shape
+    gen = torch.Generator(device="cuda").manual_seed(M + N + K)
+    A = torch.randn(M, (K + 7) // 8 * 8, generator=gen, device="cuda").bfloat16()[:, :K]
+    B = torch.randn(K, (N + 7) // 8 * 8, generator=gen, device="cuda").bfloat16()[:, :N]
+    C = torch.empty(M, (N + 7) // 8 * 8, device="cuda", dtype=torch.bfloat16)[:, :N]
+    dg.gemm_act(A, B, C, act="silu", workspace=torch.empty(8 << 20, device="cuda", dtype=torch.uint8))
+    assert torch.equal(dg.linear(A, B, act="silu"), C)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", GATED, ids=lambda s: "x".join(map(str, s)))
 def test_gated_with_its_bytes_as_with_more(shape):
