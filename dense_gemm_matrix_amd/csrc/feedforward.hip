@@ -51,7 +51,7 @@ TileCand block_tile(int i, bool each) {
 // grid tiles and K splits by the common estimate.  us, slices of 32 / of 64 / best grid plan:
 // bf16 C, 64 x 4096 x 4096 5.8 / 12.0 / 14.5, 17 x 8192 x 1024 3.6 / 6.3 / 8.5, 300 x 1000 x 2000 8.5 /
 // 9.4 / 13.3, 1000^3 13.1 / 9.2 / 10.2, 512 x 4096 x 4096 38.5 / 25.1 / 25.3, 700 x 5000 x 3000 67.7 / 45.1 /
-// 26.6; fp32 C, 700 x 5000 x 3000 71 / 55 / 35.
+// 26.6; fp32 C, 700 x 5000 x 3000 71 / 55 / 35.  bm = 0: none fits.
 Plan plan_block(int of, int rows_b, int M, int N, int K, uint64_t ws) {
     const int in = block_in(of, M);
     if (M > 0 && M <= SKINNY_M && N > 0) return plan_skinny(in, LAY_NT, M, N, K, 0);
@@ -86,7 +86,7 @@ Plan plan_block(int of, int rows_b, int M, int N, int K, uint64_t ws) {
             if (p.splits != s || (forced && (t.bm != fm || s != fs))) continue;
             const double us = estimate_us(in, out_esize(of), M, N, t, s, s == 1 ? nk : p.kchunk / F8_BLOCK, p.ldw) /
                                   (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US;
-            if (us < best_us || forced) {
+            if (best_us < 0.0 || us < best_us || forced) {
                 best_us = us;
                 best = p;
                 if (forced) return best;
@@ -188,6 +188,7 @@ GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
     return ceil_div(N, 32) > NUM_CU ? strips(64, 8, 1) : strips(32, 16, 1);
 }
 
+// bm = 0: none fits.
 GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
     if (M > 0 && M <= SKINNY_M && N > 0) return plan_gated_skinny(in, M, N, K, ws);
     const TileCand* tiles = in == IN_F32 ? TILES_G32 : TILES_G16;
@@ -234,7 +235,7 @@ GatedPlan plan_gated(int in, int es_out, int M, int N, int K, uint64_t ws) {
             if (p.splits != s) continue;
             double us = estimate_us(in, es_out, M, N2, t, s, s == 1 ? nk : p.kchunk / bk, s == 1 ? 0 : 2 * p.ldw);
             us = us / (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US + (s > 1 ? SPLIT_US : 0.0);
-            if (us < best_us) {
+            if (best_us < 0.0 || us < best_us) {
                 best_us = us;
                 best = p;
             }
@@ -540,6 +541,7 @@ int gemm_f8_block(int out, int rows_b, int M, int N, int K, const void* A, int l
         return st;
     if (!reads) return DGEMM_OK;
     const Plan p = plan_block(of, rows_b, M, N, K, workspace ? workspace_bytes : 0);
+    if (p.bm == 0) return DGEMM_ERR_TOO_LARGE;
     const Mat ws = bytes_of(workspace, p.ws_bytes);
     if (check_vec(bias, 4) != DGEMM_OK || check_vec(ws.p, 16) != DGEMM_OK) return DGEMM_ERR_MISALIGNED;
     // R may be C itself (each element is read before it is written), not overlap it in any other way.
@@ -564,7 +566,8 @@ int gemm_f8_block_plan(int out, int rows_b, int M, int N, int K, size_t workspac
     const int of = row_fmt(out);
     if (of < 0 || M < 0 || N < 0 || K < 0 || (rows_b != 1 && rows_b != F8_BLOCK)) return DGEMM_ERR_INVALID_VALUE;
     if (ceil_div(M, 128) * ceil_div(N, 128) > INT32_MAX) return DGEMM_ERR_TOO_LARGE;
-    return report(plan_block(of, rows_b, M, N, K, workspace_bytes), tile_rows, tile_cols, splits, workspace_used);
+    const Plan p = plan_block(of, rows_b, M, N, K, workspace_bytes);
+    return p.bm == 0 ? DGEMM_ERR_TOO_LARGE : report(p, tile_rows, tile_cols, splits, workspace_used);
 }
 
 int layernorm(int in, int out, int M, int N, const void* X, int ldx, const void* R, int ldr, void* S, int lds,
@@ -676,6 +679,7 @@ int gemm_gated(int in, int out, int M, int N, int K, const void* A, int lda, con
         return st;
     if (!reads) return DGEMM_OK;
     const GatedPlan p = plan_gated(in, eo, M, N, K, workspace ? workspace_bytes : 0);
+    if (p.bm == 0) return DGEMM_ERR_TOO_LARGE;
     const Mat ws = bytes_of(workspace, p.ws_bytes);
     if (check_vec(bias_g, 4) != DGEMM_OK || check_vec(bias_u, 4) != DGEMM_OK || check_vec(ws.p, 16) != DGEMM_OK)
         return DGEMM_ERR_MISALIGNED;
@@ -693,6 +697,7 @@ int gemm_gated_plan(int in, int out, int M, int N, int K, size_t workspace_bytes
     if (of < 0) return DGEMM_ERR_INVALID_VALUE;
     if (ceil_div(M, 128) * ceil_div(N, 64) > INT32_MAX) return DGEMM_ERR_TOO_LARGE;
     const GatedPlan p = plan_gated(in, out_esize(of), M, N, K, workspace_bytes);
+    if (p.bm == 0) return DGEMM_ERR_TOO_LARGE;
     Plan q{};
     q.bm = p.bm;
     q.bn = p.bn;

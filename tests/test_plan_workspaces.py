@@ -72,6 +72,17 @@ def test_forced_strips_take_what_they_report(cols):
         dg.dgemm_set_plan_override(dg.DGEMM_PLAN_AUTO)
 
 
+@pytest.mark.parametrize("M, N, K", [(2 ** 31 - 1, 4096, 64), (2 ** 31 - 1, 8000, 200), (2 ** 30, 8192, 8)])
+def test_more_small_tiles_than_a_launch_counts(M, N, K):
+    """Outputs with more 64 x 64 tiles than 2^31: a larger tile's plan, not one without a tile."""
+    for fmt in ("f32", "bf16", "f16"):
+        p = dg.gemm_gated_plan(fmt, M, N, K, 0, fmt != "f32")
+        assert p["tile_rows"] >= 64 and p["tile_cols"] >= 32 and p["splits"] == 1
+        for rows_b in (1, 128):
+            p = dg.gemm_f8_block_plan(fmt, M, N, K, 0, rows_b)
+            assert p["tile_rows"] >= 64 and p["splits"] == 1
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", ACT, ids=lambda s: "x".join(map(str, s)))
 def test_rows_with_their_bytes_as_with_more(shape):
