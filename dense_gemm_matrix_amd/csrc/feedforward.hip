@@ -331,7 +331,8 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
     auto nt_tiles = [&](int t) { return dA ? ceil_div(M, t) * ceil_div(K, t) : 0; };
     auto tn_tiles = [&](int t) { return dB ? 2 * ceil_div(K, t) * ceil_div(N, t) : 0; };
     int fm, fn, fs;
-    const bool forced = forced_grid(fm, fn, fs) && fm == fn && (fm == 32 || fm == 64 || (f != IN_F32 && fm >= 128));
+    const bool forced = forced_grid(fm, fn, fs) && fm == fn &&
+                        (fm == 32 || fm == 64 || (f != IN_F32 && (fm == 128 || fm == 256)));
     auto allowed = [&](int t) { return !forced || t == fm; };
     // One product alone: us, tile and kind.
     struct Alone { double us; int tile; bool slices; };
@@ -736,6 +737,12 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
     const Mat ins[] = {mA, mBg, mBu, mdC, mG, mU};
     const Mat outs[] = {mdA, mdBg, mdBu, vec(dbias_g, N), vec(dbias_u, N), ws};
     if (any_overlap(outs, 6, ins, 6)) return DGEMM_ERR_ALIAS;
+    const bool want_a = dA && M > 0 && K > 0, want_b = dB && K > 0 && N > 0;
+    const int64_t gemm_bytes = (int64_t)std::min<uint64_t>(workspace_bytes, INT64_MAX) - b.required;
+    GatedBwdPlan p{};
+    if (want_a || want_b) p = plan_gated_bwd(in, M, N, K, want_a, want_b, (uint64_t)gemm_bytes);
+    const bool few = few_rows(in, M, N, K, p);
+    if (!few && (want_a || want_b) && !p.transposes && p.nt == 0) return DGEMM_ERR_TOO_LARGE;
     if ((st = check_device()) != DGEMM_OK) return st;
 
     char* const w = (char*)workspace;
@@ -744,7 +751,6 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
     float* const part = (float*)(w + 2 * b.dz);
     float* const w_trans = (float*)(w + 2 * b.dz + b.part);
     char* const w_gemm = w + b.required;
-    const int64_t gemm_bytes = (int64_t)std::min<uint64_t>(workspace_bytes, INT64_MAX) - b.required;
     hipStream_t s = (hipStream_t)stream;
     if (M > 0 && N > 0 && (dA || dB || bias)) {
         const bool products = (dA || dB) && K > 0;
@@ -756,14 +762,11 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
     const int G2 = M > 0 ? b.chunks : 0;
     const ColReduceArgs sg{part, dbias_g, G2, 2 * b.ldp, dbias_g ? N : 0};
     const ColReduceArgs su{part + b.ldp, dbias_u, G2, 2 * b.ldp, dbias_u ? N : 0};
-    const bool want_a = dA && M > 0 && K > 0, want_b = dB && K > 0 && N > 0;
     void* const dW[2] = {dBg, dBu};
     const int lddw[2] = {lddbg, lddbu};
     char* const dz[2] = {dG, dU};
 
-    GatedBwdPlan p{};
-    if (want_a || want_b) p = plan_gated_bwd(in, M, N, K, want_a, want_b, (uint64_t)gemm_bytes);
-    if (few_rows(in, M, N, K, p)) {
+    if (few) {
         // Few rows: the weights once through registers for dA, rank-M updates for theirs.
         if (want_a) {
             const Plan q = plan_skinny(in, LAY_NT, M, K, (int)std::min<int64_t>(2 * (int64_t)N, INT32_MAX), 0);
@@ -780,7 +783,6 @@ int gemm_gated_bwd(int in, int out, int M, int N, int K, const void* A, int lda,
         return launched(launch_col_reduce2(sg, su, s));
     }
     if (!want_a && !want_b) return launched(launch_col_reduce2(sg, su, s));
-    if (!p.transposes && p.nt == 0) return DGEMM_ERR_TOO_LARGE;
     if (!p.transposes) {
         GatedBwdLaunch L{};
         L.nt = bwd_launch(in, LAY_NT, p.nt, p.nt_slices, M, K, N, dG, b.lddz, Bg, ldbg, dA, ldda, s);

@@ -83,6 +83,37 @@ def test_more_small_tiles_than_a_launch_counts(M, N, K):
             assert p["tile_rows"] >= 64 and p["splits"] == 1
 
 
+@pytest.fixture
+def no_such_tile():
+    """A grid override that no kernel has: the automatic plans."""
+    yield lambda t=512: dg.dgemm_set_plan_override(dg.DGEMM_PLAN_GRID, t, t, 1)
+    dg.dgemm_set_plan_override(dg.DGEMM_PLAN_AUTO)
+
+
+@pytest.mark.parametrize("tile", [16, 96, 192, 512, 1024])
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "f16"])
+def test_gated_backward_under_a_tile_that_no_kernel_has(fmt, tile, no_such_tile):
+    shapes = [(8, 4096, 1024), (1000, 2744, 1032), (4096, 578, 488), (300, 1500, 900)]
+    auto = [dg.gemm_gated_bwd_workspace(fmt, *x) for x in shapes]
+    no_such_tile(tile)
+    assert [dg.gemm_gated_bwd_workspace(fmt, *x) for x in shapes] == auto
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tile", [192, 512])
+@pytest.mark.parametrize("fmt", ["f32", "bf16"])
+def test_gated_backward_runs_under_a_tile_that_no_kernel_has(fmt, tile, no_such_tile):
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[fmt]
+    gen = torch.Generator(device="cuda").manual_seed(tile)
+    M, N, K = 72, 136, 264
+    rnd = lambda r, c: torch.randn(r, c, generator=gen, device="cuda").to(dt)  # noqa: E731
+    args = rnd(M, K), rnd(K, N), rnd(K, N), rnd(M, N), rnd(M, N), rnd(M, N)
+    want = dg.linear_gated_backward(*args, bias=True)
+    no_such_tile(tile)
+    for got, ref in zip(dg.linear_gated_backward(*args, bias=True), want):
+        assert torch.equal(got, ref)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", ACT, ids=lambda s: "x".join(map(str, s)))
 def test_rows_with_their_bytes_as_with_more(shape):
