@@ -62,9 +62,16 @@ Plan plan_block(int of, int rows_b, int M, int N, int K, uint64_t ws) {
         p.waves = t == 32 ? 8 : 4;
         return p;
     };
+    const int tiles = in == IN_F8 ? 2 : 1;  // fp32 C: the small one
     int fm, fn, fs;
-    const bool forced = forced_grid(fm, fn, fs) && fm == fn;
-    if (forced && (fm == 32 || fm == 64)) return slices(fm);
+    if (forced_grid(fm, fn, fs) && fm == fn) {
+        if (fm == 32 || fm == 64) return slices(fm);
+        for (int i = 2 - tiles; i < 2; ++i)
+            if (block_tile(i, each).bm == fm) {
+                const Plan p = plan_pieces(block_tile(i, each), F8_BLOCK, M, N, K, fs, ws);
+                if (p.splits > 0) return p;
+            }
+    }
     Plan best{};
     double best_us = -1.0;
     for (int t = 32; t <= 64; t += 32) {
@@ -80,16 +87,15 @@ Plan plan_block(int of, int rows_b, int M, int N, int K, uint64_t ws) {
         }
     }
     for (int s = 1; s <= MAX_SPLITS && s <= nk; ++s)
-        for (int i = in == IN_F8 ? 0 : 1; i < 2; ++i) {
+        for (int i = 2 - tiles; i < 2; ++i) {
             const TileCand t = block_tile(i, each);
             const Plan p = plan_pieces(t, F8_BLOCK, M, N, K, s, ws);
-            if (p.splits != s || (forced && (t.bm != fm || s != fs))) continue;
+            if (p.splits != s) continue;
             const double us = estimate_us(in, out_esize(of), M, N, t, s, s == 1 ? nk : p.kchunk / F8_BLOCK, p.ldw) /
                                   (s > 1 ? SPLIT_MARGIN : 1.0) + GRID_US;
-            if (best_us < 0.0 || us < best_us || forced) {
+            if (best_us < 0.0 || us < best_us) {
                 best_us = us;
                 best = p;
-                if (forced) return best;
             }
         }
     return best;

@@ -99,6 +99,23 @@ def test_gated_backward_under_a_tile_that_no_kernel_has(fmt, tile, no_such_tile)
     assert [dg.gemm_gated_bwd_workspace(fmt, *x) for x in shapes] == auto
 
 
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "f16"])
+def test_block_products_under_a_tile_that_no_kernel_has(fmt, no_such_tile):
+    """fp32 C has no 256 x 256 tile; a split without its workspace is not a plan, and one of more pieces than
+    K has steps is reduced to whole steps (5 steps in 4 pieces: 2, 2 and 1)."""
+    shapes = [(300, 1000, 2000), (4096, 4096, 4096), (700, 5000, 3000), (2048, 4096, 8192), (40, 4096, 640)]
+    plans = lambda ws: [dg.gemm_f8_block_plan(fmt, *x, ws, r) for x in shapes for r in (1, 128)]  # noqa: E731
+    auto = {ws: plans(ws) for ws in (0, ANY)}
+    for tile in (16, 192, 512) + ((256,) if fmt == "f32" else ()):
+        no_such_tile(tile)
+        assert {ws: plans(ws) for ws in (0, ANY)} == auto, tile
+    dg.dgemm_set_plan_override(dg.DGEMM_PLAN_GRID, 128, 128, 4)
+    assert plans(0) == auto[0]
+    for p, (M, N, K) in zip(plans(ANY), [x for x in shapes for _ in (1, 128)]):
+        pieces = 3 if K == 640 else 4
+        assert p == {"tile_rows": 128, "tile_cols": 128, "splits": pieces, "workspace_bytes": pieces * M * N * 4}
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("tile", [192, 512])
 @pytest.mark.parametrize("fmt", ["f32", "bf16"])
