@@ -437,7 +437,7 @@ typedef enum { DGEMM_ROWS_SAME = 0, DGEMM_ROWS_F8 = 1, DGEMM_ROWS_F8_BLOCK = 2 }
 
 /*
  * Root-mean-square norm of rows, with the residual's addition and an output in
- * 8 bits for gemm_f8:
+ * 8 bits for gemm_f8 or gemm_f8_block:
  *
  *     s = X[i] + R[i]                    S[i] := s
  *     rstd[i] := (mean_j s_j^2 + eps)^-1/2
@@ -446,8 +446,11 @@ typedef enum { DGEMM_ROWS_SAME = 0, DGEMM_ROWS_F8 = 1, DGEMM_ROWS_F8_BLOCK = 2 }
  *
  * in: the format of X, R, S and a DGEMM_ROWS_SAME Y (DGEMM_IN_F32, _BF16 or
  * _F16).  R (NULL: none), S and rstd (NULL: not wanted) are optional; scale is
- * given with DGEMM_ROWS_F8 and only then.  weight: N fp32 values, 16-byte
- * aligned.  All arithmetic is fp32 on the unrounded sum, each output rounded
+ * given with the 8-bit outputs and only with them: M values with DGEMM_ROWS_F8;
+ * with DGEMM_ROWS_F8_BLOCK M * ceil(N / 128) of them, row i's for columns
+ * 128 b .. 128 b + 127 at scale[b * M + i], by the largest of those columns alone
+ * and with the quotient rounded once, as quant_f8_block's.  weight: N fp32 values,
+ * 16-byte aligned.  All arithmetic is fp32 on the unrounded sum, each output rounded
  * once.  S and Y may each be X or R itself (same pointer, pitch and format).
  * A row holding an infinity or a NaN gets scale NaN in 8 bits.  1 <= N <= 32768
  * (DGEMM_ERR_TOO_LARGE above); M == 0 or N == 0 is a no-op; eps >= 0.  Rows obey
