@@ -3,9 +3,11 @@
 //
 // Per row: s = x + r, S := s, then
 //   root-mean-square norm: y = s rstd w, rstd = (mean s^2 + eps)^-1/2
-//   layer norm: y = (s - mean) rstd w + b, rstd = (mean (s - mean)^2 + eps)^-1/2; the
-//     deviations are squared from registers once the mean is known, since
-//     mean s^2 - mean^2 cancels where the mean is large
+//   layer norm: y = (s - mean) rstd w + b, rstd = (mean (s - mean)^2 + eps)^-1/2.  An fp32
+//     sum gives the mean to a few half steps of |s|, many of the deviations' where the mean
+//     is large.  So the deviations from it, d = s - m in registers, are summed beside their
+//     squares (one barrier for both): c = mean d is what m lacks, d - c are the deviations
+//     and mean d^2 - c^2 their variance, where nothing cancels as it does in mean s^2 - mean^2
 // and Y := y or, in 8 bits, Y := e4m3(y / scale) with scale = max(max|y| / 448, 2^-100)
 // over the row or over each block of 128 of its columns.  The quantizer alone is the
 // same pass without the norm.
@@ -38,6 +40,29 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
     for (int i = 1; i < T / 64; ++i) s += red[i];
     return s;
+}
+// Two sums over the T threads that share a row, with one barrier; red: T / 64 words each.
+template <int T>
+__device__ __forceinline__ void row_sum2(float& x, float& y, float (*red)[(T < 256 ? 256 : T) / 64]) {
+#pragma unroll
+    for (int m = (T < 64 ? T : 64) / 2; m > 0; m >>= 1) {
+        x += __shfl_xor(x, m);
+        y += __shfl_xor(y, m);
+    }
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0) {
+            red[0][threadIdx.x >> 6] = x;
+            red[1][threadIdx.x >> 6] = y;
+        }
+        __syncthreads();
+        x = red[0][0];
+        y = red[1][0];
+#pragma unroll
+        for (int i = 1; i < T / 64; ++i) {
+            x += red[0][i];
+            y += red[1][i];
+        }
+    }
 }
 template <int T>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
@@ -165,7 +190,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
     using P = Place<T>;
     constexpr bool CENTER = MODE >= LN, PLAIN = MODE == NORM || MODE == LN;
     constexpr bool BLOCKS = MODE == NORM_F8B || MODE == LN_F8B;
-    __shared__ float red_s[P::WG / 64];
+    __shared__ float red_s[CENTER ? 2 : 1][P::WG / 64];
     __shared__ float red_c[CENTER ? P::WG / 64 : 1];
     __shared__ uint32_t red_m[P::WG / 64];
     const P pl;
@@ -205,26 +230,38 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
                 o.store(rs, at(i, a.lds, ES), a.N - col(i));
             }
         }
+        float ss = 0.0f, rstd;
         if constexpr (CENTER) {
-            float sum = 0.0f;
+            float sum = 0.0f, sd = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) sum += v[i][j];
-            const float mean = row_sum<T>(sum, red_c) / (float)a.N;
-            if (a.mean && pl.t == 0 && row < a.M) a.mean[row] = mean;
+            const float m = row_sum<T>(sum, red_c) / (float)a.N;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = col(i) + j < a.N ? v[i][j] - mean : 0.0f;
+                for (int j = 0; j < 8; ++j) {
+                    v[i][j] = col(i) + j < a.N ? v[i][j] - m : 0.0f;
+                    sd += v[i][j];
+                    ss += v[i][j] * v[i][j];
+                }
+            row_sum2<T>(sd, ss, red_s);
+            const float c = sd / (float)a.N, var = ss / (float)a.N - c * c;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] -= c;  // past N: fed to nothing stored
+            rstd = rsqrtf((var < 0.0f ? 0.0f : var) + a.eps);
+            if (a.mean && pl.t == 0 && row < a.M) a.mean[row] = c == c ? m + c : m;  // infinite: m
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
+            ss = row_sum<T>(ss, red_s[0]);
+            rstd = rsqrtf(ss / (float)a.N + a.eps);
         }
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss += v[i][j] * v[i][j];
-        ss = row_sum<T>(ss, red_s);
-        const float rstd = rsqrtf(ss / (float)a.N + a.eps);
         if (a.rstd && pl.t == 0 && row < a.M) a.rstd[row] = rstd;
         const auto rw = make_rsrc((const char*)a.weight, (int64_t)a.N * 4);
 #pragma unroll

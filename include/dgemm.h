@@ -499,8 +499,9 @@ int rmsnorm_bwd_workspace(int M, int N, size_t* required);
  *     y = (s - mean[i]) * rstd[i] * weight + bias    Y[i] := y,  or in 8 bits as rmsnorm
  *
  * bias: NULL (none) or N fp32 values, 16-byte aligned.  mean, rstd (NULL: not wanted): M fp32
- * values each.  The deviations are squared after the mean is known, from registers: rows with a
- * mean far from zero lose nothing.  DGEMM_ROWS_F8: scale[i] per row (its strides are not looked
+ * values each.  The deviations are taken from registers and centred once more before they are
+ * squared: Y and rstd are off by half steps of the deviations, not of a mean far from zero
+ * (s, the fp32 sum with R, and mean[i] are each rounded to fp32).  DGEMM_ROWS_F8: scale[i] per row (its strides are not looked
  * at); DGEMM_ROWS_F8_BLOCK: block b of row i at scale[i * scale_row + b * scale_block], kept apart
  * from each other (DGEMM_ERR_LEADING_DIM otherwise).  Otherwise as rmsnorm.
  */
