@@ -200,12 +200,12 @@ def matmul_f8(A, B, scale_a, scale_b, *, bias=None, act: str = "none", residual=
 
 def _norm_results(X, residual, f8):
     """What a norm's allocating form returns first: "Y", "scale" with f8, "total" with a residual."""
-    if f8 not in (False, True, "row", "block"):
+    if isinstance(f8, str) and f8 not in ("row", "block"):
         raise ValueError("f8 must be False, True (a scale per row), 'row' or 'block'")
     _device_tensor(X, "X")
     M, N = X.shape
     out = {"Y": _empty(M, N, F8 if f8 else X.dtype, X.device)}
-    if f8 == "block":
+    if isinstance(f8, str) and f8 == "block":
         out["scale"] = _block_scales(M, N, X.device)
     elif f8:
         out["scale"] = torch.empty(M, dtype=torch.float32, device=X.device)

@@ -26,6 +26,25 @@ def test_the_header_names_the_block_scales():
     assert "DGEMM_ROWS_F8 and only then" not in text
 
 
+@pytest.mark.parametrize("f8", [None, 0, 1, 2, False, True, "row", "block"])
+def test_norms_take_any_truth_value(f8):
+    """f8 is a truth value, or names the scales; other names are refused."""
+    x, w = torch.ones(4, 16), torch.ones(16)
+    for norm in (dg.rms_norm, dg.layer_norm):
+        with pytest.raises(ValueError, match="device tensor"):
+            norm(x, w, f8=f8)
+        for name in ("rows", "e4m3", ""):
+            with pytest.raises(ValueError, match="f8 must be"):
+                norm(x, w, f8=name)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("f8", [None, 0, 2, True])
+def test_truth_values_on_the_device(f8):
+    x, w = torch.ones(4, 16, device="cuda"), torch.ones(16, device="cuda")
+    assert ("scale" in dg.rms_norm(x, w, f8=f8)) == bool(f8)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M, N", [(1, 1), (1, 129), (3, 128), (5, 1000), (17, 257), (300, 4096)])
 def test_block_scales_where_the_header_says(M, N):
