@@ -517,11 +517,12 @@ hipError_t go(const GemmLaunch& L, const BlockScales& s) {
     int kchunk = L.kchunk;
     int64_t zs = L.c_zstride;
     if (L.slice_waves > 0) {
-        if (L.splits != 1) return hipErrorInvalidValue;
         const void* fn = nullptr;
-        if (L.tbm == 32 && L.slice_waves == 8) fn = (const void*)block_slice_kernel<IN, OUT, 1, NB>;
-        if (L.tbm == 64 && L.slice_waves == 4) fn = (const void*)block_slice_kernel<IN, OUT, 2, NB>;
-        if (!fn || L.tbm != L.tbn) return hipErrorInvalidValue;
+        if constexpr (!(IN == IN_F8 && OUT == OUT_F32)) {  // that is a K split's, and slices have none
+            if (L.tbm == 32 && L.slice_waves == 8) fn = (const void*)block_slice_kernel<IN, OUT, 1, NB>;
+            if (L.tbm == 64 && L.slice_waves == 4) fn = (const void*)block_slice_kernel<IN, OUT, 2, NB>;
+        }
+        if (!fn || L.tbm != L.tbn || L.splits != 1) return hipErrorInvalidValue;
         void* args[] = {&a, &e};
         return hipLaunchKernel(fn, dim3((unsigned)(L.tiles_m * L.tiles_n)), dim3(64 * L.slice_waves), args, 0,
                                L.stream);
