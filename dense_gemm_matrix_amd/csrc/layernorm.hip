@@ -19,6 +19,30 @@
 namespace dgemm {
 namespace {
 
+// Two sums over the T threads that share a row, with one barrier; red: T / 64 words each.
+template <int T>
+__device__ __forceinline__ void row_sum2(float& x, float& y, float (*red)[Place<T>::WG / 64]) {
+#pragma unroll
+    for (int m = (T < 64 ? T : 64) / 2; m > 0; m >>= 1) {
+        x += __shfl_xor(x, m);
+        y += __shfl_xor(y, m);
+    }
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0) {
+            red[0][threadIdx.x >> 6] = x;
+            red[1][threadIdx.x >> 6] = y;
+        }
+        __syncthreads();
+        x = red[0][0];
+        y = red[1][0];
+#pragma unroll
+        for (int i = 1; i < T / 64; ++i) {
+            x += red[0][i];
+            y += red[1][i];
+        }
+    }
+}
+
 template <int FMT>
 hipError_t ln_by_rows(const RowArgs& a, int rows, hipStream_t s) {
     if (rows == ROWS_F8_BLOCK) return row_by_size<FMT, LN_F8B>(a, s);

@@ -41,26 +41,46 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     for (int i = 1; i < T / 64; ++i) s += red[i];
     return s;
 }
-// Two sums over the T threads that share a row, with one barrier; red: T / 64 words each.
+// K sums over the T threads that share a row, with one barrier; red: T / 64 words each.  The lanes
+// of a wave trade values by DPP and lane swaps, not through LDS as __shfl_xor does: a layer norm's
+// sums are what a short row waits for (1 x 4096 bf16 with its residual 2.8 us, through LDS 3.2).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
 template <int T>
-__device__ __forceinline__ void row_sum2(float& x, float& y, float (*red)[(T < 256 ? 256 : T) / 64]) {
-#pragma unroll
-    for (int m = (T < 64 ? T : 64) / 2; m > 0; m >>= 1) {
-        x += __shfl_xor(x, m);
-        y += __shfl_xor(y, m);
+__device__ __forceinline__ float lane_sum(float v) {
+    v += dpp<0xb1>(v);   // neighbours within pairs
+    v += dpp<0x4e>(v);   // pairs within four lanes, which then hold the same
+    v += dpp<0x141>(v);  // mirrored within eight
+    v += dpp<0x140>(v);  // mirrored within 16
+    typedef uint32_t pair __attribute__((ext_vector_type(2)));
+    if constexpr (T >= 32) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        const pair p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        v = as_float(p[0]) + as_float(p[1]);
     }
-    if constexpr (T > 64) {
-        if ((threadIdx.x & 63) == 0) {
-            red[0][threadIdx.x >> 6] = x;
-            red[1][threadIdx.x >> 6] = y;
-        }
-        __syncthreads();
-        x = red[0][0];
-        y = red[1][0];
+    if constexpr (T >= 64) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        const pair p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        v = as_float(p[0]) + as_float(p[1]);
+    }
+    return v;
+}
+template <int T, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (*red)[(T < 256 ? 256 : T) / 64]) {
 #pragma unroll
-        for (int i = 1; i < T / 64; ++i) {
-            x += red[0][i];
-            y += red[1][i];
+    for (int k = 0; k < K; ++k) v[k] = lane_sum<T>(v[k]);
+    if constexpr (T > 64) {
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int k = 0; k < K; ++k) red[k][threadIdx.x >> 6] = v[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            v[k] = red[k][0];
+#pragma unroll
+            for (int i = 1; i < T / 64; ++i) v[k] += red[k][i];
         }
     }
 }
@@ -191,7 +211,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
     constexpr bool CENTER = MODE >= LN, PLAIN = MODE == NORM || MODE == LN;
     constexpr bool BLOCKS = MODE == NORM_F8B || MODE == LN_F8B;
     __shared__ float red_s[CENTER ? 2 : 1][P::WG / 64];
-    __shared__ float red_c[CENTER ? P::WG / 64 : 1];
+    __shared__ float red_c[1][CENTER ? P::WG / 64 : 1];
     __shared__ uint32_t red_m[P::WG / 64];
     const P pl;
     const int64_t row0 = (int64_t)blockIdx.x * P::RPW + P::first();
@@ -230,29 +250,27 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
                 o.store(rs, at(i, a.lds, ES), a.N - col(i));
             }
         }
-        float ss = 0.0f, rstd;
+        float ss = 0.0f, rstd, off = 0.0f;  // y = (v rstd - off) w + b
         if constexpr (CENTER) {
-            float sum = 0.0f, sd = 0.0f;
+            float sum[1] = {0.0f}, d[2] = {0.0f, 0.0f};
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) sum += v[i][j];
-            const float m = row_sum<T>(sum, red_c) / (float)a.N;
+                for (int j = 0; j < 8; ++j) sum[0] += v[i][j];
+            row_sums<T>(sum, red_c);
+            const float m = sum[0] / (float)a.N;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     v[i][j] = col(i) + j < a.N ? v[i][j] - m : 0.0f;
-                    sd += v[i][j];
-                    ss += v[i][j] * v[i][j];
+                    d[0] += v[i][j];
+                    d[1] += v[i][j] * v[i][j];
                 }
-            row_sum2<T>(sd, ss, red_s);
-            const float c = sd / (float)a.N, var = ss / (float)a.N - c * c;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] -= c;  // past N: fed to nothing stored
+            row_sums<T>(d, red_s);
+            const float c = d[0] / (float)a.N, var = d[1] / (float)a.N - c * c;
             rstd = rsqrtf((var < 0.0f ? 0.0f : var) + a.eps);
+            off = c * rstd;
             if (a.mean && pl.t == 0 && row < a.M) a.mean[row] = c == c ? m + c : m;  // infinite: m
         } else {
 #pragma unroll
@@ -271,7 +289,8 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void row_kernel(RowArgs a) {
             float w[8];
             w8.get(w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+            for (int j = 0; j < 8; ++j)
+                v[i][j] = (CENTER ? __builtin_fmaf(v[i][j], rstd, -off) : v[i][j] * rstd) * w[j];
         }
         if constexpr (CENTER) {
             if (a.bias) {
@@ -365,10 +384,12 @@ hipError_t row_by_size(const RowArgs& a, hipStream_t s) {
     if (a.N <= 512) return go_row<FMT, MODE, 64, 1>(a, s);
     if (a.N <= 1024) return go_row<FMT, MODE, 64, 2>(a, s);
     if (a.N <= 2048) return go_row<FMT, MODE, 256, 1>(a, s);
-    // Rows that have a CU each: eight columns per thread, for the time of one row (8-bit blocks, bf16, 8
-    // and 16 columns per thread or more: 1 x 4096 3.8 and 4.4 us, 1 x 8192 4.7 and 6.4, 256 x 8192 6.1
-    // and 7.8; plain output 256 x 4096 4.0 and 4.05, 1000 x 4096 6.9 and 6.5).  The order of a row's sums
-    // differs, so the root-mean-square norm's other outputs keep one width.
+    // Rows that have a CU each: eight columns per thread, for the time of one row (bf16, us, 8 and 16
+    // columns per thread or more: 8-bit blocks 1 x 4096 3.3 and 3.8, 1 x 8192 4.3 and 5.7, 256 x 8192 5.4
+    // and 6.7, root-mean-square 1 x 8192 3.6 and 5.2; a scale per row 1 x 8192 4.3 and 4.5; plain output
+    // 256 x 3000 3.1 and 3.4, 1 x 4096 2.6 both, 256 x 8192 4.2 and 4.1).  The order of a row's sums
+    // differs, and so its last bits between the two sides of this rule; the root-mean-square norm's other
+    // outputs, which were there before it, keep one width.
     if constexpr (MODE >= NORM_F8B) {
         if (a.M <= NUM_CU && a.N > 2048 && a.N <= 4096) return go_row<FMT, MODE, 512, 1>(a, s);
         if (a.M <= NUM_CU && a.N > 4096 && a.N <= 8192) return go_row<FMT, MODE, 1024, 1>(a, s);
