@@ -122,6 +122,12 @@ __global__ __launch_bounds__(64 * W) void act_grad_kernel(ActGradArgs a) {
 
 // The same for a gated layer: dG = dC U act'(G) and dU = dC act(G), with both column sums.  Bound by
 // memory too, five arrays instead of three.
+//
+// In 16 bits dG and dU are rounded to the operands' format, since the products that read them run at
+// the 16-bit matrix rate (a second term for what the rounding drops would double their work): the
+// gradients are off by 2.3e-3 of their 2-norm in bf16 and 2.9e-4 in fp16, where products of the
+// unrounded values give, with the results' own rounding, 1.7e-3 and 2.1e-4.  The column sums take the
+// unrounded values.
 template <int CF, int DF, int W, int T>
 __global__ __launch_bounds__(64 * W) void gated_grad_kernel(GatedGradArgs a) {
     constexpr int RP = 64 / T;  // rows per wave and pass

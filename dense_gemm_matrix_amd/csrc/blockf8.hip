@@ -19,7 +19,7 @@
 // The vector unit adds to ordinary registers only, not to the accumulation half of the register
 // file, so a wave cannot hold 256 running sums as gemmt.hip's do: a wave owns 128 x 64 outputs
 // (256 x 256 tile, 8 waves, two to a SIMD) or 64 x 64 (128 x 128 tile, 4 waves, two workgroups
-// to a CU), and one wave's instructions fill the other's waits.  4096^3, bf16 C: 63-66 us with
+// to a CU), and one wave's instructions fill the other's waits.  4096^3, bf16 C: 62-67 us with
 // a scale per 128 x 128 (2.1 PFLOP/s; gemm_f8 with a scale per row 58-61), 70.5 with one per
 // row and block.
 //

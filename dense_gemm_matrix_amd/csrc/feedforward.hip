@@ -165,7 +165,17 @@ GatedPlan gated_pieces(int bm, int bn, int bk, int M, int N, int K, int splits, 
 // At most SKINNY_M rows: as plan_skinny's strips of B stored along the output, of both weights,
 // but never of 128 columns (two weights' loads are as wide as one's twice: 1 x 14336 x 4096 bf16, weights
 // from the last-level cache, 32 / 64 / 128 columns 43.8 / 37.4 / 38.4 us), and split from the same K on
-// in fp32.
+// in fp32.  From HBM, us, the fastest unsplit / this rule's plan (pieces):
+//            bf16                  fp32
+//    1 x  1024 x  1024    7.2 /  7.3 (1)     9.3 /  9.5 (1)
+//    1 x   512 x  8192   54.9 / 12.7 (16)   66.2 / 16.4 (16)
+//    1 x  1024 x  4096   30.0 / 11.3 (15)   34.4 / 14.9 (15)
+//    1 x  4096 x  4096   32.8 / 19.5 (4)    38.0 / 32.7 (4)
+//   16 x  4096 x  4096   35.4 / 20.7 (4)    42.2 / 33.9 (4)
+//    1 x  4096 x 11008   79.9 / 39.3 (4)    96.9 / 72.0 (4)
+//    1 x  8192 x  2048   21.0 / 21.7 (1)    25.8 / 25.9 (1)   (two pieces 19.0, 29.7)
+//    1 x 11008 x  4096   37.5 / 37.6 (1)    73.3 / 73.6 (1)   (four pieces 38.6, 70.7)
+//    1 x 14336 x  4096   47.3 / 47.9 (1)    86.0 / 85.8 (1)   (two pieces 51.5, 88.9)
 GatedPlan plan_gated_skinny(int in, int M, int N, int K, uint64_t ws) {
     auto strips = [&](int cols, int waves, int splits) {  // splits = 0 if it does not fit
         GatedPlan p = gated_pieces(SKINNY_M, cols, 32, M, N, K, splits, UINT64_MAX);
@@ -465,7 +475,9 @@ GatedBwdPlan plan_gated_bwd(int in, int M, int N, int K, bool dA, bool dB, uint6
 //          4 x 2228 x 3330   27.9 / 23.9            4 x 2228 x 3330   42.4 / 96.0
 //         16 x 4096 x 4096   54.7 / 40            16 x 4096 x 1024   60.0 / 55.5
 //          8 x 8192 x 4096   70.9 / 66.5            8 x 8192 x 4096    177 /  298
-// (16-bit, from the fourth row on, with dA's sums in runs.)
+// (16-bit, from the fourth row on, with dA's sums in runs.)  fp32 layers above the small ones all take
+// the kernels for few rows, 16 x 4096 x 1024 among them: the plan is close there and far behind at more
+// columns or terms.
 bool few_rows(int in, int M, int N, int K, const GatedBwdPlan& p) {
     const bool small = N <= 1024 && (int64_t)N * K <= 1 << 20;
     return M <= SKINNY_M && (M == 0 || (!small && (in == IN_F32 || p.ws_bytes == 0)));

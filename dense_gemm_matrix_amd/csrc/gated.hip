@@ -10,7 +10,7 @@
 // each of its outputs (accumulator blocks 0 .. NJ - 1 are G's, the rest U's) and the
 // activation and the product cost no memory traffic.  Compared with two products, A's loads
 // and LDS reads are halved, and U is neither written nor read back: bf16 8192 x 8192 x
-// 4096, G and U kept for the backward pass, 933 us (1.18 PFLOP/s, at the power cap).
+// 4096, G and U kept for the backward pass, 908 to 950 us (1.16 to 1.21 PFLOP/s, at the power cap).
 //
 // The two weights are separate matrices (or windows of one; their row pitches may
 // differ).  A direct-to-LDS load takes one base for its 64 lanes, so each weight has its

@@ -311,7 +311,8 @@ int gemm_act_plan(int in, int out, int M, int N, int K, size_t workspace_bytes,
  * The residual's gradient is dC itself.  dA, dB and dbias may each be NULL
  * (not wanted); A is read only for dB, B only for dA, and with act =
  * DGEMM_ACT_NONE Z is not read.  relu'(0) = 0.  dZ is rounded once to the input
- * format for the products (unless it is dC itself); dbias sums unrounded fp32
+ * format for the products (unless it is dC itself), in fp16 to infinity beyond 65504
+ * and to zero below 2^-25; dbias sums unrounded fp32
  * values, in an order that depends on the shape only.  Results are
  * deterministic; the products' order of sums follows the plan, which depends on
  * the sizes, formats, workspace and which of dA and dB are wanted (small
@@ -393,8 +394,9 @@ int gemm_f8_plan(int out, int M, int N, int K, size_t workspace_bytes,
  * each other (sa_row = 1) load fastest.  256 rows' scales span less than 2 GiB.
  *
  * Sums between blocks are fp32.  Within a block: exactly fp32 for fp32 C and for at most 16
- * rows; for 16-bit C the 8-bit matrix instruction, which drops bits below 2^-13 of the largest
- * of neighbouring products.  out, bias, act, R, workspace, errors and execution as gemm_f8.
+ * rows; for 16-bit C of more rows the 8-bit matrix instruction, which drops bits below 2^-13 of the
+ * largest of neighbouring products (against 64 bits no more than C's rounding shows).  out, bias,
+ * act, R, workspace, errors and execution as gemm_f8.
  */
 int gemm_f8_block(int out, int rows_b, int M, int N, int K,
                   const void* A, int lda,
@@ -501,9 +503,12 @@ int rmsnorm_bwd_workspace(int M, int N, size_t* required);
  * bias: NULL (none) or N fp32 values, 16-byte aligned.  mean, rstd (NULL: not wanted): M fp32
  * values each.  The deviations are taken from registers and centred once more before they are
  * squared: Y and rstd are off by half steps of the deviations, not of a mean far from zero
- * (s, the fp32 sum with R, and mean[i] are each rounded to fp32).  DGEMM_ROWS_F8: scale[i] per row (its strides are not looked
- * at); DGEMM_ROWS_F8_BLOCK: block b of row i at scale[i * scale_row + b * scale_block], kept apart
- * from each other (DGEMM_ERR_LEADING_DIM otherwise).  Otherwise as rmsnorm.
+ * (s, the fp32 sum with R, and mean[i] are each rounded to fp32).  DGEMM_ROWS_F8: scale[i] per row
+ * (its strides are not looked at); DGEMM_ROWS_F8_BLOCK: block b of row i at scale[i * scale_row +
+ * b * scale_block], kept apart from each other (DGEMM_ERR_LEADING_DIM otherwise).  The order of a
+ * row's sums depends on N and on whether M exceeds 256 (the same holds for rmsnorm with
+ * DGEMM_ROWS_F8_BLOCK): a row's last bits may differ between batches on either side.  Otherwise as
+ * rmsnorm.
  */
 int layernorm(int in, int out, int M, int N,
               const void* X, int ldx,
@@ -598,7 +603,9 @@ int gemm_gated_plan(int in, int out, int M, int N, int K, size_t workspace_bytes
  *     dbias_g, dbias_u := column sums of dG and dU        (fp32)
  *
  * Each output may be NULL (not wanted); A is read only for dBg and dBu, Bg and Bu only for dA.
- * relu'(0) = 0.  dG and dU are rounded once to the input format for the products; dA's two products
+ * relu'(0) = 0.  dG and dU are rounded once to the input format for the products (of 16-bit layers:
+ * the matrix instructions take them so; in fp16 values beyond 65504 become infinite, and dA and the
+ * weights' gradients with them, and values below 2^-25 zero: scale dC for that range); dA's two products
  * are one fp32 sum; the biases' sums take unrounded fp32 values.  Results are deterministic; the order
  * of sums follows the plan, as for gemm_act_bwd, and so do empty sums, aliasing, limits of M for
  * fp32 weights' gradients, and the workspace (`required` bytes of gemm_gated_bwd_workspace hold dG,
