@@ -41,9 +41,9 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     for (int i = 1; i < T / 64; ++i) s += red[i];
     return s;
 }
-// K sums over the T threads that share a row, with one barrier; red: T / 64 words each.  The lanes
-// of a wave trade values by DPP and lane swaps, not through LDS as __shfl_xor does: a layer norm's
-// sums are what a short row waits for (1 x 4096 bf16 with its residual 2.8 us, through LDS 3.2).
+// The sum over T lanes of a wave (64 for T above), the same bits in each.  The lanes trade values by
+// DPP and lane swaps, not through LDS as __shfl_xor does: a layer norm's sums are what a short row
+// waits for (1 x 4096 bf16 with its residual 2.8 us, through LDS 3.2).
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
@@ -67,6 +67,7 @@ __device__ __forceinline__ float lane_sum(float v) {
     }
     return v;
 }
+// K sums over the T threads that share a row, with one barrier; red: T / 64 words each.
 template <int T, int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], float (*red)[(T < 256 ? 256 : T) / 64]) {
 #pragma unroll
